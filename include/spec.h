@@ -431,6 +431,132 @@ int spec_lmhead_argmax_noalloc(const float* x_dev, int T, int hidden, int vocab,
                                int w_dtype, const float* gamma_dev, float eps, int32_t* out_tokens_dev,
                                uintptr_t cuda_stream);
 
+/* ---- tree verification (kernel-level entry points) -------------------------
+ * One forward can score several candidates for each position when the drafts
+ * form a tree ("End-to-end OCR expert model architecture and acceleration
+ * principles", section 6.1: the target scores every drafted position in one
+ * forward and keeps the path that agrees with it). Node i of sequence s has
+ * parent parents[s][i] < i, or -1 for a root; node 0 is the sequence's last
+ * committed token and its key and value, like every node's, sit in the cache
+ * slot n + i, right after the n = cache_len[s] committed positions (RoPE goes
+ * by n + depth, which is the caller's). A step is then
+ *   spec_tree_attention in every layer, the LM head, spec_tree_commit,
+ * with spec_token_logprobs on the same logits; spec_kv_copy_pages gives a
+ * forked sequence its own copy of a page that both would write.
+ *
+ * The cache of these entry points, the layout of a model's own pool. Device
+ * pointers, caller-owned; the struct itself is read during the call only. */
+typedef struct spec_kv_view {
+  void* kv_dev;          /* [n_pages][n_layers][n_kv_heads][2 (K, V)][page_size][head_dim], 16-byte aligned */
+  const int32_t* block_table_dev;   /* [n_seq][max_pages] page ids: entry i holds positions [i P, (i + 1) P) */
+  int32_t dtype;         /* SPEC_F32 or SPEC_BF16 */
+  int32_t n_pages, n_layers, n_kv_heads;
+  int32_t page_size;     /* P: a multiple of 16 */
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t max_pages;     /* row length of the block table */
+} spec_kv_view;
+
+#define SPEC_TREE_MAX_NODES 64      /* nodes of a tree, its root among them */
+/* Bits that the entry points below OR into *err_dev (device int, caller-owned,
+ * never cleared by them): */
+#define SPEC_DEV_ERR_PAGE 1         /* a needed page id is outside [0, n_pages) */
+#define SPEC_DEV_ERR_POS 4          /* cache_len < 0, n_nodes outside [0, max_nodes], or both past the block table */
+#define SPEC_DEV_ERR_TIMEOUT 8      /* a bounded wait inside a kernel ran out (not expected) */
+#define SPEC_DEV_ERR_TREE 16        /* a parent outside [-1, i) */
+
+/* Attention of n_seq trees over the paged cache, one layer. With A(i) node i
+ * and the nodes above it, the row of (node i, query head h) is
+ *   out = sum_j w_j V_j,  w = softmax over j of scale * q.K_j,
+ *   j over the n committed positions and the slots n + A(i),
+ * on kv head h / (n_q_heads / n_kv_heads).
+ *   q_dev, out_dev [n_seq][max_nodes][n_q_heads][head_dim] in the cache's
+ *     dtype, 16-byte aligned; rows of nodes >= n_nodes[s] are neither read
+ *     into a result nor written.
+ *   cache_len_dev [n_seq], n_nodes_dev [n_seq] (0: a padded sequence, nothing
+ *     is written), parents_dev [n_seq][max_nodes].
+ *   ws_dev: spec_tree_attention_ws_bytes bytes of device memory, 16-byte
+ *     aligned; needs no initialisation; one call at a time per workspace.
+ * Scores, softmax statistics and sums are fp32; bf16 results are rounded once.
+ * Slots past n + n_nodes[s] may hold anything. Every slot up to there has to
+ * hold finite keys and values (a NaN of one node may reach the others). The
+ * same call gives the same bits; where a sequence's keys are cut into parts
+ * summed apart depends on the batch. A sequence with a bad length is left
+ * out (SPEC_DEV_ERR_POS); rows that need a bad page hold no usable value
+ * (SPEC_DEV_ERR_PAGE); a node with a bad parent counts as a root
+ * (SPEC_DEV_ERR_TREE). Errors: SPEC_ERR_ARG; SPEC_ERR_UNSUPPORTED (head_dim,
+ * dtype, more than 128 query heads per kv head); SPEC_ERR_CUDA. */
+int64_t spec_tree_attention_ws_bytes(const spec_kv_view* kv, int n_seq, int max_nodes, int n_q_heads);
+int spec_tree_attention(const spec_kv_view* kv, int layer, const void* q_dev, int n_seq, int max_nodes,
+                        int n_q_heads, const int32_t* cache_len_dev, const int32_t* n_nodes_dev,
+                        const int32_t* parents_dev, float scale, void* out_dev, void* ws_dev, size_t ws_bytes,
+                        int32_t* err_dev, uintptr_t cuda_stream);
+
+/* Accept and commit n_seq verified trees: the walk
+ *   path_0 = 0, path_(j+1) = the lowest node c > path_j with parent path_j and
+ *   tokens[c] = target[path_j],
+ * ends at the first node without such a child, after a accepted drafts; the
+ * cache rows of the path, in every layer and head, move to the slots
+ * n, n + 1, .., n + a. target[i] is the model's token after node i: its argmax
+ * gives the greedy rule, a draw from its distribution keeps the output
+ * distributed as the model's own (the drafts only decide how far one step
+ * gets). tokens, target, parents: [n_seq][max_nodes] int32 (tokens[s][0] is
+ * not read).
+ *   out_accepted_dev [n_seq]: a; out_token_dev [n_seq]: target[path_a], to be
+ *   appended; out_path_dev [n_seq][max_nodes]: path_0 .. path_a, then -1;
+ *   out_len_dev [n_seq]: n + a + 1 (not cache_len_dev itself, SPEC_ERR_ARG:
+ *   other blocks of the call still read n; swap the two after a step).
+ * A padded sequence (n_nodes 0), one with a bad length or one whose rows
+ * need a bad page is not moved and gives a = -1, token -1, no path, and n.
+ * A sequence whose pages are shared with others has to own the pages it
+ * writes. Errors: SPEC_ERR_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA. */
+int spec_tree_commit(const spec_kv_view* kv, int n_seq, int max_nodes, const int32_t* tokens_dev,
+                     const int32_t* parents_dev, const int32_t* n_nodes_dev, const int32_t* target_dev,
+                     const int32_t* cache_len_dev, int32_t* out_accepted_dev, int32_t* out_token_dev,
+                     int32_t* out_path_dev, int32_t* out_len_dev, int32_t* err_dev, uintptr_t cuda_stream);
+
+/* Copy n whole pages (every layer and head): page dst[i] <- page src[i].
+ * block_table_dev is not used and may be NULL. A source may feed several
+ * copies; a page that is the destination of two pairs, or of one and the
+ * source of another, ends with unspecified values. A pair with an id of -1 is
+ * skipped (a padded list); one with an id past the pool is skipped too
+ * (SPEC_DEV_ERR_PAGE). src_dev, dst_dev: [n] int32, n >= 0.
+ * Errors: SPEC_ERR_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA. */
+int spec_kv_copy_pages(const spec_kv_view* kv, const int32_t* src_dev, const int32_t* dst_dev, int n,
+                       int32_t* err_dev, uintptr_t cuda_stream);
+
+/* Log probabilities of given tokens, with entropy, rank and the likeliest
+ * alternatives, in one pass over the logits. With x_v = logits[r][v] /
+ * temperature and p the softmax of x, for each row r:
+ *   out_logprob[r]  = log p(tokens[r]);
+ *   out_rank[r]     = 1 + how many v come before tokens[r], larger logits
+ *                     first and equal ones by index;
+ *   out_entropy[r]  = -sum_v p_v log p_v (a term with p_v = 0 is 0);
+ *   out_top_ids[r][j], out_top_logprobs[r][j]: the first top_n tokens of that
+ *                     order and their log probabilities.
+ * A row without a token (outside [0, vocab)) gives log probability NaN and
+ * rank 0. -inf logits are masked tokens: probability 0, log probability -inf.
+ * A row with a NaN or +inf logit, or with nothing but -inf, has NaN log
+ * probabilities and entropy (the formulas'); ids and ranks then order NaN
+ * like -inf.
+ *   logits_dev: rows of `vocab` values, dtype SPEC_F32 or SPEC_BF16, row r at
+ *     r * ld elements (ld >= vocab; no alignment beyond the element's).
+ *   tokens_dev [n_rows] int32, or NULL with out_logprob_dev and out_rank_dev
+ *     NULL; out_entropy_dev, out_rank_dev and out_logprob_dev may be NULL;
+ *     out_top_ids_dev, out_top_logprobs_dev [n_rows][top_n], NULL only when
+ *     top_n = 0. 0 <= top_n <= min(32, vocab), vocab <= 1048576.
+ *   ws_dev: a caller-owned device workspace of
+ *     spec_token_logprobs_ws_bytes(n_rows, vocab, top_n) bytes, 16-byte
+ *     aligned, zero-filled before its first use; every call leaves its
+ *     counters at zero again. One call at a time per workspace.
+ * Statistics are fp32, in a fixed order. Errors: SPEC_ERR_ARG,
+ * SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA. */
+#define SPEC_LOGPROB_MAX_TOP 32
+int64_t spec_token_logprobs_ws_bytes(int n_rows, int vocab, int top_n);
+int spec_token_logprobs(const void* logits_dev, int dtype, int64_t ld, int n_rows, int vocab,
+                        const int32_t* tokens_dev, float temperature, int top_n, float* out_logprob_dev,
+                        float* out_entropy_dev, int32_t* out_rank_dev, int32_t* out_top_ids_dev,
+                        float* out_top_logprobs_dev, void* ws_dev, size_t ws_bytes, uintptr_t cuda_stream);
+
 /* ---- paged KV allocator (host only; usable without a GPU) ---------------- */
 /* The same allocator the model uses, exposed for tests and tooling. Pages
  * hold page_size consecutive positions; a sequence's block table lists its

@@ -42,7 +42,13 @@ class spec_config(ctypes.Structure):
         "max_batch", "prefill_chunk")] + [("rope_theta", ctypes.c_float), ("rms_eps", ctypes.c_float)]
 
 
+class spec_kv_view(ctypes.Structure):
+    _fields_ = [("kv_dev", ctypes.c_void_p), ("block_table_dev", ctypes.c_void_p)] + [(n, ctypes.c_int32) for n in (
+        "dtype", "n_pages", "n_layers", "n_kv_heads", "page_size", "head_dim", "max_pages")]
+
+
 _I32P = ctypes.POINTER(ctypes.c_int32)
+_VIEWP = ctypes.POINTER(spec_kv_view)
 _lib: Optional[ctypes.CDLL] = None
 
 # (name, restype, argtypes) of every exported entry point
@@ -107,6 +113,19 @@ _SIGS = [
                                                 ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                 ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                                 ctypes.c_size_t, ctypes.c_size_t]),
+    ("spec_tree_attention_ws_bytes", ctypes.c_int64, [_VIEWP, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    ("spec_tree_attention", ctypes.c_int, [_VIEWP, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                           ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                           ctypes.c_void_p, ctypes.c_size_t]),
+    ("spec_tree_commit", ctypes.c_int, [_VIEWP, ctypes.c_int, ctypes.c_int] + [ctypes.c_void_p] * 10 +
+     [ctypes.c_size_t]),
+    ("spec_kv_copy_pages", ctypes.c_int, [_VIEWP, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                          ctypes.c_size_t]),
+    ("spec_token_logprobs_ws_bytes", ctypes.c_int64, [ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    ("spec_token_logprobs", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                           ctypes.c_void_p, ctypes.c_float, ctypes.c_int] + [ctypes.c_void_p] * 6 +
+     [ctypes.c_size_t, ctypes.c_size_t]),
     ("spec_strerror", ctypes.c_char_p, [ctypes.c_int]),
     ("spec_last_error", ctypes.c_char_p, []),
     ("spec_pool_create", ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
@@ -383,6 +402,57 @@ def spec_tc_gemm_test(a_dev, a2_dev, b_dev, b_lo_dev, M: int, N: int, K: int, du
     _check(lib().spec_tc_gemm_test(_ptr(a_dev), _ptr(a2_dev), _ptr(a_scale_dev), _ptr(a2_scale_dev), int(a_fp8),
                                    _ptr(b_dev), _ptr(b_lo_dev), M, N, K, dual, n_tile, k_split, flags,
                                    _ptr(out_dev), _ptr(err_dev), cuda_stream))
+
+
+# ---- tree verification -------------------------------------------------------
+SPEC_TREE_MAX_NODES = 64
+SPEC_LOGPROB_MAX_TOP = 32
+SPEC_DEV_ERR_PAGE, SPEC_DEV_ERR_POS, SPEC_DEV_ERR_TIMEOUT, SPEC_DEV_ERR_TREE = 1, 4, 8, 16
+
+
+def make_kv_view(kv_dev, block_table_dev, *, dtype: int, n_pages: int, n_layers: int, n_kv_heads: int, page_size: int,
+                 head_dim: int, max_pages: int) -> spec_kv_view:
+    """Cache description of the tree entry points; the tensors stay the caller's."""
+    return spec_kv_view(_ptr(kv_dev) or None, _ptr(block_table_dev) or None, dtype, n_pages, n_layers, n_kv_heads,
+                        page_size, head_dim, max_pages)
+
+
+def spec_tree_attention_ws_bytes(kv: spec_kv_view, n_seq: int, max_nodes: int, n_q_heads: int) -> int:
+    return _check(lib().spec_tree_attention_ws_bytes(ctypes.byref(kv), n_seq, max_nodes, n_q_heads))
+
+
+def spec_tree_attention(kv: spec_kv_view, layer: int, q_dev, n_seq: int, max_nodes: int, n_q_heads: int, cache_len_dev,
+                        n_nodes_dev, parents_dev, scale: float, out_dev, ws_dev, ws_bytes: int, err_dev,
+                        cuda_stream: int = 0) -> None:
+    _check(lib().spec_tree_attention(ctypes.byref(kv), layer, _ptr(q_dev), n_seq, max_nodes, n_q_heads,
+                                     _ptr(cache_len_dev), _ptr(n_nodes_dev), _ptr(parents_dev), float(scale),
+                                     _ptr(out_dev), _ptr(ws_dev), ws_bytes, _ptr(err_dev), cuda_stream))
+
+
+def spec_tree_commit(kv: spec_kv_view, n_seq: int, max_nodes: int, tokens_dev, parents_dev, n_nodes_dev, target_dev,
+                     cache_len_dev, out_accepted_dev, out_token_dev, out_path_dev, out_len_dev, err_dev,
+                     cuda_stream: int = 0) -> None:
+    _check(lib().spec_tree_commit(ctypes.byref(kv), n_seq, max_nodes, _ptr(tokens_dev), _ptr(parents_dev),
+                                  _ptr(n_nodes_dev), _ptr(target_dev), _ptr(cache_len_dev), _ptr(out_accepted_dev),
+                                  _ptr(out_token_dev), _ptr(out_path_dev), _ptr(out_len_dev), _ptr(err_dev),
+                                  cuda_stream))
+
+
+def spec_kv_copy_pages(kv: spec_kv_view, src_dev, dst_dev, n: int, err_dev, cuda_stream: int = 0) -> None:
+    _check(lib().spec_kv_copy_pages(ctypes.byref(kv), _ptr(src_dev), _ptr(dst_dev), n, _ptr(err_dev), cuda_stream))
+
+
+def spec_token_logprobs_ws_bytes(n_rows: int, vocab: int, top_n: int) -> int:
+    return _check(lib().spec_token_logprobs_ws_bytes(n_rows, vocab, top_n))
+
+
+def spec_token_logprobs(logits_dev, dtype: int, ld: int, n_rows: int, vocab: int, tokens_dev, temperature: float,
+                        top_n: int, out_logprob_dev, out_entropy_dev, out_rank_dev, out_top_ids_dev,
+                        out_top_logprobs_dev, ws_dev, ws_bytes: int, cuda_stream: int = 0) -> None:
+    _check(lib().spec_token_logprobs(_ptr(logits_dev), dtype, ld, n_rows, vocab, _ptr(tokens_dev), float(temperature),
+                                     top_n, _ptr(out_logprob_dev), _ptr(out_entropy_dev), _ptr(out_rank_dev),
+                                     _ptr(out_top_ids_dev), _ptr(out_top_logprobs_dev), _ptr(ws_dev), ws_bytes,
+                                     cuda_stream))
 
 
 def spec_strerror(code: int) -> str:
