@@ -199,6 +199,10 @@ int tc_make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t row
 // outside.
 int kv_make_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, int planes, int n_pages,
                 size_t page_elems);
+// The same dims with a box of 64 dims x box_keys keys of one half of one plane
+// (landing as [key][64], 128-byte swizzle), for the tree attention.
+int kv_make_half_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, int planes, int n_pages,
+                     size_t page_elems, int box_keys);
 // 3D byte tensor map over a stack of [rows][K] weight rows (esz bytes an
 // element) for the streamed expert GEMVs: box 128 bytes x box_rows rows x
 // box_chunks 128-byte chunks of K, landing as [chunk][row][128] with the
