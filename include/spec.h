@@ -538,8 +538,8 @@ int spec_kv_copy_pages(const spec_kv_view* kv, const int32_t* src_dev, const int
  * A row with a NaN or +inf logit, or with nothing but -inf, has NaN log
  * probabilities and entropy (the formulas'); ids and ranks then order NaN
  * like -inf.
- *   logits_dev: rows of `vocab` values, dtype SPEC_F32 or SPEC_BF16, row r at
- *     r * ld elements (ld >= vocab; no alignment beyond the element's).
+ *   logits_dev: n_rows <= 65535 rows of `vocab` values, dtype SPEC_F32 or
+ *     SPEC_BF16, row r at r * ld elements (ld >= vocab; no alignment beyond the element's).
  *   tokens_dev [n_rows] int32, or NULL with out_logprob_dev and out_rank_dev
  *     NULL; out_entropy_dev, out_rank_dev and out_logprob_dev may be NULL;
  *     out_top_ids_dev, out_top_logprobs_dev [n_rows][top_n], NULL only when

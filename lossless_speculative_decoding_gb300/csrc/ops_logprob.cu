@@ -1,10 +1,26 @@
 // Kernel-level entry point: log probabilities of given tokens, with entropy,
-// rank and the likeliest alternatives, from materialised logits.
+// rank and the likeliest alternatives, from materialised logits, in one pass
+// over them.
 //
-// With x = logits / T and m = max x: z = sum e^(x - m), log p(t) = x_t - m -
-// log z, entropy = log z - sum e^(x - m) (x - m) / z (two terms of one sign:
-// no cancellation). The order of tokens is (logit descending, index
-// ascending), NaN as -inf.
+// With m the largest logit x and y = (x - m) log2(e) / T (the difference first:
+// a row of the type's lowest values stays a row of equal ones): z = sum 2^y, log
+// p(t) = ln 2 (y_t - log2 z), and entropy = ln 2 (log2 z - sum 2^y y / z), two
+// terms of one sign, so that nothing cancels. The order of tokens is (logit
+// descending, index ascending), NaN as -inf.
+//
+// A row is cut into slices, one block each; a thread keeps a running (m, z,
+// sum) and a count of the logits that come before the token, batch by batch,
+// with the batch's maximum taken first. Alternatives: a warp holds the best 32
+// of what it has seen as sorted 64-bit keys (ordered logit, inverted index),
+// one per lane. An element joins the warp's pending buffer only if it is not
+// below the block's bound -- the largest n-th best value of any of its warps --
+// which the batch maximum decides for a whole batch at once; 32 pending keys
+// are sorted and merged at a time. The last block of a row to finish joins the
+// slices in their order (which block that is changes nothing).
+//
+// Bound: HBM. The logits are read once; some eight instructions a logit, one
+// of them an exponential, keep the SMs at about half to two thirds of their
+// issue rate while the logits stream.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -14,104 +30,381 @@
 namespace spec {
 namespace {
 
-constexpr int LP_THREADS = 512;
+typedef unsigned long long u64;
+
+constexpr int LP_THREADS = 256;
+constexpr int LP_WARPS = LP_THREADS / 32;
+constexpr int LP_UNROLL = 4;                     // 16-byte vectors a thread has in flight
+constexpr int LP_TILE = LP_THREADS * LP_UNROLL;  // vectors of a block's step
 constexpr int LP_MAX_VOCAB = 1 << 20;
+constexpr int LP_MAX_SLICES = 64;
+constexpr int LP_COUNTERS = 4096;                // rows of a call that may cut them into slices
+constexpr int LP_TOP = SPEC_LOGPROB_MAX_TOP;
+static_assert(LP_TOP == 32, "a warp's list has one key per lane");
+
+// What a slice leaves: statistics, and (behind them) its sorted keys.
+struct LpStats {
+  float m, z, zy;           // max x, sum 2^y, sum 2^y y
+  int before, bad;          // logits before the token; a NaN or +inf logit
+};
 
 struct LpArgs {
   const void* logits;
   int64_t ld;
-  int n_rows, vocab, top_n;
+  int n_rows, vocab, top_n, slices;
   const int32_t* tokens;
-  float it;                 // 1 / temperature
+  float it, c;              // 1 / temperature, log2(e) / temperature
   float* logprob;
   float* entropy;
   int32_t* rank;
   int32_t* top_ids;
   float* top_lp;
+  int* arrived;             // [LP_COUNTERS], zero between calls
+  LpStats* stats;           // [n_rows][slices]
+  u64* lists;               // [n_rows][slices][32]
 };
 
 template <class T> __device__ __forceinline__ float logit(const T* row, int v);
 template <> __device__ __forceinline__ float logit<float>(const float* row, int v) { return row[v]; }
 template <> __device__ __forceinline__ float logit<bf16_t>(const bf16_t* row, int v) { return bf16_to_f(row[v].v); }
 
-// (value, index) order: larger first, then the lower index.
-__device__ __forceinline__ bool before(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+__device__ __forceinline__ float lp_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Maximum that is NaN when either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-// One block per row: a pass for the maximum, one for the sums, one per
-// alternative.
-template <class T>
-__global__ void __launch_bounds__(LP_THREADS) k_logprob(LpArgs A) {
-  __shared__ float red[32];
-  __shared__ float bv[LP_THREADS / 32];
-  __shared__ int bi[LP_THREADS / 32];
-  const int t = threadIdx.x, lane = t & 31, w = t >> 5, V = A.vocab;
-  for (int r = blockIdx.x; r < A.n_rows; r += gridDim.x) {
-    const T* row = static_cast<const T*>(A.logits) + (int64_t)r * A.ld;
-    float pv = INFINITY, m = 0.f, lse = 0.f;
-    int pi = -1;
-    const int tok = A.tokens ? A.tokens[r] : -1;
-    const bool have = tok >= 0 && tok < V;
-    const float raw_t = have ? logit<T>(row, tok) : 0.f, key_t = am_key(raw_t);
-    auto best_after = [&](float v0, int i0) {    // the first (value, index) after (v0, i0) in the order
-      float v = -INFINITY;
-      int i = V;
-      for (int c = t; c < V; c += LP_THREADS) {
-        const float x = am_key(logit<T>(row, c));
-        if (before(v0, i0, x, c) && before(x, c, v, i)) { v = x; i = c; }
-      }
+// Keys: larger logit first, then the lower index. 0 is below every real key.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(am_key(x) + 0.f);     // one zero
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ u64 key_of(float x, int v) { return ((u64)ordered(x) << 32) | (uint32_t)~v; }
+__device__ __forceinline__ float key_value(u64 k) { return unordered((uint32_t)(k >> 32)); }
+__device__ __forceinline__ int key_index(u64 k) { return (int)~(uint32_t)k; }
+
+// Bitonic networks over a warp, one key per lane, lane 0 the largest.
+template <class K>
+__device__ __forceinline__ K exchange(K k, int j, bool larger) {
+  const K o = __shfl_xor_sync(0xffffffffu, k, j);
+  return larger == (k > o) ? k : o;
+}
+template <class K>
+__device__ __forceinline__ K warp_sort(K k) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float v2 = __shfl_xor_sync(0xffffffffu, v, o);
-        const int i2 = __shfl_xor_sync(0xffffffffu, i, o);
-        if (before(v2, i2, v, i)) { v = v2; i = i2; }
-      }
-      __syncthreads();
-      if (lane == 0) { bv[w] = v; bi[w] = i; }
-      __syncthreads();
-      pv = bv[0];
-      pi = bi[0];
-      for (int j = 1; j < LP_THREADS / 32; ++j)
-        if (before(bv[j], bi[j], pv, pi)) { pv = bv[j]; pi = bi[j]; }
-    };
-    best_after(INFINITY, -1);
-    m = pv * A.it;
-    float z = 0.f, zx = 0.f;
-    bool odd = false;                            // a NaN or +inf logit
-    int n_before = 0;
-    for (int c = t; c < V; c += LP_THREADS) {
-      const float x = logit<T>(row, c), y = x * A.it - m, e = expf(y);
-      odd = odd || !(x < INFINITY);
-      z += e;
-      if (e > 0.f) zx += e * y;
-      if (have && before(am_key(x), c, key_t, tok)) ++n_before;
-    }
-    z = block_sum(z, red);
-    zx = block_sum(zx, red);
-    int nb = n_before;
+  for (int n = 2; n <= 32; n <<= 1)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) nb += __shfl_xor_sync(0xffffffffu, nb, o);
-    if (lane == 0) bi[w] = nb;
-    const bool bad = __syncthreads_or(odd) != 0 || pv == -INFINITY;
-    nb = 0;
-    for (int j = 0; j < LP_THREADS / 32; ++j) nb += bi[j];
-    const float nan = __int_as_float(0x7fc00000);
-    const float lz = logf(z);
-    lse = bad ? nan : lz;
+    for (int j = n >> 1; j > 0; j >>= 1) k = exchange(k, j, ((lane & j) == 0) == ((lane & n) == 0 || n == 32));
+  return k;
+}
+// The best 32 of two sorted lists, sorted.
+__device__ __forceinline__ u64 warp_merge(u64 a, u64 b) {
+  const int lane = threadIdx.x & 31;
+  const u64 r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  u64 k = a > r ? a : r;
+#pragma unroll
+  for (int j = 16; j > 0; j >>= 1) k = exchange(k, j, (lane & j) == 0);
+  return k;
+}
+
+// y of a difference of logits; -inf (a masked token, nothing seen yet) stays
+// finite, so that 2^y = 0 and 0 y = 0.
+__device__ __forceinline__ float lp_y(float diff, float c) { return fmaxf(diff * c, -1e30f); }
+
+// (m, z, zy) += (m2, z2, zy2).
+__device__ __forceinline__ void stats_merge(float& m, float& z, float& zy, float m2, float z2, float zy2, float c) {
+  const float mm = fmaxf(m, m2), mb = mm == -INFINITY ? 0.f : mm;
+  const float da = lp_y(m - mb, c), db = lp_y(m2 - mb, c), a = lp_ex2(da), b = lp_ex2(db);
+  zy = fmaf(z, da, zy) * a + fmaf(z2, db, zy2) * b;
+  z = z * a + z2 * b;
+  m = mm;
+}
+
+struct LpShared {
+  float m[LP_WARPS], z[LP_WARPS], zy[LP_WARPS];
+  int before[LP_WARPS];
+  uint32_t bound;                                // ordered() of the block's bound
+  int last;
+  u64 pend[LP_WARPS][64];
+  u64 list[LP_WARPS][32];
+};
+
+// The block's lists (one per warp) into one, in warp 0's lanes.
+__device__ __forceinline__ u64 block_lists(u64 list, LpShared& sh) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int h = LP_WARPS / 2; h > 0; h >>= 1) {
     __syncthreads();
-    if (t == 0) {
-      if (A.logprob) A.logprob[r] = have ? (raw_t * A.it - m) - lse : nan;
-      if (A.rank) A.rank[r] = have ? nb + 1 : 0;
-      if (A.entropy) A.entropy[r] = bad ? nan : lz - zx / z;
-    }
-    for (int j = 0; j < A.top_n; ++j) {
-      if (t == 0) {
-        A.top_ids[(size_t)r * A.top_n + j] = pi;
-        A.top_lp[(size_t)r * A.top_n + j] = (pv * A.it - m) - lse;
+    if (w >= h && w < 2 * h) sh.list[w][lane] = list;
+    __syncthreads();
+    if (w < h) list = warp_merge(list, sh.list[w + h][lane]);
+  }
+  return list;
+}
+
+// grid (slices, rows).
+template <class T>
+__global__ void __launch_bounds__(LP_THREADS, 4) k_logprob(const __grid_constant__ LpArgs A) {
+  constexpr int PER = Elt<T>::per16;
+  __shared__ LpShared sh;
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5, V = A.vocab, n = A.top_n;
+  const int r = blockIdx.y, slice = blockIdx.x;
+  const T* row = static_cast<const T*>(A.logits) + (int64_t)r * A.ld;
+  // the row as aligned vectors: vector i holds elements i PER - skip ..
+  const int skip = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const int nv = (skip + V + PER - 1) / PER, tiles = (nv + LP_TILE - 1) / LP_TILE;
+  const int i0 = (int)((int64_t)tiles * slice / A.slices) * LP_TILE, i1 = (int)((int64_t)tiles * (slice + 1) / A.slices) * LP_TILE;
+  const int tok = A.tokens ? A.tokens[r] : -1;
+  const bool have = tok >= 0 && tok < V;
+  auto load = [&](int i) {
+    uint4 v;
+    const int e = i * PER - skip;
+    if (e >= 0 && e + PER <= V) {
+      v = ld_stream(row + e);
+    } else {                                     // the row's ends: element by element, -inf outside
+      uint32_t x[4];
+      for (int u = 0; u < 4; ++u) {
+        if (sizeof(T) == 4) {
+          x[u] = e + u >= 0 && e + u < V ? reinterpret_cast<const uint32_t*>(row)[e + u] : 0xff800000u;
+        } else {
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+          const int q = e + 2 * u;
+          x[u] = (q >= 0 && q < V ? p[q] : 0xff80u) | ((q + 1 >= 0 && q + 1 < V ? p[q + 1] : 0xff80u) << 16);
+        }
       }
-      if (j + 1 < A.top_n) best_after(pv, pi);
+      v = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    return v;
+  };
+  uint4 buf[LP_UNROLL];
+  const int first = i0 + w * 32 * LP_UNROLL + lane;        // a warp's vectors of a step are consecutive
+#pragma unroll
+  for (int u = 0; u < LP_UNROLL; ++u) buf[u] = load(first + 32 * u);
+  if (t == 0) sh.bound = 0;
+  const float raw_t = have ? logit<T>(row, tok) : 0.f, key_t = am_key(raw_t);
+  // a logit comes before the token if it is larger, or equal at a lower index:
+  // x > up in vectors behind the token's (and, but for its ties, in it), x >
+  // down, the next value below, in vectors ahead of it
+  const int tvec = have ? (tok + skip) / PER : -1;
+  const bool low = have && key_t == -INFINITY;             // ties with NaN and -inf: compared one by one
+  const float up = have && !low ? key_t : INFINITY, down = low ? INFINITY : have ? nextafterf(key_t, -INFINITY) : INFINITY;
+  float m = -INFINITY, z = 0.f, zy = 0.f;
+  int before = 0, pending = 0;
+  bool bad = false;
+  u64 list = 0;
+  u64* pend = sh.pend[w];
+  __syncthreads();
+  auto flush = [&](int count) {                            // `count` <= 32 pending keys into the list
+    __syncwarp();
+    const u64 k = lane < count ? pend[lane] : 0;
+    const u64 rest = lane < pending - count ? pend[count + lane] : 0;
+    __syncwarp();
+    if (lane < pending - count) pend[lane] = rest;
+    pending -= count;
+    list = warp_merge(list, warp_sort(k));
+    if (lane == n - 1) atomicMax(&sh.bound, (uint32_t)(list >> 32));
+    __syncwarp();
+  };
+  for (int base = first; base < i1 + lane + w * 32 * LP_UNROLL; base += LP_TILE) {
+    float x[LP_UNROLL][PER], vm[LP_UNROLL];
+#pragma unroll
+    for (int u = 0; u < LP_UNROLL; ++u) unpack<T>(buf[u], x[u]);
+    if (base + LP_TILE < i1 + lane + w * 32 * LP_UNROLL) {
+#pragma unroll
+      for (int u = 0; u < LP_UNROLL; ++u) buf[u] = load(base + LP_TILE + 32 * u);
+    }
+    float bm = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < LP_UNROLL; ++u) {
+      vm[u] = x[u][0];
+#pragma unroll
+      for (int e = 1; e < PER; ++e) vm[u] = max_nan(vm[u], x[u][e]);
+      bm = max_nan(bm, vm[u]);
+    }
+    if (!(bm < INFINITY)) {                                // NaN or +inf: the row's statistics are NaN, its order is not
+      bad = true;
+      bm = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < LP_UNROLL; ++u) {
+        vm[u] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          x[u][e] = am_key(x[u][e]);
+          vm[u] = fmaxf(vm[u], x[u][e]);
+        }
+        bm = fmaxf(bm, vm[u]);
+      }
+    }
+    if (bm > m) {
+      const float d = lp_y(m - bm, A.c), f = lp_ex2(d);
+      zy = fmaf(z, d, zy) * f;
+      z *= f;
+      m = bm;
+    }
+    const float mb = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int u = 0; u < LP_UNROLL; ++u) {
+      const float lim = base + 32 * u < tvec ? down : up;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        const float y = lp_y(x[u][e] - mb, A.c);
+        const float p = lp_ex2(y);
+        z += p;
+        zy = fmaf(p, y, zy);
+        before += x[u][e] > lim;
+      }
+    }
+    if (low) {
+#pragma unroll
+      for (int u = 0; u < LP_UNROLL; ++u)
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const int v = (base + 32 * u) * PER - skip + e;
+          before += x[u][e] > -INFINITY || (v >= 0 && v < tok);
+        }
+    }
+    if (n > 0) {
+      uint32_t bound = *reinterpret_cast<volatile uint32_t*>(&sh.bound);
+      if (base == first) {                                 // the n-th largest lane maximum bounds the n-th best
+        const uint32_t b = __shfl_sync(0xffffffffu, warp_sort(ordered(bm)), n - 1);
+        bound = bound > b ? bound : b;
+      }
+      if (__any_sync(0xffffffffu, ordered(bm) >= bound)) {
+#pragma unroll
+        for (int u = 0; u < LP_UNROLL; ++u) {
+          if (!__any_sync(0xffffffffu, ordered(vm[u]) >= bound)) continue;
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            const int v = (base + 32 * u) * PER - skip + e;
+            const u64 k = v >= 0 && v < V ? key_of(x[u][e], v) : 0;
+            const u64 least = __shfl_sync(0xffffffffu, list, n - 1);
+            const bool in = k > least && (uint32_t)(k >> 32) >= bound;
+            const uint32_t who = __ballot_sync(0xffffffffu, in);
+            if (who) {
+              if (in) pend[pending + __popc(who & ((1u << lane) - 1))] = k;
+              pending += __popc(who);
+              if (pending >= 32) {
+                flush(32);
+                const uint32_t nb = *reinterpret_cast<volatile uint32_t*>(&sh.bound);
+                bound = bound > nb ? bound : nb;
+              }
+            }
+          }
+        }
+      }
     }
   }
+  if (n > 0 && pending > 0) flush(pending);
+  // ---- the block's statistics and list ----
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), z2 = __shfl_xor_sync(0xffffffffu, z, o),
+                zy2 = __shfl_xor_sync(0xffffffffu, zy, o);
+    stats_merge(m, z, zy, m2, z2, zy2, A.c);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    sh.m[w] = m;
+    sh.z[w] = z;
+    sh.zy[w] = zy;
+    sh.before[w] = before;
+  }
+  bad = __syncthreads_or(bad) != 0;
+  if (n > 0) list = block_lists(list, sh);
+  if (t == 0) {
+    for (int i = 1; i < LP_WARPS; ++i) {
+      stats_merge(m, z, zy, sh.m[i], sh.z[i], sh.zy[i], A.c);
+      before += sh.before[i];
+    }
+  }
+  if (A.slices > 1) {
+    // ---- leave the slice; the row's last block joins them in order ----
+    const size_t at = (size_t)r * A.slices;
+    if (w == 0) {
+      if (n > 0) A.lists[(at + slice) * 32 + lane] = list;
+      if (lane == 0) A.stats[at + slice] = LpStats{m, z, zy, before, bad};
+    }
+    __threadfence();
+    __syncthreads();
+    if (t == 0) sh.last = atomicAdd(A.arrived + r, 1) == A.slices - 1;
+    __syncthreads();
+    if (!sh.last) return;
+    __threadfence();
+    list = 0;
+    if (n > 0) {
+      for (int i = w; i < A.slices; i += LP_WARPS) list = warp_merge(list, __ldcg(A.lists + (at + i) * 32 + lane));
+      list = block_lists(list, sh);
+    }
+    if (t == 0) {
+      A.arrived[r] = 0;
+      m = -INFINITY;
+      z = zy = 0.f;
+      before = 0;
+      bad = false;
+      for (int i = 0; i < A.slices; ++i) {
+        const LpStats* s = A.stats + at + i;
+        stats_merge(m, z, zy, __ldcg(&s->m), __ldcg(&s->z), __ldcg(&s->zy), A.c);
+        before += __ldcg(&s->before);
+        bad = bad || __ldcg(&s->bad) != 0;
+      }
+    }
+  }
+  if (w != 0) return;
+  const float nan = __int_as_float(0x7fc00000), LN2 = 0.6931471805599453f;
+  const bool none = bad || m == -INFINITY;
+  const float lz = __shfl_sync(0xffffffffu, none ? nan : log2f(z), 0), mm = __shfl_sync(0xffffffffu, m, 0);
+  if (lane == 0) {
+    if (A.logprob) A.logprob[r] = have ? (raw_t - mm) * A.it - lz * LN2 : nan;
+    if (A.entropy) A.entropy[r] = none ? nan : (lz - zy / z) * LN2;
+    if (A.rank) {
+      if (!low)                                            // ties inside the token's vector
+        for (int v = max(0, tvec * PER - skip); v < tok; ++v) before += am_key(logit<T>(row, v)) == key_t;
+      A.rank[r] = have ? before + 1 : 0;
+    }
+  }
+  if (lane < n) {
+    A.top_ids[(size_t)r * n + lane] = key_index(list);
+    A.top_lp[(size_t)r * n + lane] = (key_value(list) - mm) * A.it - lz * LN2;
+  }
 }
+
+// Slices of a row: as many steps of LP_TILE vectors as a row has at most; the
+// count that gives the least (waves of blocks) x (steps of a slice + 2), two
+// steps being about what a block spends on its end (measured: one row block's
+// end takes some 1.5 us, a step of 16 KB at a quarter of an SM's share 0.8 us).
+int lp_slices(int n_rows, int vocab, int esz) {
+  constexpr int resident = 4 * 152;
+  const int64_t tiles = ((int64_t)vocab * esz + 15 + LP_TILE * 16 - 1) / (LP_TILE * 16);
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  const int most = n_rows > LP_COUNTERS ? 1 : (int)std::min<int64_t>(tiles, LP_MAX_SLICES);
+  for (int s = 1; s <= most; ++s) {
+    const int64_t waves = ((int64_t)n_rows * s + resident - 1) / resident, c = waves * ((tiles + s - 1) / s + 2);
+    if (c < cost) { cost = c; best = s; }
+  }
+  return best;
+}
+
+// The counters come first and keep their place, so that calls of other shapes
+// on the same workspace find them at zero.
+struct LpWs {
+  static constexpr size_t stats = LP_COUNTERS * sizeof(int);
+  size_t lists, total;
+  LpWs(int n_rows, int slices) {
+    const size_t parts = slices > 1 ? (size_t)n_rows * slices : 0;
+    lists = (stats + parts * sizeof(LpStats) + 15) / 16 * 16;
+    total = lists + parts * 32 * sizeof(u64);
+  }
+};
 
 }  // namespace
 }  // namespace spec
@@ -119,9 +412,10 @@ __global__ void __launch_bounds__(LP_THREADS) k_logprob(LpArgs A) {
 using namespace spec;
 
 extern "C" int64_t spec_token_logprobs_ws_bytes(int n_rows, int vocab, int top_n) {
-  if (n_rows < 1 || vocab < 1 || top_n < 0 || top_n > SPEC_LOGPROB_MAX_TOP || top_n > vocab)
-    return set_last_error(SPEC_ERR_ARG, "n_rows >= 1, vocab >= 1 and 0 <= top_n <= min(32, vocab) required");
-  return 16;
+  if (n_rows < 1 || n_rows > 65535 || vocab < 1 || top_n < 0 || top_n > LP_TOP || top_n > vocab)
+    return set_last_error(SPEC_ERR_ARG, "1 <= n_rows <= 65535, vocab >= 1 and 0 <= top_n <= min(32, vocab) required");
+  if (vocab > LP_MAX_VOCAB) return set_last_error(SPEC_ERR_UNSUPPORTED, "vocab above 1048576");
+  return (int64_t)std::max(LpWs(n_rows, lp_slices(n_rows, vocab, 4)).total, LpWs(n_rows, lp_slices(n_rows, vocab, 2)).total);
 }
 
 extern "C" int spec_token_logprobs(const void* logits_dev, int dtype, int64_t ld, int n_rows, int vocab,
@@ -135,19 +429,22 @@ extern "C" int spec_token_logprobs(const void* logits_dev, int dtype, int64_t ld
       (top_n > 0 && (!out_top_ids_dev || !out_top_logprobs_dev)))
     return set_last_error(SPEC_ERR_ARG, "null pointer argument");
   if (dtype != SPEC_F32 && dtype != SPEC_BF16) return set_last_error(SPEC_ERR_UNSUPPORTED, "logits: F32 or BF16");
-  if (vocab > LP_MAX_VOCAB) return set_last_error(SPEC_ERR_UNSUPPORTED, "vocab above 1048576");
   if (ld < vocab) return set_last_error(SPEC_ERR_ARG, "ld below vocab");
-  if (!(temperature > 0.f) || !(1.f / temperature < INFINITY) || !(1.f / temperature > 0.f))
-    return set_last_error(SPEC_ERR_ARG, "temperature must be positive");
-  if (reinterpret_cast<uintptr_t>(logits_dev) % (dtype == SPEC_F32 ? 4 : 2) || !aligned16(ws_dev))
+  const float c = 1.4426950408889634f / temperature;
+  if (!(temperature > 0.f) || !(c < INFINITY) || !(1.f / temperature > 0.f)) return set_last_error(SPEC_ERR_ARG, "temperature must be positive");
+  const int esz = dtype == SPEC_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits_dev) % esz || !aligned16(ws_dev))
     return set_last_error(SPEC_ERR_ARG, "misaligned logits or workspace");
   if ((int64_t)ws_bytes < need) return set_last_error(SPEC_ERR_ARG, "workspace too small");
-  const LpArgs A{logits_dev, ld, n_rows, vocab, top_n, tokens_dev, 1.f / temperature, out_logprob_dev,
-                 out_entropy_dev, out_rank_dev, out_top_ids_dev, out_top_logprobs_dev};
+  const int slices = lp_slices(n_rows, vocab, esz);
+  const LpWs ws(n_rows, slices);
+  char* w = static_cast<char*>(ws_dev);
+  const LpArgs A{logits_dev, ld, n_rows, vocab, top_n, slices, tokens_dev, 1.f / temperature, c, out_logprob_dev, out_entropy_dev,
+                 out_rank_dev, out_top_ids_dev, out_top_logprobs_dev, reinterpret_cast<int*>(w),
+                 reinterpret_cast<LpStats*>(w + ws.stats), reinterpret_cast<u64*>(w + ws.lists)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-  const int blocks = std::min(n_rows, 65535);
-  if (dtype == SPEC_F32) k_logprob<float><<<blocks, LP_THREADS, 0, st>>>(A);
-  else k_logprob<bf16_t><<<blocks, LP_THREADS, 0, st>>>(A);
+  if (dtype == SPEC_F32) k_logprob<float><<<dim3(slices, n_rows), LP_THREADS, 0, st>>>(A);
+  else k_logprob<bf16_t><<<dim3(slices, n_rows), LP_THREADS, 0, st>>>(A);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
 }
