@@ -13,9 +13,10 @@
 // with the batch's maximum taken first. Alternatives: a warp holds the best 32
 // of what it has seen as sorted 64-bit keys (ordered logit, inverted index),
 // one per lane. An element joins the warp's pending buffer only if it is not
-// below the block's bound -- the largest n-th best value of any of its warps --
-// which the batch maximum decides for a whole batch at once; 32 pending keys
-// are sorted and merged at a time. The last block of a row to finish joins the
+// below a bound of the block's n-th best logit, which the batch maximum decides
+// for a whole batch at once; the bound is the n-th largest of the threads'
+// maxima, renewed after 1, 2, 4, .. steps. 32 pending keys are sorted and merged
+// at a time. The last block of a row to finish joins the
 // slices in their order (which block that is changes nothing).
 //
 // Bound: HBM. The logits are read once; some eight instructions a logit, one
@@ -40,6 +41,8 @@ constexpr int LP_MAX_VOCAB = 1 << 20;
 constexpr int LP_MAX_SLICES = 64;
 constexpr int LP_COUNTERS = 4096;                // rows of a call that may cut them into slices
 constexpr int LP_TOP = SPEC_LOGPROB_MAX_TOP;
+// Blocks on an SM at once: the bf16 form holds twice the values in registers.
+__host__ __device__ constexpr int lp_blocks(int esz) { return esz == 4 ? 4 : 3; }
 static_assert(LP_TOP == 32, "a warp's list has one key per lane");
 
 // What a slice leaves: statistics, and (behind them) its sorted keys.
@@ -73,12 +76,65 @@ __device__ __forceinline__ float lp_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Maximum that is NaN when either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// Two fp32 values in one 64-bit register pair, for the packed instructions.
+__device__ __forceinline__ u64 pair(float a, float b) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float2 halves(u64 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A 16-byte vector: its maximum (NaN if it holds one), its minimum, and its
+// values, two at a time.
+template <class T> struct LpVec;
+template <> struct LpVec<float> {
+  static __device__ __forceinline__ float2 at(const uint4& v, int j) {
+    return j ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+  }
+  static __device__ __forceinline__ void range(const uint4& v, float& hi, float& lo) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(hi) : "f"(hi), "f"(m), "f"(__uint_as_float(v.w)));
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)));
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(lo) : "f"(lo), "f"(m), "f"(__uint_as_float(v.w)));
+  }
+};
+template <> struct LpVec<bf16_t> {
+  static __device__ __forceinline__ float2 at(const uint4& v, int j) {
+    const uint32_t w = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ void range(const uint4& v, float& hi, float& lo) {
+    uint32_t a, b;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(hi) : "f"(hi), "f"(__uint_as_float(a << 16)), "f"(__uint_as_float(a & 0xFFFF0000u)));
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(lo) : "f"(lo), "f"(__uint_as_float(a << 16)), "f"(__uint_as_float(a & 0xFFFF0000u)));
+  }
+};
 
 // Keys: larger logit first, then the lower index. 0 is below every real key.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -108,10 +164,11 @@ __device__ __forceinline__ K warp_sort(K k) {
   return k;
 }
 // The best 32 of two sorted lists, sorted.
-__device__ __forceinline__ u64 warp_merge(u64 a, u64 b) {
+template <class K>
+__device__ __forceinline__ K warp_merge(K a, K b) {
   const int lane = threadIdx.x & 31;
-  const u64 r = __shfl_sync(0xffffffffu, b, 31 - lane);
-  u64 k = a > r ? a : r;
+  const K r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  K k = a > r ? a : r;
 #pragma unroll
   for (int j = 16; j > 0; j >>= 1) k = exchange(k, j, (lane & j) == 0);
   return k;
@@ -133,27 +190,29 @@ __device__ __forceinline__ void stats_merge(float& m, float& z, float& zy, float
 struct LpShared {
   float m[LP_WARPS], z[LP_WARPS], zy[LP_WARPS];
   int before[LP_WARPS];
-  uint32_t bound;                                // ordered() of the block's bound
   int last;
   u64 pend[LP_WARPS][64];
   u64 list[LP_WARPS][32];
+  uint32_t top[LP_WARPS][32];
+  uint4 raw[LP_UNROLL][LP_THREADS];              // a step's vectors, for the search of one with candidates
 };
 
-// The block's lists (one per warp) into one, in warp 0's lanes.
-__device__ __forceinline__ u64 block_lists(u64 list, LpShared& sh) {
+// The warps' lists into one, in warp 0's lanes.
+template <class K>
+__device__ __forceinline__ K block_lists(K list, K (*sh)[32]) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll 1
   for (int h = LP_WARPS / 2; h > 0; h >>= 1) {
+    if (w >= h && w < 2 * h) sh[w][lane] = list;
     __syncthreads();
-    if (w >= h && w < 2 * h) sh.list[w][lane] = list;
-    __syncthreads();
-    if (w < h) list = warp_merge(list, sh.list[w + h][lane]);
+    if (w < h) list = warp_merge(list, sh[w + h][lane]);
   }
   return list;
 }
 
 // grid (slices, rows).
 template <class T>
-__global__ void __launch_bounds__(LP_THREADS, 4) k_logprob(const __grid_constant__ LpArgs A) {
+__global__ void __launch_bounds__(LP_THREADS, lp_blocks(sizeof(T))) k_logprob(const __grid_constant__ LpArgs A) {
   constexpr int PER = Elt<T>::per16;
   __shared__ LpShared sh;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, V = A.vocab, n = A.top_n;
@@ -186,124 +245,155 @@ __global__ void __launch_bounds__(LP_THREADS, 4) k_logprob(const __grid_constant
     return v;
   };
   uint4 buf[LP_UNROLL];
-  const int first = i0 + w * 32 * LP_UNROLL + lane;        // a warp's vectors of a step are consecutive
 #pragma unroll
-  for (int u = 0; u < LP_UNROLL; ++u) buf[u] = load(first + 32 * u);
-  if (t == 0) sh.bound = 0;
+  for (int u = 0; u < LP_UNROLL; ++u) buf[u] = load(i0 + (w * LP_UNROLL + u) * 32 + lane);   // a warp's vectors are consecutive
   const float raw_t = have ? logit<T>(row, tok) : 0.f, key_t = am_key(raw_t);
   // a logit comes before the token if it is larger, or equal at a lower index:
   // x > up in vectors behind the token's (and, but for its ties, in it), x >
   // down, the next value below, in vectors ahead of it
   const int tvec = have ? (tok + skip) / PER : -1;
   const bool low = have && key_t == -INFINITY;             // ties with NaN and -inf: compared one by one
-  const float up = have && !low ? key_t : INFINITY, down = low ? INFINITY : have ? nextafterf(key_t, -INFINITY) : INFINITY;
-  float m = -INFINITY, z = 0.f, zy = 0.f;
-  int before = 0, pending = 0;
+  const float up = have && !low ? key_t : INFINITY, down = have && !low ? nextafterf(key_t, -INFINITY) : INFINITY;
+  float m = -INFINITY, mk = -INFINITY;                     // of the statistics; the same with NaN as -inf
+  u64 z2 = 0, zy2 = 0;                                     // two zeros
+  int before = 0, pending = 0, step = 0;
   bool bad = false;
   u64 list = 0;
-  u64* pend = sh.pend[w];
-  __syncthreads();
-  auto flush = [&](int count) {                            // `count` <= 32 pending keys into the list
-    __syncwarp();
-    const u64 k = lane < count ? pend[lane] : 0;
-    const u64 rest = lane < pending - count ? pend[count + lane] : 0;
-    __syncwarp();
-    if (lane < pending - count) pend[lane] = rest;
-    pending -= count;
-    list = warp_merge(list, warp_sort(k));
-    if (lane == n - 1) atomicMax(&sh.bound, (uint32_t)(list >> 32));
-    __syncwarp();
-  };
-  for (int base = first; base < i1 + lane + w * 32 * LP_UNROLL; base += LP_TILE) {
-    float x[LP_UNROLL][PER], vm[LP_UNROLL];
-#pragma unroll
-    for (int u = 0; u < LP_UNROLL; ++u) unpack<T>(buf[u], x[u]);
-    if (base + LP_TILE < i1 + lane + w * 32 * LP_UNROLL) {
-#pragma unroll
-      for (int u = 0; u < LP_UNROLL; ++u) buf[u] = load(base + LP_TILE + 32 * u);
-    }
-    float bm = -INFINITY;
+  uint32_t bound = 0;                                      // no key below it can be among the block's best n
+  const u64 c2 = pair(A.c, A.c);
+#pragma unroll 1
+  for (int at = i0; at < i1; at += LP_TILE, ++step) {
+    const int base = at + w * 32 * LP_UNROLL + lane;
+    uint4 cur[LP_UNROLL];
+    float bm = -INFINITY, lo = INFINITY;
 #pragma unroll
     for (int u = 0; u < LP_UNROLL; ++u) {
-      vm[u] = x[u][0];
+      cur[u] = buf[u];
+      LpVec<T>::range(cur[u], bm, lo);
+    }
+    if (at + LP_TILE < i1) {
 #pragma unroll
-      for (int e = 1; e < PER; ++e) vm[u] = max_nan(vm[u], x[u][e]);
-      bm = max_nan(bm, vm[u]);
+      for (int u = 0; u < LP_UNROLL; ++u) buf[u] = load(base + LP_TILE + 32 * u);
     }
     if (!(bm < INFINITY)) {                                // NaN or +inf: the row's statistics are NaN, its order is not
       bad = true;
       bm = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < LP_UNROLL; ++u) {
-        vm[u] = -INFINITY;
+      for (int u = 0; u < LP_UNROLL; ++u)
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          x[u][e] = am_key(x[u][e]);
-          vm[u] = fmaxf(vm[u], x[u][e]);
+        for (int j = 0; j < PER / 2; ++j) {
+          const float2 x = LpVec<T>::at(cur[u], j);
+          bm = fmaxf(bm, fmaxf(am_key(x.x), am_key(x.y)));
         }
-        bm = fmaxf(bm, vm[u]);
-      }
     }
     if (bm > m) {
       const float d = lp_y(m - bm, A.c), f = lp_ex2(d);
-      zy = fmaf(z, d, zy) * f;
-      z *= f;
+      const u64 f2 = pair(f, f);
+      zy2 = mul2(fma2(z2, pair(d, d), zy2), f2);
+      z2 = mul2(z2, f2);
       m = bm;
     }
     const float mb = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int u = 0; u < LP_UNROLL; ++u) {
-      const float lim = base + 32 * u < tvec ? down : up;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        const float y = lp_y(x[u][e] - mb, A.c);
-        const float p = lp_ex2(y);
-        z += p;
-        zy = fmaf(p, y, zy);
-        before += x[u][e] > lim;
-      }
-    }
-    if (low) {
+    const u64 nm2 = pair(-mb, -mb);
+    if ((lo - mb) * A.c > -1e30f) {
 #pragma unroll
       for (int u = 0; u < LP_UNROLL; ++u)
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          const int v = (base + 32 * u) * PER - skip + e;
-          before += x[u][e] > -INFINITY || (v >= 0 && v < tok);
+        for (int j = 0; j < PER / 2; ++j) {
+          const float2 x = LpVec<T>::at(cur[u], j);
+          const u64 y2 = mul2(add2(pair(x.x, x.y), nm2), c2);
+          const float2 y = halves(y2);
+          const u64 p2 = pair(lp_ex2(y.x), lp_ex2(y.y));
+          z2 = add2(z2, p2);
+          zy2 = fma2(p2, y2, zy2);
+        }
+    } else {                                               // masked tokens, or values as far down: y stays finite
+#pragma unroll
+      for (int u = 0; u < LP_UNROLL; ++u)
+#pragma unroll
+        for (int j = 0; j < PER / 2; ++j) {
+          const float2 x = LpVec<T>::at(cur[u], j);
+          const u64 y2 = pair(lp_y(x.x - mb, A.c), lp_y(x.y - mb, A.c));
+          const float2 y = halves(y2);
+          const u64 p2 = pair(lp_ex2(y.x), lp_ex2(y.y));
+          z2 = add2(z2, p2);
+          zy2 = fma2(p2, y2, zy2);
         }
     }
+    if (bm > down) {                                       // some may come before the token
+#pragma unroll
+      for (int u = 0; u < LP_UNROLL; ++u) {
+        const float lim = base + 32 * u < tvec ? down : up;
+#pragma unroll
+        for (int j = 0; j < PER / 2; ++j) {
+          const float2 x = LpVec<T>::at(cur[u], j);
+          before += (x.x > lim) + (x.y > lim);
+        }
+      }
+    }
+    if (low) {
+#pragma unroll 1
+      for (int e = 0; e < LP_UNROLL * PER; ++e) {
+        const int v = (base + 32 * (e / PER)) * PER - skip + e % PER;
+        if (v >= 0 && v < V) before += logit<T>(row, v) > -INFINITY || v < tok;
+      }
+    }
     if (n > 0) {
-      uint32_t bound = *reinterpret_cast<volatile uint32_t*>(&sh.bound);
-      if (base == first) {                                 // the n-th largest lane maximum bounds the n-th best
-        const uint32_t b = __shfl_sync(0xffffffffu, warp_sort(ordered(bm)), n - 1);
+      mk = fmaxf(mk, bm);
+      // at steps 1, 2, 4, ..: the n-th largest thread maximum of the block is a
+      // bound of its n-th best logit, and a near one
+      if ((step & (step + 1)) == 0) {
+        const uint32_t k = block_lists(warp_sort(ordered(mk)), sh.top);
+        if (w == 0) sh.top[0][lane] = k;
+        __syncthreads();
+        const uint32_t b = sh.top[0][n - 1];
         bound = bound > b ? bound : b;
+        __syncthreads();
       }
       if (__any_sync(0xffffffffu, ordered(bm) >= bound)) {
 #pragma unroll
+        for (int u = 0; u < LP_UNROLL; ++u) sh.raw[u][t] = cur[u];
+#pragma unroll 1
         for (int u = 0; u < LP_UNROLL; ++u) {
-          if (!__any_sync(0xffffffffu, ordered(vm[u]) >= bound)) continue;
+          const uint4 v4 = sh.raw[u][t];
+          float vm = -INFINITY;
 #pragma unroll
+          for (int j = 0; j < PER / 2; ++j) {
+            const float2 x = LpVec<T>::at(v4, j);
+            vm = fmaxf(vm, fmaxf(x.x, x.y));               // NaN as -inf
+          }
+          if (!__any_sync(0xffffffffu, ordered(vm) >= bound)) continue;
+#pragma unroll 1
           for (int e = 0; e < PER; ++e) {
             const int v = (base + 32 * u) * PER - skip + e;
-            const u64 k = v >= 0 && v < V ? key_of(x[u][e], v) : 0;
+            const u64 k = v >= 0 && v < V ? key_of(logit<T>(reinterpret_cast<const T*>(&sh.raw[u][t]), e), v) : 0;
             const u64 least = __shfl_sync(0xffffffffu, list, n - 1);
             const bool in = k > least && (uint32_t)(k >> 32) >= bound;
             const uint32_t who = __ballot_sync(0xffffffffu, in);
-            if (who) {
-              if (in) pend[pending + __popc(who & ((1u << lane) - 1))] = k;
-              pending += __popc(who);
-              if (pending >= 32) {
-                flush(32);
-                const uint32_t nb = *reinterpret_cast<volatile uint32_t*>(&sh.bound);
-                bound = bound > nb ? bound : nb;
-              }
+            if (in) sh.pend[w][pending + __popc(who & ((1u << lane) - 1))] = k;
+            pending += __popc(who);
+            if (pending >= 32) {                           // 32 of them into the list
+              __syncwarp();
+              const u64 p = sh.pend[w][lane], rest = sh.pend[w][32 + lane];
+              __syncwarp();
+              sh.pend[w][lane] = rest;
+              pending -= 32;
+              list = warp_merge(list, warp_sort(p));
+              const uint32_t nth = (uint32_t)(__shfl_sync(0xffffffffu, list, n - 1) >> 32);
+              bound = bound > nth ? bound : nth;
+              __syncwarp();
             }
           }
         }
       }
     }
   }
-  if (n > 0 && pending > 0) flush(pending);
+  if (n > 0 && pending > 0) {
+    __syncwarp();
+    list = warp_merge(list, warp_sort(lane < pending ? sh.pend[w][lane] : 0));
+  }
+  const float2 zh = halves(z2), yh = halves(zy2);
+  float z = zh.x + zh.y, zy = yh.x + yh.y;
   // ---- the block's statistics and list ----
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -319,7 +409,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) k_logprob(const __grid_constant
     sh.before[w] = before;
   }
   bad = __syncthreads_or(bad) != 0;
-  if (n > 0) list = block_lists(list, sh);
+  if (n > 0) list = block_lists(list, sh.list);
   if (t == 0) {
     for (int i = 1; i < LP_WARPS; ++i) {
       stats_merge(m, z, zy, sh.m[i], sh.z[i], sh.zy[i], A.c);
@@ -342,7 +432,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) k_logprob(const __grid_constant
     list = 0;
     if (n > 0) {
       for (int i = w; i < A.slices; i += LP_WARPS) list = warp_merge(list, __ldcg(A.lists + (at + i) * 32 + lane));
-      list = block_lists(list, sh);
+      list = block_lists(list, sh.list);
     }
     if (t == 0) {
       A.arrived[r] = 0;
@@ -382,7 +472,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) k_logprob(const __grid_constant
 // steps being about what a block spends on its end (measured: one row block's
 // end takes some 1.5 us, a step of 16 KB at a quarter of an SM's share 0.8 us).
 int lp_slices(int n_rows, int vocab, int esz) {
-  constexpr int resident = 4 * 152;
+  const int resident = lp_blocks(esz) * 152;
   const int64_t tiles = ((int64_t)vocab * esz + 15 + LP_TILE * 16 - 1) / (LP_TILE * 16);
   int best = 1;
   int64_t cost = INT64_MAX;
