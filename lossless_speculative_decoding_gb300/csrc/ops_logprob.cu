@@ -2,26 +2,27 @@
 // rank and the likeliest alternatives, from materialised logits, in one pass
 // over them.
 //
-// With m the largest logit x and y = (x - m) log2(e) / T (the difference first:
-// a row of the type's lowest values stays a row of equal ones): z = sum 2^y, log
+// With c = log2(e) / T, R the largest logit times c (rounded; any R near it
+// serves, as long as all sums use the same) and y = c x - R: z = sum 2^y, log
 // p(t) = ln 2 (y_t - log2 z), and entropy = ln 2 (log2 z - sum 2^y y / z), two
 // terms of one sign, so that nothing cancels. The order of tokens is (logit
 // descending, index ascending), NaN as -inf.
 //
-// A row is cut into slices, one block each; a thread keeps a running (m, z,
-// sum) and a count of the logits that come before the token, batch by batch,
-// with the batch's maximum taken first. Alternatives: a warp holds the best 32
-// of what it has seen as sorted 64-bit keys (ordered logit, inverted index),
-// one per lane. An element joins the warp's pending buffer only if it is not
-// below a bound of the block's n-th best logit, which the batch maximum decides
-// for a whole batch at once; the bound is the n-th largest of the threads'
-// maxima, renewed after 1, 2, 4, .. steps. 32 pending keys are sorted and merged
-// at a time. The last block of a row to finish joins the
-// slices in their order (which block that is changes nothing).
+// The rows' steps of 32 KB, row after row, are cut into one even run for each
+// block that the GPU holds at once, so that a few rows use all of it and many
+// rows leave no tail. Within a row a thread keeps a running (R, z, sum) and a
+// count of the logits that come before the token; a step is added with packed
+// fp32 arithmetic, and again with care (masked tokens, NaN) if the sum came out
+// as NaN. Alternatives: a warp holds the best 32 of what it has seen as sorted
+// 64-bit keys (ordered logit, inverted index), one per lane. A thread's step is
+// searched only if its maximum is not below a bound of the block's n-th best
+// logit; the bound comes from the threads' maxima and is renewed after 1, 4,
+// 16, .. steps. 32 found keys are sorted and merged at a time. One warp of the
+// block ends a row while the others go on to the next; a row that several
+// blocks share is joined, in the blocks' order, by the last of them to finish
+// (which one that is changes nothing).
 //
-// Bound: HBM. The logits are read once; some eight instructions a logit, one
-// of them an exponential, keep the SMs at about half to two thirds of their
-// issue rate while the logits stream.
+// Bound: HBM. The logits are read once.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,26 +36,26 @@ typedef unsigned long long u64;
 
 constexpr int LP_THREADS = 256;
 constexpr int LP_WARPS = LP_THREADS / 32;
-constexpr int LP_UNROLL = 4;                     // 16-byte vectors a thread has in flight
+constexpr int LP_UNROLL = 8;                     // 16-byte vectors a thread has in flight
 constexpr int LP_TILE = LP_THREADS * LP_UNROLL;  // vectors of a block's step
+constexpr int LP_STAGES = 2;                     // steps in shared memory: one being added, one on its way
+constexpr int LP_BLOCKS = 3;                     // blocks on an SM at once
 constexpr int LP_MAX_VOCAB = 1 << 20;
-constexpr int LP_MAX_SLICES = 64;
-constexpr int LP_COUNTERS = 4096;                // rows of a call that may cut them into slices
+constexpr int LP_MAX_BLOCKS = 512;
 constexpr int LP_TOP = SPEC_LOGPROB_MAX_TOP;
-// Blocks on an SM at once: the bf16 form holds twice the values in registers.
-__host__ __device__ constexpr int lp_blocks(int esz) { return esz == 4 ? 4 : 3; }
 static_assert(LP_TOP == 32, "a warp's list has one key per lane");
 
-// What a slice leaves: statistics, and (behind them) its sorted keys.
+// What a block leaves of a row it shares: statistics, and a sorted list apart.
 struct LpStats {
-  float m, z, zy;           // max x, sum 2^y, sum 2^y y
+  float r, z, zy;           // R, sum 2^y, sum 2^y y
   int before, bad;          // logits before the token; a NaN or +inf logit
 };
 
 struct LpArgs {
   const void* logits;
   int64_t ld;
-  int n_rows, vocab, top_n, slices;
+  int n_rows, vocab, top_n, tiles;               // tiles: steps of a row
+
   const int32_t* tokens;
   float it, c;              // 1 / temperature, log2(e) / temperature
   float* logprob;
@@ -62,9 +63,9 @@ struct LpArgs {
   int32_t* rank;
   int32_t* top_ids;
   float* top_lp;
-  int* arrived;             // [LP_COUNTERS], zero between calls
-  LpStats* stats;           // [n_rows][slices]
-  u64* lists;               // [n_rows][slices][32]
+  int* arrived;             // [LP_MAX_BLOCKS], of the row that starts in a block and goes on; zero between calls
+  LpStats* stats;           // [LP_MAX_BLOCKS][2]: of a row begun in an earlier block, of one that goes on in the next
+  u64* lists;               // [LP_MAX_BLOCKS][2][32]
 };
 
 template <class T> __device__ __forceinline__ float logit(const T* row, int v);
@@ -103,19 +104,37 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
   return r;
 }
 
-// A 16-byte vector: its maximum (NaN if it holds one), its minimum, and its
-// values, two at a time.
+__device__ __forceinline__ float above(float x, float lim) {
+  float r;
+  asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lim));
+  return r;
+}
+
+// A vector from shared memory; volatile, so that it is read again and not kept
+// in registers from one use to the next.
+__device__ __forceinline__ uint4 reread(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"((uint32_t)__cvta_generic_to_shared(p)) : "memory");
+  return v;
+}
+
+// A 16-byte vector's values, two at a time, and the maximum of a step's vectors
+// (NaN as -inf).
 template <class T> struct LpVec;
 template <> struct LpVec<float> {
   static __device__ __forceinline__ float2 at(const uint4& v, int j) {
     return j ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
   }
-  static __device__ __forceinline__ void range(const uint4& v, float& hi, float& lo) {
-    float m;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)));
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(hi) : "f"(hi), "f"(m), "f"(__uint_as_float(v.w)));
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)), "f"(__uint_as_float(v.z)));
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(lo) : "f"(lo), "f"(m), "f"(__uint_as_float(v.w)));
+  static __device__ __forceinline__ float max_of(const uint4* p) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < LP_UNROLL; ++j) {
+      const uint4 v = reread(p + j * LP_THREADS);
+      asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)));
+      asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w)));
+    }
+    return m;
   }
 };
 template <> struct LpVec<bf16_t> {
@@ -123,16 +142,18 @@ template <> struct LpVec<bf16_t> {
     const uint32_t w = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ void range(const uint4& v, float& hi, float& lo) {
-    uint32_t a, b;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(hi) : "f"(hi), "f"(__uint_as_float(a << 16)), "f"(__uint_as_float(a & 0xFFFF0000u)));
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v.x), "r"(v.y));
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v.z), "r"(v.w));
-    asm("min.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(lo) : "f"(lo), "f"(__uint_as_float(a << 16)), "f"(__uint_as_float(a & 0xFFFF0000u)));
+  static __device__ __forceinline__ float max_of(const uint4* p) {
+    uint32_t a = 0xff80ff80u, b = a;             // -inf
+#pragma unroll
+    for (int j = 0; j < LP_UNROLL; ++j) {
+      const uint4 v = reread(p + j * LP_THREADS);
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(v.x));
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(v.y));
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(v.z));
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(v.w));
+    }
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
   }
 };
 
@@ -174,327 +195,330 @@ __device__ __forceinline__ K warp_merge(K a, K b) {
   return k;
 }
 
-// y of a difference of logits; -inf (a masked token, nothing seen yet) stays
-// finite, so that 2^y = 0 and 0 y = 0.
-__device__ __forceinline__ float lp_y(float diff, float c) { return fmaxf(diff * c, -1e30f); }
+// c x of a logit that may be masked or lie at the type's end: finite, so that a
+// row of the type's lowest values stays a row of equal ones.
+__device__ __forceinline__ float lp_scaled(float x, float c) { return fminf(fmaxf(x * c, -1e30f), 1e30f); }
 
-// (m, z, zy) += (m2, z2, zy2).
-__device__ __forceinline__ void stats_merge(float& m, float& z, float& zy, float m2, float z2, float zy2, float c) {
-  const float mm = fmaxf(m, m2), mb = mm == -INFINITY ? 0.f : mm;
-  const float da = lp_y(m - mb, c), db = lp_y(m2 - mb, c), a = lp_ex2(da), b = lp_ex2(db);
+// (R, z, zy) += (r2, z2, zy2), either of which may hold nothing (R = -inf).
+__device__ __forceinline__ void stats_merge(float& r, float& z, float& zy, float r2, float z2, float zy2) {
+  const float rr = fmaxf(r, r2), rb = rr == -INFINITY ? 0.f : rr;
+  const float da = fmaxf(r - rb, -1e30f), db = fmaxf(r2 - rb, -1e30f), a = lp_ex2(da), b = lp_ex2(db);
   zy = fmaf(z, da, zy) * a + fmaf(z2, db, zy2) * b;
   z = z * a + z2 * b;
-  m = mm;
+  r = rr;
 }
 
 struct LpShared {
-  float m[LP_WARPS], z[LP_WARPS], zy[LP_WARPS];
-  int before[LP_WARPS];
-  int last;
-  u64 pend[LP_WARPS][64];
-  u64 list[LP_WARPS][32];
-  uint32_t top[LP_WARPS][32];
-  uint4 raw[LP_UNROLL][LP_THREADS];              // a step's vectors, for the search of one with candidates
+  LpStats stats[2][LP_WARPS];                    // the warps' parts of a row, for the warp that ends it
+  u64 list[2][LP_WARPS][32];
+  u64 pend[LP_WARPS][64];                        // found keys
+  uint32_t top[2][32];                           // each warp's four largest thread maxima
 };
 
-// The warps' lists into one, in warp 0's lanes.
-template <class K>
-__device__ __forceinline__ K block_lists(K list, K (*sh)[32]) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll 1
-  for (int h = LP_WARPS / 2; h > 0; h >>= 1) {
-    if (w >= h && w < 2 * h) sh[w][lane] = list;
-    __syncthreads();
-    if (w < h) list = warp_merge(list, sh[w + h][lane]);
-  }
-  return list;
-}
-
-// grid (slices, rows).
 template <class T>
-__global__ void __launch_bounds__(LP_THREADS, lp_blocks(sizeof(T))) k_logprob(const __grid_constant__ LpArgs A) {
-  constexpr int PER = Elt<T>::per16;
+__global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_constant__ LpArgs A) {
+  constexpr int PER = Elt<T>::per16, U = LP_UNROLL, STEP = U * PER;
   __shared__ LpShared sh;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, V = A.vocab, n = A.top_n;
-  const int r = blockIdx.y, slice = blockIdx.x;
-  const T* row = static_cast<const T*>(A.logits) + (int64_t)r * A.ld;
-  // the row as aligned vectors: vector i holds elements i PER - skip ..
-  const int skip = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-  const int nv = (skip + V + PER - 1) / PER, tiles = (nv + LP_TILE - 1) / LP_TILE;
-  const int i0 = (int)((int64_t)tiles * slice / A.slices) * LP_TILE, i1 = (int)((int64_t)tiles * (slice + 1) / A.slices) * LP_TILE;
-  const int tok = A.tokens ? A.tokens[r] : -1;
-  const bool have = tok >= 0 && tok < V;
-  auto load = [&](int i) {
-    uint4 v;
-    const int e = i * PER - skip;
-    if (e >= 0 && e + PER <= V) {
-      v = ld_stream(row + e);
-    } else {                                     // the row's ends: element by element, -inf outside
-      uint32_t x[4];
-      for (int u = 0; u < 4; ++u) {
-        if (sizeof(T) == 4) {
-          x[u] = e + u >= 0 && e + u < V ? reinterpret_cast<const uint32_t*>(row)[e + u] : 0xff800000u;
-        } else {
-          const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-          const int q = e + 2 * u;
-          x[u] = (q >= 0 && q < V ? p[q] : 0xff80u) | ((q + 1 >= 0 && q + 1 < V ? p[q + 1] : 0xff80u) << 16);
-        }
-      }
-      v = make_uint4(x[0], x[1], x[2], x[3]);
-    }
-    return v;
-  };
-  uint4 buf[LP_UNROLL];
-#pragma unroll
-  for (int u = 0; u < LP_UNROLL; ++u) buf[u] = load(i0 + (w * LP_UNROLL + u) * 32 + lane);   // a warp's vectors are consecutive
-  const float raw_t = have ? logit<T>(row, tok) : 0.f, key_t = am_key(raw_t);
-  // a logit comes before the token if it is larger, or equal at a lower index:
-  // x > up in vectors behind the token's (and, but for its ties, in it), x >
-  // down, the next value below, in vectors ahead of it
-  const int tvec = have ? (tok + skip) / PER : -1;
-  const bool low = have && key_t == -INFINITY;             // ties with NaN and -inf: compared one by one
-  const float up = have && !low ? key_t : INFINITY, down = have && !low ? nextafterf(key_t, -INFINITY) : INFINITY;
-  float m = -INFINITY, mk = -INFINITY;                     // of the statistics; the same with NaN as -inf
-  u64 z2 = 0, zy2 = 0;                                     // two zeros
-  int before = 0, pending = 0, step = 0;
-  bool bad = false;
-  u64 list = 0;
-  uint32_t bound = 0;                                      // no key below it can be among the block's best n
+  const int64_t units = (int64_t)A.n_rows * A.tiles, end = units * (blockIdx.x + 1) / gridDim.x;
+  int64_t pos = units * blockIdx.x / gridDim.x;  // (the grid has no more blocks than there are units)
+  const float nan = __int_as_float(0x7fc00000), LN2 = 0.6931471805599453f;
   const u64 c2 = pair(A.c, A.c);
+  int r = (int)(pos / A.tiles), s0 = (int)(pos % A.tiles), turn = 0, rows = 0;
+  // Steps go through shared memory, every thread's vectors by itself: the wait
+  // of a thread for its own copies is all the order they need.
+  extern __shared__ __align__(16) uint4 stage[];           // [LP_STAGES][U][LP_THREADS]
+  int fetched = 0, used = 0;
+  auto row_of = [&](int i) { return static_cast<const T*>(A.logits) + (int64_t)i * A.ld; };
+  auto skip_of = [&](const T* row) { return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)); };
+  auto fetch = [&](const T* row, int skip, int st) {
+    uint4* dst = stage + ((fetched++ & 1) * U) * LP_THREADS + t;
+    const int e0 = (st * LP_TILE + w * 32 * U) * PER - skip, first = st * LP_TILE + w * 32 * U + lane;
+    auto copy = [&](int j) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                   ::"r"((uint32_t)__cvta_generic_to_shared(dst + j * LP_THREADS)), "l"(row + ((first + 32 * j) * PER - skip)) : "memory");
+    };
+    if (e0 >= 0 && e0 + 32 * U * PER <= V) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) copy(j);
+    } else if (e0 < V) {                         // a warp with an end of the row: -inf outside it
 #pragma unroll 1
-  for (int at = i0; at < i1; at += LP_TILE, ++step) {
-    const int base = at + w * 32 * LP_UNROLL + lane;
-    uint4 cur[LP_UNROLL];
-    float bm = -INFINITY, lo = INFINITY;
-#pragma unroll
-    for (int u = 0; u < LP_UNROLL; ++u) {
-      cur[u] = buf[u];
-      LpVec<T>::range(cur[u], bm, lo);
-    }
-    if (at + LP_TILE < i1) {
-#pragma unroll
-      for (int u = 0; u < LP_UNROLL; ++u) buf[u] = load(base + LP_TILE + 32 * u);
-    }
-    if (!(bm < INFINITY)) {                                // NaN or +inf: the row's statistics are NaN, its order is not
-      bad = true;
-      bm = -INFINITY;
-#pragma unroll
-      for (int u = 0; u < LP_UNROLL; ++u)
-#pragma unroll
-        for (int j = 0; j < PER / 2; ++j) {
-          const float2 x = LpVec<T>::at(cur[u], j);
-          bm = fmaxf(bm, fmaxf(am_key(x.x), am_key(x.y)));
-        }
-    }
-    if (bm > m) {
-      const float d = lp_y(m - bm, A.c), f = lp_ex2(d);
-      const u64 f2 = pair(f, f);
-      zy2 = mul2(fma2(z2, pair(d, d), zy2), f2);
-      z2 = mul2(z2, f2);
-      m = bm;
-    }
-    const float mb = m == -INFINITY ? 0.f : m;
-    const u64 nm2 = pair(-mb, -mb);
-    if ((lo - mb) * A.c > -1e30f) {
-#pragma unroll
-      for (int u = 0; u < LP_UNROLL; ++u)
-#pragma unroll
-        for (int j = 0; j < PER / 2; ++j) {
-          const float2 x = LpVec<T>::at(cur[u], j);
-          const u64 y2 = mul2(add2(pair(x.x, x.y), nm2), c2);
-          const float2 y = halves(y2);
-          const u64 p2 = pair(lp_ex2(y.x), lp_ex2(y.y));
-          z2 = add2(z2, p2);
-          zy2 = fma2(p2, y2, zy2);
-        }
-    } else {                                               // masked tokens, or values as far down: y stays finite
-#pragma unroll
-      for (int u = 0; u < LP_UNROLL; ++u)
-#pragma unroll
-        for (int j = 0; j < PER / 2; ++j) {
-          const float2 x = LpVec<T>::at(cur[u], j);
-          const u64 y2 = pair(lp_y(x.x - mb, A.c), lp_y(x.y - mb, A.c));
-          const float2 y = halves(y2);
-          const u64 p2 = pair(lp_ex2(y.x), lp_ex2(y.y));
-          z2 = add2(z2, p2);
-          zy2 = fma2(p2, y2, zy2);
-        }
-    }
-    if (bm > down) {                                       // some may come before the token
-#pragma unroll
-      for (int u = 0; u < LP_UNROLL; ++u) {
-        const float lim = base + 32 * u < tvec ? down : up;
-#pragma unroll
-        for (int j = 0; j < PER / 2; ++j) {
-          const float2 x = LpVec<T>::at(cur[u], j);
-          before += (x.x > lim) + (x.y > lim);
-        }
-      }
-    }
-    if (low) {
+      for (int j = 0; j < U; ++j) {
+        const int e = (first + 32 * j) * PER - skip;
+        if (e >= 0 && e + PER <= V) {
+          copy(j);
+        } else {
+          T* x = reinterpret_cast<T*>(dst + j * LP_THREADS);
 #pragma unroll 1
-      for (int e = 0; e < LP_UNROLL * PER; ++e) {
-        const int v = (base + 32 * (e / PER)) * PER - skip + e % PER;
-        if (v >= 0 && v < V) before += logit<T>(row, v) > -INFINITY || v < tok;
-      }
-    }
-    if (n > 0) {
-      mk = fmaxf(mk, bm);
-      // at steps 1, 2, 4, ..: the n-th largest thread maximum of the block is a
-      // bound of its n-th best logit, and a near one
-      if ((step & (step + 1)) == 0) {
-        const uint32_t k = block_lists(warp_sort(ordered(mk)), sh.top);
-        if (w == 0) sh.top[0][lane] = k;
-        __syncthreads();
-        const uint32_t b = sh.top[0][n - 1];
-        bound = bound > b ? bound : b;
-        __syncthreads();
-      }
-      if (__any_sync(0xffffffffu, ordered(bm) >= bound)) {
-#pragma unroll
-        for (int u = 0; u < LP_UNROLL; ++u) sh.raw[u][t] = cur[u];
-#pragma unroll 1
-        for (int u = 0; u < LP_UNROLL; ++u) {
-          const uint4 v4 = sh.raw[u][t];
-          float vm = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < PER / 2; ++j) {
-            const float2 x = LpVec<T>::at(v4, j);
-            vm = fmaxf(vm, fmaxf(x.x, x.y));               // NaN as -inf
+          for (int q = 0; q < PER; ++q) {
+            if constexpr (sizeof(T) == 4) x[q] = e + q >= 0 && e + q < V ? row[e + q] : -INFINITY;
+            else x[q].v = e + q >= 0 && e + q < V ? row[e + q].v : 0xff80;
           }
-          if (!__any_sync(0xffffffffu, ordered(vm) >= bound)) continue;
+        }
+      }
+    }
+  };
+  fetch(row_of(r), skip_of(row_of(r)), s0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll 1
-          for (int e = 0; e < PER; ++e) {
-            const int v = (base + 32 * u) * PER - skip + e;
-            const u64 k = v >= 0 && v < V ? key_of(logit<T>(reinterpret_cast<const T*>(&sh.raw[u][t]), e), v) : 0;
-            const u64 least = __shfl_sync(0xffffffffu, list, n - 1);
-            const bool in = k > least && (uint32_t)(k >> 32) >= bound;
-            const uint32_t who = __ballot_sync(0xffffffffu, in);
-            if (in) sh.pend[w][pending + __popc(who & ((1u << lane) - 1))] = k;
-            pending += __popc(who);
-            if (pending >= 32) {                           // 32 of them into the list
-              __syncwarp();
-              const u64 p = sh.pend[w][lane], rest = sh.pend[w][32 + lane];
-              __syncwarp();
-              sh.pend[w][lane] = rest;
-              pending -= 32;
-              list = warp_merge(list, warp_sort(p));
-              const uint32_t nth = (uint32_t)(__shfl_sync(0xffffffffu, list, n - 1) >> 32);
-              bound = bound > nth ? bound : nth;
-              __syncwarp();
+  for (; pos < end; ++r, s0 = 0, ++rows) {
+    const int s1 = (int)min((int64_t)A.tiles, s0 + (end - pos));
+    pos += s1 - s0;
+    // the row as aligned vectors, a warp's of a step next to each other: vector i holds elements i PER - skip ..
+    const T* row = row_of(r);
+    const int skip = skip_of(row);
+    const int tok = A.tokens ? A.tokens[r] : -1;
+    const bool have = tok >= 0 && tok < V;
+    const float raw_t = have ? logit<T>(row, tok) : 0.f, key_t = am_key(raw_t);
+    // a logit comes before the token if it is larger, or equal at a lower
+    // index: x > up in vectors behind the token's (and, but for its ties, in
+    // it), x > down, the next value below, in vectors ahead of it
+    const int tvec = have ? (tok + skip) / PER : -1;
+    const bool low = have && key_t == -INFINITY;           // ties with NaN and -inf: compared one by one
+    const float up = have && !low ? key_t : INFINITY, down = have && !low ? nextafterf(key_t, -INFINITY) : INFINITY;
+    float R = -INFINITY, mk = -INFINITY;                   // c times the largest logit; the largest
+    u64 z2 = 0, zy2 = 0, ahead = 0;                        // two sums each
+    int before = 0, pending = 0;
+    bool bad = false;
+    u64 list = 0;
+    uint32_t bound = 0;                                    // no key below it can be among the block's best n
+#pragma unroll 1
+    for (int st = s0; st < s1; ++st) {
+      const int first = st * LP_TILE + w * 32 * U + lane;
+      if (st + 1 < s1) fetch(row, skip, st + 1);
+      else if (pos < end) fetch(row_of(r + 1), skip_of(row_of(r + 1)), 0);
+      asm volatile("cp.async.commit_group;\ncp.async.wait_group 1;" ::: "memory");
+      const uint4* mine = stage + ((used++ & 1) * U) * LP_THREADS + t;
+      float bm = -INFINITY;
+      if ((st * LP_TILE + w * 32 * U) * PER - skip < V) {  // (the last step may end before the warp's part of it)
+        bm = LpVec<T>::max_of(mine);
+        if (bm > mk) {
+          mk = bm;
+          const float to = lp_scaled(bm, A.c), d = fmaxf(R - to, -1e30f), f = lp_ex2(d);
+          const u64 f2 = pair(f, f);
+          zy2 = mul2(fma2(z2, pair(d, d), zy2), f2);
+          z2 = mul2(z2, f2);
+          R = to;
+        }
+        const float rb = R == -INFINITY ? 0.f : R;
+        const u64 nr2 = pair(-rb, -rb), z_old = z2, zy_old = zy2;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const uint4 v = reread(mine + j * LP_THREADS);
+#pragma unroll
+          for (int q = 0; q < PER / 2; ++q) {
+            const float2 x = LpVec<T>::at(v, q);
+            const u64 y2 = fma2(pair(x.x, x.y), c2, nr2);
+            const float2 y = halves(y2);
+            const u64 p2 = pair(lp_ex2(y.x), lp_ex2(y.y));
+            z2 = add2(z2, p2);
+            zy2 = fma2(p2, y2, zy2);
+          }
+        }
+        const float2 sum = halves(zy2);
+        if (!(sum.x + sum.y > -INFINITY) || fabsf(rb) > 1e29f) {   // masked tokens (0 times -inf), NaN, values at the type's ends
+          float z = 0.f, zy = 0.f;
+#pragma unroll 4
+          for (int e = 0; e < STEP; ++e) {
+            const float x = logit<T>(reinterpret_cast<const T*>(mine + e / PER * LP_THREADS), e % PER), y = lp_scaled(x, A.c) - rb;
+            const float p = x > -INFINITY ? lp_ex2(y) : 0.f;
+            bad = bad || !(x < INFINITY);
+            z += p;
+            zy = fmaf(p, y, zy);
+          }
+          z2 = add2(z_old, pair(z, 0.f));
+          zy2 = add2(zy_old, pair(zy, 0.f));
+        }
+        if (bm > down) {                                     // some may come before the token
+#pragma unroll
+          for (int j = 0; j < U; ++j) {
+            const uint4 v = reread(mine + j * LP_THREADS);
+            const float lim = first + 32 * j < tvec ? down : up;
+#pragma unroll
+            for (int q = 0; q < PER / 2; ++q) {
+              const float2 x = LpVec<T>::at(v, q);
+              ahead = add2(ahead, pair(above(x.x, lim), above(x.y, lim)));
             }
           }
         }
+        if (low) {
+#pragma unroll 1
+          for (int e = 0; e < STEP; ++e) {
+            const int i = (first + 32 * (e / PER)) * PER - skip + e % PER;
+            if (i >= 0 && i < V) before += logit<T>(row, i) > -INFINITY || i < tok;
+          }
+        }
       }
-    }
-  }
-  if (n > 0 && pending > 0) {
-    __syncwarp();
-    list = warp_merge(list, warp_sort(lane < pending ? sh.pend[w][lane] : 0));
-  }
-  const float2 zh = halves(z2), yh = halves(zy2);
-  float z = zh.x + zh.y, zy = yh.x + yh.y;
-  // ---- the block's statistics and list ----
+      if (n == 0) continue;
+      // after 1, 4, 16, .. steps: with the eight largest thread maxima of every
+      // warp, the n-th largest of those 32 bounds the n-th best logit seen
+      const int done = st - s0 + 1;
+      if ((done & (done - 1)) == 0 && (done & 0x55555555)) {
+        uint32_t k = ordered(mk);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), z2 = __shfl_xor_sync(0xffffffffu, z, o),
-                zy2 = __shfl_xor_sync(0xffffffffu, zy, o);
-    stats_merge(m, z, zy, m2, z2, zy2, A.c);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if (lane == 0) {
-    sh.m[w] = m;
-    sh.z[w] = z;
-    sh.zy[w] = zy;
-    sh.before[w] = before;
-  }
-  bad = __syncthreads_or(bad) != 0;
-  if (n > 0) list = block_lists(list, sh.list);
-  if (t == 0) {
-    for (int i = 1; i < LP_WARPS; ++i) {
-      stats_merge(m, z, zy, sh.m[i], sh.z[i], sh.zy[i], A.c);
-      before += sh.before[i];
+        for (int i = 0; i < 32 / LP_WARPS; ++i) {
+          const uint32_t mx = __reduce_max_sync(0xffffffffu, k);
+          if (lane == 0) sh.top[turn & 1][32 / LP_WARPS * w + i] = mx;
+          if (lane == __ffs(__ballot_sync(0xffffffffu, k == mx)) - 1) k = 0;
+        }
+        __syncthreads();                                   // (the other half of `top` is written next time)
+        const uint32_t b = __shfl_sync(0xffffffffu, warp_sort(sh.top[turn & 1][lane]), n - 1);
+        bound = bound > b ? bound : b;
+        ++turn;
+      }
+      const bool cand = ordered(bm) >= bound;
+      uint32_t rest = __ballot_sync(0xffffffffu, cand);
+      if (!rest) continue;
+      __syncwarp();                                        // (the others' copies are waited for)
+      do {                                                 // a thread's step, a logit per lane at a time
+        const int src = __ffs(rest) - 1;
+        rest &= rest - 1;
+        const uint4* its = mine - lane + src;
+#pragma unroll 1
+        for (int e = lane; e < STEP; e += 32) {
+          const int i = (st * LP_TILE + (w * U + e / PER) * 32 + src) * PER - skip + e % PER;
+          const u64 k = i >= 0 && i < V ? key_of(logit<T>(reinterpret_cast<const T*>(its + e / PER * LP_THREADS), e % PER), i) : 0;
+          const u64 least = __shfl_sync(0xffffffffu, list, n - 1);
+          const bool in = k > least && (uint32_t)(k >> 32) >= bound;
+          const uint32_t who = __ballot_sync(0xffffffffu, in);
+          if (in) sh.pend[w][pending + __popc(who & ((1u << lane) - 1))] = k;
+          pending += __popc(who);
+          if (pending >= 32) {                             // 32 of them into the list
+            __syncwarp();
+            const u64 p = sh.pend[w][lane], more = sh.pend[w][32 + lane];
+            __syncwarp();
+            sh.pend[w][lane] = more;
+            pending -= 32;
+            list = warp_merge(list, warp_sort(p));
+            const uint32_t nth = (uint32_t)(__shfl_sync(0xffffffffu, list, n - 1) >> 32);
+            bound = bound > nth ? bound : nth;
+            __syncwarp();
+          }
+        }
+      } while (rest);
+      __syncwarp();                                        // before the next step's vectors
     }
-  }
-  if (A.slices > 1) {
-    // ---- leave the slice; the row's last block joins them in order ----
-    const size_t at = (size_t)r * A.slices;
-    if (w == 0) {
-      if (n > 0) A.lists[(at + slice) * 32 + lane] = list;
-      if (lane == 0) A.stats[at + slice] = LpStats{m, z, zy, before, bad};
+
+    // ---- the block's part of the row: the warps' statistics and lists to one of them ----
+    if (n > 0 && pending > 0) {
+      __syncwarp();
+      list = warp_merge(list, warp_sort(lane < pending ? sh.pend[w][lane] : 0));
+      __syncwarp();
     }
-    __threadfence();
+    const float2 zh = halves(z2), yh = halves(zy2), ah = halves(ahead);
+    float z = zh.x + zh.y, zy = yh.x + yh.y;
+    before = __reduce_add_sync(0xffffffffu, before + (int)(ah.x + ah.y));
+    bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float ro = __shfl_xor_sync(0xffffffffu, R, o), zo = __shfl_xor_sync(0xffffffffu, z, o),
+                  zyo = __shfl_xor_sync(0xffffffffu, zy, o);
+      stats_merge(R, z, zy, ro, zo, zyo);
+    }
+    const int half = rows & 1;                             // the next row takes the other one
+    if (lane == 0) sh.stats[half][w] = LpStats{R, z, zy, before, bad};
+    if (n > 0) sh.list[half][w][lane] = list;
     __syncthreads();
-    if (t == 0) sh.last = atomicAdd(A.arrived + r, 1) == A.slices - 1;
-    __syncthreads();
-    if (!sh.last) return;
-    __threadfence();
-    list = 0;
-    if (n > 0) {
-      for (int i = w; i < A.slices; i += LP_WARPS) list = warp_merge(list, __ldcg(A.lists + (at + i) * 32 + lane));
-      list = block_lists(list, sh.list);
-    }
-    if (t == 0) {
-      A.arrived[r] = 0;
-      m = -INFINITY;
+    if (w != r % LP_WARPS) continue;
+    // `parts` statistics, in lanes 0 .. (at most 32 at a time), in a fixed tree
+    auto gather = [&](auto&& of, int parts) {
+      R = -INFINITY;
       z = zy = 0.f;
       before = 0;
       bad = false;
-      for (int i = 0; i < A.slices; ++i) {
-        const LpStats* s = A.stats + at + i;
-        stats_merge(m, z, zy, __ldcg(&s->m), __ldcg(&s->z), __ldcg(&s->zy), A.c);
-        before += __ldcg(&s->before);
-        bad = bad || __ldcg(&s->bad) != 0;
+      for (int p0 = 0; p0 < parts; p0 += 32) {
+        LpStats q{-INFINITY, 0.f, 0.f, 0, 0};
+        if (p0 + lane < parts) q = of(p0 + lane);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const float ro = __shfl_xor_sync(0xffffffffu, q.r, o), zo = __shfl_xor_sync(0xffffffffu, q.z, o),
+                      zyo = __shfl_xor_sync(0xffffffffu, q.zy, o);
+          stats_merge(q.r, q.z, q.zy, ro, zo, zyo);
+        }
+        stats_merge(R, z, zy, q.r, q.z, q.zy);
+        before += __reduce_add_sync(0xffffffffu, q.before);
+        bad = bad || __any_sync(0xffffffffu, q.bad != 0);
+      }
+    };
+    gather([&](int i) { return sh.stats[half][i]; }, LP_WARPS);
+    if (n > 0)
+      for (int i = 1; i < LP_WARPS; ++i) list = warp_merge(list, sh.list[half][(w + i) % LP_WARPS][lane]);
+    if (s0 > 0 || s1 < A.tiles) {
+      // ---- a shared row: leave the part; the last of its blocks, b0 .. b1, joins them ----
+      const int64_t u0 = (int64_t)r * A.tiles;
+      auto block_of = [&](int64_t unit) { return (int)(((unit + 1) * gridDim.x - 1) / units); };
+      const int b0 = block_of(u0), b1 = block_of(u0 + A.tiles - 1);
+      auto slot = [&](int b) { return (size_t)b * 2 + (b == b0 ? 1 : 0); };
+      const size_t mine = slot(blockIdx.x);
+      if (n > 0) A.lists[mine * 32 + lane] = list;
+      if (lane == 0) A.stats[mine] = LpStats{R, z, zy, before, bad};
+      __threadfence();
+      __syncwarp();
+      int last = 0;
+      if (lane == 0) last = atomicAdd(A.arrived + b0, 1) == b1 - b0;
+      if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+      __threadfence();
+      if (lane == 0) A.arrived[b0] = 0;
+      gather([&](int i) {
+        const LpStats* q = A.stats + slot(b0 + i);
+        return LpStats{__ldcg(&q->r), __ldcg(&q->z), __ldcg(&q->zy), __ldcg(&q->before), __ldcg(&q->bad)};
+      }, b1 - b0 + 1);
+      if (n > 0) {
+        list = 0;
+        for (int b = b0; b <= b1; b += 4) {                // four loads in flight
+          u64 k[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) k[i] = b + i <= b1 ? __ldcg(A.lists + slot(b + i) * 32 + lane) : 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) list = warp_merge(list, k[i]);
+        }
       }
     }
-  }
-  if (w != 0) return;
-  const float nan = __int_as_float(0x7fc00000), LN2 = 0.6931471805599453f;
-  const bool none = bad || m == -INFINITY;
-  const float lz = __shfl_sync(0xffffffffu, none ? nan : log2f(z), 0), mm = __shfl_sync(0xffffffffu, m, 0);
-  if (lane == 0) {
-    if (A.logprob) A.logprob[r] = have ? (raw_t - mm) * A.it - lz * LN2 : nan;
-    if (A.entropy) A.entropy[r] = none ? nan : (lz - zy / z) * LN2;
-    if (A.rank) {
-      if (!low)                                            // ties inside the token's vector
-        for (int v = max(0, tvec * PER - skip); v < tok; ++v) before += am_key(logit<T>(row, v)) == key_t;
-      A.rank[r] = have ? before + 1 : 0;
+    const bool none = bad || R == -INFINITY;
+    const float lz = none ? nan : log2f(z);
+    auto logp = [&](float x) {
+      const float y = fmaf(x, A.c, -R);
+      return y > -1e30f ? (y - lz) * LN2 : fmaf(x, A.it, -(R + lz) * LN2);
+    };
+    if (lane == 0) {
+      if (A.logprob) A.logprob[r] = have ? logp(raw_t) : nan;
+      if (A.entropy) A.entropy[r] = none ? nan : (lz - zy / z) * LN2;
+      if (A.rank) {
+        if (!low)                                          // ties inside the token's vector
+          for (int i = max(0, tvec * PER - skip); i < tok; ++i) before += am_key(logit<T>(row, i)) == key_t;
+        A.rank[r] = have ? before + 1 : 0;
+      }
+    }
+    if (lane < n) {
+      A.top_ids[(size_t)r * n + lane] = key_index(list);
+      A.top_lp[(size_t)r * n + lane] = logp(key_value(list));
     }
   }
-  if (lane < n) {
-    A.top_ids[(size_t)r * n + lane] = key_index(list);
-    A.top_lp[(size_t)r * n + lane] = (key_value(list) - mm) * A.it - lz * LN2;
-  }
 }
 
-// Slices of a row: as many steps of LP_TILE vectors as a row has at most; the
-// count that gives the least (waves of blocks) x (steps of a slice + 2), two
-// steps being about what a block spends on its end (measured: one row block's
-// end takes some 1.5 us, a step of 16 KB at a quarter of an SM's share 0.8 us).
-int lp_slices(int n_rows, int vocab, int esz) {
-  const int resident = lp_blocks(esz) * 152;
-  const int64_t tiles = ((int64_t)vocab * esz + 15 + LP_TILE * 16 - 1) / (LP_TILE * 16);
-  int best = 1;
-  int64_t cost = INT64_MAX;
-  const int most = n_rows > LP_COUNTERS ? 1 : (int)std::min<int64_t>(tiles, LP_MAX_SLICES);
-  for (int s = 1; s <= most; ++s) {
-    const int64_t waves = ((int64_t)n_rows * s + resident - 1) / resident, c = waves * ((tiles + s - 1) / s + 2);
-    if (c < cost) { cost = c; best = s; }
-  }
-  return best;
-}
-
-// The counters come first and keep their place, so that calls of other shapes
-// on the same workspace find them at zero.
+// Counters first, then statistics and lists; the same for every shape, so that
+// any calls may follow each other on a workspace.
 struct LpWs {
-  static constexpr size_t stats = LP_COUNTERS * sizeof(int);
-  size_t lists, total;
-  LpWs(int n_rows, int slices) {
-    const size_t parts = slices > 1 ? (size_t)n_rows * slices : 0;
-    lists = (stats + parts * sizeof(LpStats) + 15) / 16 * 16;
-    total = lists + parts * 32 * sizeof(u64);
-  }
+  static constexpr size_t stats = LP_MAX_BLOCKS * sizeof(int);
+  static constexpr size_t lists = (stats + 2 * LP_MAX_BLOCKS * sizeof(LpStats) + 15) / 16 * 16;
+  static constexpr size_t total = lists + 2 * LP_MAX_BLOCKS * 32 * sizeof(u64);
 };
+
+template <class T>
+cudaError_t launch_logprob(LpArgs A, cudaStream_t st) {
+  // vectors of a row at the least alignment, steps of those, blocks for the steps
+  constexpr int per = 16 / (int)sizeof(T), tile = LP_TILE;
+  A.tiles = ((A.vocab + per - 1 + per - 1) / per + tile - 1) / tile;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int blocks = (int)std::min<int64_t>((int64_t)A.n_rows * A.tiles, std::min(LP_BLOCKS * sms, LP_MAX_BLOCKS));
+  constexpr size_t smem = LP_STAGES * LP_TILE * 16;
+  if ((e = allow_dyn_smem(k_logprob<T>)) != cudaSuccess) return e;
+  k_logprob<T><<<blocks, LP_THREADS, smem, st>>>(A);
+  return cudaGetLastError();
+}
 
 }  // namespace
 }  // namespace spec
@@ -505,7 +529,7 @@ extern "C" int64_t spec_token_logprobs_ws_bytes(int n_rows, int vocab, int top_n
   if (n_rows < 1 || n_rows > 65535 || vocab < 1 || top_n < 0 || top_n > LP_TOP || top_n > vocab)
     return set_last_error(SPEC_ERR_ARG, "1 <= n_rows <= 65535, vocab >= 1 and 0 <= top_n <= min(32, vocab) required");
   if (vocab > LP_MAX_VOCAB) return set_last_error(SPEC_ERR_UNSUPPORTED, "vocab above 1048576");
-  return (int64_t)std::max(LpWs(n_rows, lp_slices(n_rows, vocab, 4)).total, LpWs(n_rows, lp_slices(n_rows, vocab, 2)).total);
+  return (int64_t)LpWs::total;
 }
 
 extern "C" int spec_token_logprobs(const void* logits_dev, int dtype, int64_t ld, int n_rows, int vocab,
@@ -526,15 +550,11 @@ extern "C" int spec_token_logprobs(const void* logits_dev, int dtype, int64_t ld
   if (reinterpret_cast<uintptr_t>(logits_dev) % esz || !aligned16(ws_dev))
     return set_last_error(SPEC_ERR_ARG, "misaligned logits or workspace");
   if ((int64_t)ws_bytes < need) return set_last_error(SPEC_ERR_ARG, "workspace too small");
-  const int slices = lp_slices(n_rows, vocab, esz);
-  const LpWs ws(n_rows, slices);
   char* w = static_cast<char*>(ws_dev);
-  const LpArgs A{logits_dev, ld, n_rows, vocab, top_n, slices, tokens_dev, 1.f / temperature, c, out_logprob_dev, out_entropy_dev,
-                 out_rank_dev, out_top_ids_dev, out_top_logprobs_dev, reinterpret_cast<int*>(w),
-                 reinterpret_cast<LpStats*>(w + ws.stats), reinterpret_cast<u64*>(w + ws.lists)};
+  const LpArgs A{logits_dev, ld, n_rows, vocab, top_n, 0, tokens_dev, 1.f / temperature, c, out_logprob_dev,
+                 out_entropy_dev, out_rank_dev, out_top_ids_dev, out_top_logprobs_dev, reinterpret_cast<int*>(w),
+                 reinterpret_cast<LpStats*>(w + LpWs::stats), reinterpret_cast<u64*>(w + LpWs::lists)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-  if (dtype == SPEC_F32) k_logprob<float><<<dim3(slices, n_rows), LP_THREADS, 0, st>>>(A);
-  else k_logprob<bf16_t><<<dim3(slices, n_rows), LP_THREADS, 0, st>>>(A);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = dtype == SPEC_F32 ? launch_logprob<float>(A, st) : launch_logprob<bf16_t>(A, st);
   return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
 }
