@@ -349,57 +349,64 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// Tensor-core form (bf16 cache). One block per SM, ten warps: a TMA producer,
-// an MMA issuer and two softmax groups of four warps. Keys come in tiles of
-// 128. S = Q K^T (M = 128 rows, N = 128 keys) goes to tensor memory; a softmax
-// thread owns one TMEM lane, reads its scores, and writes the weights over
-// them as two bf16 parts (hi = bf16(p), lo = bf16(p - hi): 16 bits, so that the
-// result is as near as the one rounding of the output lets it be); O += hi V +
-// lo V takes them from TMEM as the A operand and V as an MN-major B operand.
+// Tensor-core form (bf16 cache). One block per SM, twelve warps: a TMA producer,
+// an MMA issuer, two loaders (the next segment's queries, masks and sizes) and
+// two softmax groups of four warps. Keys come in tiles of 128. S = Q K^T (M = 128
+// rows, N = 128 keys) goes to tensor memory; a softmax thread owns one TMEM lane,
+// reads its scores, and writes the weights over them as bf16, and what that
+// rounding leaves as bf16 too (hi = bf16(p), lo = bf16(p - hi): 16 bits, so that
+// the result is as near as the one rounding of the output lets it be); O += hi V
+// + lo V takes them from TMEM as the A operand and V as an MN-major B operand.
 // The running maximum moves, and O is rescaled, only when a tile's maximum is
 // more than 8 (a factor of 256) above it.
 //
-// The two softmax groups work on two (S, O) slots in turn, so one group's
-// exponentials overlap the other slot's MMAs. More than 128 rows: slot i has
-// rows 128 i .. 128 i + 127 and both use every key tile. Up to 128 rows: the
-// slots take the segment's tiles alternately and their results are joined at
-// its end. Up to 64 (32) rows would leave most lanes idle, so the rows are
-// repeated 2 (4) times down the 128 lanes and repetition p takes the keys 128 /
-// nq p .. of each tile alone, with weights 0 for the others: the MMA, which has
-// M = 128 in any case, sums each repetition apart.
+// The two softmax groups have a buffer for S and an accumulator for O ("slot")
+// each and take turns, so that one's exponentials run beside the other's MMAs.
+// More than 128 rows: slot i has rows 128 i .. 128 i + 127 and both use every
+// key tile. Up to 128 rows: the slots take the segment's tiles alternately and
+// their results are joined at its end. Up to 64 rows would leave half of the
+// lanes idle: the rows are repeated, the upper 64 lanes holding the lo parts of
+// the weights where the lower ones hold the hi parts, which saves the second
+// MMA; up to 32 rows are repeated once more, and repetition p of two takes keys
+// 64 p .. 64 p + 63 of each tile alone, with weights 0 for the others (the MMA
+// has M = 128 in any case, and sums each lane apart).
 //
-// Bound: HBM for up to some 128 rows (two MMAs of 128 x 128 x 128 and one more
-// for the low part take about 1,540 cycles a tile, the tile's 64 KB some 2,800
-// at an SM's share of the measured copy rate), the tensor cores above that.
+// Bound: HBM for up to 128 rows (an MMA of 128 x 128 x 16 takes some 85 cycles,
+// so a tile 1,400 with the hi parts alone and 2,100 with both; its 64 KB take
+// 2,800 at an SM's share of the measured copy rate), the tensor cores above
+// that. (Tiles of 64 keys with two S buffers a slot were slower: an MMA of N = 64
+// takes 67 cycles, not half.)
 constexpr int TT_KEYS = 128;
-constexpr int TT_THREADS = 320;
-constexpr int TT_HALF = TT_KEYS * 128;           // bytes of 64 dims of a tile
-constexpr int TT_MAXBUF = 12;
+constexpr int TT_THREADS = 384;
+constexpr int TT_HALF = 128 * 128;               // bytes of 64 dims of a tile, and of 128 rows of Q
+constexpr int TT_MAXBUF = 16;
+constexpr int TT_OCOL = 256;                     // TMEM columns: S of a slot at 128 slot, its O behind at TT_OCOL + D slot
+constexpr int TT_STAGE = 2 * 128 * 64;           // staged output: two groups x 128 lanes x 16 columns
 
 template <int D>
 struct TtCfg {
-  static constexpr int BUF = TT_KEYS * D * 2;    // K or V of a tile, and Q of a slot
-  // Q (one slot, or two for more than 128 rows); at a segment's end the same
-  // bytes hold the statistics and the staged output (32 KB)
-  static constexpr int q_bytes(bool two) { return (two ? 2 : 1) * BUF < 32768 ? 32768 : (two ? 2 : 1) * BUF; }
-  static constexpr int TAIL = 2048;              // alignment slack and the header
-  static constexpr int nbuf(bool two) {
-    return (232448 - 512 - TAIL - q_bytes(two)) / BUF < TT_MAXBUF ? (232448 - 512 - TAIL - q_bytes(two)) / BUF : TT_MAXBUF;
-  }
-  static constexpr int smem(bool two) { return nbuf(two) * BUF + q_bytes(two) + TAIL; }
+  static constexpr int BUF = TT_KEYS * D * 2;    // K or V of a tile
+  static constexpr int QSLOT = 128 * D * 2;      // 128 rows of Q
+  static constexpr int TAIL = 5120;              // alignment slack and the header
+  static constexpr int q_bytes(bool two) { return (two ? 2 : 1) * QSLOT; }
+  static constexpr int fit(bool two) { return (232448 - 512 - TAIL - q_bytes(two) - TT_STAGE) / BUF; }
+  static constexpr int nbuf(bool two) { return fit(two) < TT_MAXBUF ? fit(two) : TT_MAXBUF; }
+  static constexpr int smem(bool two) { return nbuf(two) * BUF + q_bytes(two) + TT_STAGE + TAIL; }
 };
 
 struct TtHeader {
-  uint64_t kv_full[TT_MAXBUF], kv_empty[TT_MAXBUF], s_full[2], p_full[2], o_done[2], q_full, fin;
+  uint64_t kv_full[TT_MAXBUF], kv_empty[TT_MAXBUF], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2], q_free, fin;
   uint32_t tmem;
   int abort;
+  TreeSeg seg[2];                                // nt = 0: no more
   int parent[TREE_N];
+  unsigned long long mask[2][TREE_N];
+  float2 ml[2][128];                             // the lanes' (maximum, sum) in both slots
 };
-static_assert(sizeof(TtHeader) <= 1024, "header and alignment slack share 2 KB");
 
 __device__ __forceinline__ uint32_t sm_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// 32 columns of this warp's lanes; the values are there when it returns.
+// 32 (16) columns of this warp's lanes; the values are there when it returns.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
   __syncwarp();
   asm volatile(
@@ -412,6 +419,27 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16x2(uint32_t a0, uint32_t a1, uint32_t (&r)[16], uint32_t (&q)[16]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+        "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+        "=&r"(q[0]), "=&r"(q[1]), "=&r"(q[2]), "=&r"(q[3]), "=&r"(q[4]), "=&r"(q[5]), "=&r"(q[6]), "=&r"(q[7]),
+        "=&r"(q[8]), "=&r"(q[9]), "=&r"(q[10]), "=&r"(q[11]), "=&r"(q[12]), "=&r"(q[13]), "=&r"(q[14]), "=&r"(q[15])
+      : "r"(a0), "r"(a1) : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   __syncwarp();
   asm volatile(
@@ -423,20 +451,75 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// (the first 16 values)
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[32]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  __syncwarp();
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// 1 in one lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+// Issued by the lanes with one != 0: D (+)= A B with A in shared memory (ss) or
+// in tensor memory (ts); the barrier arrival when all MMAs so far are done.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(one) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(one) : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(one) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+// A wait that was not over at once, out of line: the waits are many, the code of
+// the roles is better short.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int* abort, int32_t* err) {
+  if (mbar_wait_deadline(bar, parity, abort)) return true;
+  *reinterpret_cast<volatile int*>(abort) = DERR_TIMEOUT;
+  atomicOr(err, DERR_TIMEOUT);
+  return false;
 }
 __device__ __forceinline__ void mbar_init(const uint64_t* bar, int count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sm_addr(bar)), "r"(count));
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The same, true when v holds in every thread of it.
+__device__ __forceinline__ bool named_sync_and(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(r) : "r"((uint32_t)v), "r"(id), "r"(threads) : "memory");
+  return r != 0;
 }
 // Shared-memory matrix descriptor, 128-byte swizzle, 8-row groups 1024 bytes
 // apart. lbo: bytes between 64-element groups of the leading dimension (an
@@ -456,33 +539,62 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
+// Two fp32 values in a register pair, for the packed instructions.
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // Rows of a segment and how they lie on the 128 lanes of the two slots.
 struct TtRows {
-  int row0, rows, nq, rpp;     // first row, rows, repetitions, lanes of one
-  bool two;                    // slots split the rows, not the key tiles
+  int row0, rows, rpp, kparts; // first row, rows, lanes of a repetition, parts of a tile's keys
+  bool two, hl;                // slots split the rows, not the tiles; hi parts on the lower lanes, lo parts on the upper
   __device__ TtRows(const TreeArgs& A, const TreeSeg& g) {
     row0 = g.rt * A.rows;
     rows = min(A.rows, g.k * A.G - row0);
     two = rows > 128;
-    nq = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
-    rpp = 128 / nq;
+    hl = rows <= 64;
+    rpp = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    kparts = rows <= 32 ? 2 : 1;
   }
 };
 
 template <int D>
 __global__ void __launch_bounds__(TT_THREADS, 1)
-    k_tree_tc(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ TreeArgs A, int nbuf, int q_bytes, int kb) {
+    k_tree_tc(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ TreeArgs A, int kb, int NBUF, int q_bytes) {
   using C = TtCfg<D>;
-  constexpr int HALVES = D / 64, OCOL = 256;
+  constexpr int HALVES = D / 64;
   extern __shared__ unsigned char tt_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tt_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char* qsm = base + nbuf * C::BUF;
-  TtHeader& H = *reinterpret_cast<TtHeader*>(qsm + q_bytes);
+  unsigned char* qsm = base + NBUF * C::BUF;
+  unsigned char* stg = qsm + q_bytes;
+  TtHeader& H = *reinterpret_cast<TtHeader*>(stg + TT_STAGE);
+  static_assert(sizeof(TtHeader) + 1024 <= C::TAIL, "header and alignment slack");
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t bufs = sm_addr(base), q_addr = sm_addr(qsm);
   if (t == 0) {
-    for (int i = 0; i < nbuf; ++i) {
+    for (int i = 0; i < NBUF; ++i) {
       mbar_init(H.kv_full + i, 1);
       mbar_init(H.kv_empty + i, 1);
     }
@@ -490,8 +602,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       mbar_init(H.s_full + i, 1);
       mbar_init(H.p_full + i, 4);
       mbar_init(H.o_done + i, 1);
+      mbar_init(H.seg_full + i, 2);              // the loaders' warps
+      mbar_init(H.seg_free + i, 8);              // the softmax warps
     }
-    mbar_init(&H.q_full, 8);
+    mbar_init(&H.q_free, 1);                     // a segment's last S
     mbar_init(&H.fin, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     H.abort = 0;
@@ -512,15 +626,11 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other
-  // waits at once: the producer and the issuer stop, the softmax groups go on
-  // through their barriers without results.
+  // waits at once: the producer and the issuer stop, the softmax groups finish
+  // the segment without a result and stop, the loaders run to their end.
   auto wait = [&](const uint64_t* bar, uint32_t parity) {
-    if (mbar_wait_deadline(sm_addr(bar), parity & 1, &H.abort)) return true;
-    *reinterpret_cast<volatile int*>(&H.abort) = DERR_TIMEOUT;
-    atomicOr(A.err, DERR_TIMEOUT);
-    return false;
+    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err);
   };
-  TreeSeg g;
   const int P = A.kv.page_size;
 
   if (warp == 8) {
@@ -529,19 +639,26 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     int b = 0;
     uint32_t turn = 0;                           // passes over the ring
     bool ok = true;
+    TreeSeg g;
     while (ok && walk.next(g)) {
       const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
       const int plane = (A.layer * A.kv.n_kv_heads + g.hk) * 2;
-      for (int tile = g.t0; ok && tile < g.t1; ++tile) {
+      auto page_of = [&](int tile) {             // of this lane's box; -1 reads zeros
         const int key = tile * TT_KEYS + kb * j;
-        int page = -1;                           // reads zeros
-        if (lane < nbox * HALVES && key < g.n + g.k) {
+        int page = -1;
+        if (lane < nbox * HALVES && tile < g.t1 && key < g.n + g.k) {
           page = bt[key / P];
           if (page < 0 || page >= A.kv.n_pages) {
             page = -1;
             atomicOr(A.err, DERR_PAGE);
           }
         }
+        return page;
+      };
+      int next = page_of(g.t0);
+      for (int tile = g.t0; ok && tile < g.t1; ++tile) {
+        const int key = tile * TT_KEYS + kb * j, page = next;
+        next = page_of(tile + 1);
         for (int kv = 0; kv < 2; ++kv) {
           if (turn > 0 && !wait(H.kv_empty + b, turn - 1)) { ok = false; break; }
           const uint32_t full = sm_addr(H.kv_full + b);
@@ -554,197 +671,248 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
                 ::"r"(bufs + b * C::BUF + half * TT_HALF + j * kb * 128), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0),
                   "r"(key % P), "r"(half), "r"(plane + kv), "r"(page), "r"(full)
                 : "memory");
-          if (++b == nbuf) { b = 0; ++turn; }
+          if (++b == NBUF) { b = 0; ++turn; }
         }
       }
     }
     if (!ok)                                     // shared memory outlives the copies in flight
-      for (int i = 0; i < nbuf; ++i) mbar_wait_deadline(sm_addr(H.kv_full + i), (i < b ? turn : turn - 1) & 1, nullptr);
+      for (int i = 0; i < NBUF; ++i) mbar_wait_deadline(sm_addr(H.kv_full + i), (i < b ? turn : turn - 1) & 1, nullptr);
   } else if (warp == 9) {
-    if (lane == 0) {
-      // ---- MMA issuer: S of a job, then P V of the job before it ----
-      // instruction descriptors: bf16 x bf16 -> f32, M = 128; V is MN-major
-      const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TT_KEYS >> 3) << 17) | (8u << 24);
-      const uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
-      uint32_t jobs[2] = {0, 0}, tiles = 0, segs = 0;
-      bool ok = true;
-      struct { int slot, steps; bool first, last; uint32_t v; } pend = {0, 0, false, false, 0};   // v: index of the V load
-      bool have = false;
-      auto buf_of = [&](uint32_t idx) { return bufs + (idx % nbuf) * C::BUF; };
-      auto pv = [&]() {
-        have = false;
-        if (!wait(H.p_full + pend.slot, jobs[pend.slot] - 1) || !wait(H.kv_full + pend.v % nbuf, pend.v / nbuf)) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + OCOL + pend.slot * D, a = tmem + pend.slot * TT_KEYS;
-        const uint64_t bd = tt_desc(buf_of(pend.v), TT_HALF);
-        uint32_t acc = pend.first ? 0u : 1u;
-        for (int k = 0; k < pend.steps; ++k) {
+    // ---- MMA issuer: S of a job, then P V of the job before it. The whole
+    // warp runs the loop on values that are the same in every lane, so that the
+    // descriptors stay in uniform registers; one lane issues (an issue from
+    // divergent code takes some 85 cycles, as long as the MMA itself).
+    // instruction descriptors: bf16 x bf16 -> f32, M = 128; V is MN-major
+    const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(TT_KEYS >> 3) << 17) | (8u << 24);
+    const uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+    const uint32_t one = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    auto waitw = [&](const uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+    uint32_t n0 = 0, n1 = 0;                     // jobs of the slots
+    int kbuf = 0, kturn = 0;                     // ring position of the next tile's K
+    bool ok = true;
+    // the job whose P V is due: slot, job of the slot, 16-key steps, V's buffer
+    // and turn, first of the slot's segment, last use of V, lo parts apart
+    struct Job { int slot; uint32_t k; int steps, vbuf, vturn; bool first, last, lo; } q{};
+    bool due = false;
+    auto pv = [&]() {
+      due = false;
+      const bool go = waitw(H.kv_full + q.vbuf, q.vturn) && waitw(H.p_full + q.slot, q.k);
+      if (!go) return false;
+      tc_fence_after();
+      const uint32_t d = tm + TT_OCOL + q.slot * D, a = tm + q.slot * 128;
+      const uint64_t bd = tt_desc(bufs + q.vbuf * C::BUF, TT_HALF);
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {   // the hi, then the lo weights of 16 keys
-            asm volatile(
-                "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-                ::"r"(d), "r"(a + 32 * (k / 2) + 8 * (k & 1) + 16 * part), "l"(bd + (uint64_t)(k * (2048 >> 4))), "r"(id_o), "r"(acc));
-            acc = 1u;
-          }
+      for (int k = 0; k < TT_KEYS / 16; ++k) {
+        if (k < q.steps) {
+          mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1), bd + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 || !q.first, one);
+          if (q.lo) mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1) + 16, bd + (uint64_t)(k * (2048 >> 4)), id_o, true, one);
         }
-        tc_commit(sm_addr(H.o_done + pend.slot));
-        if (pend.last) tc_commit(sm_addr(H.kv_empty + pend.v % nbuf));
-        return true;
-      };
-      while (ok && walk.next(g)) {
-        const TtRows R(A, g);
-        const int nt = g.t1 - g.t0, nj = R.two ? 2 * nt : nt;
-        ok = wait(&H.q_full, segs++);
-        for (int jb = 0; ok && jb < nj; ++jb) {
-          const int slot = jb & 1, ti = R.two ? jb >> 1 : jb;
-          const uint32_t kidx = 2 * (tiles + ti);
-          // the slot's weights are read: the P V of its last job is done
-          ok = wait(H.kv_full + kidx % nbuf, kidx / nbuf) && (jobs[slot] == 0 || wait(H.o_done + slot, jobs[slot] - 1));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t ad = tt_desc(q_addr + (R.two ? slot * C::BUF : 0), 16), bd = tt_desc(buf_of(kidx), 16);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = (uint64_t)(((k >> 2) * TT_HALF + (k & 3) * 32) >> 4);
-            asm volatile(
-                "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-                ::"r"(tmem + slot * TT_KEYS), "l"(ad + off), "l"(bd + off), "r"(id_s), "r"(k ? 1u : 0u));
-          }
-          const bool last = !R.two || slot == 1;
-          tc_commit(sm_addr(H.s_full + slot));
-          if (last) tc_commit(sm_addr(H.kv_empty + kidx % nbuf));
-          if (have) ok = pv();
-          ++jobs[slot];
-          pend = {slot, (min(TT_KEYS, g.n + g.k - (g.t0 + ti) * TT_KEYS) + 15) / 16, ti == (R.two ? 0 : slot), last, kidx + 1};
-          have = true;
-        }
-        if (ok && have) ok = pv();
-        tiles += nt;
       }
-      // everything issued is done before TMEM is freed (also after an abort)
-      tc_commit(sm_addr(&H.fin));
-      mbar_wait_deadline(sm_addr(&H.fin), 0, nullptr);
+      tc_commit(sm_addr(H.o_done + q.slot), one);
+      if (q.last) tc_commit(sm_addr(H.kv_empty + q.vbuf), one);
+      return true;
+    };
+    for (uint32_t seg = 0; ok; ++seg) {
+      const int sb = seg & 1;
+      if (!(ok = waitw(H.seg_full + sb, seg >> 1))) break;
+      TreeSeg g = H.seg[sb];
+      g.nt = same(g.nt); g.t0 = same(g.t0); g.t1 = same(g.t1); g.n = same(g.n); g.k = same(g.k); g.rt = same(g.rt);
+      if (g.nt == 0) break;
+      const TtRows R(A, g);
+      const int nt = g.t1 - g.t0, nj = R.two ? 2 * nt : nt;
+      for (int jb = 0; ok && jb < nj; ++jb) {
+        const int slot = jb & 1, ti = R.two ? jb >> 1 : jb;
+        const uint32_t k = slot ? n1++ : n0++;
+        // S goes over the slot's last weights: their P V is done
+        ok = waitw(H.kv_full + kbuf, kturn) && (k == 0 || waitw(H.o_done + slot, k - 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ad = tt_desc(q_addr + (R.two ? slot * C::QSLOT : 0), 16), bd = tt_desc(bufs + kbuf * C::BUF, 16);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t in = (uint64_t)(((i & 3) * 32 + (i >> 2) * TT_HALF) >> 4);
+          mma_ss(tm + slot * 128, ad + in, bd + in, id_s, i > 0, one);
+        }
+        const bool last = !R.two || slot == 1;
+        tc_commit(sm_addr(H.s_full + slot), one);
+        if (last) tc_commit(sm_addr(H.kv_empty + kbuf), one);
+        if (jb == nj - 1) tc_commit(sm_addr(&H.q_free), one);
+        if (due) ok = pv();
+        const bool wrap = kbuf + 1 == NBUF;      // V follows K in the ring
+        q = Job{slot, k, (min(TT_KEYS, g.n + g.k - (g.t0 + ti) * TT_KEYS) + 15) / 16, wrap ? 0 : kbuf + 1,
+                wrap ? kturn + 1 : kturn, ti == (R.two ? 0 : slot), last, !R.hl};
+        due = true;
+        if (last) {
+          kbuf += 2;
+          if (kbuf >= NBUF) { kbuf -= NBUF; ++kturn; }
+        }
+      }
+      if (ok && due) ok = pv();
+    }
+    // everything issued is done before TMEM is freed (also after an abort)
+    tc_commit(sm_addr(&H.fin), one);
+    mbar_wait_deadline(sm_addr(&H.fin), 0, nullptr);
+  } else if (warp >= 10) {
+    // ---- loaders: the segments' sizes, queries (repeated down the lanes) and masks ----
+    const int i0 = t - 320;
+    TreeSeg g;
+    for (uint32_t seg = 0;; ++seg) {
+      const int sb = seg & 1;
+      const bool have = walk.next(g);
+      if (seg >= 2) wait(H.seg_free + sb, (seg >> 1) - 1);
+      if (!have) g.nt = 0;
+      if (i0 == 0) H.seg[sb] = g;
+      if (have) {
+        const TtRows R(A, g);
+        int par = -1;
+        if (i0 < g.k) par = A.parents[(size_t)g.s * A.max_nodes + i0];
+        // thread i0: 16-byte piece c of rows x, x + step, ..
+        constexpr int PPR = D / 8, STEP = 64 / PPR;
+        const int c = i0 % PPR, nrep = R.two ? 1 : 128 / R.rpp;
+        int node = (R.row0 + i0 / PPR) / A.G, head = (R.row0 + i0 / PPR) % A.G;
+        const bf16_t* qg = static_cast<const bf16_t*>(A.q) + ((size_t)g.s * A.max_nodes * A.hq + g.hk * A.G) * D + 8 * c;
+        const uint32_t qd = q_addr + (c >> 3) * TT_HALF;
+        if (seg > 0) wait(&H.q_free, seg - 1);
+#pragma unroll 1
+        for (int x = i0 / PPR; x < R.rows; x += STEP) {
+          const bf16_t* src = qg + ((size_t)node * A.hq + head) * D;
+          uint32_t y = (uint32_t)(x & 127), dst = qd + (x >> 7) * C::QSLOT + y * 128 + (((c & 7) ^ (y & 7)) << 4);
+          for (int p = 0; p < nrep; ++p, dst += R.rpp * 128)   // (a repetition starts at a multiple of 8 rows)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+          for (head += STEP; head >= A.G; head -= A.G) ++node;
+        }
+        if (g.t1 * TT_KEYS > g.n) {              // the segment reaches the tree's slots
+          if (i0 < g.k) {
+            H.parent[i0] = par;
+            if (g.t1 == g.nt && (par < -1 || par >= i0)) atomicOr(A.err, SPEC_DEV_ERR_TREE);
+          }
+          named_sync(4, 64);
+          if (i0 < g.k) H.mask[sb][i0] = ancestors(H.parent, i0);
+          named_sync(4, 64);
+        }
+        asm volatile("cp.async.wait_all;\nfence.proxy.async.shared::cta;" ::: "memory");
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm_addr(H.seg_full + sb));
+      if (!have) break;
     }
   } else {
     // ---- softmax groups ----
     const int slot = warp >> 2, r = t & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t sT = tmem + lanes + slot * TT_KEYS, oT = tmem + lanes + OCOL + slot * D;
+    const uint32_t oT = tmem + lanes + TT_OCOL + slot * D;
+    const unsigned long long sc2 = pair(A.scale_l2e, A.scale_l2e);
     uint32_t jobs = 0, tiles = 0;                // of this slot; of the block
-    while (walk.next(g)) {
+    for (uint32_t seg = 0;; ++seg) {
+      const int sb = seg & 1;
+      // all eight warps together: O and the staging bytes of the last segment
+      // are free, and either all of them or none go on after an abort
+      if (!named_sync_and(1, 256, wait(H.seg_full + sb, seg >> 1))) break;
+      const TreeSeg g = H.seg[sb];
+      if (g.nt == 0) break;
       const TtRows R(A, g);
       const int nt = g.t1 - g.t0;
-      const int part = R.two ? 0 : r / R.rpp, lr = R.two ? slot * 128 + r : r % R.rpp;
-      const bool live = lr < R.rows;
-      // Q rows, repeated nq times down the lanes, and the nodes' masks
-      for (int i = t; i < R.rows * (D / 8); i += 256) {
-        const int x = i / (D / 8), c = i % (D / 8), rr = R.row0 + x;
-        const uint4 v = *reinterpret_cast<const uint4*>(
-            static_cast<const bf16_t*>(A.q) +
-            (((size_t)g.s * A.max_nodes + rr / A.G) * A.hq + g.hk * A.G + rr % A.G) * D + 8 * c);
-        unsigned char* dst = qsm + (R.two ? (x >> 7) * C::BUF : 0) + (c >> 3) * TT_HALF;
-        for (int p = 0; p < R.nq; ++p) {
-          const int y = (x & 127) + p * R.rpp;
-          *reinterpret_cast<uint4*>(dst + y * 128 + (((c & 7) ^ (y & 7)) << 4)) = v;
-        }
-      }
-      const bool tree = g.t1 * TT_KEYS > g.n;    // the segment reaches the tree's slots
-      if (tree && t < g.k) {
-        const int par = A.parents[(size_t)g.s * A.max_nodes + t];
-        H.parent[t] = par;
-        if (g.t1 == g.nt && (par < -1 || par >= t)) atomicOr(A.err, SPEC_DEV_ERR_TREE);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sm_addr(&H.q_full));
-      unsigned long long mask = 0;
-      if (tree) {
-        named_sync(1, 256);
-        if (live) mask = ancestors(H.parent, (R.row0 + lr) / A.G);
-      }
-      float m = -INFINITY, l = 0.f;
+      const int rep = R.two ? 0 : r / R.rpp, lr = R.two ? slot * 128 + r : r % R.rpp;
+      const int kpart = R.kparts == 2 ? rep & 1 : 0;
+      const bool live = lr < R.rows, low = R.hl && r >= 64;
       const bool any_live = __any_sync(0xffffffffu, live);
-      const int nc = 4 / R.nq, c_lo = part * nc;  // this repetition's 32-key chunks of a tile
+      unsigned long long mask = 0;
+      if (live && g.t1 * TT_KEYS > g.n) mask = H.mask[sb][(R.row0 + lr) / A.G];
+      float m = -INFINITY, l = 0.f;
       for (int ti = R.two ? 0 : slot; ti < nt; ti += R.two ? 1 : 2) {
         const int k0 = (g.t0 + ti) * TT_KEYS;
         const bool first = ti == (R.two ? 0 : slot);
-        wait(H.s_full + slot, jobs++);
+        const uint32_t k = jobs++, sT = tmem + lanes + slot * 128;
+        wait(H.s_full + slot, k);
         tc_fence_after();
         if (any_live) {
-          const bool edge = k0 + TT_KEYS > g.n;
-          auto bits_of = [&](int c) {            // visible keys of chunk c, for an edge tile
-            const int sh = k0 + 32 * c - g.n;    // tree slot of the chunk's first key
-            if (!live) return 0u;
-            if (sh <= -32) return 0xffffffffu;
-            if (sh < 0) return (uint32_t)(mask << -sh) | ((1u << -sh) - 1);
-            return sh < TREE_N ? (uint32_t)(mask >> sh) : 0u;
-          };
-          float mt = -INFINITY;
-          for (int c = c_lo; c < c_lo + nc; ++c) {
-            uint32_t v[32];
+          // this lane's chunks of 32 keys: all four, or a key part's two
+          const int c0 = 2 * kpart, c1 = R.kparts == 2 ? c0 + 2 : 4;
+          const bool edge = k0 + TT_KEYS > g.n;  // tree slots, or slots past the last
+          auto chunk = [&](int c, uint32_t (&v)[32]) {
             tmem_ld32(sT + 32 * c, v);
-            const uint32_t bits = edge ? bits_of(c) : 0xffffffffu;
+            if (edge) {
+              const int sh = k0 + 32 * c - g.n;  // tree slot of the chunk's first key
+              uint32_t bits = 0u;
+              if (sh <= -32) bits = 0xffffffffu;
+              else if (sh < 0) bits = (uint32_t)(mask << -sh) | ((1u << -sh) - 1);
+              else if (sh < TREE_N) bits = (uint32_t)(mask >> sh);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((bits >> i) & 1) mt = fmaxf(mt, __uint_as_float(v[i]));
+              for (int i = 0; i < 32; ++i)
+                if (!((bits >> i) & 1)) v[i] = 0xff800000u;
+            }
+          };
+          float mt = -INFINITY, mu = -INFINITY;
+          uint32_t v[32];
+#pragma unroll 1
+          for (int c = c1 - 1; c >= c0; --c) {   // (chunk c0 last: its values are used first)
+            chunk(c, v);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              mt = max3(mt, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+              mu = max3(mu, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+            }
           }
-          mt *= A.scale_l2e;
+          mt = fmaxf(mt, mu) * A.scale_l2e;
           if (first) {
             m = mt;
           } else {
             const bool grow = live && mt > m + 8.f;
-            if (__any_sync(0xffffffffu, grow)) {
+            if (__any_sync(0xffffffffu, grow)) { // (S of this tile came after the slot's last P V)
               const float corr = grow ? ex2(m - mt) : 1.f;
               if (grow) m = mt;
               l *= corr;
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld32(oT + 32 * c, v);
+                uint32_t o[32];
+                tmem_ld32(oT + 32 * c, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * corr);
-                tmem_st32(oT + 32 * c, v);
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                tmem_st32(oT + 32 * c, o);
               }
             }
           }
           const float mb = m == -INFINITY ? 0.f : m;
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            if (c >= c_lo && c < c_lo + nc) {    // warp-uniform: a warp's lanes lie in one repetition
-              tmem_ld32(sT + 32 * c, v);
-              const uint32_t bits = edge ? bits_of(c) : 0xffffffffu;
-              uint32_t w[32];
-              float s0 = 0.f, s1 = 0.f;
+          const unsigned long long nm2 = pair(-mb, -mb);
+          unsigned long long sum = 0;
+#pragma unroll 1
+          for (int c = c0;;) {
+            uint32_t w[32];
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float p0 = ex2(fmaf(__uint_as_float(v[i]), A.scale_l2e, -mb));
-                float p1 = ex2(fmaf(__uint_as_float(v[i + 1]), A.scale_l2e, -mb));
-                if (!((bits >> i) & 1)) p0 = 0.f;
-                if (!((bits >> (i + 1)) & 1)) p1 = 0.f;
-                s0 += p0;
-                s1 += p1;
-                const uint32_t hi = pack_bf16(p0, p1);
-                w[i / 2] = hi;
-                w[16 + i / 2] = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
-              }
-              l += s0 + s1;
-              tmem_st32(sT + 32 * c, w);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0u;
-              tmem_st32(sT + 32 * c, v);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = halves(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2));
+              const float p0 = ex2(y.x), p1 = ex2(y.y);
+              const unsigned long long p2 = pair(p0, p1);
+              sum = add2(sum, p2);
+              const uint32_t hi = pack_bf16(p0, p1);
+              const float2 e = halves(add2(p2, pair(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xFFFF0000u))));
+              const uint32_t lo = pack_bf16(e.x, e.y);
+              w[i / 2] = low ? lo : hi;
+              w[16 + i / 2] = lo;
             }
+            if (R.hl) tmem_st16(sT + 32 * c, w);
+            else tmem_st32(sT + 32 * c, w);
+            if (++c == c1) break;
+            chunk(c, v);
           }
-          __syncwarp();
+          if (R.kparts == 2) {                   // the other part's keys: weights 0
+            uint32_t x[32];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = 0u;
+            tmem_st16(sT + 32 * (2 - c0), x);
+            tmem_st16(sT + 32 * (3 - c0), x);
+          }
+          const float2 s2 = halves(sum);
+          l += s2.x + s2.y;
           tmem_wait_st();
         }
         // slots past the last node may hold anything: their V rows become zeros
         const int nk = g.n + g.k - k0;
         if (nk < TT_KEYS) {
           const uint32_t vi = 2 * (tiles + ti) + 1;
-          wait(H.kv_full + vi % nbuf, vi / nbuf);
-          unsigned char* vb = base + (vi % nbuf) * C::BUF;
+          wait(H.kv_full + vi % NBUF, vi / NBUF);
+          unsigned char* vb = base + (vi % NBUF) * C::BUF;
           for (int i = r; i < (TT_KEYS - nk) * HALVES * 8; i += 128) {
             const int hf = i / ((TT_KEYS - nk) * 8), e = i % ((TT_KEYS - nk) * 8);
             *reinterpret_cast<uint4*>(vb + hf * TT_HALF + (nk + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
@@ -759,33 +927,36 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 
       // ---- the segment's end ----
       const int wpart = part_of(g);
-      // 4 output values of row x (final ones where the block holds the segment alone), columns col .. col + 3
-      auto emit4 = [&](int x, int col, float4 v) {
-        if (wpart < 0) {
-          const int rr = R.row0 + x;
-          bf16_t* og = static_cast<bf16_t*>(A.out) +
-                       (((size_t)g.s * A.max_nodes + rr / A.G) * A.hq + g.hk * A.G + rr % A.G) * D + col;
-          *reinterpret_cast<uint2*>(og) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-        } else {
-          *reinterpret_cast<float4*>(A.part_o + (((size_t)blockIdx.x * 2 + wpart) * A.rows + x) * D + col) = v;
-        }
+      // where row x goes: the result, or this block's part of it
+      auto out_row = [&](int x) -> unsigned char* {
+        const int rr = R.row0 + x, node = rr / A.G;
+        if (wpart < 0)
+          return static_cast<unsigned char*>(A.out) +
+                 (((size_t)g.s * A.max_nodes + node) * A.hq + g.hk * A.G + rr - node * A.G) * D * 2;
+        return reinterpret_cast<unsigned char*>(A.part_o + (((size_t)blockIdx.x * 2 + wpart) * A.rows + x) * D);
+      };
+      auto emit4 = [&](unsigned char* o, int col, float4 v) {
+        if (wpart < 0) *reinterpret_cast<uint2*>(o + col * 2) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+        else *reinterpret_cast<float4*>(o + col * 4) = v;
       };
       auto emit_ml = [&](int x, float mm, float ll) {
         if (wpart >= 0) A.part_ml[((size_t)blockIdx.x * 2 + wpart) * A.rows + x] = make_float2(mm, ll);
       };
       // each group waits for its own slot's last P V; the barriers pass that on
       if (R.two || slot < nt) wait(H.o_done + slot, jobs - 1);
+      tc_fence_after();
       if (R.two) {
-        tc_fence_after();
-        const float w = wpart < 0 ? 1.f / l : 1.f;
         if (any_live) {
+          const float w = wpart < 0 ? 1.f / l : 1.f;
+          unsigned char* og = out_row(live ? lr : 0);
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
             tmem_ld32(oT + 32 * c, v);
             if (live) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
-                emit4(lr, 32 * c + i, make_float4(__uint_as_float(v[i]) * w, __uint_as_float(v[i + 1]) * w,
+                emit4(og, 32 * c + i, make_float4(__uint_as_float(v[i]) * w, __uint_as_float(v[i + 1]) * w,
                                                   __uint_as_float(v[i + 2]) * w, __uint_as_float(v[i + 3]) * w));
             }
           }
@@ -793,65 +964,71 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         }
       } else {
         const bool both = nt > 1;                // slot 1 had tiles
-        // statistics of the row's repetitions in both slots, in Q's bytes: a slot's last P V comes after every S but
-        // the one of a single tile, which slot 1 has not waited for
-        if (!both) named_sync(1, 256);
-        float2* ml = reinterpret_cast<float2*>(qsm);
-        ml[slot * 128 + r] = make_float2(live ? m : -INFINITY, live ? l : 0.f);
+        H.ml[slot][r] = make_float2(live ? m : -INFINITY, live ? l : 0.f);
         tc_fence_before();
         named_sync(1, 256);
         tc_fence_after();
         float M = -INFINITY, L = 0.f;
-        for (int p = 0; p < R.nq; ++p)
-          M = fmaxf(M, fmaxf(ml[p * R.rpp + r % R.rpp].x, ml[128 + p * R.rpp + r % R.rpp].x));
-        const float Mb = M == -INFINITY ? 0.f : M;
-        for (int p = 0; p < R.nq; ++p) {
-          const float2 a = ml[p * R.rpp + r % R.rpp], b = ml[128 + p * R.rpp + r % R.rpp];
-          L += a.y * ex2(a.x - Mb) + b.y * ex2(b.x - Mb);
+        for (int p = 0; p < R.kparts; ++p) {     // (the upper lanes repeat the lower ones' statistics)
+          const float2 a = H.ml[0][p * R.rpp + r % R.rpp], b = H.ml[1][p * R.rpp + r % R.rpp];
+          const float mn = max3(M, a.x, b.x), mb = mn == -INFINITY ? 0.f : mn;
+          L = L * ex2(M - mb) + a.y * ex2(a.x - mb) + b.y * ex2(b.x - mb);
+          M = mn;
         }
-        const float inv = wpart < 0 ? 1.f / L : 1.f;
-        const float w0 = ex2(ml[r].x - Mb) * inv, w1 = ex2(ml[128 + r].x - Mb) * inv;
-        named_sync(1, 256);                      // the staged output takes the same bytes
-        if (slot == 0 && live && part == 0) emit_ml(lr, M, L);
+        const float Mb = M == -INFINITY ? 0.f : M, inv = wpart < 0 ? 1.f / L : 1.f;
+        const float w0 = ex2(H.ml[0][r].x - Mb) * inv, w1 = ex2(H.ml[1][r].x - Mb) * inv;
+        if (slot == 0 && live && rep == 0) emit_ml(lr, M, L);
         // group `slot` has columns slot D / 2 .. of both slots' outputs
-        const uint32_t o0 = tmem + lanes + OCOL + slot * (D / 2), o1 = o0 + D;
-        float4* stage = reinterpret_cast<float4*>(qsm + slot * 16384);   // [128 lanes][32 columns]
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t v[32], u[32];
-          tmem_ld32(o0 + 32 * c, v);
-          if (both) tmem_ld32(o1 + 32 * c, u);
-          float4 x[8];
+        const uint32_t o0 = tmem + lanes + TT_OCOL + slot * (D / 2), o1 = o0 + D;
+        float4* stage = reinterpret_cast<float4*>(stg + slot * (TT_STAGE / 2));   // [128 lanes][16 columns]
+        const int nrep = 128 / R.rpp;
+        unsigned char* og[2];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+        for (int q = 0; q < 2; ++q) {            // the rows this thread writes: its own, or those it sums
+          const int y = nrep == 1 ? lr : (r + 128 * q) / 4;
+          og[q] = out_row(y < R.rows ? y : 0);
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[16], u[16];
+          if (both) tmem_ld16x2(o0 + 16 * c, o1 + 16 * c, v, u);
+          else tmem_ld16(o0 + 16 * c, v);
+          float4 x[4];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
             float y = __uint_as_float(v[i]) * w0;
             if (both) y = fmaf(__uint_as_float(u[i]), w1, y);
             reinterpret_cast<float*>(x)[i] = y;
           }
-          const int col = slot * (D / 2) + 32 * c;
-          if (R.nq == 1) {
+          const int col = slot * (D / 2) + 16 * c;
+          if (nrep == 1) {
             if (live)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) emit4(lr, col + 4 * i, x[i]);
+              for (int i = 0; i < 4; ++i) emit4(og[0], col + 4 * i, x[i]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) stage[r * 8 + (i ^ (r & 7))] = x[i];
+            for (int i = 0; i < 4; ++i) stage[r * 4 + (i ^ ((r >> 1) & 3))] = x[i];
             named_sync(2 + slot, 128);
-            for (int i = r; i < R.rows * 8; i += 128) {
-              const int y = i / 8, pc = i % 8;
-              float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-              for (int p = 0; p < R.nq; ++p) {
-                const int ln = p * R.rpp + y;
-                const float4 z = stage[ln * 8 + (pc ^ (ln & 7))];
-                a.x += z.x; a.y += z.y; a.z += z.z; a.w += z.w;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int y = (r + 128 * q) / 4, pc = r & 3;
+              if (y < R.rows) {
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int p = 0; p < nrep; ++p) {
+                  const int ln = p * R.rpp + y;
+                  const float4 z = stage[ln * 4 + (pc ^ ((ln >> 1) & 3))];
+                  a.x += z.x; a.y += z.y; a.z += z.z; a.w += z.w;
+                }
+                emit4(og[q], col + 4 * pc, a);
               }
-              emit4(y, col + 4 * pc, a);
             }
             named_sync(2 + slot, 128);
           }
         }
       }
       tc_fence_before();
-      named_sync(1, 256);                        // O, Q and the statistics are free
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm_addr(H.seg_free + sb));
       if (wpart == 1 && t == 0)
         A.joint[blockIdx.x] = make_int4(g.s, g.rt, g.hk, parts_until(walk.U, blockIdx.x, walk.blocks, walk.u1 + g.nt - g.t1));
     }
@@ -882,19 +1059,36 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_tree_join(const __grid_cons
   // part 0 of the join is this block's part 1, then part 0 of the blocks after it
   auto at = [&](int c) { return ((size_t)(blockIdx.x + c) * 2 + (c == 0 ? 1 : 0)) * A.rows + r; };
   float M = -INFINITY;
-  for (int c = lane; c < parts; c += 32) M = fmaxf(M, A.part_ml[at(c)].x);
+  for (int c = lane; c < parts; c += 32) M = fmaxf(M, __ldcg(&A.part_ml[at(c)]).x);
   M = warp_max(M);
-  constexpr int NV = D / 32;
+  constexpr int NV = D / 32, FLY = 8;            // parts whose values are in flight at once
   float o[NV], l = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) o[i] = 0.f;
-  for (int c = 0; c < parts; ++c) {
-    const float2 ml = A.part_ml[at(c)];
-    const float w = exp2f(ml.x - M);
-    l = fmaf(ml.y, w, l);
-    const float* v = A.part_o + at(c) * D + NV * lane;
+  for (int c0 = 0; c0 < parts; c0 += FLY) {
+    float2 ml[FLY];
+    float v[FLY][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) o[i] = fmaf(v[i], w, o[i]);
+    for (int c = 0; c < FLY; ++c) {
+      const bool in = c0 + c < parts;
+      const size_t e = at(in ? c0 + c : c0);
+      ml[c] = in ? __ldcg(A.part_ml + e) : make_float2(-INFINITY, 0.f);
+      const float* p = A.part_o + e * D + NV * lane;
+      if constexpr (NV == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(p));
+        v[c][0] = f.x; v[c][1] = f.y; v[c][2] = f.z; v[c][3] = f.w;
+      } else {
+        const float2 f = __ldcg(reinterpret_cast<const float2*>(p));
+        v[c][0] = f.x; v[c][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < FLY; ++c) {
+      const float w = exp2f(ml[c].x - M);
+      l = fmaf(ml[c].y, w, l);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) o[i] = fmaf(v[c][i], w, o[i]);
+    }
   }
   KT* og = static_cast<KT*>(A.out) + (((size_t)s * A.max_nodes + rr / A.G) * A.hq + jt.z * A.G + rr % A.G) * D + NV * lane;
 #pragma unroll
@@ -964,11 +1158,11 @@ cudaError_t launch_fma(const TreeArgs& A, int blocks, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_tc(const TreeArgs& A, const CUtensorMap& map, int kb, int blocks, cudaStream_t st) {
-  using C = TtCfg<D>;
-  const bool two = A.rows > 128;
   cudaError_t e = allow_dyn_smem(k_tree_tc<D>);
+  const bool two = A.rows > 128;
   if (e == cudaSuccess)
-    e = launch_k(k_tree_tc<D>, dim3(blocks), dim3(TT_THREADS), C::smem(two), st, map, A, C::nbuf(two), C::q_bytes(two), kb);
+    e = launch_k(k_tree_tc<D>, dim3(blocks), dim3(TT_THREADS), TtCfg<D>::smem(two), st, map, A, kb, TtCfg<D>::nbuf(two),
+                 TtCfg<D>::q_bytes(two));
   return e == cudaSuccess ? join<D, bf16_t>(A, blocks, st) : e;
 }
 
