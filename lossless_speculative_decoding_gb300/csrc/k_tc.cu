@@ -726,8 +726,8 @@ int tc_make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t row
   return r == CUDA_SUCCESS ? 0 : -3;
 }
 
-static int kv_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, int planes, int n_pages,
-                  size_t page_elems, uint32_t box_keys, uint32_t box_halves, uint32_t box_planes) {
+int kv_make_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, int planes, int n_pages,
+                size_t page_elems) {
   auto fn = encode_fn();
   if (!fn) return -1;
   if ((reinterpret_cast<uintptr_t>(kv) & 15) || head_dim % 64 || page_size % 16) return -2;
@@ -738,7 +738,7 @@ static int kv_map(CUtensorMap* map, const void* kv, int head_dim, int page_size,
                               (cuuint64_t)n_pages};
   const cuuint64_t strides[4] = {(cuuint64_t)head_dim * 2, 128, (cuuint64_t)page_size * head_dim * 2,
                                  (cuuint64_t)page_elems * 2};
-  const cuuint32_t box[5] = {64, box_keys, box_halves, box_planes, 1};
+  const cuuint32_t box[5] = {64, (cuuint32_t)(page_size % 64 == 0 ? 64 : 16), (cuuint32_t)halves, 2, 1};
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(kv), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -746,14 +746,32 @@ static int kv_map(CUtensorMap* map, const void* kv, int head_dim, int page_size,
   return r == CUDA_SUCCESS ? 0 : -3;
 }
 
-int kv_make_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, int planes, int n_pages,
-                size_t page_elems) {
-  return kv_map(map, kv, head_dim, page_size, planes, n_pages, page_elems, page_size % 64 == 0 ? 64 : 16, head_dim / 64, 2);
+int kv_make_group_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, uint64_t planes, int box_keys) {
+  auto fn = encode_fn();
+  if (!fn) return -1;
+  if ((reinterpret_cast<uintptr_t>(kv) & 15) || head_dim % 64 || page_size % 16 || box_keys % 8) return -2;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)head_dim / 64, (cuuint64_t)page_size / 8, planes};
+  const cuuint64_t strides[4] = {(cuuint64_t)head_dim * 2, 128, (cuuint64_t)head_dim * 16, (cuuint64_t)page_size * head_dim * 2};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)head_dim / 64, (cuuint32_t)box_keys / 8, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(kv), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -3;
 }
 
-int kv_make_half_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, int planes, int n_pages,
-                     size_t page_elems, int box_keys) {
-  return kv_map(map, kv, head_dim, page_size, planes, n_pages, page_elems, box_keys, 1, 1);
+int q_make_map(CUtensorMap* map, const void* q, int head_dim, int heads, uint64_t nodes, int box_heads, int box_nodes) {
+  auto fn = encode_fn();
+  if (!fn) return -1;
+  if ((reinterpret_cast<uintptr_t>(q) & 15) || head_dim % 64) return -2;
+  const cuuint64_t dims[4] = {64, (cuuint64_t)head_dim / 64, (cuuint64_t)heads, nodes};
+  const cuuint64_t strides[3] = {128, (cuuint64_t)head_dim * 2, (cuuint64_t)heads * head_dim * 2};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)box_heads, (cuuint32_t)box_nodes};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -3;
 }
 
 }  // namespace spec

@@ -199,10 +199,16 @@ int tc_make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t row
 // outside.
 int kv_make_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, int planes, int n_pages,
                 size_t page_elems);
-// The same dims with a box of 64 dims x box_keys keys of one half of one plane
-// (landing as [key][64], 128-byte swizzle), for the tree attention.
-int kv_make_half_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, int planes, int n_pages,
-                     size_t page_elems, int box_keys);
+// 5D bf16 map over the same pool for the tree attention: dims (64 dims, 8 keys,
+// head_dim / 64 halves, page_size / 8 key groups, planes of all pages), box 64 x
+// 8 x halves x box_keys / 8 x 1 -- box_keys consecutive keys of one plane, one
+// contiguous read, landing as [group][half][key][64] -- 128-byte swizzle, zero
+// fill outside.
+int kv_make_group_map(CUtensorMap* map, const void* kv, int head_dim, int page_size, uint64_t planes, int box_keys);
+// 4D bf16 map over queries [nodes][heads][head_dim]: dims (64 dims, halves,
+// heads, nodes), box 64 x 1 x box_heads x box_nodes (landing as [node][head][64]),
+// 128-byte swizzle, zero fill outside.
+int q_make_map(CUtensorMap* map, const void* q, int head_dim, int heads, uint64_t nodes, int box_heads, int box_nodes);
 // 3D byte tensor map over a stack of [rows][K] weight rows (esz bytes an
 // element) for the streamed expert GEMVs: box 128 bytes x box_rows rows x
 // box_chunks 128-byte chunks of K, landing as [chunk][row][128] with the

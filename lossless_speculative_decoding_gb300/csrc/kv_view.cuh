@@ -22,9 +22,10 @@ inline int check_kv_view(const spec_kv_view* kv, bool table) {
   if (kv->page_size < 16 || kv->page_size % 16) return set_last_error(SPEC_ERR_ARG, "page_size must be a multiple of 16");
   if (kv->n_pages < 1 || kv->n_layers < 1 || kv->n_kv_heads < 1 || (table && kv->max_pages < 1))
     return set_last_error(SPEC_ERR_ARG, "empty cache view");
-  // positions, and a page's (layer, head, K | V) planes, are counted in 32 bits
+  // positions, a page's rows and the cache's (page, layer, head, K | V) planes are counted in 32 bits
   if ((table && (int64_t)kv->max_pages * kv->page_size > (1 << 30)) ||
-      (int64_t)kv->n_layers * kv->n_kv_heads * 2 * kv->page_size > (1 << 30))
+      (int64_t)kv->n_layers * kv->n_kv_heads * 2 * kv->page_size > (1 << 30) ||
+      (int64_t)kv->n_pages * kv->n_layers * kv->n_kv_heads * 2 > (1 << 30))
     return set_last_error(SPEC_ERR_UNSUPPORTED, "cache view too large");
   if (!aligned16(kv->kv_dev)) return set_last_error(SPEC_ERR_ARG, "the cache must be 16-byte aligned");
   return SPEC_OK;

@@ -41,6 +41,7 @@ struct TreeArgs {
   int4* joint;         // [blocks]: (sequence, row tile, kv head, parts) of the shared segment that starts in a block
   int layer, n_seq, max_nodes, hq, G;
   int rows;            // rows of a tile
+  int q_box;           // rows of a box of the query's tensor map (tensor-core form)
   int tile_k;          // keys of a unit
   float scale_l2e;     // scale * log2 e
 };
@@ -349,9 +350,9 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// Tensor-core form (bf16 cache). One block per SM, twelve warps: a TMA producer,
-// an MMA issuer, two loaders (the next segment's queries, masks and sizes) and
-// two softmax groups of four warps. Keys come in tiles of 128. S = Q K^T (M = 128
+// Tensor-core form (bf16 cache). One block per SM, eleven warps: a TMA producer,
+// an MMA issuer, a loader (the next segment's sizes, queries and masks) and two
+// softmax groups of four warps. Keys come in tiles of 128. S = Q K^T (M = 128
 // rows, N = 128 keys) goes to tensor memory; a softmax thread owns one TMEM lane,
 // reads its scores, and writes the weights over them as bf16, and what that
 // rounding leaves as bf16 too (hi = bf16(p), lo = bf16(p - hi): 16 bits, so that
@@ -377,8 +378,8 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
 // that. (Tiles of 64 keys with two S buffers a slot were slower: an MMA of N = 64
 // takes 67 cycles, not half.)
 constexpr int TT_KEYS = 128;
-constexpr int TT_THREADS = 384;
-constexpr int TT_HALF = 128 * 128;               // bytes of 64 dims of a tile, and of 128 rows of Q
+constexpr int TT_THREADS = 352;
+constexpr int TT_HALF = 128 * 128;               // bytes of 64 dims of 128 rows of Q
 constexpr int TT_MAXBUF = 16;
 constexpr int TT_OCOL = 256;                     // TMEM columns: S of a slot at 128 slot, its O behind at TT_OCOL + D slot
 constexpr int TT_STAGE = 2 * 128 * 64;           // staged output: two groups x 128 lanes x 16 columns
@@ -395,7 +396,8 @@ struct TtCfg {
 };
 
 struct TtHeader {
-  uint64_t kv_full[TT_MAXBUF], kv_empty[TT_MAXBUF], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2], q_free, fin;
+  uint64_t kv_full[TT_MAXBUF], kv_empty[TT_MAXBUF], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2], mask_full[2];
+  uint64_t q_full, q_free, fin;
   uint32_t tmem;
   int abort;
   TreeSeg seg[2];                                // nt = 0: no more
@@ -521,11 +523,11 @@ __device__ __forceinline__ bool named_sync_and(int id, int threads, bool v) {
                : "=r"(r) : "r"((uint32_t)v), "r"(id), "r"(threads) : "memory");
   return r != 0;
 }
-// Shared-memory matrix descriptor, 128-byte swizzle, 8-row groups 1024 bytes
-// apart. lbo: bytes between 64-element groups of the leading dimension (an
+// Shared-memory matrix descriptor, 128-byte swizzle. sbo: bytes between 8-row
+// groups; lbo: bytes between 64-element groups of the leading dimension (an
 // MN-major operand; unused for a K-major one).
-__device__ __forceinline__ uint64_t tt_desc(uint32_t saddr, uint32_t lbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+__device__ __forceinline__ uint64_t tt_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -566,25 +568,33 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Rows of a segment and how they lie on the 128 lanes of the two slots.
+// Rows of a segment and how they lie on the 128 lanes of the two slots. Queries
+// come in boxes of whole nodes, so a few rows behind the segment's may be there
+// too; nothing is made of them.
 struct TtRows {
-  int row0, rows, rpp, kparts; // first row, rows, lanes of a repetition, parts of a tile's keys
+  int row0, rows, boxes;       // first row, rows, boxes of queries
+  int rpp, kparts;             // lanes of a repetition, parts of a tile's keys
   bool two, hl;                // slots split the rows, not the tiles; hi parts on the lower lanes, lo parts on the upper
   __device__ TtRows(const TreeArgs& A, const TreeSeg& g) {
     row0 = g.rt * A.rows;
     rows = min(A.rows, g.k * A.G - row0);
-    two = rows > 128;
-    hl = rows <= 64;
-    rpp = rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    kparts = rows <= 32 ? 2 : 1;
+    boxes = (rows + A.q_box - 1) / A.q_box;
+    const int lie = boxes * A.q_box;
+    two = lie > 128;
+    hl = lie <= 64;
+    rpp = lie <= 32 ? 32 : lie <= 64 ? 64 : 128;
+    kparts = lie <= 32 ? 2 : 1;
   }
 };
 
 template <int D>
 __global__ void __launch_bounds__(TT_THREADS, 1)
-    k_tree_tc(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ TreeArgs A, int kb, int NBUF, int q_bytes) {
+    k_tree_tc(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
+              const __grid_constant__ TreeArgs A, int kb, int NBUF, int q_bytes) {
   using C = TtCfg<D>;
   constexpr int HALVES = D / 64;
+  // a K or V tile lies as [8 keys][64-dim half][key][64 dims], as a box of whole pages brings it
+  constexpr int GROUP = 1024 * HALVES;
   extern __shared__ unsigned char tt_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tt_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* qsm = base + NBUF * C::BUF;
@@ -602,9 +612,11 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       mbar_init(H.s_full + i, 1);
       mbar_init(H.p_full + i, 4);
       mbar_init(H.o_done + i, 1);
-      mbar_init(H.seg_full + i, 2);              // the loaders' warps
+      mbar_init(H.seg_full + i, 1);
+      mbar_init(H.mask_full + i, 1);
       mbar_init(H.seg_free + i, 8);              // the softmax warps
     }
+    mbar_init(&H.q_full, 1);
     mbar_init(&H.q_free, 1);                     // a segment's last S
     mbar_init(&H.fin, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -627,26 +639,26 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other
   // waits at once: the producer and the issuer stop, the softmax groups finish
-  // the segment without a result and stop, the loaders run to their end.
+  // the segment without a result and stop, the loader runs to its end.
   auto wait = [&](const uint64_t* bar, uint32_t parity) {
     return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err);
   };
   const int P = A.kv.page_size;
 
   if (warp == 8) {
-    // ---- producer: K and V of every tile, boxes of kb keys x 64 dims ----
-    const int nbox = TT_KEYS / kb, j = lane % nbox, half = lane / nbox;
+    // ---- producer: K and V of every tile, a box for each kb keys of a page ----
+    const int nbox = TT_KEYS / kb, j = lane;
     int b = 0;
     uint32_t turn = 0;                           // passes over the ring
     bool ok = true;
     TreeSeg g;
     while (ok && walk.next(g)) {
       const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
-      const int plane = (A.layer * A.kv.n_kv_heads + g.hk) * 2;
+      const int planes = A.kv.n_layers * A.kv.n_kv_heads * 2, plane = (A.layer * A.kv.n_kv_heads + g.hk) * 2;
       auto page_of = [&](int tile) {             // of this lane's box; -1 reads zeros
         const int key = tile * TT_KEYS + kb * j;
         int page = -1;
-        if (lane < nbox * HALVES && tile < g.t1 && key < g.n + g.k) {
+        if (lane < nbox && tile < g.t1 && key < g.n + g.k) {
           page = bt[key / P];
           if (page < 0 || page >= A.kv.n_pages) {
             page = -1;
@@ -655,24 +667,32 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         }
         return page;
       };
-      int next = page_of(g.t0);
-      for (int tile = g.t0; ok && tile < g.t1; ++tile) {
-        const int key = tile * TT_KEYS + kb * j, page = next;
-        next = page_of(tile + 1);
-        for (int kv = 0; kv < 2; ++kv) {
-          if (turn > 0 && !wait(H.kv_empty + b, turn - 1)) { ok = false; break; }
-          const uint32_t full = sm_addr(H.kv_full + b);
-          if (lane == 0)
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"((uint32_t)C::BUF) : "memory");
-          __syncwarp();
-          if (lane < nbox * HALVES)
-            asm volatile(
-                "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                ::"r"(bufs + b * C::BUF + half * TT_HALF + j * kb * 128), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0),
-                  "r"(key % P), "r"(half), "r"(plane + kv), "r"(page), "r"(full)
-                : "memory");
-          if (++b == NBUF) { b = 0; ++turn; }
+      // in the order of their use: K of tile t + 1 before V of tile t, unless both slots use every tile
+      const bool ahead = !TtRows(A, g).two;
+      int page = page_of(g.t0), last = -1, next = page_of(g.t0 + 1);   // of the newest tile, the one before, the one after
+      for (int i = 0, n = 2 * (g.t1 - g.t0); ok && i < n; ++i) {
+        // load i: K, then K V K V .. V V (ahead), or K V K V ..
+        const bool v = ahead ? (i == n - 1 || (i > 0 && i % 2 == 0)) : i % 2 == 1;
+        const int tile = g.t0 + (ahead ? (v ? (i == n - 1 ? n / 2 - 1 : i / 2 - 1) : (i + 1) / 2) : i / 2);
+        if (!v && i > 0) {                       // a new tile's K: its pages
+          last = page;
+          page = next;
+          next = page_of(tile + 1);
         }
+        // V of the tile before the newest one (ahead), else of the newest
+        const int pg = v && ahead && i < n - 1 ? last : page, key = tile * TT_KEYS + kb * j;
+        if (turn > 0 && !wait(H.kv_empty + b, turn - 1)) { ok = false; break; }
+        const uint32_t full = sm_addr(H.kv_full + b);
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"((uint32_t)C::BUF) : "memory");
+        __syncwarp();
+        if (lane < nbox)
+          asm volatile(
+              "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
+              ::"r"(bufs + b * C::BUF + j * kb * D * 2), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0), "r"(key % P / 8),
+                "r"(pg < 0 ? -1 : pg * planes + plane + (v ? 1 : 0)), "r"(full)
+              : "memory");
+        if (++b == NBUF) { b = 0; ++turn; }
       }
     }
     if (!ok)                                     // shared memory outlives the copies in flight
@@ -689,24 +709,33 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     auto waitw = [&](const uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     uint32_t n0 = 0, n1 = 0;                     // jobs of the slots
-    int kbuf = 0, kturn = 0;                     // ring position of the next tile's K
+    int rbuf = 0, rturn = 0;                     // ring position of the next load
+    auto step = [&]() {
+      if (++rbuf == NBUF) { rbuf = 0; ++rturn; }
+    };
     bool ok = true;
     // the job whose P V is due: slot, job of the slot, 16-key steps, V's buffer
-    // and turn, first of the slot's segment, last use of V, lo parts apart
+    // and turn (when its load is not simply the next one), first of the slot's
+    // segment, last use of V, lo parts apart
     struct Job { int slot; uint32_t k; int steps, vbuf, vturn; bool first, last, lo; } q{};
     bool due = false;
     auto pv = [&]() {
       due = false;
+      if (q.vbuf < 0) {
+        q.vbuf = rbuf;
+        q.vturn = rturn;
+        step();
+      }
       const bool go = waitw(H.kv_full + q.vbuf, q.vturn) && waitw(H.p_full + q.slot, q.k);
       if (!go) return false;
       tc_fence_after();
       const uint32_t d = tm + TT_OCOL + q.slot * D, a = tm + q.slot * 128;
-      const uint64_t bd = tt_desc(bufs + q.vbuf * C::BUF, TT_HALF);
+      const uint64_t bd = tt_desc(bufs + q.vbuf * C::BUF, 1024, GROUP);
 #pragma unroll
       for (int k = 0; k < TT_KEYS / 16; ++k) {
         if (k < q.steps) {
-          mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1), bd + (uint64_t)(k * (2048 >> 4)), id_o, k > 0 || !q.first, one);
-          if (q.lo) mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1) + 16, bd + (uint64_t)(k * (2048 >> 4)), id_o, true, one);
+          mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1), bd + (uint64_t)(k * 2 * GROUP >> 4), id_o, k > 0 || !q.first, one);
+          if (q.lo) mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1) + 16, bd + (uint64_t)(k * 2 * GROUP >> 4), id_o, true, one);
         }
       }
       tc_commit(sm_addr(H.o_done + q.slot), one);
@@ -721,82 +750,98 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (g.nt == 0) break;
       const TtRows R(A, g);
       const int nt = g.t1 - g.t0, nj = R.two ? 2 * nt : nt;
+      const uint32_t qhalf = R.two ? 2 * TT_HALF : TT_HALF;
+      int kbuf = 0, kturn = 0, vbuf = -1, vturn = 0;
+      if (!(ok = waitw(&H.q_full, seg))) break;
       for (int jb = 0; ok && jb < nj; ++jb) {
         const int slot = jb & 1, ti = R.two ? jb >> 1 : jb;
         const uint32_t k = slot ? n1++ : n0++;
+        if (!R.two || slot == 0) {
+          kbuf = rbuf;
+          kturn = rturn;
+          step();
+        }
+        if (R.two && slot == 0) {
+          vbuf = rbuf;
+          vturn = rturn;
+          step();
+        }
         // S goes over the slot's last weights: their P V is done
         ok = waitw(H.kv_full + kbuf, kturn) && (k == 0 || waitw(H.o_done + slot, k - 1));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ad = tt_desc(q_addr + (R.two ? slot * C::QSLOT : 0), 16), bd = tt_desc(bufs + kbuf * C::BUF, 16);
+        const uint64_t ad = tt_desc(q_addr + (R.two ? slot * TT_HALF : 0), 16, 1024), bd = tt_desc(bufs + kbuf * C::BUF, 16, GROUP);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint64_t in = (uint64_t)(((i & 3) * 32 + (i >> 2) * TT_HALF) >> 4);
-          mma_ss(tm + slot * 128, ad + in, bd + in, id_s, i > 0, one);
-        }
+        for (int i = 0; i < D / 16; ++i)
+          mma_ss(tm + slot * 128, ad + (uint64_t)(((i & 3) * 32 + (i >> 2) * qhalf) >> 4),
+                 bd + (uint64_t)(((i & 3) * 32 + (i >> 2) * 1024) >> 4), id_s, i > 0, one);
         const bool last = !R.two || slot == 1;
         tc_commit(sm_addr(H.s_full + slot), one);
         if (last) tc_commit(sm_addr(H.kv_empty + kbuf), one);
         if (jb == nj - 1) tc_commit(sm_addr(&H.q_free), one);
         if (due) ok = pv();
-        const bool wrap = kbuf + 1 == NBUF;      // V follows K in the ring
-        q = Job{slot, k, (min(TT_KEYS, g.n + g.k - (g.t0 + ti) * TT_KEYS) + 15) / 16, wrap ? 0 : kbuf + 1,
-                wrap ? kturn + 1 : kturn, ti == (R.two ? 0 : slot), last, !R.hl};
+        q = Job{slot, k, (min(TT_KEYS, g.n + g.k - (g.t0 + ti) * TT_KEYS) + 15) / 16, vbuf, vturn, ti == (R.two ? 0 : slot), last, !R.hl};
         due = true;
-        if (last) {
-          kbuf += 2;
-          if (kbuf >= NBUF) { kbuf -= NBUF; ++kturn; }
-        }
       }
       if (ok && due) ok = pv();
     }
     // everything issued is done before TMEM is freed (also after an abort)
     tc_commit(sm_addr(&H.fin), one);
     mbar_wait_deadline(sm_addr(&H.fin), 0, nullptr);
-  } else if (warp >= 10) {
-    // ---- loaders: the segments' sizes, queries (repeated down the lanes) and masks ----
-    const int i0 = t - 320;
+  } else if (warp == 10) {
+    // ---- loader: the segments' sizes, queries (repeated down the lanes) and masks ----
     TreeSeg g;
+    uint32_t asked = 0;                          // segments whose queries were asked for
     for (uint32_t seg = 0;; ++seg) {
       const int sb = seg & 1;
       const bool have = walk.next(g);
       if (seg >= 2) wait(H.seg_free + sb, (seg >> 1) - 1);
       if (!have) g.nt = 0;
-      if (i0 == 0) H.seg[sb] = g;
-      if (have) {
-        const TtRows R(A, g);
-        int par = -1;
-        if (i0 < g.k) par = A.parents[(size_t)g.s * A.max_nodes + i0];
-        // thread i0: 16-byte piece c of rows x, x + step, ..
-        constexpr int PPR = D / 8, STEP = 64 / PPR;
-        const int c = i0 % PPR, nrep = R.two ? 1 : 128 / R.rpp;
-        int node = (R.row0 + i0 / PPR) / A.G, head = (R.row0 + i0 / PPR) % A.G;
-        const bf16_t* qg = static_cast<const bf16_t*>(A.q) + ((size_t)g.s * A.max_nodes * A.hq + g.hk * A.G) * D + 8 * c;
-        const uint32_t qd = q_addr + (c >> 3) * TT_HALF;
-        if (seg > 0) wait(&H.q_free, seg - 1);
-#pragma unroll 1
-        for (int x = i0 / PPR; x < R.rows; x += STEP) {
-          const bf16_t* src = qg + ((size_t)node * A.hq + head) * D;
-          uint32_t y = (uint32_t)(x & 127), dst = qd + (x >> 7) * C::QSLOT + y * 128 + (((c & 7) ^ (y & 7)) << 4);
-          for (int p = 0; p < nrep; ++p, dst += R.rpp * 128)   // (a repetition starts at a multiple of 8 rows)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-          for (head += STEP; head >= A.G; head -= A.G) ++node;
-        }
-        if (g.t1 * TT_KEYS > g.n) {              // the segment reaches the tree's slots
-          if (i0 < g.k) {
-            H.parent[i0] = par;
-            if (g.t1 == g.nt && (par < -1 || par >= i0)) atomicOr(A.err, SPEC_DEV_ERR_TREE);
-          }
-          named_sync(4, 64);
-          if (i0 < g.k) H.mask[sb][i0] = ancestors(H.parent, i0);
-          named_sync(4, 64);
-        }
-        asm volatile("cp.async.wait_all;\nfence.proxy.async.shared::cta;" ::: "memory");
+      if (lane == 0) {
+        H.seg[sb] = g;
+        mbar_arrive(sm_addr(H.seg_full + sb));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sm_addr(H.seg_full + sb));
       if (!have) break;
+      const TtRows R(A, g);
+      const bool tree = g.t1 * TT_KEYS > g.n;    // the segment reaches the tree's slots
+      const int32_t* par = A.parents + (size_t)g.s * A.max_nodes;
+      int p[2] = {-1, -1};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (tree && lane + 32 * u < g.k) p[u] = par[lane + 32 * u];
+      if (seg > 0 && !__all_sync(0xffffffffu, wait(&H.q_free, seg - 1))) continue;   // (aborted: no more copies)
+      const int nrep = R.two ? 1 : 128 / R.rpp, copies = R.boxes * nrep * HALVES;
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                     ::"r"(sm_addr(&H.q_full)), "r"((uint32_t)(copies * A.q_box * 128)) : "memory");
+      __syncwarp();
+      ++asked;
+      for (int i = lane; i < copies; i += 32) {
+        const int half = i % HALVES, x = i / HALVES % R.boxes, rp = i / HALVES / R.boxes;
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+            ::"r"(q_addr + half * (R.two ? 2 * TT_HALF : TT_HALF) + (x * A.q_box + rp * R.rpp) * 128),
+              "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(0), "r"(half), "r"(g.hk * A.G),
+              "r"(g.s * A.max_nodes + (R.row0 + x * A.q_box) / A.G), "r"(sm_addr(&H.q_full))
+            : "memory");
+      }
+      if (tree) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int i = lane + 32 * u;
+          if (i < g.k) {
+            H.parent[i] = p[u];
+            if (g.t1 == g.nt && (p[u] < -1 || p[u] >= i)) atomicOr(A.err, SPEC_DEV_ERR_TREE);
+          }
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int i = lane; i < g.k; i += 32) H.mask[sb][i] = ancestors(H.parent, i);
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(sm_addr(H.mask_full + sb));
     }
+    if (asked > 0) mbar_wait_deadline(sm_addr(&H.q_full), (asked - 1) & 1, nullptr);   // (over, unless aborted)
   } else {
     // ---- softmax groups ----
     const int slot = warp >> 2, r = t & 127;
@@ -818,7 +863,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       const bool live = lr < R.rows, low = R.hl && r >= 64;
       const bool any_live = __any_sync(0xffffffffu, live);
       unsigned long long mask = 0;
-      if (live && g.t1 * TT_KEYS > g.n) mask = H.mask[sb][(R.row0 + lr) / A.G];
+      if (g.t1 * TT_KEYS > g.n) {
+        wait(H.mask_full + sb, seg >> 1);
+        if (live) mask = H.mask[sb][(R.row0 + lr) / A.G];
+      }
       float m = -INFINITY, l = 0.f;
       for (int ti = R.two ? 0 : slot; ti < nt; ti += R.two ? 1 : 2) {
         const int k0 = (g.t0 + ti) * TT_KEYS;
@@ -910,12 +958,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         // slots past the last node may hold anything: their V rows become zeros
         const int nk = g.n + g.k - k0;
         if (nk < TT_KEYS) {
-          const uint32_t vi = 2 * (tiles + ti) + 1;
+          const uint32_t vi = 2 * (tiles + nt) - 1;            // (the segment's last tile: its last load)
           wait(H.kv_full + vi % NBUF, vi / NBUF);
           unsigned char* vb = base + (vi % NBUF) * C::BUF;
           for (int i = r; i < (TT_KEYS - nk) * HALVES * 8; i += 128) {
-            const int hf = i / ((TT_KEYS - nk) * 8), e = i % ((TT_KEYS - nk) * 8);
-            *reinterpret_cast<uint4*>(vb + hf * TT_HALF + (nk + e / 8) * 128 + (e % 8) * 16) = make_uint4(0, 0, 0, 0);
+            const int key = nk + i / (HALVES * 8), hf = i / 8 % HALVES;
+            *reinterpret_cast<uint4*>(vb + key / 8 * GROUP + hf * 1024 + key % 8 * 128 + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
@@ -1109,6 +1157,7 @@ int sm_count() {
 struct TreePlan {
   bool tc;                  // bf16 cache: the tensor-core form
   int rows, tile_k;
+  int q_box;                // rows of a box of queries, whole nodes
   int max_blocks;           // of any grid (the workspace is sized without a device)
   size_t ml, joint, total;  // workspace: outputs at 0, statistics, joints
   TreePlan(const spec_kv_view& kv, int max_nodes, int hq) {
@@ -1117,11 +1166,20 @@ struct TreePlan {
     if (tc) {
       // tiles of at most 256 rows, whole nodes, as even as they come
       const int most = std::max(1, 256 / G), nrt = (max_nodes + most - 1) / most;
-      rows = (max_nodes + nrt - 1) / nrt * G;
+      int nodes = (max_nodes + nrt - 1) / nrt, box = 8;
+      while (box > 1 && box / 2 * G % 8 == 0) box /= 2;
+      // boxes start at multiples of 8 rows (the swizzle's period), up to 32 rows
+      // each where that many nodes do; one box when the tile has no more nodes,
+      // or when whole boxes would go past 256 rows
+      box *= std::max(1, 32 / (box * G));
+      if (box >= nodes || (nodes + box - 1) / box * box * G > 256) box = nodes;
+      q_box = box * G;
+      rows = nodes * G;
       tile_k = TT_KEYS;
       max_blocks = 160;     // one block per SM
     } else {
       rows = FM_ROWS;
+      q_box = 0;
       tile_k = FM_KEYS;
       max_blocks = 320;     // two blocks per SM
     }
@@ -1157,11 +1215,11 @@ cudaError_t launch_fma(const TreeArgs& A, int blocks, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t launch_tc(const TreeArgs& A, const CUtensorMap& map, int kb, int blocks, cudaStream_t st) {
+cudaError_t launch_tc(const TreeArgs& A, const CUtensorMap& map, const CUtensorMap& qmap, int kb, int blocks, cudaStream_t st) {
   cudaError_t e = allow_dyn_smem(k_tree_tc<D>);
-  const bool two = A.rows > 128;
+  const bool two = (A.rows + A.q_box - 1) / A.q_box * A.q_box > 128;
   if (e == cudaSuccess)
-    e = launch_k(k_tree_tc<D>, dim3(blocks), dim3(TT_THREADS), TtCfg<D>::smem(two), st, map, A, kb, TtCfg<D>::nbuf(two),
+    e = launch_k(k_tree_tc<D>, dim3(blocks), dim3(TT_THREADS), TtCfg<D>::smem(two), st, map, qmap, A, kb, TtCfg<D>::nbuf(two),
                  TtCfg<D>::q_bytes(two));
   return e == cudaSuccess ? join<D, bf16_t>(A, blocks, st) : e;
 }
@@ -1197,7 +1255,7 @@ extern "C" int spec_tree_attention(const spec_kv_view* kv, int layer, const void
   char* w = static_cast<char*>(ws_dev);
   const TreeArgs A{*kv, q_dev, out_dev, cache_len_dev, n_nodes_dev, parents_dev, err_dev, reinterpret_cast<float*>(w),
                    reinterpret_cast<float2*>(w + plan.ml), reinterpret_cast<int4*>(w + plan.joint), layer, n_seq,
-                   max_nodes, n_q_heads, n_q_heads / kv->n_kv_heads, plan.rows, plan.tile_k, scale * LOG2E};
+                   max_nodes, n_q_heads, n_q_heads / kv->n_kv_heads, plan.rows, plan.q_box, plan.tile_k, scale * LOG2E};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   const int blocks = std::min((plan.tc ? 1 : 2) * sms, plan.max_blocks);
   cudaError_t e;
@@ -1205,11 +1263,11 @@ extern "C" int spec_tree_attention(const spec_kv_view* kv, int layer, const void
     // a box never straddles pages: the largest power of two up to a tile that divides a page
     int kb = 16;
     while (kb < TT_KEYS && kv->page_size % (2 * kb) == 0) kb *= 2;
-    CUtensorMap map;
-    if (kv_make_half_map(&map, kv->kv_dev, d, kv->page_size, kv->n_layers * kv->n_kv_heads * 2, kv->n_pages,
-                         (size_t)kv->n_layers * kv->n_kv_heads * 2 * kv->page_size * d, kb))
+    CUtensorMap map, qmap;
+    if (q_make_map(&qmap, q_dev, d, n_q_heads, (uint64_t)n_seq * max_nodes, A.G, plan.q_box / A.G) ||
+        kv_make_group_map(&map, kv->kv_dev, d, kv->page_size, (uint64_t)kv->n_pages * kv->n_layers * kv->n_kv_heads * 2, kb))
       return set_last_error(SPEC_ERR_UNSUPPORTED, "tensor map encoding failed");
-    e = d == 128 ? launch_tc<128>(A, map, kb, blocks, st) : launch_tc<64>(A, map, kb, blocks, st);
+    e = d == 128 ? launch_tc<128>(A, map, qmap, kb, blocks, st) : launch_tc<64>(A, map, qmap, kb, blocks, st);
   } else {
     e = d == 128 ? launch_fma<128>(A, blocks, st) : launch_fma<64>(A, blocks, st);
   }
