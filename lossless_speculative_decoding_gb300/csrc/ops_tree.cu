@@ -38,7 +38,7 @@ struct TreeArgs {
   int32_t* err;
   float* part_o;       // [blocks][2][rows][d]: part 0 of a block began in an earlier block, part 1 goes on in the next
   float2* part_ml;     // [blocks][2][rows]: maximum (log2 units), sum
-  int4* joint;         // [blocks]: (sequence, row tile, kv head, parts) of the shared segment that starts in a block
+  int4* joint;         // [blocks]: (sequence, row tile, kv head, parts and rows) of the shared segment that starts in a block
   int layer, n_seq, max_nodes, hq, G;
   int rows;            // rows of a tile
   int q_box;           // rows of a box of the query's tensor map (tensor-core form)
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
       }
     }
     if (part == 1 && t == 0)
-      A.joint[blockIdx.x] = make_int4(g.s, g.rt, g.hk, parts_until(walk.U, blockIdx.x, walk.blocks, walk.u1 + g.nt - g.t1));
+      A.joint[blockIdx.x] = make_int4(g.s, g.rt, g.hk, parts_until(walk.U, blockIdx.x, walk.blocks, walk.u1 + g.nt - g.t1) << 16 | nrows);
   }
 }
 
@@ -987,31 +987,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         if (wpart < 0) *reinterpret_cast<uint2*>(o + col * 2) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
         else *reinterpret_cast<float4*>(o + col * 4) = v;
       };
-      auto emit_ml = [&](int x, float mm, float ll) {
-        if (wpart >= 0) A.part_ml[((size_t)blockIdx.x * 2 + wpart) * A.rows + x] = make_float2(mm, ll);
-      };
       // each group waits for its own slot's last P V; the barriers pass that on
       if (R.two || slot < nt) wait(H.o_done + slot, jobs - 1);
-      tc_fence_after();
+      float w0 = 1.f, w1 = 0.f;                  // of this lane's O in slot 0 (its own slot, two), in slot 1
+      const bool both = !R.two && nt > 1;        // slot 1 had tiles
       if (R.two) {
-        if (any_live) {
-          const float w = wpart < 0 ? 1.f / l : 1.f;
-          unsigned char* og = out_row(live ? lr : 0);
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[32];
-            tmem_ld32(oT + 32 * c, v);
-            if (live) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                emit4(og, 32 * c + i, make_float4(__uint_as_float(v[i]) * w, __uint_as_float(v[i + 1]) * w,
-                                                  __uint_as_float(v[i + 2]) * w, __uint_as_float(v[i + 3]) * w));
-            }
-          }
-          if (live) emit_ml(lr, m, l);
-        }
+        tc_fence_after();
+        if (wpart < 0) w0 = 1.f / l;
+        else if (live) A.part_ml[((size_t)blockIdx.x * 2 + wpart) * A.rows + lr] = make_float2(m, l);
       } else {
-        const bool both = nt > 1;                // slot 1 had tiles
         H.ml[slot][r] = make_float2(live ? m : -INFINITY, live ? l : 0.f);
         tc_fence_before();
         named_sync(1, 256);
@@ -1024,61 +1008,62 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
           M = mn;
         }
         const float Mb = M == -INFINITY ? 0.f : M, inv = wpart < 0 ? 1.f / L : 1.f;
-        const float w0 = ex2(H.ml[0][r].x - Mb) * inv, w1 = ex2(H.ml[1][r].x - Mb) * inv;
-        if (slot == 0 && live && rep == 0) emit_ml(lr, M, L);
-        // group `slot` has columns slot D / 2 .. of both slots' outputs
-        const uint32_t o0 = tmem + lanes + TT_OCOL + slot * (D / 2), o1 = o0 + D;
-        float4* stage = reinterpret_cast<float4*>(stg + slot * (TT_STAGE / 2));   // [128 lanes][16 columns]
-        const int nrep = 128 / R.rpp;
-        unsigned char* og[2];
+        w0 = ex2(H.ml[0][r].x - Mb) * inv;
+        w1 = ex2(H.ml[1][r].x - Mb) * inv;
+        if (wpart >= 0 && slot == 0 && live && rep == 0)
+          A.part_ml[((size_t)blockIdx.x * 2 + wpart) * A.rows + lr] = make_float2(M, L);
+      }
+      // 16 columns at a time through shared memory: a row's repetitions are
+      // summed, and four lanes write 64 bytes of a row together. Two: each group
+      // its own slot's columns; else the groups take half of both slots' each.
+      const int nrep = R.two ? 1 : 128 / R.rpp, col0 = R.two ? 0 : slot * (D / 2);
+      const uint32_t o0 = tmem + lanes + TT_OCOL + (R.two ? slot * D : col0), o1 = o0 + D;
+      float4* stage = reinterpret_cast<float4*>(stg + slot * (TT_STAGE / 2));   // [128 lanes][16 columns]
+      unsigned char* og[4];                      // the rows whose columns 4 (r % 4) .. this thread writes
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {            // the rows this thread writes: its own, or those it sums
-          const int y = nrep == 1 ? lr : (r + 128 * q) / 4;
-          og[q] = out_row(y < R.rows ? y : 0);
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int y = (R.two ? slot * 128 : 0) + r / 4 + 32 * u;
+        og[u] = u * nrep < 4 && y < R.rows ? out_row(y) : nullptr;
+      }
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t v[16], u[16];
-          if (both) tmem_ld16x2(o0 + 16 * c, o1 + 16 * c, v, u);
-          else tmem_ld16(o0 + 16 * c, v);
-          float4 x[4];
+      for (int c = 0; c < (R.two ? D / 16 : D / 32); ++c) {
+        uint32_t v[16], x[16];
+        if (both) tmem_ld16x2(o0 + 16 * c, o1 + 16 * c, v, x);
+        else tmem_ld16(o0 + 16 * c, v);
+        float y[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float y = __uint_as_float(v[i]) * w0;
-            if (both) y = fmaf(__uint_as_float(u[i]), w1, y);
-            reinterpret_cast<float*>(x)[i] = y;
-          }
-          const int col = slot * (D / 2) + 16 * c;
-          if (nrep == 1) {
-            if (live)
+        for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(v[i]) * w0;
+        if (both) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) emit4(og[0], col + 4 * i, x[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) stage[r * 4 + (i ^ ((r >> 1) & 3))] = x[i];
-            named_sync(2 + slot, 128);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const int y = (r + 128 * q) / 4, pc = r & 3;
-              if (y < R.rows) {
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int p = 0; p < nrep; ++p) {
-                  const int ln = p * R.rpp + y;
-                  const float4 z = stage[ln * 4 + (pc ^ ((ln >> 1) & 3))];
-                  a.x += z.x; a.y += z.y; a.z += z.z; a.w += z.w;
-                }
-                emit4(og[q], col + 4 * pc, a);
-              }
-            }
-            named_sync(2 + slot, 128);
-          }
+          for (int i = 0; i < 16; ++i) y[i] = fmaf(__uint_as_float(x[i]), w1, y[i]);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          stage[r * 4 + (i ^ ((r >> 1) & 3))] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        named_sync(2 + slot, 128);
+        float4 z[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int ln = r / 4 + 32 * u;
+          z[u] = stage[ln * 4 + ((r & 3) ^ ((ln >> 1) & 3))];
+        }
+        auto add = [](float4& a, const float4& b) { a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w; };
+        if (nrep == 4) add(z[0], z[1]);
+        if (nrep == 4) add(z[0], z[2]);
+        if (nrep == 4) add(z[0], z[3]);
+        if (nrep == 2) add(z[0], z[2]);
+        if (nrep == 2) add(z[1], z[3]);
+        const int col = col0 + 16 * c + 4 * (r & 3);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (og[u]) emit4(og[u], col, z[u]);
+        named_sync(2 + slot, 128);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sm_addr(H.seg_free + sb));
       if (wpart == 1 && t == 0)
-        A.joint[blockIdx.x] = make_int4(g.s, g.rt, g.hk, parts_until(walk.U, blockIdx.x, walk.blocks, walk.u1 + g.nt - g.t1));
+        A.joint[blockIdx.x] = make_int4(g.s, g.rt, g.hk, parts_until(walk.U, blockIdx.x, walk.blocks, walk.u1 + g.nt - g.t1) << 16 | R.rows);
     }
   }
   __syncwarp();
@@ -1091,37 +1076,27 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 // ---------------------------------------------------------------------------
 // Joins the parts of the segment that starts in block blockIdx.x and ends in a
 // later one: M = max m_c, out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M),
-// parts in key order. One warp per row.
+// parts in key order. One warp per row; a row's statistics and its first eight
+// parts are on their way together, so that the launch is two round trips to L2
+// (the description, the parts) long.
 constexpr int JOIN_WARPS = 8;
 
 template <int D, class KT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) k_tree_join(const __grid_constant__ TreeArgs A) {
   pdl_wait();
   pdl_trigger();
-  const int4 jt = A.joint[blockIdx.x];
+  const int4 jt = __ldcg(A.joint + blockIdx.x);
   const int r = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int parts = jt.w;
-  if (parts == 0) return;
-  const int s = jt.x, rr = jt.y * A.rows + r;
-  if (r >= A.rows || rr >= tree_size(A, s).k * A.G) return;
+  const int parts = jt.w >> 16, rr = jt.y * A.rows + r;
+  if (r >= (jt.w & 0xFFFF)) return;
   // part 0 of the join is this block's part 1, then part 0 of the blocks after it
   auto at = [&](int c) { return ((size_t)(blockIdx.x + c) * 2 + (c == 0 ? 1 : 0)) * A.rows + r; };
-  float M = -INFINITY;
-  for (int c = lane; c < parts; c += 32) M = fmaxf(M, __ldcg(&A.part_ml[at(c)]).x);
-  M = warp_max(M);
-  constexpr int NV = D / 32, FLY = 8;            // parts whose values are in flight at once
-  float o[NV], l = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) o[i] = 0.f;
-  for (int c0 = 0; c0 < parts; c0 += FLY) {
-    float2 ml[FLY];
-    float v[FLY][NV];
+  constexpr int NV = D / 32, FLY = 8;            // values a lane; parts in flight at once
+  float v[FLY][NV];
+  auto fetch = [&](int c0) {
 #pragma unroll
     for (int c = 0; c < FLY; ++c) {
-      const bool in = c0 + c < parts;
-      const size_t e = at(in ? c0 + c : c0);
-      ml[c] = in ? __ldcg(A.part_ml + e) : make_float2(-INFINITY, 0.f);
-      const float* p = A.part_o + e * D + NV * lane;
+      const float* p = A.part_o + at(c0 + c < parts ? c0 + c : c0) * D + NV * lane;
       if constexpr (NV == 4) {
         const float4 f = __ldcg(reinterpret_cast<const float4*>(p));
         v[c][0] = f.x; v[c][1] = f.y; v[c][2] = f.z; v[c][3] = f.w;
@@ -1130,19 +1105,37 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_tree_join(const __grid_cons
         v[c][0] = f.x; v[c][1] = f.y;
       }
     }
+  };
+  fetch(0);
+  float M = -INFINITY, l = 0.f, o[NV];
+  for (int c = lane; c < parts; c += 32) M = fmaxf(M, __ldcg(A.part_ml + at(c)).x);
+  M = warp_max(M);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) o[i] = 0.f;
+  for (int c0 = 0;;) {
+    // lane c has the weight of part c0 + c
+    const float2 ml = c0 + (lane & 7) < parts ? __ldcg(A.part_ml + at(c0 + (lane & 7))) : make_float2(-INFINITY, 0.f);
+    const float wl = exp2f(ml.x - M);
 #pragma unroll
     for (int c = 0; c < FLY; ++c) {
-      const float w = exp2f(ml[c].x - M);
-      l = fmaf(ml[c].y, w, l);
+      const float w = __shfl_sync(0xffffffffu, wl, c);
+      l = fmaf(__shfl_sync(0xffffffffu, ml.y, c), w, l);
 #pragma unroll
       for (int i = 0; i < NV; ++i) o[i] = fmaf(v[c][i], w, o[i]);
     }
+    if ((c0 += FLY) >= parts) break;
+    fetch(c0);
   }
-  KT* og = static_cast<KT*>(A.out) + (((size_t)s * A.max_nodes + rr / A.G) * A.hq + jt.z * A.G + rr % A.G) * D + NV * lane;
+  KT* og = static_cast<KT*>(A.out) + (((size_t)jt.x * A.max_nodes + rr / A.G) * A.hq + jt.z * A.G + rr % A.G) * D + NV * lane;
+  const float inv = 1.f / l;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if constexpr (sizeof(KT) == 4) og[i] = o[i] / l;
-    else reinterpret_cast<uint16_t*>(og)[i] = f_to_bf16(o[i] / l);
+  for (int i = 0; i < NV; ++i) o[i] *= inv;
+  if constexpr (sizeof(KT) == 4) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) og[i] = o[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; i += 2) reinterpret_cast<uint32_t*>(og)[i / 2] = pack_bf16(o[i], o[i + 1]);
   }
 }
 
