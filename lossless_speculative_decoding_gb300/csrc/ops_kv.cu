@@ -16,6 +16,7 @@ constexpr int COMMIT_ROWS = 8;          // rows a thread holds in flight
 
 struct CommitShared {
   int parent[TREE_N], token[TREE_N], target[TREE_N], path[TREE_N];
+  int page[TREE_N];                     // of slots n, n + 1, ..
   long long src[TREE_N], dst[TREE_N];   // row offsets (16-byte pieces) of the moves
   int accepted, moves, ok;
 };
@@ -23,8 +24,7 @@ struct CommitShared {
 // Walk of sequence s by warp 0. Lane l looks at nodes l and l + 32; the lowest
 // child that agrees is the lowest set bit of the two ballots. A child's index
 // is above its parent's, so the walk ends.
-__device__ void walk_tree(const spec_kv_view& kv, int s, int n, int k, int max_nodes, CommitShared& sh, int32_t* err,
-                          bool report) {
+__device__ void walk_tree(const spec_kv_view& kv, int n, int k, CommitShared& sh, int32_t* err, bool report) {
   const int lane = threadIdx.x;
   __syncwarp();
   int cur = 0, a = 0;
@@ -47,7 +47,6 @@ __device__ void walk_tree(const spec_kv_view& kv, int s, int n, int k, int max_n
   // the moves: rows whose slot changes, in path order
   const int esz = kv.dtype == SPEC_F32 ? 4 : 2;
   const long long row16 = kv.head_dim * esz / 16, page16 = (long long)kv.n_layers * kv.n_kv_heads * 2 * kv.page_size * row16;
-  const int32_t* bt = kv.block_table_dev + (size_t)s * kv.max_pages;
   int moves = 0;
   bool fine = true;
   for (int j0 = 0; j0 <= a; j0 += 32) {
@@ -56,7 +55,7 @@ __device__ void walk_tree(const spec_kv_view& kv, int s, int n, int k, int max_n
     const uint32_t who = __ballot_sync(0xffffffffu, mv);
     if (mv) {
       const int ps = n + sh.path[j], pd = n + j;
-      const int gs = bt[ps / kv.page_size], gd = bt[pd / kv.page_size];
+      const int gs = sh.page[sh.path[j]], gd = sh.page[j];
       fine = fine && gs >= 0 && gs < kv.n_pages && gd >= 0 && gd < kv.n_pages;
       const int at = moves + __popc(who & ((1u << lane) - 1));
       sh.src[at] = gs * page16 + (ps % kv.page_size) * row16;
@@ -86,6 +85,12 @@ __global__ void __launch_bounds__(COMMIT_THREADS) k_tree_commit(spec_kv_view kv,
                                                                 int32_t* out_len, int32_t* err) {
   __shared__ CommitShared sh;
   const int s = blockIdx.y, t = threadIdx.x;
+  if (t < max_nodes) {                           // (on their way beside the sizes)
+    const size_t e = (size_t)s * max_nodes + t;
+    sh.parent[t] = parents[e];
+    sh.token[t] = tokens[e];
+    sh.target[t] = target[e];
+  }
   const TreeSize z(cache_len, n_nodes, s, max_nodes, kv.max_pages * kv.page_size);
   const bool first = blockIdx.x == 0;
   if (z.k == 0) {
@@ -99,15 +104,10 @@ __global__ void __launch_bounds__(COMMIT_THREADS) k_tree_commit(spec_kv_view kv,
     }
     return;
   }
-  if (t < z.k) {
-    const size_t e = (size_t)s * max_nodes + t;
-    sh.parent[t] = parents[e];
-    sh.token[t] = tokens[e];
-    sh.target[t] = target[e];
-    if (first && (sh.parent[t] < -1 || sh.parent[t] >= t)) atomicOr(err, SPEC_DEV_ERR_TREE);
-  }
+  if (t < z.k && first && (sh.parent[t] < -1 || sh.parent[t] >= t)) atomicOr(err, SPEC_DEV_ERR_TREE);
+  if (t >= 64 && t < 64 + z.k) sh.page[t - 64] = kv.block_table_dev[(size_t)s * kv.max_pages + (z.n + t - 64) / kv.page_size];
   __syncthreads();
-  if (t < 32) walk_tree(kv, s, z.n, z.k, max_nodes, sh, err, first);
+  if (t < 32) walk_tree(kv, z.n, z.k, sh, err, first);
   __syncthreads();
   const int a = sh.accepted;
   if (first) {

@@ -78,9 +78,9 @@ struct TreeWalk {
     A = &args;
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int per = (args.n_seq + THREADS - 1) / THREADS;
-    const int a = min(t * per, args.n_seq), b = min(a + per, args.n_seq);
+    const int a = min(t * per, args.n_seq), a1 = min(a + per, args.n_seq);
     long long sum = 0;
-    for (int i = a; i < b; ++i) sum += units_of(args, i);
+    for (int i = a; i < a1; ++i) sum += units_of(args, i);
     long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -96,8 +96,11 @@ struct TreeWalk {
     }
     U = total;
     blocks = (int)min((long long)gridDim.x, max(U, 1ll));
-    u = U * min((int)blockIdx.x, blocks) / blocks;
-    u1 = U * min((int)blockIdx.x + 1, blocks) / blocks;
+    // floor(U b / blocks) = (U / blocks) b + floor((U % blocks) b / blocks)
+    const long long each = U / blocks;
+    const int rest = (int)(U - each * blocks), b = min((int)blockIdx.x, blocks), b1 = min((int)blockIdx.x + 1, blocks);
+    u = each * b + rest * b / blocks;
+    u1 = each * b1 + rest * b1 / blocks;
     long long at = before + inc - sum;
     if (u < u1 && at <= u && u < at + sum) {     // one thread's chunk holds unit u
       int i = a;
@@ -155,11 +158,9 @@ __device__ __forceinline__ unsigned long long ancestors(const int32_t* parents, 
 __device__ __forceinline__ int part_of(const TreeSeg& g) { return g.t0 > 0 ? 0 : (g.t1 < g.nt ? 1 : -1); }
 
 // Number of blocks that hold units of the segment that ends at unit `end`,
-// from block `block` on.
+// from block `block` on (unit u is in block floor(((u + 1) blocks - 1) / U)).
 __device__ __forceinline__ int parts_until(long long U, int block, int blocks, long long end) {
-  int n = 1;
-  while (U * (block + n) / blocks < end) ++n;
-  return n;
+  return (int)((end * blocks - 1) / U) - block + 1;
 }
 
 // ---------------------------------------------------------------------------
@@ -179,7 +180,12 @@ struct FmSmem {
   float v[FM_KEYS][D];
   float p[FM_ROWS][PST];
   unsigned long long mask[TREE_N];
+  int parent[TREE_N], page[FM_KEYS];
 };
+
+__device__ __forceinline__ void cp_async16(void* smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem) : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__ TreeArgs A) {
@@ -206,9 +212,9 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
                       (((size_t)A.layer * A.kv.n_kv_heads + g.hk) * 2) * P * D;
     __syncthreads();                             // the last segment's reads of q and mask are done
     if (t < g.k) {
-      const int32_t* par = A.parents + (size_t)g.s * A.max_nodes;
-      sm.mask[t] = ancestors(par, t);
-      if (g.t0 == 0 && (par[t] < -1 || par[t] >= t)) atomicOr(A.err, SPEC_DEV_ERR_TREE);
+      const int par = A.parents[(size_t)g.s * A.max_nodes + t];
+      sm.parent[t] = par;
+      if (g.t0 == 0 && (par < -1 || par >= t)) atomicOr(A.err, SPEC_DEV_ERR_TREE);
     }
     for (int i = t; i < FM_ROWS * (D / 4); i += FM_THREADS) {
       const int r = i / (D / 4), c = 4 * (i % (D / 4)), rr = row0 + r;
@@ -232,22 +238,32 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
     for (int tile = g.t0; tile < g.t1; ++tile) {
       const int k0 = tile * FM_KEYS, nk = min(FM_KEYS, g.n + g.k - k0);
       __syncthreads();                           // the last tile's reads of k, v and p are done
-      for (int i = t; i < FM_KEYS * (D / 4); i += FM_THREADS) {
-        const int key = i / (D / 4), c = 4 * (i % (D / 4));
-        float4 kv4 = make_float4(0.f, 0.f, 0.f, 0.f), vv4 = kv4;     // slots past the last: zeros
-        if (key < nk) {
-          const int page = bt[(k0 + key) / P];
+      if (t < FM_KEYS) {
+        int page = -1;                           // slots past the last, and bad pages: zeros
+        if (t < nk) {
+          page = bt[(k0 + t) / P];
           if (page < 0 || page >= A.kv.n_pages) {
+            page = -1;
             atomicOr(A.err, DERR_PAGE);
-          } else {
-            const float* e = plane + page * page_elems + (size_t)((k0 + key) % P) * D + c;
-            kv4 = *reinterpret_cast<const float4*>(e);
-            vv4 = *reinterpret_cast<const float4*>(e + (size_t)P * D);
           }
         }
-        *reinterpret_cast<float4*>(&sm.k[key][c]) = kv4;
-        *reinterpret_cast<float4*>(&sm.v[key][c]) = vv4;
+        sm.page[t] = page;
       }
+      __syncthreads();
+      if (tile == g.t0 && t < g.k) sm.mask[t] = ancestors(sm.parent, t);   // (read after the next barrier)
+#pragma unroll 4
+      for (int i = t; i < FM_KEYS * (D / 4); i += FM_THREADS) {
+        const int key = i / (D / 4), c = 4 * (i % (D / 4)), page = sm.page[key];
+        float *kd = &sm.k[key][c], *vd = &sm.v[key][c];
+        if (page >= 0) {
+          const float* e = plane + page * page_elems + (size_t)((k0 + key) % P) * D + c;
+          cp_async16(kd, e);
+          cp_async16(vd, e + (size_t)P * D);
+        } else {
+          *reinterpret_cast<float4*>(kd) = *reinterpret_cast<float4*>(vd) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();
       float x[4][4];
 #pragma unroll
@@ -621,6 +637,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     mbar_init(&H.fin, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     H.abort = 0;
+  }
+  if (t == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kvmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&H.tmem)), "r"(512));
