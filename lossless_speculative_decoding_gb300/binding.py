@@ -174,7 +174,8 @@ def _ptr(x) -> int:
     """Device pointer of a torch tensor or a raw integer address."""
     if x is None:
         return 0
-    return int(x.data_ptr()) if hasattr(x, "data_ptr") else int(x)
+    p = getattr(x, "data_ptr", None)
+    return p() if p is not None else int(x)
 
 
 def make_config(**kw) -> spec_config:

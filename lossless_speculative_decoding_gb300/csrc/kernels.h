@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace spec {
 
 constexpr int ATT_CHUNK = 64;     // keys per split-KV chunk (fixed at absolute positions)
@@ -310,6 +312,29 @@ inline cudaError_t allow_dyn_smem(K kernel) {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin - (int)fa.sharedSizeBytes);
   return e;
+}
+// The same once per device (the current one) and kernel, and the device's SM
+// count, for entry points that are called often: the first call on a device
+// asks the driver, which a stream capture allows.
+template <auto Kernel>
+inline cudaError_t allow_dyn_smem_once() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  if ((e = allow_dyn_smem(Kernel)) == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+inline int sm_count_once() {
+  static std::atomic<int> count[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = count[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) count[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 cudaError_t configure_gemv_kernels();
 cudaError_t configure_stream_kernels();

@@ -12,7 +12,9 @@ namespace spec {
 namespace {
 
 constexpr int COMMIT_THREADS = 256;
-constexpr int COMMIT_ROWS = 8;          // rows a thread holds in flight
+// Rows a thread holds in flight. Scattered rows of 256 bytes: 32 sequences with
+// up to 14 moves in 36 layers took 16.5 us with 4 rows, 17.6 with 8, 22.6 with 16.
+constexpr int COMMIT_ROWS = 4;
 
 struct CommitShared {
   int parent[TREE_N], token[TREE_N], target[TREE_N], path[TREE_N];

@@ -10,19 +10,23 @@
 //
 // The rows' steps of 32 KB, row after row, are cut into one even run for each
 // block that the GPU holds at once, so that a few rows use all of it and many
-// rows leave no tail. Within a row a thread keeps a running (R, z, sum) and a
-// count of the logits that come before the token; a step is added with packed
-// fp32 arithmetic, and again with care (masked tokens, NaN) if the sum came out
-// as NaN. Alternatives: a warp holds the best 32 of what it has seen as sorted
-// 64-bit keys (ordered logit, inverted index), one per lane. A thread's step is
-// searched only if its maximum is not below a bound of the block's n-th best
-// logit; the bound comes from the threads' maxima and is renewed after 1, 4,
-// 16, .. steps. 32 found keys are sorted and merged at a time. One warp of the
-// block ends a row while the others go on to the next; a row that several
-// blocks share is joined, in the blocks' order, by the last of them to finish
-// (which one that is changes nothing).
+// rows leave no tail. A warp takes 4 KB of a step, one ahead by a bulk copy into
+// its own shared memory, and no warp waits for another's. Within a row a thread
+// keeps a running (R, z, sum) and a count of the logits that come before the
+// token; a step whose sum comes out as NaN (masked tokens, NaN logits) is added
+// again with care. Alternatives: a warp holds the best 32 of what it has seen as
+// sorted 64-bit keys (ordered logit, inverted index), one per lane. A thread's
+// step is searched only if its maximum is not below a bound of the block's n-th
+// best logit, which comes from the threads' maxima (it only saves work: what is
+// found does not depend on it). 32 found keys are sorted and merged at a time. A
+// ninth warp ends the rows while the others go on; a row that several blocks
+// share is joined, in the blocks' order, by the last of them to finish (which
+// one that is changes nothing).
 //
-// Bound: HBM. The logits are read once.
+// Bound: fp32 logits by HBM (1,024 rows of 129,280 without alternatives: 6.4 TB/s,
+// 0.94 of the measured copy rate; with 20 of them 5.2), 16-bit ones by the
+// instructions of a logit, ten or so (1,100 rows of 151,936, one alternative:
+// 3.7 TB/s), and a few rows by the chain of a row's end, some 10 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -34,12 +38,13 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int LP_THREADS = 256;
+constexpr int LP_THREADS = 256;                  // that take the logits; one more warp ends the rows
+constexpr int LP_ALL = LP_THREADS + 32;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_UNROLL = 8;                     // 16-byte vectors a thread has in flight
 constexpr int LP_TILE = LP_THREADS * LP_UNROLL;  // vectors of a block's step
-constexpr int LP_STAGES = 2;                     // steps in shared memory: one being added, one on its way
-constexpr int LP_BLOCKS = 3;                     // blocks on an SM at once
+constexpr int LP_STAGES = 2;                     // steps of a warp in shared memory: one being added, the others on their way
+constexpr int LP_BLOCKS = 2;                     // blocks on an SM at once (three, with fewer registers each: no faster)
 constexpr int LP_MAX_VOCAB = 1 << 20;
 constexpr int LP_MAX_BLOCKS = 512;
 constexpr int LP_TOP = SPEC_LOGPROB_MAX_TOP;
@@ -77,33 +82,6 @@ __device__ __forceinline__ float lp_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two fp32 values in one 64-bit register pair, for the packed instructions.
-__device__ __forceinline__ u64 pair(float a, float b) {
-  u64 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 halves(u64 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 __device__ __forceinline__ float above(float x, float lim) {
   float r;
   asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(lim));
@@ -126,33 +104,50 @@ template <> struct LpVec<float> {
   static __device__ __forceinline__ float2 at(const uint4& v, int j) {
     return j ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
   }
-  static __device__ __forceinline__ float max_of(const uint4* p) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < LP_UNROLL; ++j) {
-      const uint4 v = reread(p + j * LP_THREADS);
-      asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)));
-      asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w)));
-    }
-    return m;
+  // the value below x in the order of the type; how many of a vector are above lim
+  static __device__ __forceinline__ float below(float x) { return nextafterf(x, -INFINITY); }
+  static __device__ __forceinline__ float count(const uint4& v, float lim) {
+    return (above(__uint_as_float(v.x), lim) + above(__uint_as_float(v.y), lim)) +
+           (above(__uint_as_float(v.z), lim) + above(__uint_as_float(v.w), lim));
   }
+  // A running maximum (NaN left out).
+  typedef float Max;
+  static __device__ __forceinline__ Max none() { return -INFINITY; }
+  static __device__ __forceinline__ void larger(Max& m, const uint4& v) {
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)));
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w)));
+  }
+  static __device__ __forceinline__ float value(Max m) { return m; }
 };
 template <> struct LpVec<bf16_t> {
   static __device__ __forceinline__ float2 at(const uint4& v, int j) {
     const uint32_t w = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
-  static __device__ __forceinline__ float max_of(const uint4* p) {
-    uint32_t a = 0xff80ff80u, b = a;             // -inf
+  static __device__ __forceinline__ float below(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return x == 0.f ? __uint_as_float(0x80010000u) : __uint_as_float(b & 0x80000000u ? b + 0x10000u : b - 0x10000u);
+  }
+  static __device__ __forceinline__ float count(const uint4& v, float lim) {
+    const __nv_bfloat162 l2 = __float2bfloat162_rn(lim);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    __nv_bfloat162 n = __float2bfloat162_rn(0.f);          // (up to 4 each: exact)
 #pragma unroll
-    for (int j = 0; j < LP_UNROLL; ++j) {
-      const uint4 v = reread(p + j * LP_THREADS);
-      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(v.x));
-      asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(v.y));
-      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(v.z));
-      asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(b), "r"(v.w));
-    }
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    for (int j = 0; j < 4; ++j) n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), l2));
+    const float2 f = __bfloat1622float2(n);
+    return f.x + f.y;
+  }
+  typedef uint2 Max;
+  static __device__ __forceinline__ Max none() { return make_uint2(0xff80ff80u, 0xff80ff80u); }   // -inf
+  static __device__ __forceinline__ void larger(Max& m, const uint4& v) {
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m.x) : "r"(m.x), "r"(v.x));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m.y) : "r"(m.y), "r"(v.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m.x) : "r"(m.x), "r"(v.z));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(m.y) : "r"(m.y), "r"(v.w));
+  }
+  static __device__ __forceinline__ float value(Max m) {
+    uint32_t a;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(m.x), "r"(m.y));
     return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
   }
 };
@@ -212,54 +207,83 @@ struct LpShared {
   LpStats stats[2][LP_WARPS];                    // the warps' parts of a row, for the warp that ends it
   u64 list[2][LP_WARPS][32];
   u64 pend[LP_WARPS][64];                        // found keys
-  uint32_t top[2][32];                           // each warp's four largest thread maxima
+  uint64_t full[LP_WARPS][LP_STAGES];            // a warp's step is there
+  int abort;
+  u64 top[32];                                   // each warp's four largest thread maxima, with their row
 };
 
 template <class T>
-__global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_constant__ LpArgs A) {
+__global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_constant__ LpArgs A) {
   constexpr int PER = Elt<T>::per16, U = LP_UNROLL, STEP = U * PER;
   __shared__ LpShared sh;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, V = A.vocab, n = A.top_n;
   const int64_t units = (int64_t)A.n_rows * A.tiles, end = units * (blockIdx.x + 1) / gridDim.x;
   int64_t pos = units * blockIdx.x / gridDim.x;  // (the grid has no more blocks than there are units)
   const float nan = __int_as_float(0x7fc00000), LN2 = 0.6931471805599453f;
-  const u64 c2 = pair(A.c, A.c);
-  int r = (int)(pos / A.tiles), s0 = (int)(pos % A.tiles), turn = 0, rows = 0;
-  // Steps go through shared memory, every thread's vectors by itself: the wait
-  // of a thread for its own copies is all the order they need.
-  extern __shared__ __align__(16) uint4 stage[];           // [LP_STAGES][U][LP_THREADS]
-  int fetched = 0, used = 0;
+  int r = (int)(pos / A.tiles), s0 = (int)(pos % A.tiles), rows = 0;
+  // Rows are handed over through the two halves of `stats` and `list`: barrier
+  // 1 + half when one is written, 3 + half when it is read.
+  auto bar_sync = [](int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); };
+  auto bar_arrive = [](int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); };
+  if (w < LP_WARPS) {
+  // A warp's part of a step is 4 KB of the row in one piece. It goes through the
+  // warp's own stages of shared memory, by a bulk copy; no other warp waits for it.
+  extern __shared__ __align__(16) uint4 stage_mem[];       // [LP_WARPS][LP_STAGES][U * 32]
+  uint4* stage = stage_mem + w * LP_STAGES * U * 32;
+  if (lane == 0) {
+    for (int i = 0; i < LP_STAGES; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"((uint32_t)__cvta_generic_to_shared(&sh.full[w][i])));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    sh.abort = 0;
+  }
+  if (lane < 32 / LP_WARPS) sh.top[32 / LP_WARPS * w + lane] = 0;
+  bar_sync(5, LP_THREADS);
+  int in = 0, out = 0, phase = 0;                          // stages to fill and to read next; the latter's phase
   auto row_of = [&](int i) { return static_cast<const T*>(A.logits) + (int64_t)i * A.ld; };
   auto skip_of = [&](const T* row) { return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)); };
-  auto fetch = [&](const T* row, int skip, int st) {
-    uint4* dst = stage + ((fetched++ & 1) * U) * LP_THREADS + t;
-    const int e0 = (st * LP_TILE + w * 32 * U) * PER - skip, first = st * LP_TILE + w * 32 * U + lane;
-    auto copy = [&](int j) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                   ::"r"((uint32_t)__cvta_generic_to_shared(dst + j * LP_THREADS)), "l"(row + ((first + 32 * j) * PER - skip)) : "memory");
-    };
-    if (e0 >= 0 && e0 + 32 * U * PER <= V) {
-#pragma unroll
-      for (int j = 0; j < U; ++j) copy(j);
-    } else if (e0 < V) {                         // a warp with an end of the row: -inf outside it
+  auto fetch = [&](const T* row, int skip, int st) {       // (every lane has read what the stage held)
+    uint4* dst = stage + in * U * 32;
+    const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&sh.full[w][in]);
+    if (++in == LP_STAGES) in = 0;
+    const int e0 = (st * LP_TILE + w * 32 * U) * PER - skip;
+    int v0 = 0, v1 = U * 32;                               // vectors that lie whole in the row
+    if (e0 < 0 || e0 + U * 32 * PER > V) {                 // an end of the row: -inf outside it
+      v0 = e0 < 0 ? 1 : 0;
+      v1 = max(v0, min(v1, (V - e0) / PER));
+      if (e0 >= V) v1 = v0;
+      for (int i = lane; i < U * 32; i += 32) {
+        if (i >= v0 && i < v1) continue;
+        const int e = e0 + i * PER;
+        T* x = reinterpret_cast<T*>(dst + i);
 #pragma unroll 1
-      for (int j = 0; j < U; ++j) {
-        const int e = (first + 32 * j) * PER - skip;
-        if (e >= 0 && e + PER <= V) {
-          copy(j);
-        } else {
-          T* x = reinterpret_cast<T*>(dst + j * LP_THREADS);
-#pragma unroll 1
-          for (int q = 0; q < PER; ++q) {
-            if constexpr (sizeof(T) == 4) x[q] = e + q >= 0 && e + q < V ? row[e + q] : -INFINITY;
-            else x[q].v = e + q >= 0 && e + q < V ? row[e + q].v : 0xff80;
-          }
+        for (int q = 0; q < PER; ++q) {
+          if constexpr (sizeof(T) == 4) x[q] = e + q >= 0 && e + q < V ? row[e + q] : -INFINITY;
+          else x[q].v = e + q >= 0 && e + q < V ? row[e + q].v : 0xff80;
         }
       }
     }
+    if (lane == 0) {
+      const uint32_t bytes = (uint32_t)(v1 - v0) * 16;
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+      if (bytes)
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                     ::"r"((uint32_t)__cvta_generic_to_shared(dst + v0)), "l"(row + (e0 + v0 * PER)), "r"(bytes), "r"(bar) : "memory");
+    }
   };
-  fetch(row_of(r), skip_of(row_of(r)), s0);
-  asm volatile("cp.async.commit_group;" ::: "memory");
+  // the fetches run LP_STAGES - 1 steps ahead of (r, st), over the block's rows
+  int left = (int)(end - pos), f_step = s0, f_skip = skip_of(row_of(r));   // (a block has far fewer than 2^31 steps)
+  const T* f_row = row_of(r);
+  auto fetch_next = [&]() {
+    if (left == 0) return;
+    fetch(f_row, f_skip, f_step);
+    --left;
+    if (++f_step == A.tiles) {
+      f_step = 0;
+      f_row += A.ld;
+      f_skip = skip_of(f_row);
+    }
+  };
+  for (int i = 0; i < LP_STAGES - 1; ++i) fetch_next();
 #pragma unroll 1
   for (; pos < end; ++r, s0 = 0, ++rows) {
     const int s1 = (int)min((int64_t)A.tiles, s0 + (end - pos));
@@ -275,9 +299,9 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
     // it), x > down, the next value below, in vectors ahead of it
     const int tvec = have ? (tok + skip) / PER : -1;
     const bool low = have && key_t == -INFINITY;           // ties with NaN and -inf: compared one by one
-    const float up = have && !low ? key_t : INFINITY, down = have && !low ? nextafterf(key_t, -INFINITY) : INFINITY;
+    const float up = have && !low ? key_t : INFINITY, down = have && !low ? LpVec<T>::below(key_t) : INFINITY;
     float R = -INFINITY, mk = -INFINITY;                   // c times the largest logit; the largest
-    u64 z2 = 0, zy2 = 0, ahead = 0;                        // two sums each
+    float z = 0.f, zy = 0.f, ahead = 0.f;
     int before = 0, pending = 0;
     bool bad = false;
     u64 list = 0;
@@ -285,60 +309,76 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
 #pragma unroll 1
     for (int st = s0; st < s1; ++st) {
       const int first = st * LP_TILE + w * 32 * U + lane;
-      if (st + 1 < s1) fetch(row, skip, st + 1);
-      else if (pos < end) fetch(row_of(r + 1), skip_of(row_of(r + 1)), 0);
-      asm volatile("cp.async.commit_group;\ncp.async.wait_group 1;" ::: "memory");
-      const uint4* mine = stage + ((used++ & 1) * U) * LP_THREADS + t;
+      fetch_next();
+      if (!mbar_wait_deadline((uint32_t)__cvta_generic_to_shared(&sh.full[w][out]), phase, &sh.abort)) {
+        *reinterpret_cast<volatile int*>(&sh.abort) = DERR_TIMEOUT;      // (not expected: the row's values become NaN)
+        bad = true;
+      }
+      __syncwarp();
+      const uint4* mine = stage + out * U * 32 + lane;
+      if (++out == LP_STAGES) {
+        out = 0;
+        phase ^= 1;
+      }
       float bm = -INFINITY;
       if ((st * LP_TILE + w * 32 * U) * PER - skip < V) {  // (the last step may end before the warp's part of it)
-        bm = LpVec<T>::max_of(mine);
-        if (bm > mk) {
-          mk = bm;
-          const float to = lp_scaled(bm, A.c), d = fmaxf(R - to, -1e30f), f = lp_ex2(d);
-          const u64 f2 = pair(f, f);
-          zy2 = mul2(fma2(z2, pair(d, d), zy2), f2);
-          z2 = mul2(z2, f2);
+        auto move_to = [&](float to) {                       // another R
+          const float d = fmaxf(R - to, -1e30f), f = lp_ex2(d);
+          zy = fmaf(z, d, zy) * f;
+          z *= f;
           R = to;
+        };
+        typename LpVec<T>::Max run = LpVec<T>::none();
+        if (R == -INFINITY) {                                // nothing seen yet: the step's own maximum first
+#pragma unroll
+          for (int j = 0; j < U; ++j) LpVec<T>::larger(run, reread(mine + j * 32));
+          bm = LpVec<T>::value(run);
+          if (bm > -INFINITY) R = lp_scaled(bm, A.c);
         }
         const float rb = R == -INFINITY ? 0.f : R;
-        const u64 nr2 = pair(-rb, -rb), z_old = z2, zy_old = zy2;
+        float z0 = 0.f, z1 = 0.f, zy0 = 0.f, zy1 = 0.f;      // (the step's own sums: two chains each)
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-          const uint4 v = reread(mine + j * LP_THREADS);
+          const uint4 v = reread(mine + j * 32);
+          LpVec<T>::larger(run, v);
 #pragma unroll
           for (int q = 0; q < PER / 2; ++q) {
             const float2 x = LpVec<T>::at(v, q);
-            const u64 y2 = fma2(pair(x.x, x.y), c2, nr2);
-            const float2 y = halves(y2);
-            const u64 p2 = pair(lp_ex2(y.x), lp_ex2(y.y));
-            z2 = add2(z2, p2);
-            zy2 = fma2(p2, y2, zy2);
+            const float ya = fmaf(x.x, A.c, -rb), yb = fmaf(x.y, A.c, -rb), pa = lp_ex2(ya), pb = lp_ex2(yb);
+            z0 += pa;
+            z1 += pb;
+            zy0 = fmaf(pa, ya, zy0);
+            zy1 = fmaf(pb, yb, zy1);
           }
         }
-        const float2 sum = halves(zy2);
-        if (!(sum.x + sum.y > -INFINITY) || fabsf(rb) > 1e29f) {   // masked tokens (0 times -inf), NaN, values at the type's ends
-          float z = 0.f, zy = 0.f;
+        bm = LpVec<T>::value(run);
+        zy0 += zy1;
+        z0 += z1;
+        // masked tokens (0 times -inf), NaN, values at the type's ends, or a
+        // logit so far above all before that its power is infinite
+        if (!(fabsf(zy0) < INFINITY) || fabsf(rb) > 1e29f) {
+          if (bm > mk) move_to(lp_scaled(bm, A.c));
+          const float rc = R == -INFINITY ? 0.f : R;
+          z0 = zy0 = 0.f;
 #pragma unroll 4
           for (int e = 0; e < STEP; ++e) {
-            const float x = logit<T>(reinterpret_cast<const T*>(mine + e / PER * LP_THREADS), e % PER), y = lp_scaled(x, A.c) - rb;
+            const float x = logit<T>(reinterpret_cast<const T*>(mine + e / PER * 32), e % PER), y = lp_scaled(x, A.c) - rc;
             const float p = x > -INFINITY ? lp_ex2(y) : 0.f;
             bad = bad || !(x < INFINITY);
-            z += p;
-            zy = fmaf(p, y, zy);
+            z0 += p;
+            zy0 = fmaf(p, y, zy0);
           }
-          z2 = add2(z_old, pair(z, 0.f));
-          zy2 = add2(zy_old, pair(zy, 0.f));
+        }
+        z += z0;
+        zy += zy0;
+        if (bm > mk) {                                       // R follows the maximum, so that the entropy's terms keep one sign
+          mk = bm;
+          move_to(lp_scaled(bm, A.c));
         }
         if (bm > down) {                                     // some may come before the token
 #pragma unroll
           for (int j = 0; j < U; ++j) {
-            const uint4 v = reread(mine + j * LP_THREADS);
-            const float lim = first + 32 * j < tvec ? down : up;
-#pragma unroll
-            for (int q = 0; q < PER / 2; ++q) {
-              const float2 x = LpVec<T>::at(v, q);
-              ahead = add2(ahead, pair(above(x.x, lim), above(x.y, lim)));
-            }
+            ahead += LpVec<T>::count(reread(mine + j * 32), first + 32 * j < tvec ? down : up);
           }
         }
         if (low) {
@@ -349,27 +389,37 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
           }
         }
       }
-      if (n == 0) continue;
-      // after 1, 4, 16, .. steps: with the eight largest thread maxima of every
-      // warp, the n-th largest of those 32 bounds the n-th best logit seen
+      if (n == 0) {
+        __syncwarp();                                      // before the stage is filled again
+        continue;
+      }
+      // After 1, 4, 16, .. steps a warp makes its four largest thread maxima
+      // known, marked with the row. The n-th largest of those that are there
+      // bounds the n-th best logit seen, and so does the warp's own n-th largest.
+      // A few alternatives take what is there; more wait for the other warps,
+      // whose maxima they need (20 of 256 rows: 36 us, 48 without the barrier; 1
+      // of 1,100 rows: 92 us with it, 89 without).
       const int done = st - s0 + 1;
       if ((done & (done - 1)) == 0 && (done & 0x55555555)) {
         uint32_t k = ordered(mk);
 #pragma unroll
         for (int i = 0; i < 32 / LP_WARPS; ++i) {
           const uint32_t mx = __reduce_max_sync(0xffffffffu, k);
-          if (lane == 0) sh.top[turn & 1][32 / LP_WARPS * w + i] = mx;
+          if (lane == 0) *reinterpret_cast<volatile u64*>(&sh.top[32 / LP_WARPS * w + i]) = ((u64)(rows + 1) << 32) | mx;
           if (lane == __ffs(__ballot_sync(0xffffffffu, k == mx)) - 1) k = 0;
         }
-        __syncthreads();                                   // (the other half of `top` is written next time)
-        const uint32_t b = __shfl_sync(0xffffffffu, warp_sort(sh.top[turn & 1][lane]), n - 1);
+        if (n > 4) bar_sync(5, LP_THREADS);
+        else __syncwarp();
+        const u64 known = *reinterpret_cast<volatile u64*>(&sh.top[lane]);
+        const uint32_t mine_or_none = (uint32_t)(known >> 32) == (uint32_t)(rows + 1) ? (uint32_t)known : 0u;
+        uint32_t b = n == 1 ? __reduce_max_sync(0xffffffffu, mine_or_none) : __shfl_sync(0xffffffffu, warp_sort(mine_or_none), n - 1);
+        if (b == 0) b = __shfl_sync(0xffffffffu, warp_sort(ordered(mk)), n - 1);
         bound = bound > b ? bound : b;
-        ++turn;
       }
       const bool cand = ordered(bm) >= bound;
       uint32_t rest = __ballot_sync(0xffffffffu, cand);
+      __syncwarp();
       if (!rest) continue;
-      __syncwarp();                                        // (the others' copies are waited for)
       do {                                                 // a thread's step, a logit per lane at a time
         const int src = __ffs(rest) - 1;
         rest &= rest - 1;
@@ -377,7 +427,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
 #pragma unroll 1
         for (int e = lane; e < STEP; e += 32) {
           const int i = (st * LP_TILE + (w * U + e / PER) * 32 + src) * PER - skip + e % PER;
-          const u64 k = i >= 0 && i < V ? key_of(logit<T>(reinterpret_cast<const T*>(its + e / PER * LP_THREADS), e % PER), i) : 0;
+          const u64 k = i >= 0 && i < V ? key_of(logit<T>(reinterpret_cast<const T*>(its + e / PER * 32), e % PER), i) : 0;
           const u64 least = __shfl_sync(0xffffffffu, list, n - 1);
           const bool in = k > least && (uint32_t)(k >> 32) >= bound;
           const uint32_t who = __ballot_sync(0xffffffffu, in);
@@ -396,7 +446,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
           }
         }
       } while (rest);
-      __syncwarp();                                        // before the next step's vectors
+      __syncwarp();                                        // before the stage is filled again
     }
 
     // ---- the block's part of the row: the warps' statistics and lists to one of them ----
@@ -405,9 +455,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
       list = warp_merge(list, warp_sort(lane < pending ? sh.pend[w][lane] : 0));
       __syncwarp();
     }
-    const float2 zh = halves(z2), yh = halves(zy2), ah = halves(ahead);
-    float z = zh.x + zh.y, zy = yh.x + yh.y;
-    before = __reduce_add_sync(0xffffffffu, before + (int)(ah.x + ah.y));
+    before = __reduce_add_sync(0xffffffffu, before + (int)ahead);
     bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -416,10 +464,38 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
       stats_merge(R, z, zy, ro, zo, zyo);
     }
     const int half = rows & 1;                             // the next row takes the other one
+    if (rows >= 2) bar_sync(3 + half, LP_ALL);
     if (lane == 0) sh.stats[half][w] = LpStats{R, z, zy, before, bad};
     if (n > 0) sh.list[half][w][lane] = list;
-    __syncthreads();
-    if (w != r % LP_WARPS) continue;
+    bar_arrive(1 + half, LP_ALL);
+  }
+  // shared memory outlives the copies (they are over, unless one was given up)
+  if (sh.abort)
+    for (int i = 0; i < LP_STAGES; ++i)
+      mbar_wait_deadline((uint32_t)__cvta_generic_to_shared(&sh.full[w][i]), i < out ? phase : phase ^ 1, nullptr);
+  return;
+  }
+
+  // ---- the ninth warp: a row's end ----
+#pragma unroll 1
+  for (; pos < end; ++r, s0 = 0, ++rows) {
+    const int s1 = (int)min((int64_t)A.tiles, s0 + (end - pos)), half = rows & 1;
+    pos += s1 - s0;
+    const T* row = static_cast<const T*>(A.logits) + (int64_t)r * A.ld;
+    const int skip = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+    const int tok = A.tokens ? A.tokens[r] : -1;
+    const bool have = tok >= 0 && tok < V;
+    const float raw_t = have ? logit<T>(row, tok) : 0.f, key_t = am_key(raw_t);
+    const bool low = have && key_t == -INFINITY;
+    // ties of the token ahead of it in its vector, which the others left out
+    int before = 0, ties = 0;
+    if (have && !low && A.rank) {
+      const int v0 = max(0, (tok + skip) / PER * PER - skip);
+      ties = __popc(__ballot_sync(0xffffffffu, v0 + lane < tok && am_key(logit<T>(row, v0 + lane)) == key_t));
+    }
+    float R, z, zy;
+    bool bad;
+    u64 list = 0;
     // `parts` statistics, in lanes 0 .. (at most 32 at a time), in a fixed tree
     auto gather = [&](auto&& of, int parts) {
       R = -INFINITY;
@@ -440,9 +516,15 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
         bad = bad || __any_sync(0xffffffffu, q.bad != 0);
       }
     };
+    bar_sync(1 + half, LP_ALL);
     gather([&](int i) { return sh.stats[half][i]; }, LP_WARPS);
-    if (n > 0)
-      for (int i = 1; i < LP_WARPS; ++i) list = warp_merge(list, sh.list[half][(w + i) % LP_WARPS][lane]);
+    if (n > 0) {
+      list = sh.list[half][0][lane];
+#pragma unroll 1
+      for (int i = 1; i < LP_WARPS; ++i) list = warp_merge(list, sh.list[half][i][lane]);
+    }
+    __syncwarp();
+    bar_arrive(3 + half, LP_ALL);
     if (s0 > 0 || s1 < A.tiles) {
       // ---- a shared row: leave the part; the last of its blocks, b0 .. b1, joins them ----
       const int64_t u0 = (int64_t)r * A.tiles;
@@ -483,11 +565,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_BLOCKS) k_logprob(const __grid_
     if (lane == 0) {
       if (A.logprob) A.logprob[r] = have ? logp(raw_t) : nan;
       if (A.entropy) A.entropy[r] = none ? nan : (lz - zy / z) * LN2;
-      if (A.rank) {
-        if (!low)                                          // ties inside the token's vector
-          for (int i = max(0, tvec * PER - skip); i < tok; ++i) before += am_key(logit<T>(row, i)) == key_t;
-        A.rank[r] = have ? before + 1 : 0;
-      }
+      if (A.rank) A.rank[r] = have ? before + ties + 1 : 0;
     }
     if (lane < n) {
       A.top_ids[(size_t)r * n + lane] = key_index(list);
@@ -509,14 +587,13 @@ cudaError_t launch_logprob(LpArgs A, cudaStream_t st) {
   // vectors of a row at the least alignment, steps of those, blocks for the steps
   constexpr int per = 16 / (int)sizeof(T), tile = LP_TILE;
   A.tiles = ((A.vocab + per - 1 + per - 1) / per + tile - 1) / tile;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  const int sms = sm_count_once();
+  if (sms < 1) return cudaErrorInvalidDevice;
   const int blocks = (int)std::min<int64_t>((int64_t)A.n_rows * A.tiles, std::min(LP_BLOCKS * sms, LP_MAX_BLOCKS));
   constexpr size_t smem = LP_STAGES * LP_TILE * 16;
-  if ((e = allow_dyn_smem(k_logprob<T>)) != cudaSuccess) return e;
-  k_logprob<T><<<blocks, LP_THREADS, smem, st>>>(A);
+  const cudaError_t e = allow_dyn_smem_once<k_logprob<T>>();
+  if (e != cudaSuccess) return e;
+  k_logprob<T><<<blocks, LP_ALL, smem, st>>>(A);
   return cudaGetLastError();
 }
 

@@ -1159,13 +1159,6 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_tree_join(const __grid_cons
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return n;
-}
-
 // Shape of a launch, from sizes and types alone.
 struct TreePlan {
   bool tc;                  // bf16 cache: the tensor-core form
@@ -1222,14 +1215,14 @@ cudaError_t join(const TreeArgs& A, int blocks, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_fma(const TreeArgs& A, int blocks, cudaStream_t st) {
-  cudaError_t e = allow_dyn_smem(k_tree_fma<D>);
+  cudaError_t e = allow_dyn_smem_once<k_tree_fma<D>>();
   if (e == cudaSuccess) e = launch_k(k_tree_fma<D>, dim3(blocks), dim3(FM_THREADS), sizeof(FmSmem<D>), st, A);
   return e == cudaSuccess ? join<D, float>(A, blocks, st) : e;
 }
 
 template <int D>
 cudaError_t launch_tc(const TreeArgs& A, const CUtensorMap& map, const CUtensorMap& qmap, int kb, int blocks, cudaStream_t st) {
-  cudaError_t e = allow_dyn_smem(k_tree_tc<D>);
+  cudaError_t e = allow_dyn_smem_once<k_tree_tc<D>>();
   const bool two = (A.rows + A.q_box - 1) / A.q_box * A.q_box > 128;
   if (e == cudaSuccess)
     e = launch_k(k_tree_tc<D>, dim3(blocks), dim3(TT_THREADS), TtCfg<D>::smem(two), st, map, qmap, A, kb, TtCfg<D>::nbuf(two),
@@ -1263,7 +1256,7 @@ extern "C" int spec_tree_attention(const spec_kv_view* kv, int layer, const void
   const int d = kv->head_dim;
   const TreePlan plan(*kv, max_nodes, n_q_heads);
   if (ws_bytes < plan.total) return set_last_error(SPEC_ERR_ARG, "workspace too small");
-  const int sms = sm_count();
+  const int sms = sm_count_once();
   if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
   char* w = static_cast<char*>(ws_dev);
   const TreeArgs A{*kv, q_dev, out_dev, cache_len_dev, n_nodes_dev, parents_dev, err_dev, reinterpret_cast<float*>(w),
