@@ -444,6 +444,11 @@ int spec_lmhead_argmax_noalloc(const float* x_dev, int T, int hidden, int vocab,
  * with spec_token_logprobs on the same logits; spec_kv_copy_pages gives a
  * forked sequence its own copy of a page that both would write.
  *
+ * Every call runs on the current device, which owns the stream and the
+ * pointers, checks its host arguments before any launch, and may be captured.
+ * Lengths and ids stay on the device: they may change between replays, but
+ * not while a call runs.
+ *
  * The cache of these entry points, the layout of a model's own pool. Device
  * pointers, caller-owned; the struct itself is read during the call only. */
 typedef struct spec_kv_view {
@@ -461,7 +466,7 @@ typedef struct spec_kv_view {
  * never cleared by them): */
 #define SPEC_DEV_ERR_PAGE 1         /* a needed page id is outside [0, n_pages) */
 #define SPEC_DEV_ERR_POS 4          /* cache_len < 0, n_nodes outside [0, max_nodes], or both past the block table */
-#define SPEC_DEV_ERR_TIMEOUT 8      /* a bounded wait inside a kernel ran out (not expected) */
+#define SPEC_DEV_ERR_TIMEOUT 8      /* a bounded wait inside a kernel ran out (not expected): the call's results are void */
 #define SPEC_DEV_ERR_TREE 16        /* a parent outside [-1, i) */
 
 /* Attention of n_seq trees over the paged cache, one layer. With A(i) node i
@@ -471,7 +476,8 @@ typedef struct spec_kv_view {
  * on kv head h / (n_q_heads / n_kv_heads).
  *   q_dev, out_dev [n_seq][max_nodes][n_q_heads][head_dim] in the cache's
  *     dtype, 16-byte aligned; rows of nodes >= n_nodes[s] are neither read
- *     into a result nor written.
+ *     into a result nor written. out_dev may be q_dev itself, but not overlap
+ *     it otherwise.
  *   cache_len_dev [n_seq], n_nodes_dev [n_seq] (0: a padded sequence, nothing
  *     is written), parents_dev [n_seq][max_nodes].
  *   ws_dev: spec_tree_attention_ws_bytes bytes of device memory, 16-byte
@@ -518,7 +524,7 @@ int spec_tree_commit(const spec_kv_view* kv, int n_seq, int max_nodes, const int
  * block_table_dev is not used and may be NULL. A source may feed several
  * copies; a page that is the destination of two pairs, or of one and the
  * source of another, ends with unspecified values. A pair with an id of -1 is
- * skipped (a padded list); one with an id past the pool is skipped too
+ * skipped (a padded list), one of equal ids too; one with an id past the pool is skipped
  * (SPEC_DEV_ERR_PAGE). src_dev, dst_dev: [n] int32, n >= 0.
  * Errors: SPEC_ERR_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA. */
 int spec_kv_copy_pages(const spec_kv_view* kv, const int32_t* src_dev, const int32_t* dst_dev, int n,
@@ -548,7 +554,9 @@ int spec_kv_copy_pages(const spec_kv_view* kv, const int32_t* src_dev, const int
  *     spec_token_logprobs_ws_bytes(n_rows, vocab, top_n) bytes, 16-byte
  *     aligned, zero-filled before its first use; every call leaves its
  *     counters at zero again. One call at a time per workspace.
- * Statistics are fp32, in a fixed order. Errors: SPEC_ERR_ARG,
+ * Statistics are fp32, in a fixed order: the same call gives the same bits. (A
+ * bounded wait inside the kernel that ran out, which is not expected, gives
+ * NaN log probabilities and entropies.) Errors: SPEC_ERR_ARG,
  * SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA. */
 #define SPEC_LOGPROB_MAX_TOP 32
 int64_t spec_token_logprobs_ws_bytes(int n_rows, int vocab, int top_n);

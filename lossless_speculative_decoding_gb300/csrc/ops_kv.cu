@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(COPY_THREADS) k_copy_pages(uint4* kv, long lon
                                                              const int32_t* dst, int n, int32_t* err) {
   for (int i = blockIdx.y; i < n; i += gridDim.y) {
     const int a = src[i], b = dst[i];
-    if (a == -1 || b == -1) continue;
+    if (a == -1 || b == -1 || (a == b && a >= 0 && a < n_pages)) continue;
     if (a < 0 || a >= n_pages || b < 0 || b >= n_pages) {
       if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, DERR_PAGE);
       continue;

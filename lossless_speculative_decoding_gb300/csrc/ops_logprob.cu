@@ -60,7 +60,6 @@ struct LpArgs {
   const void* logits;
   int64_t ld;
   int n_rows, vocab, top_n, tiles;               // tiles: steps of a row
-
   const int32_t* tokens;
   float it, c;              // 1 / temperature, log2(e) / temperature
   float* logprob;
@@ -273,6 +272,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
   // the fetches run LP_STAGES - 1 steps ahead of (r, st), over the block's rows
   int left = (int)(end - pos), f_step = s0, f_skip = skip_of(row_of(r));   // (a block has far fewer than 2^31 steps)
   const T* f_row = row_of(r);
+  bool lost = false;                                       // a copy was given up
   auto fetch_next = [&]() {
     if (left == 0) return;
     fetch(f_row, f_skip, f_step);
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
     float R = -INFINITY, mk = -INFINITY;                   // c times the largest logit; the largest
     float z = 0.f, zy = 0.f, ahead = 0.f;
     int before = 0, pending = 0;
-    bool bad = false;
+    bool bad = lost;
     u64 list = 0;
     uint32_t bound = 0;                                    // no key below it can be among the block's best n
 #pragma unroll 1
@@ -311,8 +311,10 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       const int first = st * LP_TILE + w * 32 * U + lane;
       fetch_next();
       if (!mbar_wait_deadline((uint32_t)__cvta_generic_to_shared(&sh.full[w][out]), phase, &sh.abort)) {
-        *reinterpret_cast<volatile int*>(&sh.abort) = DERR_TIMEOUT;      // (not expected: the row's values become NaN)
-        bad = true;
+        // (not expected: the values of this row and the block's later ones become NaN; no more copies)
+        *reinterpret_cast<volatile int*>(&sh.abort) = DERR_TIMEOUT;
+        bad = lost = true;
+        left = 0;
       }
       __syncwarp();
       const uint4* mine = stage + out * U * 32 + lane;

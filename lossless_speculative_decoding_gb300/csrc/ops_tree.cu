@@ -56,8 +56,8 @@ struct TreeSeg {
   int n, k;                                      // committed positions, nodes
 };
 
-// A block's walk over its units. All threads of the block call the
-// constructor (it has block barriers); next() is free of barriers.
+// A block's walk over its units. All threads of the block call init (it has
+// block barriers); next() is called by whole warps.
 struct TreeWalk {
   long long u, u1, U;                            // units left: [u, u1) of U
   int blocks;                                    // blocks that have units (no more than there are units)
@@ -123,8 +123,16 @@ struct TreeWalk {
         const int nrt = (z.k * A->G + A->rows - 1) / A->rows;
         if (in < g.nt * nrt * A->kv.n_kv_heads) break;
       }
-      ++s;
-      in = 0;
+      in = 0;                                    // the next sequence that is not padded, of 32 at a time
+      for (++s;; s += 32) {
+        if (s >= A->n_seq) return false;         // (only if the lengths changed meanwhile)
+        const int i = s + (threadIdx.x & 31);
+        const uint32_t live = __ballot_sync(0xffffffffu, i < A->n_seq && tree_size(*A, i).k > 0);
+        if (live) {
+          s += __ffs(live) - 1;
+          break;
+        }
+      }
       z = tree_size(*A, s);
     }
     g.s = s;
@@ -701,7 +709,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         }
         // V of the tile before the newest one (ahead), else of the newest
         const int pg = v && ahead && i < n - 1 ? last : page, key = tile * TT_KEYS + kb * j;
-        if (turn > 0 && !wait(H.kv_empty + b, turn - 1)) { ok = false; break; }
+        if (turn > 0 && !__all_sync(0xffffffffu, wait(H.kv_empty + b, turn - 1))) { ok = false; break; }
         const uint32_t full = sm_addr(H.kv_full + b);
         if (lane == 0)
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"((uint32_t)C::BUF) : "memory");
@@ -1203,7 +1211,7 @@ int check_tree(const spec_kv_view* kv, int n_seq, int max_nodes, int hq) {
   if (hq < 1 || hq % kv->n_kv_heads) return set_last_error(SPEC_ERR_ARG, "n_q_heads must be a multiple of n_kv_heads");
   if (hq / kv->n_kv_heads > TREE_MAX_G) return set_last_error(SPEC_ERR_UNSUPPORTED, "more than 128 query heads per kv head");
   // a sequence's units are counted in 32 bits
-  if ((double)kv->max_pages * kv->page_size / FM_KEYS * ((double)max_nodes * hq / FM_ROWS + kv->n_kv_heads) > 2e9)
+  if (((double)kv->max_pages * kv->page_size / FM_KEYS + 1) * ((double)max_nodes * hq / FM_ROWS + kv->n_kv_heads) > 2e9)
     return set_last_error(SPEC_ERR_UNSUPPORTED, "block table too long for this many heads");
   return SPEC_OK;
 }

@@ -189,3 +189,15 @@ def test_logprobs_captured_and_replayed():
         torch.cuda.synchronize()
         _compare([t.cpu().numpy() for t in (lp, ent, rank, ids, tl)], _ref(x, tok.cpu().numpy(), 1.0, top), V)
         assert bool((rank == V).all())
+
+
+@pytest.mark.parametrize("dtype", [T.F32, T.BF16])
+@pytest.mark.parametrize("R,V,top", [(65535, 1, 1), (65535, 5, 0), (20000, 9, 4), (305, 16385, 20), (609, 8192, 6)])
+def test_logprobs_of_many_short_rows(dtype, R, V, top):
+    """More rows than blocks: rows that start and end inside a block's run, with few tokens."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = torch.randn((R, V), generator=g, device="cuda")
+    x = x if dtype == T.F32 else x.bfloat16()
+    tokens = np.random.default_rng(V).integers(0, V, R).astype(np.int32)
+    _compare(_run(x, tokens, 1.0, top), _ref(x, tokens, 1.0, top), V)

@@ -407,3 +407,176 @@ def test_a_tree_step_of_the_operators_together():
             seqs, lens, text = [0, 1], lens * 2, [text[0], text[0][:-1] + [(text[0][-1] + 1) % V]]
     assert text[0] != text[1]
     B.spec_pool_destroy(pool)
+
+
+# ---- calls that the entry points allow and nothing above makes -------------------
+@pytest.mark.parametrize("dtype,G,hkv,d,page,max_nodes,layers", [
+    (T.BF16, 3, 2, 128, 16, 64, 1), (T.BF16, 5, 2, 64, 80, 13, 1), (T.BF16, 7, 1, 128, 144, 64, 2), (T.BF16, 25, 1, 64, 16, 64, 1),
+    (T.BF16, 33, 1, 128, 256, 9, 1), (T.BF16, 127, 1, 64, 16, 5, 1), (T.BF16, 128, 1, 128, 32, 64, 1), (T.BF16, 2, 3, 64, 16, 1, 1),
+    (T.BF16, 6, 2, 128, 112, 43, 1), (T.F32, 3, 2, 128, 80, 64, 1), (T.F32, 33, 1, 64, 16, 11, 2), (T.F32, 128, 1, 64, 256, 3, 1)])
+def test_attention_odd_groups_and_pages(dtype, G, hkv, d, page, max_nodes, layers):
+    """Head groups that share no factor with a tile's rows, trees of every width
+    up to the widest, pages longer than a tile and not powers of two."""
+    rng = np.random.default_rng(G)
+    nodes = sorted({1, 2, max_nodes // 2, max_nodes - 1, max_nodes} & set(range(1, max_nodes + 1)))
+    lens = [int(rng.integers(0, 700)) for _ in nodes]
+    lens[0], lens[-1] = 0, page
+    c = T.Cache(rng, lens, nodes, dtype=dtype, layers=layers, hkv=hkv, d=d, page=page, seed=G)
+    parents = np.stack([np.resize(T.rand_parents(rng, k, forest=True), max_nodes) for k in nodes])
+    q = _q(G, len(lens), max_nodes, G * hkv, d, dtype, sharp=2.0)
+    out, err = T.attention(c, layers - 1, q, lens, nodes, parents, 0.11)
+    assert err == 0
+    _check(c, layers - 1, q, lens, nodes, parents, out, 0.11)
+
+
+@pytest.mark.parametrize("dtype", [T.F32, T.BF16])
+@pytest.mark.parametrize("live", [[], [0], [1029], [3, 4, 300, 301, 302, 640, 999]])
+def test_attention_and_commit_of_a_mostly_padded_batch(dtype, live):
+    """More sequences than a block has threads, nearly all of them padded."""
+    import torch
+    rng = np.random.default_rng(9)
+    S, k = 1030, 6
+    lens, nodes = np.full(S, 5, np.int32), np.zeros(S, np.int32)
+    for s in live:
+        lens[s], nodes[s] = rng.integers(0, 400), rng.integers(1, k + 1)
+    c = T.Cache(rng, np.where(nodes > 0, lens, 0).tolist(), nodes.tolist(), dtype=dtype, layers=1, hkv=2, d=64, page=16)
+    if not live:
+        c.bt.fill_(-1)
+    parents = np.stack([T.rand_parents(rng, int(n))[:k] for n in nodes])
+    q = _q(1, S, k, 6, 64, dtype)
+    out, err = T.attention(c, 0, q, lens.tolist(), nodes.tolist(), parents, 0.125)
+    assert err == 0
+    _check(c, 0, q, lens.tolist(), nodes.tolist(), parents, out, 0.125)
+    tokens, target = rng.integers(0, 3, (S, k)).astype(np.int32), rng.integers(0, 3, (S, k)).astype(np.int32)
+    before = c.kv.clone()
+    acc, tok, ln, path, err = _commit(c, tokens, parents, target, lens, nodes)
+    assert err == 0
+    pad = nodes == 0
+    assert (acc[pad] == -1).all() and (ln[pad] == 5).all() and (path[pad] == -1).all()
+    for s in live:
+        p = T.ref_walk(parents[s], tokens[s], target[s], int(nodes[s]))
+        assert acc[s] == len(p) - 1 and ln[s] == lens[s] + len(p)
+    if not live:
+        assert bool(torch.equal(c.kv.nan_to_num(3.0), before.nan_to_num(3.0)))
+
+
+@pytest.mark.parametrize("dtype", [T.F32, T.BF16])
+def test_attention_in_place(dtype):
+    """The result over its own queries: rows in row tiles of several kinds, alone and shared between blocks."""
+    rng = np.random.default_rng(2)
+    lens, nodes = [1900, 40, 0, 260] * 8, [64, 5, 64, 33] * 8
+    c = T.Cache(rng, lens, nodes, dtype=dtype, layers=1, hkv=2, d=128, page=16)
+    parents = np.stack([T.rand_parents(rng, k) for k in nodes])
+    q = _q(3, len(lens), T.N, 12, 128, dtype)
+    out, err = T.attention(c, 0, q, lens, nodes, parents, 0.09)
+    assert err == 0
+    both = q.clone()
+    T.attention(c, 0, both, lens, nodes, parents, 0.09, out=both)
+    for s, k in enumerate(nodes):
+        assert bool((both[s, :k] == out[s, :k]).all()) and bool((both[s, k:] == q[s, k:]).all())
+
+
+def test_two_calls_at_once():
+    """Attention, and log probabilities, twice at the same time on two streams with a workspace each."""
+    import torch
+    from lossless_speculative_decoding_gb300 import binding as B
+    rng = np.random.default_rng(5)
+    lens, nodes = [700, 64, 2100, 5] * 4, [9, 64, 17, 40] * 4
+    c = T.Cache(rng, lens, nodes, dtype=T.BF16, layers=2, hkv=4, d=128, page=16)
+    parents = np.stack([T.rand_parents(rng, k) for k in nodes])
+    S, V = len(lens), 70001
+    q = [_q(i, S, T.N, 8, 128, T.BF16) for i in range(2)]
+    x = [torch.randn((3, V), device="cuda", generator=torch.Generator(device="cuda").manual_seed(i)) for i in range(2)]
+    want = [T.attention(c, i, q[i], lens, nodes, parents, 0.09)[0] for i in range(2)]
+    args = (T.dev(lens), T.dev(nodes), T.dev(parents))
+    nb, nl = B.spec_tree_attention_ws_bytes(c.view, S, T.N, 8), B.spec_token_logprobs_ws_bytes(3, V, 9)
+    ws = [torch.empty(nb, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    wl = [torch.zeros(nl, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out = [torch.full_like(q[0], 77.0) for _ in range(2)]
+    ids = [torch.zeros((3, 9), dtype=torch.int32, device="cuda") for _ in range(2)]
+    top, ent = [torch.zeros((3, 9), device="cuda") for _ in range(2)], [torch.zeros(3, device="cuda") for _ in range(2)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    st = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for turn in range(6):
+        for i in range(2):
+            B.spec_tree_attention(c.view, i, q[i], S, T.N, 8, *args, 0.09, out[i], ws[i], nb, err, st[i].cuda_stream)
+            B.spec_token_logprobs(x[i], T.F32, V, 3, V, None, 1.0, 9, None, ent[i], None, ids[i], top[i], wl[i], nl,
+                                  st[i].cuda_stream)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for i in range(2):
+        assert bool((out[i] == want[i]).all())
+        ref = torch.log_softmax(x[i].double(), -1)
+        v, k = ref.sort(dim=-1, descending=True, stable=True)
+        assert bool((ids[i] == k[:, :9]).all())
+        e = 8 * 8 * 2.0 ** -24 + 2.0 ** -21 + V * 2.0 ** -24              # |x| < 8: as in the log probabilities' own tests
+        assert float((top[i].double() - v[:, :9]).abs().max()) <= e + 16 * 2.0 ** -23
+
+
+def test_a_captured_step_replayed():
+    """Attention, commit and log probabilities of a step in one graph; the
+    lengths are handed on between replays, so that each replay commits behind
+    the one before it."""
+    import torch
+    from lossless_speculative_decoding_gb300 import binding as B
+    rng = np.random.default_rng(15)
+    S, k, V = 3, 8, 900
+    start = [10, 47, 16]
+    c = T.Cache(rng, [n + 40 for n in start], [k] * S, dtype=T.BF16, layers=2, hkv=2, d=64, page=16, junk=0.0)
+    parents = np.stack([T.rand_parents(rng, k)[:k] for _ in range(S)])
+    q = _q(1, S, k, 8, 64, T.BF16)
+    out = torch.full_like(q, 77.0)
+    lens, new, nodes, par = T.dev(start), T.dev(start), T.dev([k] * S), T.dev(parents)
+    tokens, target = (torch.zeros((S, k), dtype=torch.int32, device="cuda") for _ in range(2))
+    acc, tok = (torch.zeros(S, dtype=torch.int32, device="cuda") for _ in range(2))
+    path, err = torch.zeros((S, k), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    logits = torch.randn((S * k, V), device="cuda")
+    lp = torch.zeros(S * k, device="cuda")
+    nb, nl = B.spec_tree_attention_ws_bytes(c.view, S, k, 8), B.spec_token_logprobs_ws_bytes(S * k, V, 0)
+    ws, wl = torch.empty(nb, dtype=torch.uint8, device="cuda"), torch.zeros(nl, dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+
+    def step():
+        p = st.cuda_stream
+        B.spec_tree_attention(c.view, 1, q, S, k, 8, lens, nodes, par, 0.125, out, ws, nb, err, p)
+        B.spec_tree_commit(c.view, S, k, tokens, par, nodes, target, lens, acc, tok, path, new, err, p)
+        B.spec_token_logprobs(logits, T.F32, V, S * k, V, target, 1.0, 0, lp, None, None, None, None, wl, nl, p)
+
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        step()
+    for turn in range(3):
+        ids = [rng.integers(0, 3, (S, k)).astype(np.int32) for _ in range(2)]
+        tokens.copy_(T.dev(ids[0])), target.copy_(T.dev(ids[1]))
+        n = lens.cpu().numpy()
+        kv = c.kv.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        for s in range(S):
+            rows = kv[c.bt[s].long().clamp(min=0)].permute(0, 4, 1, 2, 3, 5).reshape(-1, 2, 2, 2, 64).double()[:n[s] + k]
+            ref, tol = T.ref_attention(rows, 1, q[s], int(n[s]), k, parents[s], 0.125)
+            assert bool(((out[s].double() - ref).abs() <= HALF[T.BF16] * ref.abs() + tol).all())
+            p = T.ref_walk(parents[s], ids[0][s], ids[1][s], k)
+            assert int(new[s]) == n[s] + len(p) and path[s].tolist() == p + [-1] * (k - len(p))
+            for j, i in enumerate(p):
+                a, b = n[s] + i, n[s] + j
+                assert bool((c.kv[c.table[s, b // 16], :, :, :, b % 16] == kv[c.table[s, a // 16], :, :, :, a % 16]).all())
+        want = torch.log_softmax(logits.double(), -1).gather(1, target.view(-1, 1).long())[:, 0]
+        assert float((lp.double() - want).abs().max()) <= 8 * 6 * 2.0 ** -24 + 2.0 ** -21 + V * 2.0 ** -24 + 16 * 2.0 ** -23
+        lens.copy_(new)
+
+
+def test_copy_pages_of_equal_ids_and_one_source():
+    import torch
+    from lossless_speculative_decoding_gb300 import binding as B
+    kv = torch.randn((6, 2, 2, 2, 16, 64), device="cuda")
+    want = kv.clone()
+    want[[1, 2, 5]] = kv[4]
+    view = B.make_kv_view(kv, None, dtype=T.F32, n_pages=6, n_layers=2, n_kv_heads=2, page_size=16, head_dim=64, max_pages=0)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.spec_kv_copy_pages(view, T.dev([4, 3, 4, 4, 4]), T.dev([1, 3, 2, 4, 5]), 5, err, 0)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and bool(torch.equal(kv, want))

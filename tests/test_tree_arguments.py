@@ -87,3 +87,12 @@ def test_logprobs_refusals(B):
     for bad in ((0, 10, 1), (1, 0, 0), (1, 10, 11), (1, 10, -1), (1, 100, 33)):
         with pytest.raises(B.SpecError):
             B.spec_token_logprobs_ws_bytes(*bad)
+
+
+def test_views_past_32_bits_are_refused(B):
+    """Planes, a page's rows and positions are counted in 32 bits."""
+    ok = dict(layer=0, q_dev=FAKE, n_seq=2, max_nodes=64, n_q_heads=4, cache_len_dev=FAKE, n_nodes_dev=FAKE, parents_dev=FAKE,
+              scale=0.1, out_dev=FAKE, ws_dev=FAKE, ws_bytes=1 << 40, err_dev=FAKE)
+    for v in (dict(n_pages=1 << 29), dict(page_size=1 << 28), dict(n_layers=1 << 25), dict(max_pages=1 << 27, page_size=16)):
+        _refused(B, B.spec_tree_attention, {**ok, "kv": _view(B, **v)}, -6)
+    _refused(B, B.spec_tree_attention, {**ok, "kv": _view(B, max_pages=1 << 26, n_kv_heads=16), "n_q_heads": 2048}, -6)
