@@ -378,49 +378,55 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
 // an MMA issuer, a loader (the next segment's sizes, queries and masks) and two
 // softmax groups of four warps. Keys come in tiles of 128. S = Q K^T (M = 128
 // rows, N = 128 keys) goes to tensor memory; a softmax thread owns one TMEM lane,
-// reads its scores, and writes the weights over them as bf16, and what that
-// rounding leaves as bf16 too (hi = bf16(p), lo = bf16(p - hi): 16 bits, so that
-// the result is as near as the one rounding of the output lets it be); O += hi V
-// + lo V takes them from TMEM as the A operand and V as an MN-major B operand.
-// The running maximum moves, and O is rescaled, only when a tile's maximum is
-// more than 8 (a factor of 256) above it.
+// reads its scores 32 at a time, and writes the weights over them as bf16, and
+// what that rounding leaves as bf16 too (hi = bf16(p), lo = bf16(p - hi): 16 bits,
+// so that the result is as near as the one rounding of the output lets it be);
+// O += hi V + lo V takes them from TMEM as the A operand and V as an MN-major B
+// operand. The running maximum m is a whole number and only follows a score more
+// than 2^32 above it: the weights are floats, whose precision a lower m leaves as
+// it is, so one pass over the scores serves, and the rare step rescales O and the
+// tile's earlier weights by an exact power of two.
 //
 // The two softmax groups have a buffer for S and an accumulator for O ("slot")
-// each and take turns, so that one's exponentials run beside the other's MMAs.
-// More than 128 rows: slot i has rows 128 i .. 128 i + 127 and both use every
-// key tile. Up to 128 rows: the slots take the segment's tiles alternately and
-// their results are joined at its end. Up to 64 rows would leave half of the
-// lanes idle: the rows are repeated, the upper 64 lanes holding the lo parts of
-// the weights where the lower ones hold the hi parts, which saves the second
-// MMA; up to 32 rows are repeated once more, and repetition p of two takes keys
-// 64 p .. 64 p + 63 of each tile alone, with weights 0 for the others (the MMA
-// has M = 128 in any case, and sums each lane apart).
+// each, take the segment's tiles in turn, so that one's exponentials run beside
+// the other's MMAs, and join their results at its end. Up to 64 rows would leave
+// half of the lanes idle: the rows are repeated, the upper 64 lanes holding the lo
+// parts of the weights where the lower ones hold the hi parts, which saves the
+// second MMA; up to 32 rows are repeated once more, and repetition p of two takes
+// keys 64 p .. 64 p + 63 of each tile alone, with weights 0 for the others (the
+// MMA has M = 128 in any case, and sums each lane apart).
 //
-// Bound: HBM for up to 128 rows (an MMA of 128 x 128 x 16 takes some 85 cycles,
-// so a tile 1,400 with the hi parts alone and 2,100 with both; its 64 KB take
-// 2,800 at an SM's share of the measured copy rate), the tensor cores above
-// that. (Tiles of 64 keys with two S buffers a slot were slower: an MMA of N = 64
-// takes 67 cycles, not half.)
+// Bound. An MMA of 128 x 128 x 16 takes 64 cycles (measured), so a tile takes the
+// tensor cores 1,024 cycles with the hi parts alone and 1,536 with both; its 64 KB
+// take 2,800 at an SM's share of the measured copy rate. So HBM, where a tile's
+// keys are read for one row tile: 64 sequences, 10 heads, 16 nodes, 0.93 GB:
+// 168 us, 5.5 TB/s, 0.82 of the copy rate; 4 long sequences, 8 kv heads, 84 rows
+// each: 74 us, 0.71. With 256 rows a sequence and head (8 sequences of 64 nodes,
+// 32 query heads) the chain S, softmax, P V of a slot: 2,400 cycles a tile, 56 us.
+// (Row tiles of 256, each slot with 128 rows of its own, read keys once for all of
+// them, but took 59.5 us there, 176 and 79 above: less room for keys, twice the
+// bytes of parts to join, more code. Scores 64 at a time: 55.7 and 168. A next
+// chunk's scores on their way beside the exponentials: 67 and 178. All 128 in
+// registers: 68 and 243. The loops are better short.)
 constexpr int TT_KEYS = 128;
 constexpr int TT_THREADS = 352;
 constexpr int TT_HALF = 128 * 128;               // bytes of 64 dims of 128 rows of Q
-constexpr int TT_MAXBUF = 16;
 constexpr int TT_OCOL = 256;                     // TMEM columns: S of a slot at 128 slot, its O behind at TT_OCOL + D slot
+constexpr float TT_GROW = 32.f;                  // the running maximum follows a larger one from 2^32 on
 constexpr int TT_STAGE = 2 * 128 * 64;           // staged output: two groups x 128 lanes x 16 columns
 
 template <int D>
 struct TtCfg {
   static constexpr int BUF = TT_KEYS * D * 2;    // K or V of a tile
-  static constexpr int QSLOT = 128 * D * 2;      // 128 rows of Q
+  static constexpr int Q = 128 * D * 2;          // 128 rows of Q
   static constexpr int TAIL = 5120;              // alignment slack and the header
-  static constexpr int q_bytes(bool two) { return (two ? 2 : 1) * QSLOT; }
-  static constexpr int fit(bool two) { return (232448 - 512 - TAIL - q_bytes(two) - TT_STAGE) / BUF; }
-  static constexpr int nbuf(bool two) { return fit(two) < TT_MAXBUF ? fit(two) : TT_MAXBUF; }
-  static constexpr int smem(bool two) { return nbuf(two) * BUF + q_bytes(two) + TT_STAGE + TAIL; }
+  static constexpr int NBUF = (232448 - 512 - TAIL - Q - TT_STAGE) / BUF;
+  static constexpr int SMEM = NBUF * BUF + Q + TT_STAGE + TAIL;
 };
 
+template <int NBUF>
 struct TtHeader {
-  uint64_t kv_full[TT_MAXBUF], kv_empty[TT_MAXBUF], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2], mask_full[2];
+  uint64_t kv_full[NBUF], kv_empty[NBUF], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2], mask_full[2];
   uint64_t q_full, q_free, fin;
   uint32_t tmem;
   int abort;
@@ -478,7 +484,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
       : "memory");
 }
 // (the first 16 values)
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[32]) {
+template <int N>
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[N]) {
   __syncwarp();
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
@@ -598,13 +605,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct TtRows {
   int row0, rows, boxes;       // first row, rows, boxes of queries
   int rpp, kparts;             // lanes of a repetition, parts of a tile's keys
-  bool two, hl;                // slots split the rows, not the tiles; hi parts on the lower lanes, lo parts on the upper
+  bool hl;                     // hi parts on the lower lanes, lo parts on the upper ones
   __device__ TtRows(const TreeArgs& A, const TreeSeg& g) {
     row0 = g.rt * A.rows;
     rows = min(A.rows, g.k * A.G - row0);
     boxes = (rows + A.q_box - 1) / A.q_box;
     const int lie = boxes * A.q_box;
-    two = lie > 128;
     hl = lie <= 64;
     rpp = lie <= 32 ? 32 : lie <= 64 ? 64 : 128;
     kparts = lie <= 32 ? 2 : 1;
@@ -614,17 +620,17 @@ struct TtRows {
 template <int D>
 __global__ void __launch_bounds__(TT_THREADS, 1)
     k_tree_tc(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
-              const __grid_constant__ TreeArgs A, int kb, int NBUF, int q_bytes) {
+              const __grid_constant__ TreeArgs A, int kb) {
   using C = TtCfg<D>;
-  constexpr int HALVES = D / 64;
+  constexpr int HALVES = D / 64, NBUF = C::NBUF;
   // a K or V tile lies as [8 keys][64-dim half][key][64 dims], as a box of whole pages brings it
   constexpr int GROUP = 1024 * HALVES;
   extern __shared__ unsigned char tt_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tt_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* qsm = base + NBUF * C::BUF;
-  unsigned char* stg = qsm + q_bytes;
-  TtHeader& H = *reinterpret_cast<TtHeader*>(stg + TT_STAGE);
-  static_assert(sizeof(TtHeader) + 1024 <= C::TAIL, "header and alignment slack");
+  unsigned char* stg = qsm + C::Q;
+  TtHeader<NBUF>& H = *reinterpret_cast<TtHeader<NBUF>*>(stg + TT_STAGE);
+  static_assert(sizeof(TtHeader<NBUF>) + 1024 <= C::TAIL, "header and alignment slack");
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t bufs = sm_addr(base), q_addr = sm_addr(qsm);
   if (t == 0) {
@@ -695,20 +701,17 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         }
         return page;
       };
-      // in the order of their use: K of tile t + 1 before V of tile t, unless both slots use every tile
-      const bool ahead = !TtRows(A, g).two;
       int page = page_of(g.t0), last = -1, next = page_of(g.t0 + 1);   // of the newest tile, the one before, the one after
       for (int i = 0, n = 2 * (g.t1 - g.t0); ok && i < n; ++i) {
-        // load i: K, then K V K V .. V V (ahead), or K V K V ..
-        const bool v = ahead ? (i == n - 1 || (i > 0 && i % 2 == 0)) : i % 2 == 1;
-        const int tile = g.t0 + (ahead ? (v ? (i == n - 1 ? n / 2 - 1 : i / 2 - 1) : (i + 1) / 2) : i / 2);
+        // in the order of their use: K, then K V K V .. V V, a tile's K before the V of the tile ahead of it
+        const bool v = i == n - 1 || (i > 0 && i % 2 == 0);
+        const int tile = g.t0 + (v ? (i == n - 1 ? n / 2 - 1 : i / 2 - 1) : (i + 1) / 2);
         if (!v && i > 0) {                       // a new tile's K: its pages
           last = page;
           page = next;
           next = page_of(tile + 1);
         }
-        // V of the tile before the newest one (ahead), else of the newest
-        const int pg = v && ahead && i < n - 1 ? last : page, key = tile * TT_KEYS + kb * j;
+        const int pg = v && i < n - 1 ? last : page, key = tile * TT_KEYS + kb * j;
         if (turn > 0 && !__all_sync(0xffffffffu, wait(H.kv_empty + b, turn - 1))) { ok = false; break; }
         const uint32_t full = sm_addr(H.kv_full + b);
         if (lane == 0)
@@ -742,32 +745,45 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (++rbuf == NBUF) { rbuf = 0; ++rturn; }
     };
     bool ok = true;
-    // the job whose P V is due: slot, job of the slot, 16-key steps, V's buffer
-    // and turn (when its load is not simply the next one), first of the slot's
-    // segment, last use of V, lo parts apart
-    struct Job { int slot; uint32_t k; int steps, vbuf, vturn; bool first, last, lo; } q{};
+    // the tile whose P V is due: slot, tile of the slot, 16-key steps, first of
+    // the slot's segment, lo parts apart
+    struct Job { int slot; uint32_t k; int steps; bool first, lo; } q{};
     bool due = false;
     auto pv = [&]() {
       due = false;
-      if (q.vbuf < 0) {
-        q.vbuf = rbuf;
-        q.vturn = rturn;
-        step();
-      }
-      const bool go = waitw(H.kv_full + q.vbuf, q.vturn) && waitw(H.p_full + q.slot, q.k);
+      const int vbuf = rbuf;
+      bool go = waitw(H.kv_full + vbuf, rturn);
+      step();
+      if (go) go = waitw(H.p_full + q.slot, q.k);
       if (!go) return false;
       tc_fence_after();
       const uint32_t d = tm + TT_OCOL + q.slot * D, a = tm + q.slot * 128;
-      const uint64_t bd = tt_desc(bufs + q.vbuf * C::BUF, 1024, GROUP);
+      const uint64_t bd = tt_desc(bufs + vbuf * C::BUF, 1024, GROUP);
+      // 16 keys a step: their hi weights lie in columns 32 (k / 2) + 8 (k % 2) .., the lo ones 16 behind
+      auto part = [&](int k, int at, bool acc) { mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1) + at, bd + (uint64_t)(k * 2 * GROUP >> 4), id_o, acc, one); };
+      part(0, 0, !q.first);
+      if (q.steps == TT_KEYS / 16) {
+        if (q.lo) {
+          part(0, 16, true);
 #pragma unroll
-      for (int k = 0; k < TT_KEYS / 16; ++k) {
-        if (k < q.steps) {
-          mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1), bd + (uint64_t)(k * 2 * GROUP >> 4), id_o, k > 0 || !q.first, one);
-          if (q.lo) mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1) + 16, bd + (uint64_t)(k * 2 * GROUP >> 4), id_o, true, one);
+          for (int k = 1; k < TT_KEYS / 16; ++k) {
+            part(k, 0, true);
+            part(k, 16, true);
+          }
+        } else {
+#pragma unroll
+          for (int k = 1; k < TT_KEYS / 16; ++k) part(k, 0, true);
+        }
+      } else {
+        if (q.lo) part(0, 16, true);
+#pragma unroll 1
+        for (int k = 1; k < q.steps; ++k) {
+          part(k, 0, true);
+          if (q.lo) part(k, 16, true);
         }
       }
       tc_commit(sm_addr(H.o_done + q.slot), one);
-      if (q.last) tc_commit(sm_addr(H.kv_empty + q.vbuf), one);
+      tc_commit(sm_addr(H.kv_empty + vbuf), one);
       return true;
     };
     for (uint32_t seg = 0; ok; ++seg) {
@@ -777,38 +793,27 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       g.nt = same(g.nt); g.t0 = same(g.t0); g.t1 = same(g.t1); g.n = same(g.n); g.k = same(g.k); g.rt = same(g.rt);
       if (g.nt == 0) break;
       const TtRows R(A, g);
-      const int nt = g.t1 - g.t0, nj = R.two ? 2 * nt : nt;
-      const uint32_t qhalf = R.two ? 2 * TT_HALF : TT_HALF;
-      int kbuf = 0, kturn = 0, vbuf = -1, vturn = 0;
+      const int nt = g.t1 - g.t0;
       if (!(ok = waitw(&H.q_full, seg))) break;
-      for (int jb = 0; ok && jb < nj; ++jb) {
-        const int slot = jb & 1, ti = R.two ? jb >> 1 : jb;
+      for (int ti = 0; ok && ti < nt; ++ti) {
+        const int slot = ti & 1, kbuf = rbuf;
         const uint32_t k = slot ? n1++ : n0++;
-        if (!R.two || slot == 0) {
-          kbuf = rbuf;
-          kturn = rturn;
-          step();
-        }
-        if (R.two && slot == 0) {
-          vbuf = rbuf;
-          vturn = rturn;
-          step();
-        }
         // S goes over the slot's last weights: their P V is done
-        ok = waitw(H.kv_full + kbuf, kturn) && (k == 0 || waitw(H.o_done + slot, k - 1));
+        ok = waitw(H.kv_full + kbuf, rturn);
+        step();
+        if (ok && k > 0) ok = waitw(H.o_done + slot, k - 1);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ad = tt_desc(q_addr + (R.two ? slot * TT_HALF : 0), 16, 1024), bd = tt_desc(bufs + kbuf * C::BUF, 16, GROUP);
+        const uint64_t ad = tt_desc(q_addr, 16, 1024), bd = tt_desc(bufs + kbuf * C::BUF, 16, GROUP);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          mma_ss(tm + slot * 128, ad + (uint64_t)(((i & 3) * 32 + (i >> 2) * qhalf) >> 4),
+          mma_ss(tm + slot * 128, ad + (uint64_t)(((i & 3) * 32 + (i >> 2) * TT_HALF) >> 4),
                  bd + (uint64_t)(((i & 3) * 32 + (i >> 2) * 1024) >> 4), id_s, i > 0, one);
-        const bool last = !R.two || slot == 1;
         tc_commit(sm_addr(H.s_full + slot), one);
-        if (last) tc_commit(sm_addr(H.kv_empty + kbuf), one);
-        if (jb == nj - 1) tc_commit(sm_addr(&H.q_free), one);
+        tc_commit(sm_addr(H.kv_empty + kbuf), one);
+        if (ti == nt - 1) tc_commit(sm_addr(&H.q_free), one);
         if (due) ok = pv();
-        q = Job{slot, k, (min(TT_KEYS, g.n + g.k - (g.t0 + ti) * TT_KEYS) + 15) / 16, vbuf, vturn, ti == (R.two ? 0 : slot), last, !R.hl};
+        q = Job{slot, k, (min(TT_KEYS, g.n + g.k - (g.t0 + ti) * TT_KEYS) + 15) / 16, ti < 2, !R.hl};
         due = true;
       }
       if (ok && due) ok = pv();
@@ -838,7 +843,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       for (int u = 0; u < 2; ++u)
         if (tree && lane + 32 * u < g.k) p[u] = par[lane + 32 * u];
       if (seg > 0 && !__all_sync(0xffffffffu, wait(&H.q_free, seg - 1))) continue;   // (aborted: no more copies)
-      const int nrep = R.two ? 1 : 128 / R.rpp, copies = R.boxes * nrep * HALVES;
+      const int nrep = 128 / R.rpp, copies = R.boxes * nrep * HALVES;
       if (lane == 0)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                      ::"r"(sm_addr(&H.q_full)), "r"((uint32_t)(copies * A.q_box * 128)) : "memory");
@@ -848,7 +853,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         const int half = i % HALVES, x = i / HALVES % R.boxes, rp = i / HALVES / R.boxes;
         asm volatile(
             "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-            ::"r"(q_addr + half * (R.two ? 2 * TT_HALF : TT_HALF) + (x * A.q_box + rp * R.rpp) * 128),
+            ::"r"(q_addr + half * TT_HALF + (x * A.q_box + rp * R.rpp) * 128),
               "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(0), "r"(half), "r"(g.hk * A.G),
               "r"(g.s * A.max_nodes + (R.row0 + x * A.q_box) / A.G), "r"(sm_addr(&H.q_full))
             : "memory");
@@ -886,7 +891,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (g.nt == 0) break;
       const TtRows R(A, g);
       const int nt = g.t1 - g.t0;
-      const int rep = R.two ? 0 : r / R.rpp, lr = R.two ? slot * 128 + r : r % R.rpp;
+      const int rep = r / R.rpp, lr = r % R.rpp;
       const int kpart = R.kparts == 2 ? rep & 1 : 0;
       const bool live = lr < R.rows, low = R.hl && r >= 64;
       const bool any_live = __any_sync(0xffffffffu, live);
@@ -896,9 +901,9 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         if (live) mask = H.mask[sb][(R.row0 + lr) / A.G];
       }
       float m = -INFINITY, l = 0.f;
-      for (int ti = R.two ? 0 : slot; ti < nt; ti += R.two ? 1 : 2) {
+      for (int ti = slot; ti < nt; ti += 2) {
         const int k0 = (g.t0 + ti) * TT_KEYS;
-        const bool first = ti == (R.two ? 0 : slot);
+        const bool first = ti < 2;
         const uint32_t k = jobs++, sT = tmem + lanes + slot * 128;
         wait(H.s_full + slot, k);
         tc_fence_after();
@@ -919,48 +924,58 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
                 if (!((bits >> i) & 1)) v[i] = 0xff800000u;
             }
           };
-          float mt = -INFINITY, mu = -INFINITY;
-          uint32_t v[32];
-#pragma unroll 1
-          for (int c = c1 - 1; c >= c0; --c) {   // (chunk c0 last: its values are used first)
-            chunk(c, v);
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              mt = max3(mt, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-              mu = max3(mu, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-            }
-          }
-          mt = fmaxf(mt, mu) * A.scale_l2e;
-          if (first) {
-            m = mt;
-          } else {
-            const bool grow = live && mt > m + 8.f;
-            if (__any_sync(0xffffffffu, grow)) { // (S of this tile came after the slot's last P V)
-              const float corr = grow ? ex2(m - mt) : 1.f;
-              if (grow) m = mt;
+          // A larger maximum at chunk c: the lane's weights so far are of another m.
+          auto rescale = [&](int c, float mt, bool grow) {
+            float corr = 1.f;
+            tmem_wait_st();                      // the chunks' weights are read back
+            if (grow) {
+              const float to = ceilf(mt), by = to - m;
+              corr = by < 127.f ? __uint_as_float((127 - (int)by) << 23) : 0.f;    // 2^-by, exact
+              m = to;
               l *= corr;
+            }
+            if (!first) {                        // (S of this tile came after the slot's last P V)
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(oT + 32 * c, o);
+              for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
+                tmem_ld16(oT + i, o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-                tmem_st32(oT + 32 * c, o);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                tmem_st16(oT + i, o);
               }
             }
-          }
-          const float mb = m == -INFINITY ? 0.f : m;
-          const unsigned long long nm2 = pair(-mb, -mb);
-          unsigned long long sum = 0;
 #pragma unroll 1
-          for (int c = c0;;) {
+            for (int i = 32 * c0; i < 32 * c; i += 16) {
+              uint32_t w[16];
+              tmem_ld16(sT + i, w);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[j] = pack_bf16(__uint_as_float(w[j] << 16) * corr, __uint_as_float(w[j] & 0xFFFF0000u) * corr);
+              tmem_st16(sT + i, w);
+            }
+          };
+#pragma unroll 1
+          for (int c = c0; c < c1; ++c) {
+            uint32_t v[32];
+            chunk(c, v);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], __uint_as_float(v[i + 2 * u]), __uint_as_float(v[i + 2 * u + 1]));
+            const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * A.scale_l2e;
+            const bool grow = live && mt > m + TT_GROW;
+            if (__any_sync(0xffffffffu, grow)) rescale(c, mt, grow);
+            const float mb = m == -INFINITY ? 0.f : m;
+            const unsigned long long nm2 = pair(-mb, -mb);
+            unsigned long long sum[2] = {0, 0};
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 y = halves(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2));
               const float p0 = ex2(y.x), p1 = ex2(y.y);
               const unsigned long long p2 = pair(p0, p1);
-              sum = add2(sum, p2);
+              sum[i / 2 & 1] = add2(sum[i / 2 & 1], p2);
               const uint32_t hi = pack_bf16(p0, p1);
               const float2 e = halves(add2(p2, pair(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xFFFF0000u))));
               const uint32_t lo = pack_bf16(e.x, e.y);
@@ -969,8 +984,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
             }
             if (R.hl) tmem_st16(sT + 32 * c, w);
             else tmem_st32(sT + 32 * c, w);
-            if (++c == c1) break;
-            chunk(c, v);
+            const float2 s2 = halves(add2(sum[0], sum[1]));
+            l += s2.x + s2.y;
           }
           if (R.kparts == 2) {                   // the other part's keys: weights 0
             uint32_t x[32];
@@ -979,8 +994,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
             tmem_st16(sT + 32 * (2 - c0), x);
             tmem_st16(sT + 32 * (3 - c0), x);
           }
-          const float2 s2 = halves(sum);
-          l += s2.x + s2.y;
           tmem_wait_st();
         }
         // slots past the last node may hold anything: their V rows become zeros
@@ -1016,45 +1029,38 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         else *reinterpret_cast<float4*>(o + col * 4) = v;
       };
       // each group waits for its own slot's last P V; the barriers pass that on
-      if (R.two || slot < nt) wait(H.o_done + slot, jobs - 1);
-      float w0 = 1.f, w1 = 0.f;                  // of this lane's O in slot 0 (its own slot, two), in slot 1
-      const bool both = !R.two && nt > 1;        // slot 1 had tiles
-      if (R.two) {
-        tc_fence_after();
-        if (wpart < 0) w0 = 1.f / l;
-        else if (live) A.part_ml[((size_t)blockIdx.x * 2 + wpart) * A.rows + lr] = make_float2(m, l);
-      } else {
-        H.ml[slot][r] = make_float2(live ? m : -INFINITY, live ? l : 0.f);
-        tc_fence_before();
-        named_sync(1, 256);
-        tc_fence_after();
-        float M = -INFINITY, L = 0.f;
-        for (int p = 0; p < R.kparts; ++p) {     // (the upper lanes repeat the lower ones' statistics)
-          const float2 a = H.ml[0][p * R.rpp + r % R.rpp], b = H.ml[1][p * R.rpp + r % R.rpp];
-          const float mn = max3(M, a.x, b.x), mb = mn == -INFINITY ? 0.f : mn;
-          L = L * ex2(M - mb) + a.y * ex2(a.x - mb) + b.y * ex2(b.x - mb);
-          M = mn;
-        }
-        const float Mb = M == -INFINITY ? 0.f : M, inv = wpart < 0 ? 1.f / L : 1.f;
-        w0 = ex2(H.ml[0][r].x - Mb) * inv;
-        w1 = ex2(H.ml[1][r].x - Mb) * inv;
-        if (wpart >= 0 && slot == 0 && live && rep == 0)
-          A.part_ml[((size_t)blockIdx.x * 2 + wpart) * A.rows + lr] = make_float2(M, L);
+      if (slot < nt) wait(H.o_done + slot, jobs - 1);
+      const bool both = nt > 1;                  // slot 1 had tiles
+      H.ml[slot][r] = make_float2(live ? m : -INFINITY, live ? l : 0.f);
+      tc_fence_before();
+      named_sync(1, 256);
+      tc_fence_after();
+      float M = -INFINITY, L = 0.f;
+      for (int p = 0; p < R.kparts; ++p) {       // (the upper lanes repeat the lower ones' statistics)
+        const float2 a = H.ml[0][p * R.rpp + lr], b = H.ml[1][p * R.rpp + lr];
+        const float mn = max3(M, a.x, b.x), mb = mn == -INFINITY ? 0.f : mn;
+        L = L * ex2(M - mb) + a.y * ex2(a.x - mb) + b.y * ex2(b.x - mb);
+        M = mn;
       }
+      // the weight of this lane's O in slot 0, in slot 1
+      const float Mb = M == -INFINITY ? 0.f : M, inv = wpart < 0 ? 1.f / L : 1.f;
+      const float w0 = ex2(H.ml[0][r].x - Mb) * inv, w1 = ex2(H.ml[1][r].x - Mb) * inv;
+      if (wpart >= 0 && slot == 0 && live && rep == 0)
+        A.part_ml[((size_t)blockIdx.x * 2 + wpart) * A.rows + lr] = make_float2(M, L);
       // 16 columns at a time through shared memory: a row's repetitions are
-      // summed, and four lanes write 64 bytes of a row together. Two: each group
-      // its own slot's columns; else the groups take half of both slots' each.
-      const int nrep = R.two ? 1 : 128 / R.rpp, col0 = R.two ? 0 : slot * (D / 2);
-      const uint32_t o0 = tmem + lanes + TT_OCOL + (R.two ? slot * D : col0), o1 = o0 + D;
+      // summed, and four lanes write 64 bytes of a row together. Each group takes
+      // half of the columns, of both slots.
+      const int nrep = 128 / R.rpp, col0 = slot * (D / 2);
+      const uint32_t o0 = tmem + lanes + TT_OCOL + col0, o1 = o0 + D;
       float4* stage = reinterpret_cast<float4*>(stg + slot * (TT_STAGE / 2));   // [128 lanes][16 columns]
       unsigned char* og[4];                      // the rows whose columns 4 (r % 4) .. this thread writes
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int y = (R.two ? slot * 128 : 0) + r / 4 + 32 * u;
+        const int y = r / 4 + 32 * u;
         og[u] = u * nrep < 4 && y < R.rows ? out_row(y) : nullptr;
       }
 #pragma unroll 1
-      for (int c = 0; c < (R.two ? D / 16 : D / 32); ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t v[16], x[16];
         if (both) tmem_ld16x2(o0 + 16 * c, o1 + 16 * c, v, x);
         else tmem_ld16(o0 + 16 * c, v);
@@ -1178,15 +1184,15 @@ struct TreePlan {
     const int G = hq / kv.n_kv_heads;
     tc = kv.dtype == SPEC_BF16;
     if (tc) {
-      // tiles of at most 256 rows, whole nodes, as even as they come
-      const int most = std::max(1, 256 / G), nrt = (max_nodes + most - 1) / most;
+      // tiles of at most 128 rows, whole nodes, as even as they come
+      const int most = std::max(1, 128 / G), nrt = (max_nodes + most - 1) / most;
       int nodes = (max_nodes + nrt - 1) / nrt, box = 8;
       while (box > 1 && box / 2 * G % 8 == 0) box /= 2;
       // boxes start at multiples of 8 rows (the swizzle's period), up to 32 rows
       // each where that many nodes do; one box when the tile has no more nodes,
-      // or when whole boxes would go past 256 rows
+      // or when whole boxes would go past 128 rows
       box *= std::max(1, 32 / (box * G));
-      if (box >= nodes || (nodes + box - 1) / box * box * G > 256) box = nodes;
+      if (box >= nodes || (nodes + box - 1) / box * box * G > 128) box = nodes;
       q_box = box * G;
       rows = nodes * G;
       tile_k = TT_KEYS;
@@ -1231,10 +1237,8 @@ cudaError_t launch_fma(const TreeArgs& A, int blocks, cudaStream_t st) {
 template <int D>
 cudaError_t launch_tc(const TreeArgs& A, const CUtensorMap& map, const CUtensorMap& qmap, int kb, int blocks, cudaStream_t st) {
   cudaError_t e = allow_dyn_smem_once<k_tree_tc<D>>();
-  const bool two = (A.rows + A.q_box - 1) / A.q_box * A.q_box > 128;
   if (e == cudaSuccess)
-    e = launch_k(k_tree_tc<D>, dim3(blocks), dim3(TT_THREADS), TtCfg<D>::smem(two), st, map, qmap, A, kb, TtCfg<D>::nbuf(two),
-                 TtCfg<D>::q_bytes(two));
+    e = launch_k(k_tree_tc<D>, dim3(blocks), dim3(TT_THREADS), TtCfg<D>::SMEM, st, map, qmap, A, kb);
   return e == cudaSuccess ? join<D, bf16_t>(A, blocks, st) : e;
 }
 

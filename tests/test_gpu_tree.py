@@ -580,3 +580,32 @@ def test_copy_pages_of_equal_ids_and_one_source():
     B.spec_kv_copy_pages(view, T.dev([4, 3, 4, 4, 4]), T.dev([1, 3, 2, 4, 5]), 5, err, 0)
     torch.cuda.synchronize()
     assert int(err.item()) == 0 and bool(torch.equal(kv, want))
+
+
+@pytest.mark.parametrize("dtype", [T.F32, T.BF16])
+@pytest.mark.parametrize("hq,nodes", [(4, 7), (4, 24), (8, 24), (24, 10)])
+def test_attention_scores_that_jump(dtype, hq, nodes):
+    """Scores that rise by hundreds within a tile, fall again, and rise in other
+    places for other rows: the running maximum moves within and between tiles,
+    over weights and sums that are already there."""
+    import torch
+    rng = np.random.default_rng(hq)
+    lens, ks = [0, 300, 1111, 40], [nodes, nodes, max(1, nodes // 2), 3]
+    c = T.Cache(rng, lens, ks, dtype=dtype, layers=1, hkv=2, d=64, page=16, seed=5)
+    parents = np.stack([T.rand_parents(rng, k) for k in ks])
+    u = torch.randn((2, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    td = torch.float32 if dtype == T.F32 else torch.bfloat16
+    for s in range(4):
+        t = lens[s] + ks[s]
+        pos = torch.arange(t, device="cuda")
+        step = torch.floor(pos / 23) * ((pos // 200) % 2 * -2 + 1)     # up for 200 keys, down for 200, a step each 23 keys
+        k = (step[:, None] * u[0] * 0.2 + (pos % 50)[:, None] * u[1] * 0.05).to(td)
+        pg = c.bt[s].long()[pos // 16]
+        c.kv[pg, 0, 1, 0, pos % 16] = k
+        c.rows[s][:, 0, 1, 0] = k.double()
+    q = _q(4, 4, T.N, hq, 64, dtype)
+    q[:, :, hq // 2:] = (q[:, :, hq // 2:] * 0.1 + u[0] * 1.5).to(td)
+    q[:, 1::3, hq // 2:] = (-u[0] + u[1] * 2).to(td)                   # other rows: the other way
+    out, err = T.attention(c, 0, q, lens, ks, parents, 0.5)
+    assert err == 0
+    _check(c, 0, q, lens, ks, parents, out, 0.5)
