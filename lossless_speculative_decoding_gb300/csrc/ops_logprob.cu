@@ -26,7 +26,7 @@
 // Bound: fp32 logits by HBM (1,024 rows of 129,280 without alternatives: 6.4 TB/s,
 // 0.94 of the measured copy rate; with 20 of them 5.2), 16-bit ones by the
 // instructions of a logit, ten or so (1,100 rows of 151,936, one alternative:
-// 3.7 TB/s), and a few rows by the chain of a row's end, some 10 us.
+// 3.9 TB/s), and a few rows by the chain of a row's end, some 10 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -87,12 +87,12 @@ __device__ __forceinline__ float above(float x, float lim) {
   return r;
 }
 
-// A vector from shared memory; volatile, so that it is read again and not kept
-// in registers from one use to the next.
-__device__ __forceinline__ uint4 reread(const uint4* p) {
+// Vector j of a lane's part of a step, at shared address a; volatile, so that it
+// is read again and not kept in registers from one use to the next.
+__device__ __forceinline__ uint4 reread(uint32_t a, int j) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"((uint32_t)__cvta_generic_to_shared(p)) : "memory");
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a + j * 512) : "memory");
   return v;
 }
 
@@ -105,10 +105,13 @@ template <> struct LpVec<float> {
   }
   // the value below x in the order of the type; how many of a vector are above lim
   static __device__ __forceinline__ float below(float x) { return nextafterf(x, -INFINITY); }
-  static __device__ __forceinline__ float count(const uint4& v, float lim) {
-    return (above(__uint_as_float(v.x), lim) + above(__uint_as_float(v.y), lim)) +
-           (above(__uint_as_float(v.z), lim) + above(__uint_as_float(v.w), lim));
+  typedef float Lim;
+  typedef float Count;
+  static __device__ __forceinline__ Lim lim(float x) { return x; }
+  static __device__ __forceinline__ void count(Count& n, const uint4& v, Lim l) {
+    n += (above(__uint_as_float(v.x), l) + above(__uint_as_float(v.y), l)) + (above(__uint_as_float(v.z), l) + above(__uint_as_float(v.w), l));
   }
+  static __device__ __forceinline__ float total(Count n) { return n; }
   // A running maximum (NaN left out).
   typedef float Max;
   static __device__ __forceinline__ Max none() { return -INFINITY; }
@@ -127,12 +130,16 @@ template <> struct LpVec<bf16_t> {
     const uint32_t b = __float_as_uint(x);
     return x == 0.f ? __uint_as_float(0x80010000u) : __uint_as_float(b & 0x80000000u ? b + 0x10000u : b - 0x10000u);
   }
-  static __device__ __forceinline__ float count(const uint4& v, float lim) {
-    const __nv_bfloat162 l2 = __float2bfloat162_rn(lim);
+  typedef __nv_bfloat162 Lim;
+  typedef __nv_bfloat162 Count;                  // two counts of a step, exact up to 256
+  static_assert(LP_UNROLL * 4 <= 256, "counts in bf16");
+  static __device__ __forceinline__ Lim lim(float x) { return __float2bfloat162_rn(x); }
+  static __device__ __forceinline__ void count(Count& n, const uint4& v, Lim l) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    __nv_bfloat162 n = __float2bfloat162_rn(0.f);          // (up to 4 each: exact)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), l2));
+    for (int j = 0; j < 4; ++j) n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]), l));
+  }
+  static __device__ __forceinline__ float total(Count n) {
     const float2 f = __bfloat1622float2(n);
     return f.x + f.y;
   }
@@ -214,6 +221,7 @@ struct LpShared {
 template <class T>
 __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_constant__ LpArgs A) {
   constexpr int PER = Elt<T>::per16, U = LP_UNROLL, STEP = U * PER;
+  static_assert(STEP % 32 == 0, "whole warps search a thread's step");
   __shared__ LpShared sh;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, V = A.vocab, n = A.top_n;
   const int64_t units = (int64_t)A.n_rows * A.tiles, end = units * (blockIdx.x + 1) / gridDim.x;
@@ -249,8 +257,8 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
     if (e0 < 0 || e0 + U * 32 * PER > V) {                 // an end of the row: -inf outside it
       v0 = e0 < 0 ? 1 : 0;
       v1 = max(v0, min(v1, (V - e0) / PER));
-      if (e0 >= V) v1 = v0;
-      for (int i = lane; i < U * 32; i += 32) {
+      if (e0 >= V) v1 = v0;                                // (nothing of it is looked at)
+      else for (int i = lane; i < U * 32; i += 32) {
         if (i >= v0 && i < v1) continue;
         const int e = e0 + i * PER;
         T* x = reinterpret_cast<T*>(dst + i);
@@ -318,6 +326,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       }
       __syncwarp();
       const uint4* mine = stage + out * U * 32 + lane;
+      const uint32_t at = (uint32_t)__cvta_generic_to_shared(mine);
       if (++out == LP_STAGES) {
         out = 0;
         phase ^= 1;
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
         typename LpVec<T>::Max run = LpVec<T>::none();
         if (R == -INFINITY) {                                // nothing seen yet: the step's own maximum first
 #pragma unroll
-          for (int j = 0; j < U; ++j) LpVec<T>::larger(run, reread(mine + j * 32));
+          for (int j = 0; j < U; ++j) LpVec<T>::larger(run, reread(at, j));
           bm = LpVec<T>::value(run);
           if (bm > -INFINITY) R = lp_scaled(bm, A.c);
         }
@@ -341,7 +350,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
         float z0 = 0.f, z1 = 0.f, zy0 = 0.f, zy1 = 0.f;      // (the step's own sums: two chains each)
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-          const uint4 v = reread(mine + j * 32);
+          const uint4 v = reread(at, j);
           LpVec<T>::larger(run, v);
 #pragma unroll
           for (int q = 0; q < PER / 2; ++q) {
@@ -378,10 +387,11 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
           move_to(lp_scaled(bm, A.c));
         }
         if (bm > down) {                                     // some may come before the token
+          typename LpVec<T>::Count some = LpVec<T>::lim(0.f);
+          const typename LpVec<T>::Lim lu = LpVec<T>::lim(up), ld = LpVec<T>::lim(down);
 #pragma unroll
-          for (int j = 0; j < U; ++j) {
-            ahead += LpVec<T>::count(reread(mine + j * 32), first + 32 * j < tvec ? down : up);
-          }
+          for (int j = 0; j < U; ++j) LpVec<T>::count(some, reread(at, j), first + 32 * j < tvec ? ld : lu);
+          ahead += LpVec<T>::total(some);
         }
         if (low) {
 #pragma unroll 1
