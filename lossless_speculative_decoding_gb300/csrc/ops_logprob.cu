@@ -196,6 +196,15 @@ __device__ __forceinline__ K warp_merge(K a, K b) {
   return k;
 }
 
+// The best 32 of eight of them, as a tree: three merges' latency.
+__device__ __forceinline__ u64 warp_merge8(u64 (&k)[8]) {
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < 8; i += 2 * d) k[i] = warp_merge(k[i], k[i + d]);
+  return k[0];
+}
+
 // c x of a logit that may be masked or lie at the type's end: finite, so that a
 // row of the type's lowest values stays a row of equal ones.
 __device__ __forceinline__ float lp_scaled(float x, float c) { return fminf(fmaxf(x * c, -1e30f), 1e30f); }
@@ -530,10 +539,11 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
     };
     bar_sync(1 + half, LP_ALL);
     gather([&](int i) { return sh.stats[half][i]; }, LP_WARPS);
+    u64 k[LP_WARPS];
     if (n > 0) {
-      list = sh.list[half][0][lane];
-#pragma unroll 1
-      for (int i = 1; i < LP_WARPS; ++i) list = warp_merge(list, sh.list[half][i][lane]);
+#pragma unroll
+      for (int i = 0; i < LP_WARPS; ++i) k[i] = sh.list[half][i][lane];
+      list = warp_merge8(k);
     }
     __syncwarp();
     bar_arrive(3 + half, LP_ALL);
@@ -553,18 +563,20 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       if (!__shfl_sync(0xffffffffu, last, 0)) continue;
       __threadfence();
       if (lane == 0) A.arrived[b0] = 0;
+      auto fetch = [&](int b) {                            // eight lists' loads in flight
+#pragma unroll
+        for (int i = 0; i < LP_WARPS; ++i) k[i] = b + i <= b1 ? __ldcg(A.lists + slot(b + i) * 32 + lane) : 0;
+      };
+      if (n > 0) fetch(b0);
       gather([&](int i) {
         const LpStats* q = A.stats + slot(b0 + i);
         return LpStats{__ldcg(&q->r), __ldcg(&q->z), __ldcg(&q->zy), __ldcg(&q->before), __ldcg(&q->bad)};
       }, b1 - b0 + 1);
       if (n > 0) {
-        list = 0;
-        for (int b = b0; b <= b1; b += 4) {                // four loads in flight
-          u64 k[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) k[i] = b + i <= b1 ? __ldcg(A.lists + slot(b + i) * 32 + lane) : 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) list = warp_merge(list, k[i]);
+        list = warp_merge8(k);
+        for (int b = b0 + LP_WARPS; b <= b1; b += LP_WARPS) {
+          fetch(b);
+          list = warp_merge(list, warp_merge8(k));
         }
       }
     }
