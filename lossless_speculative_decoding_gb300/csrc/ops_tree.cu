@@ -8,8 +8,8 @@
 // (sequence, kv head, row tile) reads its keys once for all of its rows.
 //
 // Work split. Units of tile_k keys are numbered sequence by sequence, row tile
-// by row tile, kv head by kv head; block c of G takes units [c U / G, (c + 1)
-// U / G) of all U. The blocks stay equally busy whatever the lengths, at most
+// by row tile, kv head by kv head; block c of B takes units [c U / B, (c + 1)
+// U / B) of all U. The blocks stay equally busy whatever the lengths, at most
 // two of a block's (sequence, tile, head) segments are shared with other
 // blocks, and everything follows from lengths that stay on the device. One
 // pass over a segment's keys keeps a running maximum, sum and output (scores
@@ -172,8 +172,11 @@ __device__ __forceinline__ int parts_until(long long U, int block, int blocks, l
 }
 
 // ---------------------------------------------------------------------------
-// FMA form (f32 cache). 128 threads, 32 rows and 64 keys at a time, everything in fp32:
-// thread (ty, tx) = (t / 16, t % 16) has rows 4 ty .. 4 ty + 3, in the score
+// FMA form (f32 cache). 128 threads, 32 rows and 64 keys at a time, everything in
+// fp32 (the matrix instructions round their operands). Bound: FMA and the shared
+// memory that feeds it, 16 bytes read for each 8 FMAs; a few short sequences by
+// latency (4 of up to 200 positions, 8 nodes, 4 heads of 64: 11.8 us with the join).
+// Thread (ty, tx) = (t / 16, t % 16) has rows 4 ty .. 4 ty + 3, in the score
 // product keys tx + 16 j, in the output product dims 4 tx + 64 j. Rows of K are
 // padded by 16 bytes, so eight lanes' reads cover all banks.
 constexpr int FM_THREADS = 128;
@@ -399,10 +402,11 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
 // Bound. An MMA of 128 x 128 x 16 takes 64 cycles (measured), so a tile takes the
 // tensor cores 1,024 cycles with the hi parts alone and 1,536 with both; its 64 KB
 // take 2,800 at an SM's share of the measured copy rate. So HBM, where a tile's
-// keys are read for one row tile: 64 sequences, 10 heads, 16 nodes, 0.93 GB:
-// 168 us, 5.5 TB/s, 0.82 of the copy rate; 4 long sequences, 8 kv heads, 84 rows
-// each: 74 us, 0.71. With 256 rows a sequence and head (8 sequences of 64 nodes,
-// 32 query heads) the chain S, softmax, P V of a slot: 2,400 cycles a tile, 56 us.
+// keys are read for one row tile: 64 sequences of 336 to 5,236 positions and 17 to
+// 32 nodes, 10 heads, 0.93 GB: 168 us with the join, 5.5 TB/s, 0.82 of the copy
+// rate; two of up to 65,521 positions, 21 nodes, 32 on 8 heads: 74 us, 0.71. With
+// two row tiles (8 sequences of 64 nodes, 32 on 8 heads) the chain S, softmax, P V
+// of a slot: 2,400 cycles a tile, 56 us.
 // (Row tiles of 256, each slot with 128 rows of its own, read keys once for all of
 // them, but took 59.5 us there, 176 and 79 above: less room for keys, twice the
 // bytes of parts to join, more code. Scores 64 at a time: 55.7 and 168. A next
@@ -1112,7 +1116,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 // later one: M = max m_c, out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M),
 // parts in key order. One warp per row; a row's statistics and its first eight
 // parts are on their way together, so that the launch is two round trips to L2
-// (the description, the parts) long.
+// (the description, the parts) long: under the profiler 7 us behind the 64
+// sequences, 12 where parts of 17 MB are joined (8 sequences of 256 rows a head).
+// (Blocks of one launch that wait for one another would need flags that somebody
+// has cleared, and the workspace comes as it is.)
 constexpr int JOIN_WARPS = 8;
 
 template <int D, class KT>
