@@ -609,3 +609,23 @@ def test_attention_scores_that_jump(dtype, hq, nodes):
     out, err = T.attention(c, 0, q, lens, ks, parents, 0.5)
     assert err == 0
     _check(c, 0, q, lens, ks, parents, out, 0.5)
+
+
+def test_attention_of_large_values():
+    """Values of 1e35 on some positions and 1e-35 on others: weights near 2^9 times
+    them stay in range, and the sums are those of the formula."""
+    import torch
+    rng = np.random.default_rng(21)
+    lens, nodes = [700, 130], [20, 64]
+    c = T.Cache(rng, lens, nodes, dtype=T.BF16, layers=1, hkv=2, d=64, page=16, seed=2)
+    parents = np.stack([T.rand_parents(rng, k) for k in nodes])
+    for s in range(2):
+        pos = torch.arange(lens[s] + nodes[s], device="cuda")
+        size = torch.where(pos % 7 < 3, 1e35, 1e-35)[:, None, None]
+        v = (c.rows[s][:, 0, :, 1] * size).to(torch.bfloat16)
+        c.kv[c.bt[s].long()[pos // 16], 0, :, 1, pos % 16] = v
+        c.rows[s][:, 0, :, 1] = v.double()
+    q = _q(6, 2, T.N, 4, 64, T.BF16, sharp=4.0)
+    out, err = T.attention(c, 0, q, lens, nodes, parents, 0.3)
+    assert err == 0 and bool(torch.isfinite(out[0, :20].float()).all())
+    _check(c, 0, q, lens, nodes, parents, out, 0.3)
