@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
 // passes m + 8: the weights are floats, whose precision another m leaves as it is,
 // so one pass over the scores serves, and the rare step rescales O and the tile's
 // earlier weights by an exact power of two. (Weights stay below 2^8, so that large
-// values keep their range, and those that float cannot hold are below 2^-94 of the
+// values keep their range, and those that float cannot hold are below 2^-100 of the
 // largest; a row of values all below 2^-100 would lose bits of its sums. With m
 // the maximum itself and moved from 8 above it: 61 us for 57, 170 for 168.)
 //
