@@ -2,17 +2,22 @@
 // rank and the likeliest alternatives, from materialised logits, in one pass
 // over them.
 //
-// With c = log2(e) / T, R the largest logit times c (rounded; any R near it
-// serves, as long as all sums use the same) and y = c x - R: z = sum 2^y, log
+// With c = log2(e) / T, m the largest logit and y = c (x - m): z = sum 2^y, log
 // p(t) = ln 2 (y_t - log2 z), and entropy = ln 2 (log2 z - sum 2^y y / z), two
 // terms of one sign, so that nothing cancels. The order of tokens is (logit
 // descending, index ascending), NaN as -inf.
+//
+// A step's sums take y' = c x - R in one instruction, R the rounded product c m,
+// and are set right at its end by 2^-d, d = c m - R = y' - y (one more rounding
+// gives it exactly). Where |R| is above 2^24, d may be above 1 and soon as large
+// as an exponent's range (rows masked throughout by a finite value, tiny
+// temperatures): there a step takes the differences x - m themselves.
 //
 // The rows' steps of 32 KB, row after row, are cut into one even run for each
 // block that the GPU holds at once, so that a few rows use all of it and many
 // rows leave no tail. A warp takes 4 KB of a step, one ahead by a bulk copy into
 // its own shared memory, and no warp waits for another's. Within a row a thread
-// keeps a running (R, z, sum) and a count of the logits that come before the
+// keeps a running (m, z, sum) and a count of the logits that come before the
 // token; a step whose sum comes out as NaN (masked tokens, NaN logits) is added
 // again with care. Alternatives: a warp holds the best 32 of what it has seen as
 // sorted 64-bit keys (ordered logit, inverted index), one per lane. A thread's
@@ -53,7 +58,7 @@ static_assert(LP_TOP == 32, "a warp's list has one key per lane");
 
 // What a block leaves of a row it shares: statistics, and a sorted list apart.
 struct LpStats {
-  float r, z, zy;           // R, sum 2^y, sum 2^y y
+  float m, z, zy;           // largest logit, sum 2^y, sum 2^y y
   int before, bad;          // logits before the token; a NaN or +inf logit
 };
 
@@ -206,17 +211,20 @@ __device__ __forceinline__ u64 warp_merge8(u64 (&k)[8]) {
   return k[0];
 }
 
-// c x of a logit that may be masked or lie at the type's end: finite, so that a
-// row of the type's lowest values stays a row of equal ones.
-__device__ __forceinline__ float lp_scaled(float x, float c) { return fminf(fmaxf(x * c, -1e30f), 1e30f); }
+constexpr float LP_FAR = 16777216.f;             // |c m| up to which a step's sums go by the product
 
-// (R, z, zy) += (r2, z2, zy2), either of which may hold nothing (R = -inf).
-__device__ __forceinline__ void stats_merge(float& r, float& z, float& zy, float r2, float z2, float zy2) {
-  const float rr = fmaxf(r, r2), rb = rr == -INFINITY ? 0.f : rr;
-  const float da = fmaxf(r - rb, -1e30f), db = fmaxf(r2 - rb, -1e30f), a = lp_ex2(da), b = lp_ex2(db);
+// c (x - m) of logits at the types' ends too: halves, whose difference stays in range.
+__device__ __forceinline__ float lp_diff(float x, float m, float c) { return fmaf(0.5f, x, -0.5f * m) * c * 2.f; }
+// The same with a floor below any power, for sums of 2^y y (x = -inf: masked, nothing seen).
+__device__ __forceinline__ float lp_shift(float x, float m, float c) { return fmaxf(lp_diff(x, m, c), -1e30f); }
+
+// (m, z, zy) += (m2, z2, zy2), either of which may hold nothing (m = -inf).
+__device__ __forceinline__ void stats_merge(float& m, float& z, float& zy, float m2, float z2, float zy2, float c) {
+  const float mm = fmaxf(m, m2), mb = mm == -INFINITY ? 0.f : mm;
+  const float da = lp_shift(m, mb, c), db = lp_shift(m2, mb, c), a = lp_ex2(da), b = lp_ex2(db);
   zy = fmaf(z, da, zy) * a + fmaf(z2, db, zy2) * b;
   z = z * a + z2 * b;
-  r = rr;
+  m = mm;
 }
 
 struct LpShared {
@@ -318,7 +326,9 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
     const int tvec = have ? (tok + skip) / PER : -1;
     const bool low = have && key_t == -INFINITY;           // ties with NaN and -inf: compared one by one
     const float up = have && !low ? key_t : INFINITY, down = have && !low ? LpVec<T>::below(key_t) : INFINITY;
-    float R = -INFINITY, mk = -INFINITY;                   // c times the largest logit; the largest
+    float m = -INFINITY;                                   // the largest logit
+    float R = 0.f, d = 0.f, fix = 1.f;                     // c m rounded, what that leaves of it, 2^-d
+    bool far = false;                                      // |R| above LP_FAR: sums by differences, d = 0
     float z = 0.f, zy = 0.f, ahead = 0.f;
     int before = 0, pending = 0;
     bool bad = lost;
@@ -343,20 +353,23 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       }
       float bm = -INFINITY;
       if ((st * LP_TILE + w * 32 * U) * PER - skip < V) {  // (the last step may end before the warp's part of it)
-        auto move_to = [&](float to) {                       // another R
-          const float d = fmaxf(R - to, -1e30f), f = lp_ex2(d);
-          zy = fmaf(z, d, zy) * f;
+        auto move_to = [&](float to) {                       // another m
+          const float by = lp_shift(m, to, A.c), f = lp_ex2(by);
+          zy = fmaf(z, by, zy) * f;
           z *= f;
-          R = to;
+          m = to;
+          R = A.c * to;
+          far = !(fabsf(R) <= LP_FAR);
+          d = far ? 0.f : fmaf(A.c, to, -R);
+          fix = lp_ex2(-d);
         };
         typename LpVec<T>::Max run = LpVec<T>::none();
-        if (R == -INFINITY) {                                // nothing seen yet: the step's own maximum first
+        if (m == -INFINITY) {                                // nothing seen yet: the step's own maximum first
 #pragma unroll
           for (int j = 0; j < U; ++j) LpVec<T>::larger(run, reread(at, j));
           bm = LpVec<T>::value(run);
-          if (bm > -INFINITY) R = lp_scaled(bm, A.c);
+          if (bm > -INFINITY) move_to(bm);
         }
-        const float rb = R == -INFINITY ? 0.f : R;
         float z0 = 0.f, z1 = 0.f, zy0 = 0.f, zy1 = 0.f;      // (the step's own sums: two chains each)
 #pragma unroll
         for (int j = 0; j < U; ++j) {
@@ -365,7 +378,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
 #pragma unroll
           for (int q = 0; q < PER / 2; ++q) {
             const float2 x = LpVec<T>::at(v, q);
-            const float ya = fmaf(x.x, A.c, -rb), yb = fmaf(x.y, A.c, -rb), pa = lp_ex2(ya), pb = lp_ex2(yb);
+            const float ya = fmaf(x.x, A.c, -R), yb = fmaf(x.y, A.c, -R), pa = lp_ex2(ya), pb = lp_ex2(yb);
             z0 += pa;
             z1 += pb;
             zy0 = fmaf(pa, ya, zy0);
@@ -377,25 +390,23 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
         z0 += z1;
         // masked tokens (0 times -inf), NaN, values at the type's ends, or a
         // logit so far above all before that its power is infinite
-        if (!(fabsf(zy0) < INFINITY) || fabsf(rb) > 1e29f) {
-          if (bm > mk) move_to(lp_scaled(bm, A.c));
-          const float rc = R == -INFINITY ? 0.f : R;
+        if (!(fabsf(zy0) < INFINITY) || far) {
+          if (bm > m) move_to(bm);
+          const float mb = m == -INFINITY ? 0.f : m;
           z0 = zy0 = 0.f;
 #pragma unroll 4
           for (int e = 0; e < STEP; ++e) {
-            const float x = logit<T>(reinterpret_cast<const T*>(mine + e / PER * 32), e % PER), y = lp_scaled(x, A.c) - rc;
-            const float p = x > -INFINITY ? lp_ex2(y) : 0.f;
+            const float x = logit<T>(reinterpret_cast<const T*>(mine + e / PER * 32), e % PER);
+            // (a difference that passes fp32's range is as far below zero in c (x - m), m being far)
+            const float y = fmaxf(far ? (x - mb) * A.c : fmaf(x, A.c, -R), -1e30f), p = lp_ex2(y);
             bad = bad || !(x < INFINITY);
             z0 += p;
             zy0 = fmaf(p, y, zy0);
           }
         }
-        z += z0;
-        zy += zy0;
-        if (bm > mk) {                                       // R follows the maximum, so that the entropy's terms keep one sign
-          mk = bm;
-          move_to(lp_scaled(bm, A.c));
-        }
+        z = fmaf(z0, fix, z);
+        zy = fmaf(fmaf(-d, z0, zy0), fix, zy);
+        if (bm > m) move_to(bm);                             // m follows the maximum, so that the entropy's terms keep one sign
         if (bm > down) {                                     // some may come before the token
           typename LpVec<T>::Count some = LpVec<T>::lim(0.f);
           const typename LpVec<T>::Lim lu = LpVec<T>::lim(up), ld = LpVec<T>::lim(down);
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       // of 1,100 rows: 92 us with it, 89 without).
       const int done = st - s0 + 1;
       if ((done & (done - 1)) == 0 && (done & 0x55555555)) {
-        uint32_t k = ordered(mk);
+        uint32_t k = ordered(m);
 #pragma unroll
         for (int i = 0; i < 32 / LP_WARPS; ++i) {
           const uint32_t mx = __reduce_max_sync(0xffffffffu, k);
@@ -435,7 +446,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
         const u64 known = *reinterpret_cast<volatile u64*>(&sh.top[lane]);
         const uint32_t mine_or_none = (uint32_t)(known >> 32) == (uint32_t)(rows + 1) ? (uint32_t)known : 0u;
         uint32_t b = n == 1 ? __reduce_max_sync(0xffffffffu, mine_or_none) : __shfl_sync(0xffffffffu, warp_sort(mine_or_none), n - 1);
-        if (b == 0) b = __shfl_sync(0xffffffffu, warp_sort(ordered(mk)), n - 1);
+        if (b == 0) b = __shfl_sync(0xffffffffu, warp_sort(ordered(m)), n - 1);
         bound = bound > b ? bound : b;
       }
       const bool cand = ordered(bm) >= bound;
@@ -481,13 +492,13 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
     bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const float ro = __shfl_xor_sync(0xffffffffu, R, o), zo = __shfl_xor_sync(0xffffffffu, z, o),
+      const float mo = __shfl_xor_sync(0xffffffffu, m, o), zo = __shfl_xor_sync(0xffffffffu, z, o),
                   zyo = __shfl_xor_sync(0xffffffffu, zy, o);
-      stats_merge(R, z, zy, ro, zo, zyo);
+      stats_merge(m, z, zy, mo, zo, zyo, A.c);
     }
     const int half = rows & 1;                             // the next row takes the other one
     if (rows >= 2) bar_sync(3 + half, LP_ALL);
-    if (lane == 0) sh.stats[half][w] = LpStats{R, z, zy, before, bad};
+    if (lane == 0) sh.stats[half][w] = LpStats{m, z, zy, before, bad};
     if (n > 0) sh.list[half][w][lane] = list;
     bar_arrive(1 + half, LP_ALL);
   }
@@ -515,12 +526,12 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       const int v0 = max(0, (tok + skip) / PER * PER - skip);
       ties = __popc(__ballot_sync(0xffffffffu, v0 + lane < tok && am_key(logit<T>(row, v0 + lane)) == key_t));
     }
-    float R, z, zy;
+    float m, z, zy;
     bool bad;
     u64 list = 0;
     // `parts` statistics, in lanes 0 .. (at most 32 at a time), in a fixed tree
     auto gather = [&](auto&& of, int parts) {
-      R = -INFINITY;
+      m = -INFINITY;
       z = zy = 0.f;
       before = 0;
       bad = false;
@@ -529,11 +540,11 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
         if (p0 + lane < parts) q = of(p0 + lane);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-          const float ro = __shfl_xor_sync(0xffffffffu, q.r, o), zo = __shfl_xor_sync(0xffffffffu, q.z, o),
+          const float mo = __shfl_xor_sync(0xffffffffu, q.m, o), zo = __shfl_xor_sync(0xffffffffu, q.z, o),
                       zyo = __shfl_xor_sync(0xffffffffu, q.zy, o);
-          stats_merge(q.r, q.z, q.zy, ro, zo, zyo);
+          stats_merge(q.m, q.z, q.zy, mo, zo, zyo, A.c);
         }
-        stats_merge(R, z, zy, q.r, q.z, q.zy);
+        stats_merge(m, z, zy, q.m, q.z, q.zy, A.c);
         before += __reduce_add_sync(0xffffffffu, q.before);
         bad = bad || __any_sync(0xffffffffu, q.bad != 0);
       }
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       auto slot = [&](int b) { return (size_t)b * 2 + (b == b0 ? 1 : 0); };
       const size_t mine = slot(blockIdx.x);
       if (n > 0) A.lists[mine * 32 + lane] = list;
-      if (lane == 0) A.stats[mine] = LpStats{R, z, zy, before, bad};
+      if (lane == 0) A.stats[mine] = LpStats{m, z, zy, before, bad};
       __threadfence();
       __syncwarp();
       int last = 0;
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       if (n > 0) fetch(b0);
       gather([&](int i) {
         const LpStats* q = A.stats + slot(b0 + i);
-        return LpStats{__ldcg(&q->r), __ldcg(&q->z), __ldcg(&q->zy), __ldcg(&q->before), __ldcg(&q->bad)};
+        return LpStats{__ldcg(&q->m), __ldcg(&q->z), __ldcg(&q->zy), __ldcg(&q->before), __ldcg(&q->bad)};
       }, b1 - b0 + 1);
       if (n > 0) {
         list = warp_merge8(k);
@@ -581,11 +592,11 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
         }
       }
     }
-    const bool none = bad || R == -INFINITY;
+    const bool none = bad || m == -INFINITY;
     const float lz = none ? nan : log2f(z);
-    auto logp = [&](float x) {
-      const float y = fmaf(x, A.c, -R);
-      return y > -1e30f ? (y - lz) * LN2 : fmaf(x, A.it, -(R + lz) * LN2);
+    auto logp = [&](float x) {                             // (in natural units where those of base 2 may pass fp32's range)
+      const float y = lp_diff(x, m, A.c);
+      return y > -1e30f ? (y - lz) * LN2 : fmaf(-LN2, lz, lp_diff(x, m, A.it));
     };
     if (lane == 0) {
       if (A.logprob) A.logprob[r] = have ? logp(raw_t) : nan;
