@@ -484,9 +484,11 @@ typedef struct spec_kv_view {
  *     aligned; needs no initialisation; one call at a time per workspace.
  * Scores, softmax statistics and sums are fp32; bf16 results are rounded once.
  * Slots past n + n_nodes[s] may hold anything. Every slot up to there has to
- * hold finite keys and values (a NaN of one node may reach the others). The
- * same call gives the same bits; where a sequence's keys are cut into parts
- * summed apart depends on the batch. A sequence with a bad length is left
+ * hold finite keys and values (a NaN of one node may reach the others). Scores
+ * of any size are taken (q.K and scale * q.K below 2^126), told apart as far as
+ * the rounding of fp32 sums of their size goes. The same call gives the same
+ * bits; where a sequence's keys are cut into parts summed apart depends on the
+ * batch. A sequence with a bad length is left
  * out (SPEC_DEV_ERR_POS); rows that need a bad page hold no usable value
  * (SPEC_DEV_ERR_PAGE); a node with a bad parent counts as a root
  * (SPEC_DEV_ERR_TREE). Errors: SPEC_ERR_ARG; SPEC_ERR_UNSUPPORTED (head_dim,

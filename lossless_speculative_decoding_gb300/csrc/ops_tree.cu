@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_view.cuh"
 
@@ -393,6 +394,13 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
 // values keep their range, and those that float cannot hold are below 2^-100 of the
 // largest; a row of values all below 2^-100 would lose bits of its sums. With m
 // the maximum itself and moved from 8 above it: 61 us for 57, 170 for 168.)
+// Above 2^24 float does not hold every whole number, and a rounded m is soon off by
+// more than an exponent's range. A warp that meets such a score takes its chunks
+// from there on through a second copy of the loop, out of line, in which such a
+// lane subtracts its largest score, s0, from all of them. (The test in the one loop:
+// 58 us for 56, 170 for 166; the second copy in line: 57.5.) What lanes, slots and
+// blocks are joined by is s0 in units of m, rounded: equal largest scores stay
+// equal, others are told apart as far as the rounding of a score of their size.
 //
 // The two softmax groups have a buffer for S and an accumulator for O ("slot")
 // each, take the segment's tiles in turn, so that one's exponentials run beside
@@ -422,6 +430,7 @@ constexpr int TT_THREADS = 352;
 constexpr int TT_HALF = 128 * 128;               // bytes of 64 dims of 128 rows of Q
 constexpr int TT_OCOL = 256;                     // TMEM columns: S of a slot at 128 slot, its O behind at TT_OCOL + D slot
 constexpr float TT_GROW = 8.f, TT_AHEAD = 24.f;  // m moves when a score passes m + 8, to that score + 24
+constexpr float TT_FAR = 16777216.f;             // scores up to here go by m alone
 constexpr int TT_STAGE = 2 * 128 * 64;           // staged output: two groups x 128 lanes x 16 columns
 
 template <int D>
@@ -625,6 +634,116 @@ struct TtRows {
     kparts = lie <= 32 ? 2 : 1;
   }
 };
+
+// A lane's row of a segment so far: weights are 2^(sc (S - s0) - m), l their sum. s0
+// is 0, or the largest score (m = TT_AHEAD).
+struct TtLane {
+  float m, l, s0;
+};
+// Its scores of a tile.
+struct TtTile {
+  uint32_t s, o;               // tensor memory of S and O
+  unsigned long long mask;     // tree slots it may see
+  int slot0, c0;               // tree slot of the tile's first key; the lane's first chunk
+  float sc;                    // scale * log2 e
+  bool first, live, low, hl;   // no O yet; a row; the lo parts' lane; lo parts on lanes of their own
+};
+
+// Chunks c .. c1 - 1 of 32 keys: weights in the place of scores. Without WIDE it
+// stops at a chunk with a score beyond TT_FAR, which is as it was; returns the
+// chunk it ended before.
+template <int D, bool WIDE>
+__device__ __forceinline__ int tt_chunks(const TtTile& T, int c, int c1, TtLane& a) {
+  const unsigned long long sc2 = pair(T.sc, T.sc);
+#pragma unroll 1
+  for (; c < c1; ++c) {
+    uint32_t v[32];
+    tmem_ld32(T.s + 32 * c, v);
+    const int sh = T.slot0 + 32 * c;             // tree slot of the chunk's first key
+    if (sh > -32) {                              // tree slots, or slots past the last
+      uint32_t bits = 0u;
+      if (sh < 0) bits = (uint32_t)(T.mask << -sh) | ((1u << -sh) - 1);
+      else if (sh < TREE_N) bits = (uint32_t)(T.mask >> sh);
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (!((bits >> i) & 1)) v[i] = 0xff800000u;
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], __uint_as_float(v[i + 2 * u]), __uint_as_float(v[i + 2 * u + 1]));
+    const float mv = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), mt = (WIDE ? mv - a.s0 : mv) * T.sc;
+    const bool grow = T.live && (WIDE && a.s0 != 0.f ? mv > a.s0 : mt > a.m + TT_GROW);
+    if (__any_sync(0xffffffffu, grow)) {
+      // a larger score: the lane's weights and sums so far are of another m
+      const bool away = grow && (WIDE && a.s0 != 0.f || !(fabsf(mt) <= TT_FAR));
+      if (!WIDE && __any_sync(0xffffffffu, away)) return c;
+      float corr = 1.f;
+      if (WIDE && away) {                        // (the score itself, so that equal ones differ by 0)
+        corr = ex2(a.m - mt - TT_AHEAD);
+        a.m = TT_AHEAD;
+        a.s0 = mv;
+      } else if (grow) {
+        const float to = ceilf(mt) + TT_AHEAD, by = to - a.m;
+        corr = by < 127.f ? __uint_as_float((127 - (int)by) << 23) : 0.f;    // 2^-by, exact
+        a.m = to;
+      }
+      a.l *= corr;
+      tmem_wait_st();                            // the chunks' weights are read back
+      if (!T.first) {                            // (S of this tile came after the slot's last P V)
+#pragma unroll 1
+        for (int i = 0; i < D; i += 16) {
+          uint32_t o[16];
+          tmem_ld16(T.o + i, o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+          tmem_st16(T.o + i, o);
+        }
+      }
+#pragma unroll 1
+      for (int i = 32 * T.c0; i < 32 * c; i += 16) {
+        uint32_t w[16];
+        tmem_ld16(T.s + i, w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          w[j] = pack_bf16(__uint_as_float(w[j] << 16) * corr, __uint_as_float(w[j] & 0xFFFF0000u) * corr);
+        tmem_st16(T.s + i, w);
+      }
+    }
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) - a.s0);
+    }
+    const float mb = a.m == -INFINITY ? 0.f : a.m;
+    const unsigned long long nm2 = pair(-mb, -mb);
+    unsigned long long sum[2] = {0, 0};
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 y = halves(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2));
+      const float p0 = ex2(y.x), p1 = ex2(y.y);
+      const unsigned long long p2 = pair(p0, p1);
+      sum[i / 2 & 1] = add2(sum[i / 2 & 1], p2);
+      const uint32_t hi = pack_bf16(p0, p1);
+      const float2 e = halves(add2(p2, pair(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xFFFF0000u))));
+      const uint32_t lo = pack_bf16(e.x, e.y);
+      w[i / 2] = T.low ? lo : hi;
+      w[16 + i / 2] = lo;
+    }
+    if (T.hl) tmem_st16(T.s + 32 * c, w);
+    else tmem_st32(T.s + 32 * c, w);
+    const float2 s2 = halves(add2(sum[0], sum[1]));
+    a.l += s2.x + s2.y;
+  }
+  return c;
+}
+// Out of line: rare, and the loops around it are better without it.
+template <int D>
+__device__ __noinline__ TtLane tt_chunks_wide(TtTile T, int c, int c1, TtLane a) {
+  tt_chunks<D, true>(T, c, c1, a);
+  return a;
+}
 
 template <int D>
 __global__ void __launch_bounds__(TT_THREADS, 1)
@@ -889,7 +1008,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     const int slot = warp >> 2, r = t & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t oT = tmem + lanes + TT_OCOL + slot * D;
-    const unsigned long long sc2 = pair(A.scale_l2e, A.scale_l2e);
     uint32_t jobs = 0, tiles = 0;                // of this slot; of the block
     for (uint32_t seg = 0;; ++seg) {
       const int sb = seg & 1;
@@ -909,7 +1027,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         wait(H.mask_full + sb, seg >> 1);
         if (live) mask = H.mask[sb][(R.row0 + lr) / A.G];
       }
-      float m = -INFINITY, l = 0.f;
+      TtLane st{-INFINITY, 0.f, 0.f};
+      bool far = false;                          // a lane of the warp has met a score beyond TT_FAR
       for (int ti = slot; ti < nt; ti += 2) {
         const int k0 = (g.t0 + ti) * TT_KEYS;
         const bool first = ti < 2;
@@ -919,82 +1038,11 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         if (any_live) {
           // this lane's chunks of 32 keys: all four, or a key part's two
           const int c0 = 2 * kpart, c1 = R.kparts == 2 ? c0 + 2 : 4;
-          const bool edge = k0 + TT_KEYS > g.n;  // tree slots, or slots past the last
-          auto chunk = [&](int c, uint32_t (&v)[32]) {
-            tmem_ld32(sT + 32 * c, v);
-            if (edge) {
-              const int sh = k0 + 32 * c - g.n;  // tree slot of the chunk's first key
-              uint32_t bits = 0u;
-              if (sh <= -32) bits = 0xffffffffu;
-              else if (sh < 0) bits = (uint32_t)(mask << -sh) | ((1u << -sh) - 1);
-              else if (sh < TREE_N) bits = (uint32_t)(mask >> sh);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((bits >> i) & 1)) v[i] = 0xff800000u;
-            }
-          };
-          // A larger score at chunk c: the lane's weights so far are of another m.
-          auto rescale = [&](int c, float mt, bool grow) {
-            float corr = 1.f;
-            tmem_wait_st();                      // the chunks' weights are read back
-            if (grow) {
-              const float to = ceilf(mt) + TT_AHEAD, by = to - m;
-              corr = by < 127.f ? __uint_as_float((127 - (int)by) << 23) : 0.f;    // 2^-by, exact
-              m = to;
-              l *= corr;
-            }
-            if (!first) {                        // (S of this tile came after the slot's last P V)
-#pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
-                uint32_t o[16];
-                tmem_ld16(oT + i, o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-                tmem_st16(oT + i, o);
-              }
-            }
-#pragma unroll 1
-            for (int i = 32 * c0; i < 32 * c; i += 16) {
-              uint32_t w[16];
-              tmem_ld16(sT + i, w);
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                w[j] = pack_bf16(__uint_as_float(w[j] << 16) * corr, __uint_as_float(w[j] & 0xFFFF0000u) * corr);
-              tmem_st16(sT + i, w);
-            }
-          };
-#pragma unroll 1
-          for (int c = c0; c < c1; ++c) {
-            uint32_t v[32];
-            chunk(c, v);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) mx[u] = max3(mx[u], __uint_as_float(v[i + 2 * u]), __uint_as_float(v[i + 2 * u + 1]));
-            const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * A.scale_l2e;
-            const bool grow = live && mt > m + TT_GROW;
-            if (__any_sync(0xffffffffu, grow)) rescale(c, mt, grow);
-            const float mb = m == -INFINITY ? 0.f : m;
-            const unsigned long long nm2 = pair(-mb, -mb);
-            unsigned long long sum[2] = {0, 0};
-            uint32_t w[32];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 y = halves(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2));
-              const float p0 = ex2(y.x), p1 = ex2(y.y);
-              const unsigned long long p2 = pair(p0, p1);
-              sum[i / 2 & 1] = add2(sum[i / 2 & 1], p2);
-              const uint32_t hi = pack_bf16(p0, p1);
-              const float2 e = halves(add2(p2, pair(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xFFFF0000u))));
-              const uint32_t lo = pack_bf16(e.x, e.y);
-              w[i / 2] = low ? lo : hi;
-              w[16 + i / 2] = lo;
-            }
-            if (R.hl) tmem_st16(sT + 32 * c, w);
-            else tmem_st32(sT + 32 * c, w);
-            const float2 s2 = halves(add2(sum[0], sum[1]));
-            l += s2.x + s2.y;
+          const TtTile T{sT, oT, mask, k0 - g.n, c0, A.scale_l2e, first, live, low, R.hl};
+          const int c = far ? c0 : tt_chunks<D, false>(T, c0, c1, st);
+          if (c < c1) {
+            far = true;
+            st = tt_chunks_wide<D>(T, c, c1, st);
           }
           if (R.kparts == 2) {                   // the other part's keys: weights 0
             uint32_t x[32];
@@ -1040,7 +1088,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       // each group waits for its own slot's last P V; the barriers pass that on
       if (slot < nt) wait(H.o_done + slot, jobs - 1);
       const bool both = nt > 1;                  // slot 1 had tiles
-      H.ml[slot][r] = make_float2(live ? m : -INFINITY, live ? l : 0.f);
+      const float ref = fmaf(st.s0, A.scale_l2e, st.m);      // (finite, whatever the scores)
+      H.ml[slot][r] = make_float2(live ? fminf(fmaxf(ref, -3e38f), 3e38f) : -INFINITY, live ? st.l : 0.f);
       tc_fence_before();
       named_sync(1, 256);
       tc_fence_after();

@@ -1,0 +1,71 @@
+"""Tree entry points on inputs that they take and that lie at their edges."""
+import numpy as np
+import pytest
+
+import _tree as T
+from test_gpu_tree import HALF
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- scores of large magnitude --------------------------------------------------
+def _far_cache(rng, lens, nodes, dtype, hkv, d, keys):
+    """A cache whose keys are keys[s][position] along dim 0 and zero elsewhere."""
+    import torch
+    c = T.Cache(rng, lens, nodes, dtype=dtype, layers=1, hkv=hkv, d=d, page=16)
+    for s, k in enumerate(keys):
+        pos = torch.arange(lens[s] + nodes[s], device="cuda")
+        pg = c.bt[s].long()[pos // 16]
+        row = torch.zeros((len(k), 1, d), device="cuda")
+        row[:, 0, 0] = torch.from_numpy(np.asarray(k, np.float32)).cuda()
+        row = row.expand(-1, hkv, -1).to(c.kv.dtype)
+        c.kv[pg, 0, :, 0, pos % 16] = row
+        c.rows[s][:, 0, :, 0] = row.double()
+    return c
+
+
+def _far_check(c, lens, nodes, parents, G, amps, scale):
+    """Queries amps[h % len(amps)] along dim 0, so that heads (lanes of a warp) have scores of different sizes."""
+    import torch
+    hkv, d = c.hkv, c.d
+    q = torch.zeros((len(lens), T.N, hkv * G, d), device="cuda")
+    for h in range(hkv * G):
+        q[:, :, h, 0] = amps[h % len(amps)]
+    q = q.to(c.kv.dtype)
+    out, err = T.attention(c, 0, q, lens, nodes, parents, scale)
+    assert err == 0
+    for s, (n, k) in enumerate(zip(lens, nodes)):
+        ref, _ = T.ref_attention(c.rows[s], 0, q[s], n, k, parents[s], scale)
+        # products of one term are exact, and so are differences of the scores here: no error of the scores' size
+        tol = T.tol(d, n + k, 0.0, float(c.rows[s][:, 0, :, 1].abs().max()))
+        err = (out[s, :k].double() - ref).abs()
+        assert bool((err <= HALF[c.dtype] * ref.abs() + tol).all()), (s, n, k, float(err.nan_to_num(9e9).max()))
+
+
+@pytest.mark.parametrize("dtype", [T.F32, T.BF16])
+@pytest.mark.parametrize("G,nodes", [(1, 12), (2, 28), (3, 40), (8, 64)])
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 24, 2.0 ** 28, 2.0 ** 31, 2.0 ** 34, 2.0 ** 60, 2.0 ** 120])
+def test_attention_of_equal_scores_of_any_size(dtype, G, nodes, size):
+    """All keys alike: every row is the mean of its values, whatever the scores' size and sign."""
+    rng = np.random.default_rng(nodes)
+    lens, ks = [0, 200, 1500], [nodes, nodes, max(1, nodes - 3)]
+    parents = np.stack([T.rand_parents(rng, k) for k in ks])
+    c = _far_cache(rng, lens, ks, dtype, 2, 64, [np.full(n + k, 1.37 * size ** 0.5) for n, k in zip(lens, ks)])
+    a = 1.21 * size ** 0.5                                     # (powers of two would have exact products)
+    _far_check(c, lens, ks, parents, G, [a, -a, 1.0 / a, 0.0, -1.0 / a, a / 64], 1.0)
+
+
+@pytest.mark.parametrize("dtype", [T.F32, T.BF16])
+@pytest.mark.parametrize("G,nodes", [(1, 12), (2, 28), (3, 40), (8, 64)])
+@pytest.mark.parametrize("size", [2.0 ** 26, 2.0 ** 31, 2.0 ** 33, 2.0 ** 60, 2.0 ** 120])
+def test_attention_of_scores_far_apart(dtype, G, nodes, size):
+    """Keys in steps of 1/128 of a large value, up along one sequence, down along
+    another, and of both signs in a third: the largest take the whole weight."""
+    rng = np.random.default_rng(nodes + 1)
+    lens, ks = [900, 900, 700], [nodes, nodes, nodes]
+    parents = np.stack([T.rand_parents(rng, k) for k in ks])
+    a = size ** 0.5
+    ramp = np.floor(np.arange(900 + nodes) / 60) / 128
+    keys = [a * (1 + ramp), a * (1 + ramp[::-1]), a * np.where(np.arange(700 + nodes) % 97 == 5, -1.0, 1.0)]
+    c = _far_cache(rng, lens, ks, dtype, 2, 64, keys)
+    _far_check(c, lens, ks, parents, G, [a, -a, 0.0, 1.0 / a, a], 1.0)
