@@ -513,8 +513,9 @@ int spec_tree_attention(const spec_kv_view* kv, int layer, const void* q_dev, in
  *   appended; out_path_dev [n_seq][max_nodes]: path_0 .. path_a, then -1;
  *   out_len_dev [n_seq]: n + a + 1 (not cache_len_dev itself, SPEC_ERR_ARG:
  *   other blocks of the call still read n; swap the two after a step).
- * A padded sequence (n_nodes 0), one with a bad length or one whose rows
- * need a bad page is not moved and gives a = -1, token -1, no path, and n.
+ * A padded sequence (n_nodes 0), one with a bad length or one with a bad page
+ * under a row of its path, whether that row moves or not, is not moved and
+ * gives a = -1, token -1, no path, and n.
  * A sequence whose pages are shared with others has to own the pages it
  * writes. Errors: SPEC_ERR_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA. */
 int spec_tree_commit(const spec_kv_view* kv, int n_seq, int max_nodes, const int32_t* tokens_dev,

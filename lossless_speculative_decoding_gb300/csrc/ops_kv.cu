@@ -50,19 +50,19 @@ __device__ void walk_tree(const spec_kv_view& kv, int n, int k, CommitShared& sh
     if (lane == 0) sh.path[a] = cur;
   }
   __syncwarp();
-  // the moves: rows whose slot changes, in path order
+  // the moves: rows whose slot changes, in path order; the path's other rows need their pages as well
   const int esz = kv.dtype == SPEC_F32 ? 4 : 2;
   const long long row16 = kv.head_dim * esz / 16, page16 = (long long)kv.n_layers * kv.n_kv_heads * 2 * kv.page_size * row16;
   int moves = 0;
   bool fine = true;
   for (int j0 = 0; j0 <= a; j0 += 32) {
     const int j = j0 + lane;
-    const bool mv = j <= a && sh.path[j] != j;
+    const bool on = j <= a, mv = on && sh.path[j] != j;
     const uint32_t who = __ballot_sync(0xffffffffu, mv);
+    const int gs = on ? sh.page[sh.path[j]] : 0, gd = on ? sh.page[j] : 0;
+    fine = fine && gs >= 0 && gs < kv.n_pages && gd >= 0 && gd < kv.n_pages;
     if (mv) {
       const int ps = n + sh.path[j], pd = n + j;
-      const int gs = sh.page[sh.path[j]], gd = sh.page[j];
-      fine = fine && gs >= 0 && gs < kv.n_pages && gd >= 0 && gd < kv.n_pages;
       const int at = moves + __popc(who & ((1u << lane) - 1));
       sh.src[at] = gs * page16 + (ps % kv.page_size) * row16;
       sh.dst[at] = gd * page16 + (pd % kv.page_size) * row16;

@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 import _tree as T
-from test_gpu_tree import HALF
+from test_gpu_tree import HALF, _commit
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +69,31 @@ def test_attention_of_scores_far_apart(dtype, G, nodes, size):
     keys = [a * (1 + ramp), a * (1 + ramp[::-1]), a * np.where(np.arange(700 + nodes) % 97 == 5, -1.0, 1.0)]
     c = _far_cache(rng, lens, ks, dtype, 2, 64, keys)
     _far_check(c, lens, ks, parents, G, [a, -a, 0.0, 1.0 / a, a], 1.0)
+
+
+# ---- pages of a committed path --------------------------------------------------
+@pytest.mark.parametrize("bad", [-1, 10 ** 6])
+def test_commit_needs_the_pages_of_rows_that_stay(bad):
+    """A path whose rows already lie in place needs its pages as much as one that moves."""
+    import torch
+    rng = np.random.default_rng(5)
+    lens, k = [14, 14, 30, 31], 6
+    c = T.Cache(rng, lens, [k] * 4, dtype=T.BF16, layers=2, hkv=2, d=64, page=16, junk=1.0)
+    parents = np.tile(np.append(np.arange(-1, k - 1), [-1] * (T.N - k)).astype(np.int32), (4, 1))
+    tokens = np.tile(np.arange(T.N, dtype=np.int32), (4, 1))
+    target = tokens + 1                                        # a chain, accepted in full: no row moves
+    target[3, 0] = 99                                          # the root alone
+    c.bt[1, 1] = bad                                           # positions 16 .. 31: nodes 2 and later
+    c.bt[2, 2] = bad                                           # positions 32 .. 47: nodes 2 and later
+    before = c.kv.clone()
+    acc, tok, ln, path, err = _commit(c, tokens, parents, target, lens, [k] * 4)
+    assert err == 1
+    assert acc.tolist() == [k - 1, -1, -1, 0] and ln.tolist() == [14 + k, 14, 30, 32]
+    assert tok.tolist() == [k, -1, -1, 99] and (path[1:3] == -1).all() and path[3, :2].tolist() == [0, -1]
+    c.bt[3, 1] = bad                                           # the root's own page
+    c.bt[2, 1] = bad
+    tokens[0, 2] = 77                                          # ends at position 15: the next page is not asked for
+    c.bt[0, 1] = bad
+    acc, tok, ln, path, err = _commit(c, tokens, parents, target, lens, [k] * 4)
+    assert err == 1 and acc.tolist() == [1, -1, -1, -1] and ln.tolist() == [16, 14, 30, 31]
+    assert bool(torch.equal(c.kv, before))
