@@ -286,6 +286,8 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
           else x[q].v = e + q >= 0 && e + q < V ? row[e + q].v : 0xff80;
         }
       }
+      // before a later bulk copy into the same bytes (its issue follows a __syncwarp)
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (lane == 0) {
       const uint32_t bytes = (uint32_t)(v1 - v0) * 16;
