@@ -220,10 +220,11 @@ __device__ __forceinline__ float lp_shift(float x, float m, float c) { return fm
 
 // (m, z, zy) += (m2, z2, zy2), either of which may hold nothing (m = -inf).
 __device__ __forceinline__ void stats_merge(float& m, float& z, float& zy, float m2, float z2, float zy2, float c) {
-  const float mm = fmaxf(m, m2), mb = mm == -INFINITY ? 0.f : mm;
-  const float da = lp_shift(m, mb, c), db = lp_shift(m2, mb, c), a = lp_ex2(da), b = lp_ex2(db);
-  zy = fmaf(z, da, zy) * a + fmaf(z2, db, zy2) * b;
-  z = z * a + z2 * b;
+  const bool keep = m >= m2;                     // the one with the larger logit stays as it is
+  const float mm = keep ? m : m2, by = lp_shift(keep ? m2 : m, mm == -INFINITY ? 0.f : mm, c), f = lp_ex2(by);
+  const float zl = keep ? z2 : z, zyl = keep ? zy2 : zy;
+  zy = fmaf(fmaf(zl, by, zyl), f, keep ? zy : zy2);
+  z = fmaf(zl, f, keep ? z : z2);
   m = mm;
 }
 
