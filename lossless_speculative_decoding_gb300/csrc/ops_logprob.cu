@@ -264,13 +264,16 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
   }
   if (lane < 32 / LP_WARPS) sh.top[32 / LP_WARPS * w + lane] = 0;
   bar_sync(5, LP_THREADS);
-  int in = 0, out = 0, phase = 0;                          // stages to fill and to read next; the latter's phase
+  int in = 0, out = 0, filled = 0, phase = 0;              // stages to fill and to read next; their phases
   auto row_of = [&](int i) { return static_cast<const T*>(A.logits) + (int64_t)i * A.ld; };
   auto skip_of = [&](const T* row) { return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T)); };
   auto fetch = [&](const T* row, int skip, int st) {       // (every lane has read what the stage held)
     uint4* dst = stage + in * U * 32;
     const uint32_t bar = (uint32_t)__cvta_generic_to_shared(&sh.full[w][in]);
-    if (++in == LP_STAGES) in = 0;
+    if (++in == LP_STAGES) {
+      in = 0;
+      filled ^= 1;
+    }
     const int e0 = (st * LP_TILE + w * 32 * U) * PER - skip;
     int v0 = 0, v1 = U * 32;                               // vectors that lie whole in the row
     if (e0 < 0 || e0 + U * 32 * PER > V) {                 // an end of the row: -inf outside it
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
   // the fetches run LP_STAGES - 1 steps ahead of (r, st), over the block's rows
   int left = (int)(end - pos), f_step = s0, f_skip = skip_of(row_of(r));   // (a block has far fewer than 2^31 steps)
   const T* f_row = row_of(r);
-  bool lost = false;                                       // a copy was given up
+  bool lost = false;                                       // a copy was given up (by the whole warp)
   auto fetch_next = [&]() {
     if (left == 0) return;
     fetch(f_row, f_skip, f_step);
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
     for (int st = s0; st < s1; ++st) {
       const int first = st * LP_TILE + w * 32 * U + lane;
       fetch_next();
-      if (!mbar_wait_deadline((uint32_t)__cvta_generic_to_shared(&sh.full[w][out]), phase, &sh.abort)) {
+      if (!__all_sync(0xffffffffu, mbar_wait_deadline((uint32_t)__cvta_generic_to_shared(&sh.full[w][out]), phase, &sh.abort))) {
         // (not expected: the values of this row and the block's later ones become NaN; no more copies)
         *reinterpret_cast<volatile int*>(&sh.abort) = DERR_TIMEOUT;
         bad = lost = true;
@@ -505,10 +508,10 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
     if (n > 0) sh.list[half][w][lane] = list;
     bar_arrive(1 + half, LP_ALL);
   }
-  // shared memory outlives the copies (they are over, unless one was given up)
-  if (sh.abort)
+  // shared memory outlives the copies (over, unless one was given up): each stage's last one
+  if (lost)
     for (int i = 0; i < LP_STAGES; ++i)
-      mbar_wait_deadline((uint32_t)__cvta_generic_to_shared(&sh.full[w][i]), i < out ? phase : phase ^ 1, nullptr);
+      mbar_wait_deadline((uint32_t)__cvta_generic_to_shared(&sh.full[w][i]), i < in ? filled : filled ^ 1, nullptr);
   return;
   }
 
