@@ -801,7 +801,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other
   // waits at once: the producer and the issuer stop, the softmax groups finish
-  // the segment without a result and stop, the loader runs to its end.
+  // the segment without a result and stop, and so does the loader where a
+  // segment's place is not free.
   auto wait = [&](const uint64_t* bar, uint32_t parity) {
     return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err);
   };
@@ -854,8 +855,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         if (++b == NBUF) { b = 0; ++turn; }
       }
     }
-    if (!ok)                                     // shared memory outlives the copies in flight
-      for (int i = 0; i < NBUF; ++i) mbar_wait_deadline(sm_addr(H.kv_full + i), (i < b ? turn : turn - 1) & 1, nullptr);
+    // shared memory outlives the copies (over, unless the issuer gave up a wait): each buffer's last one
+    for (int i = 0; i < NBUF; ++i) mbar_wait_deadline(sm_addr(H.kv_full + i), (i < b ? turn : turn - 1) & 1, nullptr);
   } else if (warp == 9) {
     // ---- MMA issuer: S of a job, then P V of the job before it. The whole
     // warp runs the loop on values that are the same in every lane, so that the
@@ -956,7 +957,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
     for (uint32_t seg = 0;; ++seg) {
       const int sb = seg & 1;
       const bool have = walk.next(g);
-      if (seg >= 2) wait(H.seg_free + sb, (seg >> 1) - 1);
+      // (not free: aborted. The softmax warps may still read this place; the others' waits for it end as well)
+      if (seg >= 2 && !__all_sync(0xffffffffu, wait(H.seg_free + sb, (seg >> 1) - 1))) break;
       if (!have) g.nt = 0;
       if (lane == 0) {
         H.seg[sb] = g;
