@@ -1325,7 +1325,7 @@ extern "C" int spec_tree_attention(const spec_kv_view* kv, int layer, const void
   if (!q_dev || !out_dev || !cache_len_dev || !n_nodes_dev || !parents_dev || !ws_dev || !err_dev)
     return set_last_error(SPEC_ERR_ARG, "null pointer argument");
   if (layer < 0 || layer >= kv->n_layers) return set_last_error(SPEC_ERR_ARG, "layer out of range");
-  if (!(scale > 0.f) || !(scale < INFINITY)) return set_last_error(SPEC_ERR_ARG, "scale must be positive");
+  if (!(scale > 0.f) || !(scale * LOG2E < INFINITY)) return set_last_error(SPEC_ERR_ARG, "scale must be positive, and finite times log2 e");
   if (!aligned16(q_dev) || !aligned16(out_dev) || !aligned16(ws_dev))
     return set_last_error(SPEC_ERR_ARG, "q, out and the workspace must be 16-byte aligned");
   const int d = kv->head_dim;

@@ -1,0 +1,23 @@
+"""Refusals of the tree entry points on the host, before any CUDA call (the
+pointers here are never dereferenced)."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def B():
+    from lossless_speculative_decoding_gb300 import build, binding
+    build.build()
+    return binding
+
+
+def _view(B):
+    return B.make_kv_view(1 << 20, 2 << 20, dtype=1, n_pages=8, n_layers=2, n_kv_heads=2, page_size=16, head_dim=128, max_pages=4)
+
+
+@pytest.mark.parametrize("scale", [3.4e38, 2.4e38])      # log2 e times 2.4e38 is 3.46e38
+def test_attention_scales_past_fp32_in_units_of_log2(B, scale):
+    """Finite, but not once multiplied by log2 e."""
+    with pytest.raises(B.SpecError) as e:
+        B.spec_tree_attention(_view(B), 0, 3 << 20, 2, 64, 4, 4 << 20, 5 << 20, 6 << 20, scale, 7 << 20, 8 << 20, 1 << 40,
+                              9 << 20)
+    assert e.value.code == -1 and "scale" in str(e.value)
