@@ -511,8 +511,9 @@ int spec_tree_attention(const spec_kv_view* kv, int layer, const void* q_dev, in
  * not read).
  *   out_accepted_dev [n_seq]: a; out_token_dev [n_seq]: target[path_a], to be
  *   appended; out_path_dev [n_seq][max_nodes]: path_0 .. path_a, then -1;
- *   out_len_dev [n_seq]: n + a + 1 (not cache_len_dev itself, SPEC_ERR_ARG:
- *   other blocks of the call still read n; swap the two after a step).
+ *   out_len_dev [n_seq]: n + a + 1. No output overlaps an input or another
+ *   output (SPEC_ERR_ARG: other blocks of the call still read them; swap
+ *   out_len_dev and cache_len_dev after a step).
  * A padded sequence (n_nodes 0), one with a bad length or one with a bad page
  * under a row of its path, whether that row moves or not, is not moved and
  * gives a = -1, token -1, no path, and n.

@@ -187,7 +187,21 @@ extern "C" int spec_tree_commit(const spec_kv_view* kv, int n_seq, int max_nodes
     return set_last_error(SPEC_ERR_ARG, "null pointer argument");
   if (n_seq < 1 || n_seq > 65535) return set_last_error(SPEC_ERR_ARG, "1 <= n_seq <= 65535 required");
   if (max_nodes < 1 || max_nodes > TREE_N) return set_last_error(SPEC_ERR_ARG, "1 <= max_nodes <= 64 required");
-  if (out_len_dev == cache_len_dev) return set_last_error(SPEC_ERR_ARG, "out_len_dev must not be cache_len_dev");
+  // a sequence's blocks read the inputs while one of them writes the outputs
+  struct Span { const int32_t* p; int64_t n; };
+  const int64_t all = (int64_t)n_seq * max_nodes;
+  const Span out[4] = {{out_accepted_dev, n_seq}, {out_token_dev, n_seq}, {out_path_dev, all}, {out_len_dev, n_seq}};
+  const Span in[5] = {{tokens_dev, all}, {parents_dev, all}, {target_dev, all}, {n_nodes_dev, n_seq}, {cache_len_dev, n_seq}};
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return x < y + b.n * sizeof(int32_t) && y < x + a.n * sizeof(int32_t);
+  };
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& b : in)
+      if (meet(out[i], b)) return set_last_error(SPEC_ERR_ARG, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return set_last_error(SPEC_ERR_ARG, "two outputs overlap");
+  }
   const int64_t cols = (int64_t)kv->n_layers * kv->n_kv_heads * 2 * kv->head_dim * (kv->dtype == SPEC_F32 ? 4 : 2) / 16;
   const int blocks = (int)std::min<int64_t>((cols + COMMIT_THREADS - 1) / COMMIT_THREADS, 4096);
   k_tree_commit<<<dim3(blocks, n_seq), COMMIT_THREADS, 0, reinterpret_cast<cudaStream_t>(cuda_stream)>>>(
