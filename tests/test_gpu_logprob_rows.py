@@ -24,3 +24,15 @@ def test_logprobs_of_rows_that_end_inside_a_step(dtype, V, extra):
     x.copy_(torch.randn((R, V), generator=g, device="cuda") * 0.1 + ramp * torch.where(torch.arange(R, device="cuda") % 2 == 0, 1.0, -1.0)[:, None])
     tokens = np.random.default_rng(V).integers(0, V, R).astype(np.int32)
     _check(x, tokens, 1.0, 6)
+
+
+@pytest.mark.parametrize("dtype", [T.F32, T.BF16])
+def test_logprobs_of_rows_past_32_bits(dtype):
+    """Rows more than 2^31 elements apart, from an odd address."""
+    import torch
+    V, ld = 9001, 2 ** 31 + 11
+    flat = torch.empty(ld + V + 1, dtype=torch.float32 if dtype == T.F32 else torch.bfloat16, device="cuda")
+    x = torch.as_strided(flat, (2, V), (ld, 1), 1)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x.copy_(torch.randn((2, V), generator=g, device="cuda"))
+    _check(x, np.array([V - 1, 4], np.int32), 1.0, 5)
