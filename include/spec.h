@@ -449,7 +449,8 @@ int spec_lmhead_argmax_noalloc(const float* x_dev, int T, int hidden, int vocab,
  * Lengths and ids stay on the device: they may change between replays, but
  * not while a call runs.
  *
- * The cache of these entry points, the layout of a model's own pool. Device
+ * The cache of these entry points, laid out as a model's own pool is (which no
+ * call gives out: they serve a caller's decoder and its cache). Device
  * pointers, caller-owned; the struct itself is read during the call only. */
 typedef struct spec_kv_view {
   void* kv_dev;          /* [n_pages][n_layers][n_kv_heads][2 (K, V)][page_size][head_dim], 16-byte aligned */
@@ -482,7 +483,9 @@ typedef struct spec_kv_view {
  *     is written), parents_dev [n_seq][max_nodes].
  *   ws_dev: spec_tree_attention_ws_bytes bytes of device memory, 16-byte
  *     aligned; needs no initialisation; one call at a time per workspace.
- * Scores, softmax statistics and sums are fp32; bf16 results are rounded once.
+ * Scores, softmax statistics and sums are fp32. Against a bf16 cache a weight
+ * enters the sum of values as two bf16 parts (16 bits; its sum is of the fp32
+ * weights); bf16 results are rounded once.
  * Slots past n + n_nodes[s] may hold anything. Every slot up to there has to
  * hold finite keys and values (a NaN of one node may reach the others). Scores
  * of any size are taken (q.K and scale * q.K below 2^126), told apart as far as

@@ -17,10 +17,13 @@
 // The rows' steps of 32 KB, row after row, are cut into one even run for each
 // block that the GPU holds at once, so that a few rows use all of it and many
 // rows leave no tail. A warp takes 4 KB of a step, one ahead by a bulk copy into
-// its own shared memory, and no warp waits for another's. Within a row a thread
-// keeps a running (m, z, sum) and a count of the logits that come before the
-// token; a step whose sum comes out as NaN (masked tokens, NaN logits) is added
-// again with care. Alternatives: a warp holds the best 32 of what it has seen as
+// its own shared memory; warps wait for each other where a row ends (from the third
+// on, for the place that they leave its statistics in) and, with more than four
+// alternatives, at a row's steps 1, 4, 16, .. Within a row a thread keeps a running
+// (m, z, sum) and a count of the logits that come before the token; a step whose sum
+// comes out as NaN (masked tokens, NaN logits) is added again with care, value by
+// value: 256 rows of 129,280 fp32 logits take 37 us, 44 with one token of a thousand
+// masked, 92 with half of them; 1,100 bf16 rows of 151,936 88, 166 and 350. Alternatives: a warp holds the best 32 of what it has seen as
 // sorted 64-bit keys (ordered logit, inverted index), one per lane. A thread's
 // step is searched only if its maximum is not below a bound of the block's n-th
 // best logit, which comes from the threads' maxima (it only saves work: what is
@@ -30,10 +33,11 @@
 // one that is changes nothing).
 //
 // Bound: fp32 logits by HBM (1,024 rows of 129,280 without alternatives: 6.4 TB/s,
-// 0.94 of the measured copy rate; with 20 of them 5.2), 16-bit ones by the
-// instructions of a logit, ten or so (1,100 rows of 151,936, one alternative:
-// 3.9 TB/s, 0.57), and a few rows by the chain of a row's end, some 10 us (4 rows of
-// 129,280, five alternatives: 12.3 us).
+// 0.94 of the measured copy rate). 16-bit ones (1,100 rows of 151,936, one
+// alternative: 86 us, 3.9 TB/s, 0.57) by 10.7 instructions a logit of which a
+// scheduler issues 0.60 a cycle: the warps wait at the rows' ends, as a row's short
+// last step falls to some of them, and for their own chains. A few rows by the chain of
+// a step and a row's end, some 10 us (4 rows of 129,280, five alternatives: 12.3 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -444,8 +448,9 @@ __global__ void __launch_bounds__(LP_ALL, LP_BLOCKS) k_logprob(const __grid_cons
       // known, marked with the row. The n-th largest of those that are there
       // bounds the n-th best logit seen, and so does the warp's own n-th largest.
       // A few alternatives take what is there; more wait for the other warps,
-      // whose maxima they need (20 of 256 rows: 36 us, 48 without the barrier; 1
-      // of 1,100 rows: 92 us with it, 89 without).
+      // whose maxima they need (with the barrier / without: 256 fp32 rows, top 1
+      // 30.9 / 31.0 us, 4 33.0 / 32.8, 5 33.0 / 33.8, 20 36.6 / 48.2; 1,100 bf16
+      // rows, top 1 89.0 / 88.0, 4 95.8 / 95.8, 5 97.4 / 99.0, 20 123 / 171).
       const int done = st - s0 + 1;
       if ((done & (done - 1)) == 0 && (done & 0x55555555)) {
         uint32_t k = ordered(m);

@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
 // 32 nodes, 10 heads, 0.93 GB: 168 us with the join, 5.5 TB/s, 0.82 of the copy
 // rate; two of up to 65,521 positions, 21 nodes, 32 on 8 heads: 74 us, 0.71. With
 // two row tiles (8 sequences of 64 nodes, 32 on 8 heads) the chain S, softmax, P V
-// of a slot: 2,400 cycles a tile, 56 us.
+// of a slot: 2,400 cycles a tile, 57 us with the start (5) and the join (12).
 // (Row tiles of 256, each slot with 128 rows of its own, read keys once for all of
 // them, but took 59.5 us there, 176 and 79 above: less room for keys, twice the
 // bytes of parts to join, more code. Scores 64 at a time: 55.7 and 168. A next
@@ -1174,8 +1174,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 // parts are on their way together, so that the launch is two round trips to L2
 // (the description, the parts) long: under the profiler 7 us behind the 64
 // sequences, 12 where parts of 17 MB are joined (8 sequences of 256 rows a head).
-// (Blocks of one launch that wait for one another would need flags that somebody
-// has cleared, and the workspace comes as it is.)
+// (A last block that joins within the one launch would need counters at zero: this
+// entry point takes its workspace as it comes.)
 constexpr int JOIN_WARPS = 8;
 
 template <int D, class KT>
