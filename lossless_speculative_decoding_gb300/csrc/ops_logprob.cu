@@ -17,27 +17,31 @@
 // The rows' steps of 32 KB, row after row, are cut into one even run for each
 // block that the GPU holds at once, so that a few rows use all of it and many
 // rows leave no tail. A warp takes 4 KB of a step, one ahead by a bulk copy into
-// its own shared memory; warps wait for each other where a row ends (from the third
-// on, for the place that they leave its statistics in) and, with more than four
-// alternatives, at a row's steps 1, 4, 16, .. Within a row a thread keeps a running
-// (m, z, sum) and a count of the logits that come before the token; a step whose sum
-// comes out as NaN (masked tokens, NaN logits) is added again with care, value by
-// value: 256 rows of 129,280 fp32 logits take 37 us, 44 with one token of a thousand
-// masked, 92 with half of them; 1,100 bf16 rows of 151,936 88, 166 and 350. Alternatives: a warp holds the best 32 of what it has seen as
-// sorted 64-bit keys (ordered logit, inverted index), one per lane. A thread's
-// step is searched only if its maximum is not below a bound of the block's n-th
-// best logit, which comes from the threads' maxima (it only saves work: what is
-// found does not depend on it). 32 found keys are sorted and merged at a time. A
-// ninth warp ends the rows while the others go on; a row that several blocks
-// share is joined, in the blocks' order, by the last of them to finish (which
-// one that is changes nothing).
+// its own shared memory; warps wait for each other where a row ends (from the
+// third on, for the place that they leave its statistics in) and, with more than
+// four alternatives, at a row's steps 1, 4, 16, .. Within a row a thread keeps a
+// running (m, z, sum) and a count of the logits that come before the token.
 //
-// Bound: fp32 logits by HBM (1,024 rows of 129,280 without alternatives: 6.4 TB/s,
-// 0.94 of the measured copy rate). 16-bit ones (1,100 rows of 151,936, one
-// alternative: 86 us, 3.9 TB/s, 0.57) by 10.7 instructions a logit of which a
-// scheduler issues 0.60 a cycle: the warps wait at the rows' ends, as a row's short
-// last step falls to some of them, and for their own chains. A few rows by the chain of
-// a step and a row's end, some 10 us (4 rows of 129,280, five alternatives: 12.3 us).
+// A step whose sum comes out as NaN (masked tokens, NaN logits) is added again
+// with care, value by value: 256 rows of 129,280 fp32 logits with 20 alternatives
+// take 36 us, 44 with one token of a thousand masked, 92 with half of them; 1,100
+// bf16 rows of 151,936 88, 166 and 350.
+//
+// Alternatives: a warp holds the best 32 of what it has seen as sorted 64-bit
+// keys (ordered logit, inverted index), one per lane. A thread's step is searched
+// only if its maximum is not below a bound of the block's n-th best logit, which
+// comes from the threads' maxima (it only saves work: what is found does not
+// depend on it). 32 found keys are sorted and merged at a time. A ninth warp ends
+// the rows while the others go on; a row that several blocks share is joined, in
+// the blocks' order, by the last of them to finish (which one that is changes
+// nothing).
+//
+// Bound: fp32 logits by HBM (1,024 rows of 129,280 without alternatives: 83 us,
+// 6.4 TB/s, 0.94 of the measured copy rate). 16-bit ones (1,100 rows of 151,936,
+// one alternative: 86 us, 3.9 TB/s, 0.57) take 10.7 instructions a logit, of
+// which a scheduler issues 0.60 a cycle: the largest stalls are the barrier at the
+// rows' ends and the latency of a warp's own chain. A few rows by the chain of a
+// step and a row's end, some 10 us (4 rows of 129,280, five alternatives: 12.3 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
