@@ -368,7 +368,8 @@ def _plain_mass(s):
     s["out"].zero_()
     top = p.shape[-1]
     held = (torch.arange(top, device="cuda") < (n + m)[:, None])[:, None]
-    s["out"][..., :top] = torch.where(held, s["mass"][..., :top] + p.sum((2, 3)), 0.0)
+    before = torch.where((torch.arange(top, device="cuda") < n[:, None])[:, None], s["mass"][..., :top], 0.0)
+    s["out"][..., :top] = torch.where(held, before + p.sum((2, 3)), 0.0)       # (a new position starts from nothing)
     return s["out"]
 
 
@@ -509,8 +510,9 @@ def _exact_mass(case, s):
     for b in range(case["batch"]):
         x, at = _scores(case, s, b, torch.float64, case["last"])
         lse = s["lse"][at].double().view(x.shape[2], x.shape[0], x.shape[1]).permute(1, 2, 0)
-        top = x.shape[-1]
-        out[b, :, :top] = s["mass"][b, :, :top].double() + x.sub_(lse[..., None]).exp_().sum((1, 2))
+        n, top = int(s["n_host"][b]), x.shape[-1]
+        out[b, :, :top] = x.sub_(lse[..., None]).exp_().sum((1, 2))
+        out[b, :, :n] += s["mass"][b, :, :n].double()
     return out
 
 
