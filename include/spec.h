@@ -572,6 +572,131 @@ int spec_token_logprobs(const void* logits_dev, int dtype, int64_t ld, int n_row
                         float* out_entropy_dev, int32_t* out_rank_dev, int32_t* out_top_ids_dev,
                         float* out_top_logprobs_dev, void* ws_dev, size_t ws_bytes, uintptr_t cuda_stream);
 
+/* ---- chunks of new tokens (kernel-level entry points) -----------------------
+ * The rest of a caller's layer on the same cache: new tokens enter it, attend,
+ * and positions that draw little attention leave it again. Sequence s has
+ * n = cache_len[s] positions and m = n_new[s] new tokens (a prompt, a part of
+ * one, one token of plain decoding, the rows of a verify step), whose rows are
+ * row_start[s] .. row_start[s] + m - 1 of n_rows rows; token i belongs in slot
+ * n + i and sees the positions 0 .. n + i. One step is
+ *   spec_qk_norm_rope, spec_chunk_attention (or spec_tree_attention) and, where
+ *   the cache is bounded, spec_attention_mass in every layer; then spec_kv_evict.
+ * Rows of no sequence are neither read into a result nor written; rows of two
+ * sequences must not be the same. m = 0 is a padded sequence: nothing of it is
+ * written. A sequence with n < 0, m < 0, rows outside [0, n_rows), more tokens
+ * than max_new or more positions than the block table holds is left out
+ * (SPEC_DEV_ERR_POS). What the tree entry points say about devices, streams,
+ * capture, device-side lengths and error bits holds here too. */
+
+/* Rotation of positions. Pair p of a head (dims p and p + dim / 2, p < dim / 2)
+ * turns by positions[axis[p]][row] * freq[p] radians; dims from dim on stay as
+ * they are. Several axes (time, height, width of an image's or a video's
+ * patches) are several rows of positions. */
+#define SPEC_ROPE_MAX_PAIRS 64
+#define SPEC_ROPE_MAX_AXES 4
+typedef struct spec_rope {
+  int32_t dim;           /* rotated dims: a multiple of 16, at most head_dim; 0: no rotation */
+  int32_t n_axes;        /* 1 .. SPEC_ROPE_MAX_AXES */
+  double freq[SPEC_ROPE_MAX_PAIRS];   /* finite; theta^(-2p / dim) is the usual choice */
+  uint8_t axis[SPEC_ROPE_MAX_PAIRS];  /* below n_axes */
+} spec_rope;
+
+/* New tokens' projections into queries, and into the cache of one layer: RMS norm
+ * of each query and key head, rotation, one rounding. With x a head of a row,
+ *   y = x * gamma / sqrt(mean(x^2) + eps)   (gamma NULL: y = x),
+ *   dims (p, p + dim / 2) of y turned by the pair's angle t:
+ *   (y0 cos t - y1 sin t, y1 cos t + y0 sin t);
+ * values are copied as they are.
+ *   qkv_dev: n_rows rows, ld elements apart, of n_q_heads + 2 n_kv_heads heads
+ *     (queries, keys, values) in the cache's dtype; 16-byte aligned, ld a
+ *     multiple of 16 bytes.
+ *   rope: host memory, read during the call. positions_dev [n_axes][n_rows]
+ *     int32 (any value), NULL only when rope->dim = 0.
+ *   q_gamma_dev, k_gamma_dev [head_dim] f32, NULL for no norm of that kind.
+ *   q_out_dev [n_rows][n_q_heads][head_dim], 16-byte aligned; must overlap
+ *     neither qkv_dev nor the cache.
+ * Key and value of token i go to slot n + i of layer `layer`; with n_nodes as
+ * n_new and row_start = s max_nodes the same call serves spec_tree_attention.
+ * A token whose page is bad (SPEC_DEV_ERR_PAGE) leaves its query alone.
+ * Angles are exact to 2^-32 of a turn at any position (up to the rounding of
+ * freq itself); norm and rotation are fp32.
+ * Errors: SPEC_ERR_ARG; SPEC_ERR_UNSUPPORTED (cache view); SPEC_ERR_CUDA. */
+int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* qkv_dev, int64_t ld, int n_rows, int n_seq,
+                      int n_q_heads, const int32_t* row_start_dev, const int32_t* n_new_dev,
+                      const int32_t* cache_len_dev, const spec_rope* rope, const int32_t* positions_dev,
+                      const float* q_gamma_dev, const float* k_gamma_dev, float eps, void* q_out_dev,
+                      int32_t* err_dev, uintptr_t cuda_stream);
+
+/* Attention of the chunks over the paged cache, one layer, the chunks' own keys
+ * and values in their slots already. The row of (token i, query head h) is
+ *   out = sum_j w_j V_j,  w = softmax over j <= n + i of scale * q.K_j,
+ *   lse = log sum_(j <= n + i) exp(scale * q.K_j),
+ * on kv head h / (n_q_heads / n_kv_heads).
+ *   q_dev, out_dev [n_rows][n_q_heads][head_dim] in the cache's dtype, 16-byte
+ *     aligned; out_dev may be q_dev itself, but not overlap it otherwise.
+ *   out_lse_dev [n_rows][n_q_heads] f32, or NULL.
+ *   max_new: an upper bound of n_new (it chooses the kernel's form).
+ *   ws_dev: spec_chunk_attention_ws_bytes bytes of device memory, 16-byte
+ *     aligned; needs no initialisation; one call at a time per workspace.
+ * Scores, softmax statistics and sums are fp32 (the sum of weights is of the
+ * fp32 weights). Against a bf16 cache a weight enters the sum of values as two
+ * bf16 parts where every sequence has at most 64 tokens and 128 (token, head)
+ * rows per kv head (max_new decides), as one bf16 value otherwise; bf16 results
+ * are rounded once. Slots past n + m may hold anything; every slot up to there
+ * has to hold finite keys and values. Scores of any size are taken (q.K and
+ * scale * q.K below 2^126). The same call gives the same bits; where a
+ * sequence's keys are cut into parts summed apart depends on the batch. Rows
+ * that need a bad page hold no usable value (SPEC_DEV_ERR_PAGE). Errors:
+ * SPEC_ERR_ARG; SPEC_ERR_UNSUPPORTED (head_dim, dtype, more than 128 query heads
+ * per kv head); SPEC_ERR_CUDA. */
+int64_t spec_chunk_attention_ws_bytes(const spec_kv_view* kv, int n_seq, int max_new, int n_q_heads);
+int spec_chunk_attention(const spec_kv_view* kv, int layer, const void* q_dev, int n_rows, int n_seq, int max_new,
+                         int n_q_heads, const int32_t* row_start_dev, const int32_t* n_new_dev,
+                         const int32_t* cache_len_dev, float scale, void* out_dev, float* out_lse_dev, void* ws_dev,
+                         size_t ws_bytes, int32_t* err_dev, uintptr_t cuda_stream);
+
+/* Attention weight that each position of one layer has drawn, for each kv head:
+ *   out_mass[s][h][j] = (j < n ? mass[s][h][j] : 0)
+ *     + sum over the last min(last, m) tokens i of the chunk that see j, and the
+ *       query heads g of kv head h, of exp(scale * q_(i,g).K_j - lse[i][g]),
+ * for j < n + m; what lies behind is not written. With last = max_new every
+ * token counts; with few, the end of a prompt decides.
+ *   q_dev, n_rows, max_new, row_start_dev, .. as in spec_chunk_attention, whose
+ *     lse_dev [n_rows][n_q_heads] this takes.
+ *   mass_dev, out_mass_dev [n_seq][n_kv_heads][ld] f32, out_mass_dev the same
+ *     array or one that does not overlap it; mass_dev may be NULL (zeros). A
+ *     sequence of more than ld positions is left out (SPEC_DEV_ERR_POS).
+ * fp32, in a fixed order: the same call gives the same bits. Positions on a bad
+ * page get no usable value (SPEC_DEV_ERR_PAGE).
+ * Errors: as spec_chunk_attention. */
+int spec_attention_mass(const spec_kv_view* kv, int layer, const void* q_dev, const float* lse_dev, int n_rows,
+                        int n_seq, int max_new, int last, int n_q_heads, const int32_t* row_start_dev,
+                        const int32_t* n_new_dev, const int32_t* cache_len_dev, float scale, const float* mass_dev,
+                        float* out_mass_dev, int64_t ld, int32_t* err_dev, uintptr_t cuda_stream);
+
+/* Evict positions of little weight, in every layer and kv head for itself: of a
+ * sequence with n = cache_len[s] > budget positions each (layer, head) keeps the
+ * `recent` last ones and, of the others, the budget - recent with the largest
+ * mass (equal ones by position, the first first; a NaN after every number). What
+ * is kept moves, in order of position, to the slots 0 .. budget - 1 (keys carry
+ * their rotation with them); the slots behind are free.
+ *   mass_dev, out_mass_dev [n_layers][n_seq][n_kv_heads][ld] f32: the mass of the
+ *     kept positions goes to out_mass_dev's first slots, what lies behind them
+ *     is not written. ld >= the longest sequence (a longer one is left out,
+ *     SPEC_DEV_ERR_POS).
+ *   out_kept_dev [n_layers][n_seq][n_kv_heads][budget] int32: the old slot of
+ *     each new one, -1 behind the last.
+ *   out_len_dev [n_seq]: min(n, budget). No output overlaps an input or another
+ *     output (SPEC_ERR_ARG; swap the arrays after a call).
+ * A sequence with n <= budget keeps everything where it is. One that needs a
+ * bad page (SPEC_DEV_ERR_PAGE) or has a bad length is left as it is: kept -1,
+ * length n, no mass written. A sequence whose pages are shared with others has
+ * to own the pages it writes. 1 <= budget, 0 <= recent <= budget.
+ * Errors: SPEC_ERR_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA. */
+int spec_kv_evict(const spec_kv_view* kv, int n_seq, const int32_t* cache_len_dev, const float* mass_dev, int64_t ld,
+                  int budget, int recent, float* out_mass_dev, int32_t* out_kept_dev, int32_t* out_len_dev,
+                  int32_t* err_dev, uintptr_t cuda_stream);
+
 /* ---- paged KV allocator (host only; usable without a GPU) ---------------- */
 /* The same allocator the model uses, exposed for tests and tooling. Pages
  * hold page_size consecutive positions; a sequence's block table lists its

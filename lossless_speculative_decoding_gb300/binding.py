@@ -47,6 +47,14 @@ class spec_kv_view(ctypes.Structure):
         "dtype", "n_pages", "n_layers", "n_kv_heads", "page_size", "head_dim", "max_pages")]
 
 
+SPEC_ROPE_MAX_PAIRS, SPEC_ROPE_MAX_AXES = 64, 4
+
+
+class spec_rope(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("freq", ctypes.c_double * SPEC_ROPE_MAX_PAIRS),
+                ("axis", ctypes.c_uint8 * SPEC_ROPE_MAX_PAIRS)]
+
+
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _VIEWP = ctypes.POINTER(spec_kv_view)
 _lib: Optional[ctypes.CDLL] = None
@@ -126,6 +134,17 @@ _SIGS = [
     ("spec_token_logprobs", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
                                            ctypes.c_void_p, ctypes.c_float, ctypes.c_int] + [ctypes.c_void_p] * 6 +
      [ctypes.c_size_t, ctypes.c_size_t]),
+    ("spec_qk_norm_rope", ctypes.c_int, [_VIEWP, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_int] * 3 +
+     [ctypes.c_void_p] * 3 + [ctypes.POINTER(spec_rope)] + [ctypes.c_void_p] * 3 + [ctypes.c_float, ctypes.c_void_p,
+                                                                                    ctypes.c_void_p, ctypes.c_size_t]),
+    ("spec_chunk_attention_ws_bytes", ctypes.c_int64, [_VIEWP, ctypes.c_int, ctypes.c_int, ctypes.c_int]),
+    ("spec_chunk_attention", ctypes.c_int, [_VIEWP, ctypes.c_int, ctypes.c_void_p] + [ctypes.c_int] * 4 +
+     [ctypes.c_void_p] * 3 + [ctypes.c_float] + [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p, ctypes.c_size_t]),
+    ("spec_attention_mass", ctypes.c_int, [_VIEWP, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p] + [ctypes.c_int] * 5 +
+     [ctypes.c_void_p] * 3 + [ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                              ctypes.c_size_t]),
+    ("spec_kv_evict", ctypes.c_int, [_VIEWP, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+                                     ctypes.c_int] + [ctypes.c_void_p] * 4 + [ctypes.c_size_t]),
     ("spec_strerror", ctypes.c_char_p, [ctypes.c_int]),
     ("spec_last_error", ctypes.c_char_p, []),
     ("spec_pool_create", ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
@@ -454,6 +473,52 @@ def spec_token_logprobs(logits_dev, dtype: int, ld: int, n_rows: int, vocab: int
                                      top_n, _ptr(out_logprob_dev), _ptr(out_entropy_dev), _ptr(out_rank_dev),
                                      _ptr(out_top_ids_dev), _ptr(out_top_logprobs_dev), _ptr(ws_dev), ws_bytes,
                                      cuda_stream))
+
+
+# ---- chunks of new tokens ------------------------------------------------------
+def make_rope(freq, *, axis=None, n_axes: int = 1) -> spec_rope:
+    """Rotation of len(freq) pairs of a head's dims; freq in radians a position, axis the row of positions of each
+    pair (None: the first)."""
+    f = [float(x) for x in freq]
+    a = [0] * len(f) if axis is None else [int(x) for x in axis]
+    if len(f) > SPEC_ROPE_MAX_PAIRS or len(a) != len(f) or any(not 0 <= x < 256 for x in a):
+        raise ValueError(f"at most {SPEC_ROPE_MAX_PAIRS} pairs, each with an axis")
+    return spec_rope(2 * len(f), n_axes, (ctypes.c_double * SPEC_ROPE_MAX_PAIRS)(*f), (ctypes.c_uint8 * SPEC_ROPE_MAX_PAIRS)(*a))
+
+
+def spec_qk_norm_rope(kv: spec_kv_view, layer: int, qkv_dev, ld: int, n_rows: int, n_seq: int, n_q_heads: int, row_start_dev,
+                      n_new_dev, cache_len_dev, rope: spec_rope, positions_dev, q_gamma_dev, k_gamma_dev, eps: float,
+                      q_out_dev, err_dev, cuda_stream: int = 0) -> None:
+    _check(lib().spec_qk_norm_rope(ctypes.byref(kv), layer, _ptr(qkv_dev), ld, n_rows, n_seq, n_q_heads,
+                                   _ptr(row_start_dev), _ptr(n_new_dev), _ptr(cache_len_dev), ctypes.byref(rope),
+                                   _ptr(positions_dev), _ptr(q_gamma_dev), _ptr(k_gamma_dev), float(eps),
+                                   _ptr(q_out_dev), _ptr(err_dev), cuda_stream))
+
+
+def spec_chunk_attention_ws_bytes(kv: spec_kv_view, n_seq: int, max_new: int, n_q_heads: int) -> int:
+    return _check(lib().spec_chunk_attention_ws_bytes(ctypes.byref(kv), n_seq, max_new, n_q_heads))
+
+
+def spec_chunk_attention(kv: spec_kv_view, layer: int, q_dev, n_rows: int, n_seq: int, max_new: int, n_q_heads: int,
+                         row_start_dev, n_new_dev, cache_len_dev, scale: float, out_dev, out_lse_dev, ws_dev, ws_bytes: int,
+                         err_dev, cuda_stream: int = 0) -> None:
+    _check(lib().spec_chunk_attention(ctypes.byref(kv), layer, _ptr(q_dev), n_rows, n_seq, max_new, n_q_heads,
+                                      _ptr(row_start_dev), _ptr(n_new_dev), _ptr(cache_len_dev), float(scale),
+                                      _ptr(out_dev), _ptr(out_lse_dev), _ptr(ws_dev), ws_bytes, _ptr(err_dev), cuda_stream))
+
+
+def spec_attention_mass(kv: spec_kv_view, layer: int, q_dev, lse_dev, n_rows: int, n_seq: int, max_new: int, last: int,
+                        n_q_heads: int, row_start_dev, n_new_dev, cache_len_dev, scale: float, mass_dev, out_mass_dev, ld: int,
+                        err_dev, cuda_stream: int = 0) -> None:
+    _check(lib().spec_attention_mass(ctypes.byref(kv), layer, _ptr(q_dev), _ptr(lse_dev), n_rows, n_seq, max_new, last,
+                                     n_q_heads, _ptr(row_start_dev), _ptr(n_new_dev), _ptr(cache_len_dev), float(scale),
+                                     _ptr(mass_dev), _ptr(out_mass_dev), ld, _ptr(err_dev), cuda_stream))
+
+
+def spec_kv_evict(kv: spec_kv_view, n_seq: int, cache_len_dev, mass_dev, ld: int, budget: int, recent: int, out_mass_dev,
+                  out_kept_dev, out_len_dev, err_dev, cuda_stream: int = 0) -> None:
+    _check(lib().spec_kv_evict(ctypes.byref(kv), n_seq, _ptr(cache_len_dev), _ptr(mass_dev), ld, budget, recent,
+                               _ptr(out_mass_dev), _ptr(out_kept_dev), _ptr(out_len_dev), _ptr(err_dev), cuda_stream))
 
 
 def spec_strerror(code: int) -> str:

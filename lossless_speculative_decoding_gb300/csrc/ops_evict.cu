@@ -1,0 +1,258 @@
+// Kernel-level entry point: eviction of cache positions by accumulated attention
+// weight, each (layer, kv head) for itself.
+//
+// k_evict_select, one block per (layer, sequence, head): the budget - recent
+// largest masses by radix selection. A mass becomes a key that orders as it does
+// (sign folded, NaN lowest); three passes of 11, 11 and 10 bits each count the keys
+// that share the digits found so far and fix one more digit of the threshold, the
+// smallest key that is kept. One more pass writes what is kept in order of
+// position: every key above the threshold, the first ones equal to it, the
+// `recent` last positions.
+//
+// k_evict_move, blocks per (plane, K | V, piece of a row): slot j <- slot kept[j] >=
+// j. A batch of rows is loaded, then, behind a barrier, stored. Later batches read
+// from kept[j'] >= j' past every slot stored so far, so batches need no barrier
+// between them, and rows that stay are not touched.
+//
+// Bound: HBM, by the rows moved.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "chunk.cuh"
+
+namespace spec {
+namespace {
+
+constexpr int EV_THREADS = 512;
+constexpr int EV_BINS = 2048;
+constexpr int MV_THREADS = 256;
+constexpr int MV_ROWS = 8;                       // rows a thread has in flight
+
+struct EvictArgs {
+  spec_kv_view kv;
+  const int32_t* cache_len;
+  const float* mass;
+  float* out_mass;
+  int32_t* kept;
+  int32_t* out_len;
+  int32_t* err;
+  long long ld;
+  int n_seq, budget, recent, capacity;
+};
+
+__device__ __forceinline__ uint32_t mass_key(float x) {
+  if (x != x) return 0;
+  const uint32_t b = __float_as_uint(x + 0.f);   // (one zero)
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Exclusive prefix sum over the block; total in every thread. red: one per warp.
+__device__ __forceinline__ long long block_scan(long long v, long long* red, long long& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  long long inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  __syncthreads();
+  if (lane == 31) red[w] = inc;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+  for (int i = 0; i < EV_THREADS / 32; ++i) {
+    const long long x = red[i];
+    if (i < w) before += x;
+    total += x;
+  }
+  return before + inc - v;
+}
+
+__global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_constant__ EvictArgs A) {
+  __shared__ int hist[EV_BINS];
+  __shared__ long long red[EV_THREADS / 32];
+  __shared__ uint32_t s_digit;
+  __shared__ int s_left;
+  const int t = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  // planes [layer][sequence][head]
+  const int plane = blockIdx.x, s = plane / A.kv.n_kv_heads % A.n_seq;
+  const int n = A.cache_len[s];
+  const float* mass = A.mass + (size_t)plane * A.ld;
+  float* out_mass = A.out_mass + (size_t)plane * A.ld;
+  int32_t* kept = A.kept + (size_t)plane * A.budget;
+  const bool first = plane < A.kv.n_kv_heads * A.n_seq && plane % A.kv.n_kv_heads == 0;
+  bool ok = n >= 0 && n <= A.capacity;
+  if (!ok && first && t == 0) atomicOr(A.err, DERR_POS);
+  if (ok && n > A.budget) {
+    // every page up to n: the sequence moves in all planes or in none
+    bool bad = false;
+    const int32_t* bt = A.kv.block_table_dev + (size_t)s * A.kv.max_pages;
+    for (int i = t; i < (n + A.kv.page_size - 1) / A.kv.page_size; i += EV_THREADS)
+      bad |= bt[i] < 0 || bt[i] >= A.kv.n_pages;
+    if (__syncthreads_or(bad)) {
+      ok = false;
+      if (first && t == 0) atomicOr(A.err, DERR_PAGE);
+    }
+  }
+  if (first && t == 0) A.out_len[s] = ok ? min(n, A.budget) : n;
+  if (!ok || n <= A.budget) {
+    for (int j = t; j < A.budget; j += EV_THREADS) kept[j] = ok && j < n ? j : -1;
+    if (ok)
+      for (int j = t; j < n; j += EV_THREADS) out_mass[j] = mass[j];
+    return;
+  }
+  const int old = n - A.recent;                  // positions that compete
+  int left = A.budget - A.recent;                // of them to be kept; those equal to the threshold at last
+  uint32_t key = 0, known = 0;                   // the threshold's digits so far, their bits
+  if (left > 0) {
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+      for (int i = t; i < EV_BINS; i += EV_THREADS) hist[i] = 0;
+      __syncthreads();
+      for (int i = t; i < old; i += EV_THREADS) {
+        const uint32_t x = mass_key(mass[i]);
+        if ((x & known) == key) atomicAdd(&hist[(x >> shift) & (bins - 1)], 1);
+      }
+      __syncthreads();
+      // bins from the top: thread t has bins top - 4 t ..; the digit is where the count reaches `left`
+      constexpr int PER = EV_BINS / EV_THREADS;
+      int c[PER];
+      long long sum = 0, total;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        c[i] = hist[EV_BINS - 1 - (t * PER + i)];
+        sum += c[i];
+      }
+      long long above = block_scan(sum, red, total);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (above < left && above + c[i] >= left) {
+          s_digit = EV_BINS - 1 - (t * PER + i);
+          s_left = left - (int)above;
+        }
+        above += c[i];
+      }
+      __syncthreads();
+      key |= s_digit << shift;
+      known |= (uint32_t)(bins - 1) << shift;
+      left = s_left;
+    }
+  }
+  // kept positions in order: above the threshold, the first `left` equal to it, the last `recent`
+  const bool any = A.budget > A.recent;
+  const int per = (n + EV_THREADS - 1) / EV_THREADS;
+  const int a = min(t * per, n), a1 = min(a + per, n);
+  int above = 0, equal = 0;
+  for (int i = a; i < a1; ++i) {
+    if (i >= old) ++above;
+    else if (any) {
+      const uint32_t x = mass_key(mass[i]);
+      above += x > key;
+      equal += x == key;
+    }
+  }
+  long long total;
+  const long long at = block_scan((long long)above << 32 | equal, red, total);
+  int up = (int)(at >> 32), eq = (int)(at & 0xffffffff);
+  for (int i = a; i < a1; ++i) {
+    const float f = mass[i];
+    bool keep = i >= old;
+    if (!keep && any) {
+      const uint32_t x = mass_key(f);
+      keep = x > key || (x == key && eq < left);
+      if (x == key) {
+        if (keep) { kept[up + eq] = i; out_mass[up + eq] = f; }
+        ++eq;
+        continue;
+      }
+    }
+    if (keep) {
+      const int j = up++ + min(eq, left);
+      kept[j] = i;
+      out_mass[j] = f;
+    }
+  }
+}
+
+// grid (planes x pieces of a row, K | V); SPAN 16-byte columns a block.
+template <int SPAN>
+__global__ void __launch_bounds__(MV_THREADS) k_evict_move(const __grid_constant__ EvictArgs A, int row16) {
+  constexpr int ROWS = MV_THREADS / SPAN;        // rows of the block at once
+  const int t = threadIdx.x, cols = row16 / SPAN;
+  pdl_wait();
+  pdl_trigger();
+  const int plane = blockIdx.x / cols, c = blockIdx.x % cols * SPAN + t % SPAN;
+  const int h = plane % A.kv.n_kv_heads, s = plane / A.kv.n_kv_heads % A.n_seq, layer = plane / A.kv.n_kv_heads / A.n_seq;
+  const int n = A.cache_len[s];
+  if (n <= A.budget || n > A.capacity) return;
+  const int32_t* kept = A.kept + (size_t)plane * A.budget;
+  if (kept[A.budget - 1] < 0) return;            // (a bad page)
+  const int32_t* bt = A.kv.block_table_dev + (size_t)s * A.kv.max_pages;
+  const int P = A.kv.page_size;
+  const size_t page16 = (size_t)A.kv.n_layers * A.kv.n_kv_heads * 2 * P * row16;
+  uint4* base = static_cast<uint4*>(A.kv.kv_dev) + (((size_t)layer * A.kv.n_kv_heads + h) * 2 + blockIdx.y) * P * row16 + c;
+  auto at = [&](int pos) { return base + bt[pos / P] * page16 + (size_t)(pos % P) * row16; };
+  for (int j0 = 0; j0 < A.budget; j0 += ROWS * MV_ROWS) {
+    uint4 v[MV_ROWS];
+    bool mv[MV_ROWS];
+#pragma unroll
+    for (int u = 0; u < MV_ROWS; ++u) {
+      const int j = j0 + u * ROWS + t / SPAN;
+      const int from = j < A.budget ? kept[j] : j;
+      mv[u] = from > j;
+      if (mv[u]) v[u] = *at(from);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < MV_ROWS; ++u) {
+      const int j = j0 + u * ROWS + t / SPAN;
+      if (mv[u]) *at(j) = v[u];
+    }
+  }
+}
+
+template <int SPAN>
+cudaError_t launch_move(const EvictArgs& A, int64_t planes, int row16, cudaStream_t st) {
+  return launch_k(k_evict_move<SPAN>, dim3((unsigned)(planes * (row16 / SPAN)), 2), dim3(MV_THREADS), 0, st, A, row16);
+}
+
+}  // namespace
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" int spec_kv_evict(const spec_kv_view* kv, int n_seq, const int32_t* cache_len_dev, const float* mass_dev, int64_t ld,
+                             int budget, int recent, float* out_mass_dev, int32_t* out_kept_dev, int32_t* out_len_dev,
+                             int32_t* err_dev, uintptr_t cuda_stream) {
+  const int rc = check_chunks(kv, n_seq, kv ? kv->n_kv_heads : 0);
+  if (rc) return rc;
+  if (!cache_len_dev || !mass_dev || !out_mass_dev || !out_kept_dev || !out_len_dev || !err_dev)
+    return set_last_error(SPEC_ERR_ARG, "null pointer argument");
+  if (budget < 1 || recent < 0 || recent > budget) return set_last_error(SPEC_ERR_ARG, "1 <= budget and 0 <= recent <= budget required");
+  if (ld < 1 || ld > ((int64_t)1 << 31)) return set_last_error(SPEC_ERR_ARG, "1 <= ld <= 2^31 required");
+  const int64_t planes = (int64_t)kv->n_layers * n_seq * kv->n_kv_heads;
+  const int row16 = kv->head_dim * (kv->dtype == SPEC_F32 ? 4 : 2) / 16;
+  if (planes * row16 > 0x7fffffff) return set_last_error(SPEC_ERR_UNSUPPORTED, "too many (layer, sequence, head) planes");
+  struct Span { const void* p; int64_t n; };
+  const Span out[4] = {{out_mass_dev, planes * ld * 4}, {out_kept_dev, planes * budget * 4}, {out_len_dev, (int64_t)n_seq * 4},
+                       {kv->kv_dev, cache_bytes(*kv)}};
+  const Span in[3] = {{cache_len_dev, (int64_t)n_seq * 4}, {mass_dev, planes * ld * 4},
+                      {kv->block_table_dev, (int64_t)n_seq * kv->max_pages * 4}};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& b : in)
+      if (spans_meet(out[i].p, out[i].n, b.p, b.n)) return set_last_error(SPEC_ERR_ARG, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (spans_meet(out[i].p, out[i].n, out[j].p, out[j].n)) return set_last_error(SPEC_ERR_ARG, "two outputs overlap");
+  }
+  const EvictArgs A{*kv, cache_len_dev, mass_dev, out_mass_dev, out_kept_dev, out_len_dev, err_dev, ld, n_seq, budget, recent,
+                    (int)std::min<int64_t>(ld, (int64_t)kv->max_pages * kv->page_size)};
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = launch_k(k_evict_select, dim3((unsigned)planes), dim3(EV_THREADS), 0, st, A);
+  if (e == cudaSuccess) e = launch_move<8>(A, planes, row16, st);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
+}

@@ -1,0 +1,315 @@
+// Kernel-level entry point: norm and rotation of new tokens' queries and keys, and
+// the way of their keys and values into the paged cache.
+//
+// A head of d values lies on LPH = d / (16 bytes) lanes, one 16-byte piece each,
+// so that a warp holds one to four heads of a row. A lane's piece is the same in
+// every head, so its cosines and sines are computed once for a row and kind: with
+// gamma folded in, y[i] = r (x[i] C[i] + x'[i] S[i]), x' the partner's piece (a
+// shuffle), r = 1 / sqrt(mean x^2 + eps), C = gamma cos, S = -+ gamma' sin. Pieces
+// behind the rotated dims have C = gamma, S = 0.
+//
+// The angle of position p is p F of a 64-bit turn, F = freq / 2 pi in units of
+// 2^-64 of a turn: the product wraps as the angle does, so it is as exact at
+// position 2^31 as at 1. Its upper 32 bits, reduced to an eighth of a turn either
+// way, go to sincospif.
+//
+// Bound: HBM, by the bytes of the rows.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "chunk.cuh"
+
+namespace spec {
+namespace {
+
+constexpr int RP_THREADS = 256;
+constexpr int RP_TOKENS = 64;                    // tokens whose places a block looks up at once
+constexpr int RP_FLY = 4;                        // heads a lane has in flight
+
+struct RopeArgs {
+  spec_kv_view kv;
+  ChunkIndex ix;
+  const char* qkv;
+  char* q_out;
+  const int32_t* positions;
+  const float* gamma[2];                         // of queries, of keys
+  int32_t* err;
+  long long ld;                                  // bytes of a row
+  int layer, hq, half8;                          // half8: rotated pairs / values of a piece
+  int parts;                                     // lane groups that share a row's heads
+  float eps;
+  uint64_t turn[SPEC_ROPE_MAX_PAIRS];            // freq in 2^-64 turns
+  uint8_t axis[SPEC_ROPE_MAX_PAIRS];
+};
+
+// cos and sin of a turn's 2^-32 parts.
+__device__ __forceinline__ void turn_cos_sin(uint32_t a, float& c, float& s) {
+  const uint32_t quarter = (a + 0x20000000u) >> 30;
+  const int rest = (int)(a - (quarter << 30));   // [-1/8, 1/8) of a turn
+  float s0, c0;
+  sincospif((float)rest * 4.656612873077393e-10f, &s0, &c0);   // 2^-31: half turns
+  const float x = quarter & 1 ? s0 : c0, y = quarter & 1 ? c0 : s0;
+  c = (quarter == 1 || quarter == 2) ? -x : x;
+  s = quarter >= 2 ? -y : y;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+template <int NV>
+__device__ __forceinline__ uint4 pack_piece(const float (&y)[NV]) {
+  uint4 r;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (NV == 4) w[i] = __float_as_uint(y[i]);
+    else w[i] = bf16_pair(y[2 * i], y[2 * i + 1]);
+  }
+  return r;
+}
+
+template <class KT, int D>
+__global__ void __launch_bounds__(RP_THREADS) k_qk_norm_rope(const __grid_constant__ RopeArgs A) {
+  constexpr int NV = Elt<KT>::per16, LPH = D / NV, GROUPS = RP_THREADS / LPH;
+  __shared__ long long w_sum[RP_THREADS / 32];
+  __shared__ long long s_before;
+  __shared__ int s_seq;
+  __shared__ int t_seq[RP_TOKENS], t_row[RP_TOKENS], t_pos[RP_TOKENS], t_page[RP_TOKENS];
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+  pdl_wait();
+  pdl_trigger();
+
+  // this block's tokens: [c T / B, (c + 1) T / B) of all T
+  const int per = (A.ix.n_seq + RP_THREADS - 1) / RP_THREADS;
+  const int a = min(t * per, A.ix.n_seq), a1 = min(a + per, A.ix.n_seq);
+  long long sum = 0;
+  for (int i = a; i < a1; ++i) {
+    const ChunkSeq z(A.ix, i);
+    if (z.bad && blockIdx.x == 0) atomicOr(A.err, DERR_POS);
+    sum += z.m;
+  }
+  long long inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) w_sum[w] = inc;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int i = 0; i < RP_THREADS / 32; ++i) {
+    if (i < w) before += w_sum[i];
+    total += w_sum[i];
+  }
+  const long long blocks = gridDim.x, blk = blockIdx.x;
+  const long long k0 = total / blocks * blk + total % blocks * blk / blocks;
+  const long long k1 = total / blocks * (blk + 1) + total % blocks * (blk + 1) / blocks;
+  if (k0 >= k1) return;
+  long long at = before + inc - sum;
+  if (at <= k0 && k0 < at + sum) {               // one thread's sequences hold token k0
+    int i = a;
+    for (int c; at + (c = ChunkSeq(A.ix, i).m) <= k0; ++i) at += c;
+    s_seq = i;
+    s_before = at;
+  }
+  __syncthreads();
+  int seq = s_seq;                               // warp 0's: where the next token may be, tokens before it
+  long long first = s_before;
+
+  const int g = t / LPH, gl = t % LPH, heads = A.hq + 2 * A.kv.n_kv_heads;
+  const uint32_t gmask = LPH == 32 ? 0xffffffffu : ((1u << (LPH & 31)) - 1) << (lane / LPH * LPH);
+  const int rotated = 2 * A.half8;               // pieces
+  const int partner = gl < A.half8 ? gl + A.half8 : gl < rotated ? gl - A.half8 : gl;
+  const size_t plane16 = (size_t)A.kv.page_size * LPH;
+  uint4* const cache = static_cast<uint4*>(A.kv.kv_dev);
+  for (long long k = k0; k < k1; k += RP_TOKENS) {
+    const int nt = (int)min((long long)RP_TOKENS, k1 - k);
+    __syncthreads();                             // the last tokens' places are read
+    if (w == 0) {
+      // tokens k .. k + nt - 1: sequences 32 at a time, each one's tokens by the whole warp
+      for (;;) {
+        const bool on = seq + lane < A.ix.n_seq;
+        const ChunkSeq z(A.ix, on ? seq + lane : seq);
+        const int m = on ? z.m : 0;
+        long long end = m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += v;
+        }
+        end += first;
+        uint32_t some = __ballot_sync(0xffffffffu, m > 0 && end > k && end - m < k + nt);
+        for (; some; some &= some - 1) {
+          const int l = __ffs(some) - 1;
+          const long long lo = __shfl_sync(0xffffffffu, end - m, l), hi = __shfl_sync(0xffffffffu, end, l);
+          const int n = __shfl_sync(0xffffffffu, z.n, l), r0 = __shfl_sync(0xffffffffu, z.r0, l);
+          for (long long x = max(lo, k) + lane; x < min(hi, k + nt); x += 32) {
+            const int slot = (int)(x - k), i = (int)(x - lo);
+            t_seq[slot] = seq + l;
+            t_row[slot] = r0 + i;
+            t_pos[slot] = n + i;
+          }
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, end > k + nt);
+        if (past) {                              // the next tokens are there
+          const int l = __ffs(past) - 1;
+          first = __shfl_sync(0xffffffffu, end - m, l);
+          seq += l;
+          break;
+        }
+        first = __shfl_sync(0xffffffffu, end, 31);
+        seq += 32;
+        if (first >= k1 || seq >= A.ix.n_seq) break;
+      }
+    }
+    __syncthreads();
+    if (t < nt) {
+      const int pos = t_pos[t];
+      int page = A.kv.block_table_dev[(size_t)t_seq[t] * A.kv.max_pages + pos / A.kv.page_size];
+      if (page < 0 || page >= A.kv.n_pages) {
+        page = -1;
+        atomicOr(A.err, DERR_PAGE);
+      }
+      t_page[t] = page;
+      t_pos[t] = pos % A.kv.page_size;
+    }
+    __syncthreads();
+    // a lane group takes a token's heads share, share + parts, ..
+    for (int x = g; x < nt * A.parts; x += GROUPS) {
+      const int tok = x / A.parts, share = x % A.parts, row = t_row[tok], page = t_page[tok];
+      const char* src = A.qkv + row * A.ld + gl * 16;
+      float c[NV], sn[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        c[i] = 1.f;
+        sn[i] = 0.f;
+      }
+      if (gl < rotated) {
+        const bool low = gl < A.half8;
+        const int p0 = (low ? gl : gl - A.half8) * NV;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int64_t pos = A.positions[(size_t)A.axis[p0 + i] * A.ix.n_rows + row];
+          turn_cos_sin((uint32_t)(((uint64_t)pos * A.turn[p0 + i]) >> 32), c[i], sn[i]);
+          if (low) sn[i] = -sn[i];
+        }
+      }
+      uint4* kd = page < 0 ? nullptr
+                           : cache + (((size_t)page * A.kv.n_layers + A.layer) * A.kv.n_kv_heads * 2) * plane16 +
+                                 (size_t)t_pos[tok] * LPH + gl;
+      uint4* qd = reinterpret_cast<uint4*>(A.q_out) + ((size_t)row * A.hq) * LPH + gl;
+#pragma unroll 1
+      for (int kind = 0; kind < 2; ++kind) {     // queries, then keys
+        const float* gm = A.gamma[kind];
+        float C[NV], S[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          C[i] = gm ? c[i] * __ldg(gm + gl * NV + i) : c[i];
+          S[i] = gm ? sn[i] * __ldg(gm + partner * NV + i) : sn[i];
+        }
+        const int h0 = kind ? A.hq : 0, h1 = kind ? A.hq + A.kv.n_kv_heads : A.hq;
+        for (int h = h0 + share; h < h1; h += A.parts * RP_FLY) {
+          uint4 v[RP_FLY];
+#pragma unroll
+          for (int u = 0; u < RP_FLY; ++u)
+            if (h + u * A.parts < h1) v[u] = ld_stream(src + (size_t)(h + u * A.parts) * LPH * 16);
+#pragma unroll
+          for (int u = 0; u < RP_FLY; ++u) {
+            const int hh = h + u * A.parts;
+            if (hh >= h1) break;
+            float f[NV], o[NV], y[NV];
+            unpack<KT>(v[u], f);
+            float r = 1.f;
+            if (gm) {
+              float ss = 0.f;
+#pragma unroll
+              for (int i = 0; i < NV; ++i) ss = fmaf(f[i], f[i], ss);
+#pragma unroll
+              for (int o2 = 1; o2 < LPH; o2 <<= 1) ss += __shfl_xor_sync(gmask, ss, o2, LPH);
+              r = rsqrtf(ss * (1.f / D) + A.eps);
+            }
+            uint4 pv;
+            pv.x = __shfl_sync(gmask, v[u].x, partner, LPH);
+            pv.y = __shfl_sync(gmask, v[u].y, partner, LPH);
+            pv.z = __shfl_sync(gmask, v[u].z, partner, LPH);
+            pv.w = __shfl_sync(gmask, v[u].w, partner, LPH);
+            unpack<KT>(pv, o);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) y[i] = r * fmaf(f[i], C[i], o[i] * S[i]);
+            const uint4 out = pack_piece<NV>(y);
+            if (kind == 0) qd[(size_t)hh * LPH] = out;
+            else if (kd) kd[(size_t)(hh - A.hq) * 2 * plane16] = out;
+          }
+        }
+      }
+      const int v0 = A.hq + A.kv.n_kv_heads;
+      if (kd)
+        for (int h = v0 + share; h < heads; h += A.parts)
+          kd[((size_t)(h - v0) * 2 + 1) * plane16] = ld_stream(src + (size_t)h * LPH * 16);
+    }
+  }
+}
+
+template <class KT, int D>
+cudaError_t launch_rope(const RopeArgs& A, int blocks, cudaStream_t st) {
+  return launch_k(k_qk_norm_rope<KT, D>, dim3(blocks), dim3(RP_THREADS), 0, st, A);
+}
+
+}  // namespace
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* qkv_dev, int64_t ld, int n_rows, int n_seq,
+                                 int n_q_heads, const int32_t* row_start_dev, const int32_t* n_new_dev,
+                                 const int32_t* cache_len_dev, const spec_rope* rope, const int32_t* positions_dev,
+                                 const float* q_gamma_dev, const float* k_gamma_dev, float eps, void* q_out_dev,
+                                 int32_t* err_dev, uintptr_t cuda_stream) {
+  int rc = check_chunks(kv, n_seq, n_q_heads);
+  if (rc == SPEC_OK) rc = check_layer_rows(kv, layer, n_rows, 1);
+  if (rc) return rc;
+  if (!qkv_dev || !row_start_dev || !n_new_dev || !cache_len_dev || !rope || !q_out_dev || !err_dev)
+    return set_last_error(SPEC_ERR_ARG, "null pointer argument");
+  const int esz = kv->dtype == SPEC_F32 ? 4 : 2, d = kv->head_dim;
+  const int64_t heads = (int64_t)n_q_heads + 2 * (int64_t)kv->n_kv_heads;
+  if (heads > (1 << 20)) return set_last_error(SPEC_ERR_UNSUPPORTED, "more than 2^20 heads");
+  if (ld < heads * d || ld % (16 / esz) || ld > ((int64_t)1 << 40))
+    return set_last_error(SPEC_ERR_ARG, "ld: at least a row's heads, a multiple of 16 bytes");
+  if (!aligned16(qkv_dev) || !aligned16(q_out_dev)) return set_last_error(SPEC_ERR_ARG, "qkv and q must be 16-byte aligned");
+  if (!(eps >= 0.f) || !(eps < INFINITY)) return set_last_error(SPEC_ERR_ARG, "eps must be finite and not negative");
+  if (rope->dim < 0 || rope->dim > d || rope->dim % 16) return set_last_error(SPEC_ERR_ARG, "rope dim: a multiple of 16 up to head_dim");
+  if (rope->n_axes < 1 || rope->n_axes > SPEC_ROPE_MAX_AXES) return set_last_error(SPEC_ERR_ARG, "1 to 4 axes");
+  if (rope->dim > 0 && !positions_dev) return set_last_error(SPEC_ERR_ARG, "null positions");
+  RopeArgs A{*kv, ChunkIndex{row_start_dev, n_new_dev, cache_len_dev, n_seq, n_rows, n_rows, kv->max_pages * kv->page_size},
+             static_cast<const char*>(qkv_dev), static_cast<char*>(q_out_dev), positions_dev, {q_gamma_dev, k_gamma_dev},
+             err_dev, ld * esz, layer, n_q_heads, rope->dim / 2 / (16 / esz), 1, eps, {}, {}};
+  for (int p = 0; p < rope->dim / 2; ++p) {
+    if (!std::isfinite(rope->freq[p])) return set_last_error(SPEC_ERR_ARG, "a frequency is not finite");
+    if (rope->axis[p] >= rope->n_axes) return set_last_error(SPEC_ERR_ARG, "a pair's axis is out of range");
+    double turn = rope->freq[p] / 6.283185307179586476925286766559;
+    turn -= std::floor(turn);                    // [0, 1]: whole turns do not matter
+    A.turn[p] = turn < 1.0 ? (uint64_t)std::ldexp(turn, 64) : 0;
+    A.axis[p] = rope->axis[p];
+  }
+  const int64_t in_bytes = ((n_rows - 1) * ld + heads * d) * esz, q_bytes = (int64_t)n_rows * n_q_heads * d * esz;
+  if (spans_meet(q_out_dev, q_bytes, qkv_dev, in_bytes) || spans_meet(q_out_dev, q_bytes, kv->kv_dev, cache_bytes(*kv)))
+    return set_last_error(SPEC_ERR_ARG, "q_out overlaps qkv or the cache");
+  if (spans_meet(qkv_dev, in_bytes, kv->kv_dev, cache_bytes(*kv))) return set_last_error(SPEC_ERR_ARG, "qkv overlaps the cache");
+  const int sms = sm_count_once();
+  if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
+  // few rows: each group of lanes takes RP_FLY heads of one; many: as many parts as keep the SMs full
+  const int groups = RP_THREADS / (d * esz / 16), most = (n_q_heads + RP_FLY - 1) / RP_FLY;
+  const int64_t room = (int64_t)sms * 8 * groups;
+  A.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, room / n_rows));
+  const int blocks = (int)std::min<int64_t>(((int64_t)n_rows * A.parts + groups - 1) / groups, sms * 8);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e;
+  if (esz == 2) e = d == 128 ? launch_rope<bf16_t, 128>(A, blocks, st) : launch_rope<bf16_t, 64>(A, blocks, st);
+  else e = d == 128 ? launch_rope<float, 128>(A, blocks, st) : launch_rope<float, 64>(A, blocks, st);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
+}
