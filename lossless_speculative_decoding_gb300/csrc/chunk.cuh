@@ -53,4 +53,12 @@ inline int check_layer_rows(const spec_kv_view* kv, int layer, int n_rows, int m
   return SPEC_OK;
 }
 
+// bf16 chunks of few tokens, by the tree attention's kernel (ops_tree.cu): at most
+// SPEC_TREE_MAX_NODES tokens of a sequence and 128 (token, head) rows per kv head. The
+// arguments are checked already.
+size_t chain_ws_bytes(const spec_kv_view& kv, int max_new, int hq);
+int launch_chain_attention(const spec_kv_view& kv, int layer, const void* q, int n_rows, int n_seq, int max_new, int hq,
+                           const int32_t* row_start, const int32_t* n_new, const int32_t* cache_len, float scale_l2e,
+                           void* out, float* lse, void* ws, int32_t* err, int sms, cudaStream_t st);
+
 }  // namespace spec

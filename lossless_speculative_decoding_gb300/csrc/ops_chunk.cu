@@ -24,7 +24,6 @@ namespace spec {
 namespace {
 
 constexpr int CH_MAX_G = 128;                    // query heads per kv head
-constexpr float LN2 = 0.6931471805599453f;
 
 struct ChunkArgs {
   spec_kv_view kv;
@@ -448,7 +447,13 @@ struct ChunkPlan {
   int rows, tile_k;
   int max_blocks;           // of any grid (the workspace is sized without a device)
   size_t ml, joint, total;  // workspace: outputs at 0, statistics, joints
+  bool chain;               // few tokens: the tree attention's kernel, each node the next one's parent
   ChunkPlan(const spec_kv_view& kv, int max_new, int hq) {
+    chain = kv.dtype == SPEC_BF16 && max_new <= SPEC_TREE_MAX_NODES && max_new * (hq / kv.n_kv_heads) <= 128;
+    if (chain) {
+      total = chain_ws_bytes(kv, max_new, hq);
+      return;
+    }
     rows = CF_ROWS;
     tile_k = CF_KEYS;
     max_blocks = 320;       // two blocks per SM
@@ -509,12 +514,15 @@ extern "C" int spec_chunk_attention(const spec_kv_view* kv, int layer, const voi
   if (ws_bytes < plan.total) return set_last_error(SPEC_ERR_ARG, "workspace too small");
   const int sms = sm_count_once();
   if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
+  if (plan.chain)
+    return launch_chain_attention(*kv, layer, q_dev, n_rows, n_seq, max_new, n_q_heads, row_start_dev, n_new_dev, cache_len_dev,
+                                  scale * LOG2E, out_dev, out_lse_dev, ws_dev, err_dev, sms, st);
   char* w = static_cast<char*>(ws_dev);
   const ChunkArgs A{*kv, ChunkIndex{row_start_dev, n_new_dev, cache_len_dev, n_seq, n_rows, max_new, kv->max_pages * kv->page_size},
                     q_dev, out_dev, out_lse_dev, err_dev, reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + plan.ml),
                     reinterpret_cast<int4*>(w + plan.joint), layer, n_q_heads, n_q_heads / kv->n_kv_heads, plan.rows,
                     plan.tile_k, scale * LOG2E};
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   const int blocks = std::min(2 * sms, plan.max_blocks);
   cudaError_t e;
   if (kv->dtype == SPEC_F32) e = d == 128 ? launch_fma<128, float>(A, blocks, st) : launch_fma<64, float>(A, blocks, st);

@@ -35,30 +35,50 @@ struct TreeArgs {
   void* out;
   const int32_t* cache_len;
   const int32_t* n_nodes;
-  const int32_t* parents;
+  const int32_t* parents;        // of a chunk (CHAIN): null, node i's parent is i - 1
+  const int32_t* row_start;      // first row of each sequence's nodes; null: s max_nodes
+  float* lse;                    // chunks: log sum exp of each row, or null
   int32_t* err;
   float* part_o;       // [blocks][2][rows][d]: part 0 of a block began in an earlier block, part 1 goes on in the next
   float2* part_ml;     // [blocks][2][rows]: maximum (log2 units), sum
   int4* joint;         // [blocks]: (sequence, row tile, kv head, parts and rows) of the shared segment that starts in a block
   int layer, n_seq, max_nodes, hq, G;
+  int n_rows;          // rows of q and out
   int rows;            // rows of a tile
   int q_box;           // rows of a box of the query's tensor map (tensor-core form)
   int tile_k;          // keys of a unit
   float scale_l2e;     // scale * log2 e
 };
 
+// Sizes of sequence s (k = 0: padded, or bad). A chunk's rows have to be there too.
+template <bool CHAIN>
 __device__ __forceinline__ TreeSize tree_size(const TreeArgs& A, int s) {
-  return TreeSize(A.cache_len, A.n_nodes, s, A.max_nodes, A.kv.max_pages * A.kv.page_size);
+  TreeSize z(A.cache_len, A.n_nodes, s, A.max_nodes, A.kv.max_pages * A.kv.page_size);
+  if constexpr (CHAIN) {
+    if (A.n_nodes[s] == 0) z.bad = false;
+    if (z.k > 0) {
+      const int r0 = A.row_start[s];
+      z.bad = r0 < 0 || z.k > A.n_rows || r0 > A.n_rows - z.k;
+      if (z.bad) z.k = 0;
+    }
+  }
+  return z;
+}
+template <bool CHAIN>
+__device__ __forceinline__ int tree_row0(const TreeArgs& A, int s) {
+  return CHAIN ? A.row_start[s] : s * A.max_nodes;
 }
 
 // Segment: tiles [t0, t1) of nt key tiles of (sequence s, row tile rt, kv head hk).
 struct TreeSeg {
   int s, rt, hk, nt, t0, t1;
   int n, k;                                      // committed positions, nodes
+  int r0;                                        // row of its first node
 };
 
 // A block's walk over its units. All threads of the block call init (it has
 // block barriers); next() is called by whole warps.
+template <bool CHAIN>
 struct TreeWalk {
   long long u, u1, U;                            // units left: [u, u1) of U
   int blocks;                                    // blocks that have units (no more than there are units)
@@ -66,7 +86,7 @@ struct TreeWalk {
   const TreeArgs* A;
 
   __device__ static int units_of(const TreeArgs& A, int s) {
-    const TreeSize z = tree_size(A, s);
+    const TreeSize z = tree_size<CHAIN>(A, s);
     if (z.k == 0) return 0;
     const int nt = (z.n + z.k + A.tile_k - 1) / A.tile_k, nrt = (z.k * A.G + A.rows - 1) / A.rows;
     return nt * nrt * A.kv.n_kv_heads;           // checked on the host to stay below 2^31
@@ -117,7 +137,7 @@ struct TreeWalk {
   }
   __device__ bool next(TreeSeg& g) {
     if (u >= u1) return false;
-    TreeSize z = tree_size(*A, s);
+    TreeSize z = tree_size<CHAIN>(*A, s);
     for (;;) {
       if (z.k > 0) {
         g.nt = (z.n + z.k + A->tile_k - 1) / A->tile_k;
@@ -128,17 +148,18 @@ struct TreeWalk {
       for (++s;; s += 32) {
         if (s >= A->n_seq) return false;         // (only if the lengths changed meanwhile)
         const int i = s + (threadIdx.x & 31);
-        const uint32_t live = __ballot_sync(0xffffffffu, i < A->n_seq && tree_size(*A, i).k > 0);
+        const uint32_t live = __ballot_sync(0xffffffffu, i < A->n_seq && tree_size<CHAIN>(*A, i).k > 0);
         if (live) {
           s += __ffs(live) - 1;
           break;
         }
       }
-      z = tree_size(*A, s);
+      z = tree_size<CHAIN>(*A, s);
     }
     g.s = s;
     g.n = z.n;
     g.k = z.k;
+    g.r0 = tree_row0<CHAIN>(*A, s);
     const int seg = in / g.nt;
     g.rt = seg / A->kv.n_kv_heads;
     g.hk = seg % A->kv.n_kv_heads;
@@ -209,12 +230,12 @@ __global__ void __launch_bounds__(FM_THREADS) k_tree_fma(const __grid_constant__
   const int P = A.kv.page_size;
   pdl_wait();
   pdl_trigger();
-  TreeWalk walk;
+  TreeWalk<false> walk;
   walk.init<FM_THREADS>(A);
   if (t == 0) A.joint[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (blockIdx.x == 0)
     for (int s = t; s < A.n_seq; s += FM_THREADS)
-      if (tree_size(A, s).bad) atomicOr(A.err, DERR_POS);
+      if (tree_size<false>(A, s).bad) atomicOr(A.err, DERR_POS);
   const size_t page_elems = (size_t)A.kv.n_layers * A.kv.n_kv_heads * 2 * P * D;
   TreeSeg g;
   while (walk.next(g)) {
@@ -582,7 +603,7 @@ __device__ __noinline__ TtLane tt_chunks_wide(TtTile T, int c, int c1, TtLane a)
   return a;
 }
 
-template <int D>
+template <int D, bool CHAIN>
 __global__ void __launch_bounds__(TT_THREADS, 1)
     k_tree_tc(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
               const __grid_constant__ TreeArgs A, int kb) {
@@ -630,10 +651,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   if (t == 0) A.joint[blockIdx.x] = make_int4(0, 0, 0, 0);
   if (blockIdx.x == 0)
     for (int s = t; s < A.n_seq; s += TT_THREADS)
-      if (tree_size(A, s).bad) atomicOr(A.err, DERR_POS);
-  TreeWalk walk;
+      if (tree_size<CHAIN>(A, s).bad) atomicOr(A.err, DERR_POS);
+  TreeWalk<CHAIN> walk;
   tc_fence_before();
-  walk.init<TT_THREADS>(A);                      // two block barriers
+  walk.template init<TT_THREADS>(A);                      // two block barriers
   tc_fence_after();
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other
@@ -804,11 +825,13 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (!have) break;
       const TtRows R(A, g);
       const bool tree = g.t1 * TT_KEYS > g.n;    // the segment reaches the tree's slots
-      const int32_t* par = A.parents + (size_t)g.s * A.max_nodes;
       int p[2] = {-1, -1};
+      if constexpr (!CHAIN) {
+        const int32_t* par = A.parents + (size_t)g.s * A.max_nodes;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (tree && lane + 32 * u < g.k) p[u] = par[lane + 32 * u];
+        for (int u = 0; u < 2; ++u)
+          if (tree && lane + 32 * u < g.k) p[u] = par[lane + 32 * u];
+      }
       if (seg > 0 && !__all_sync(0xffffffffu, wait(&H.q_free, seg - 1))) continue;   // (aborted: no more copies)
       const int nrep = 128 / R.rpp, copies = R.boxes * nrep * HALVES;
       if (lane == 0)
@@ -822,10 +845,14 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
             "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
             ::"r"(q_addr + half * TT_HALF + (x * A.q_box + rp * R.rpp) * 128),
               "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(0), "r"(half), "r"(g.hk * A.G),
-              "r"(g.s * A.max_nodes + (R.row0 + x * A.q_box) / A.G), "r"(sm_addr(&H.q_full))
+              "r"(g.r0 + (R.row0 + x * A.q_box) / A.G), "r"(sm_addr(&H.q_full))
             : "memory");
       }
-      if (tree) {
+      if (CHAIN && tree) {
+#pragma unroll 1
+        for (int i = lane; i < g.k; i += 32) H.mask[sb][i] = ~0ull >> (63 - i);
+        __syncwarp();
+      } else if (tree) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int i = lane + 32 * u;
@@ -917,7 +944,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
         const int rr = R.row0 + x, node = rr / A.G;
         if (wpart < 0)
           return static_cast<unsigned char*>(A.out) +
-                 (((size_t)g.s * A.max_nodes + node) * A.hq + g.hk * A.G + rr - node * A.G) * D * 2;
+                 (((size_t)g.r0 + node) * A.hq + g.hk * A.G + rr - node * A.G) * D * 2;
         return reinterpret_cast<unsigned char*>(A.part_o + (((size_t)blockIdx.x * 2 + wpart) * A.rows + x) * D);
       };
       auto emit4 = [&](unsigned char* o, int col, float4 v) {
@@ -944,6 +971,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       const float w0 = ex2(H.ml[0][r].x - Mb) * inv, w1 = ex2(H.ml[1][r].x - Mb) * inv;
       if (wpart >= 0 && slot == 0 && live && rep == 0)
         A.part_ml[((size_t)blockIdx.x * 2 + wpart) * A.rows + lr] = make_float2(M, L);
+      if (CHAIN && wpart < 0 && A.lse && slot == 0 && live && rep == 0) {
+        const int rr = R.row0 + lr, node = rr / A.G;
+        A.lse[((size_t)g.r0 + node) * A.hq + g.hk * A.G + rr - node * A.G] = (M + log2f(L)) * LN2;
+      }
       // 16 columns at a time through shared memory: a row's repetitions are
       // summed, and four lanes write 64 bytes of a row together. Each group takes
       // half of the columns, of both slots.
@@ -1015,7 +1046,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
 // entry point takes its workspace as it comes.)
 constexpr int JOIN_WARPS = 8;
 
-template <int D, class KT>
+template <int D, class KT, bool CHAIN>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) k_tree_join(const __grid_constant__ TreeArgs A) {
   pdl_wait();
   pdl_trigger();
@@ -1060,7 +1091,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) k_tree_join(const __grid_cons
     if ((c0 += FLY) >= parts) break;
     fetch(c0);
   }
-  KT* og = static_cast<KT*>(A.out) + (((size_t)jt.x * A.max_nodes + rr / A.G) * A.hq + jt.z * A.G + rr % A.G) * D + NV * lane;
+  const size_t row = ((size_t)tree_row0<CHAIN>(A, jt.x) + rr / A.G) * A.hq + jt.z * A.G + rr % A.G;
+  KT* og = static_cast<KT*>(A.out) + row * D + NV * lane;
+  if (CHAIN && A.lse && lane == 0) A.lse[row] = (M + log2f(l)) * LN2;
   const float inv = 1.f / l;
 #pragma unroll
   for (int i = 0; i < NV; ++i) o[i] *= inv;
@@ -1122,27 +1155,55 @@ int check_tree(const spec_kv_view* kv, int n_seq, int max_nodes, int hq) {
   return SPEC_OK;
 }
 
-template <int D, class KT>
+template <int D, class KT, bool CHAIN>
 cudaError_t join(const TreeArgs& A, int blocks, cudaStream_t st) {
-  return launch_k(k_tree_join<D, KT>, dim3(blocks, (A.rows + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0, st, A);
+  return launch_k(k_tree_join<D, KT, CHAIN>, dim3(blocks, (A.rows + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0, st, A);
 }
 
 template <int D>
 cudaError_t launch_fma(const TreeArgs& A, int blocks, cudaStream_t st) {
   cudaError_t e = allow_dyn_smem_once<k_tree_fma<D>>();
   if (e == cudaSuccess) e = launch_k(k_tree_fma<D>, dim3(blocks), dim3(FM_THREADS), sizeof(FmSmem<D>), st, A);
-  return e == cudaSuccess ? join<D, float>(A, blocks, st) : e;
+  return e == cudaSuccess ? join<D, float, false>(A, blocks, st) : e;
 }
 
-template <int D>
+template <int D, bool CHAIN>
 cudaError_t launch_tc(const TreeArgs& A, const CUtensorMap& map, const CUtensorMap& qmap, int kb, int blocks, cudaStream_t st) {
-  cudaError_t e = allow_dyn_smem_once<k_tree_tc<D>>();
+  cudaError_t e = allow_dyn_smem_once<k_tree_tc<D, CHAIN>>();
   if (e == cudaSuccess)
-    e = launch_k(k_tree_tc<D>, dim3(blocks), dim3(TT_THREADS), TtCfg<D>::SMEM, st, map, qmap, A, kb);
-  return e == cudaSuccess ? join<D, bf16_t>(A, blocks, st) : e;
+    e = launch_k(k_tree_tc<D, CHAIN>, dim3(blocks), dim3(TT_THREADS), TtCfg<D>::SMEM, st, map, qmap, A, kb);
+  return e == cudaSuccess ? join<D, bf16_t, CHAIN>(A, blocks, st) : e;
+}
+
+// A box of keys never straddles pages: the largest power of two up to a tile that divides a page.
+int key_box(int page_size) {
+  int kb = 16;
+  while (kb < TT_KEYS && page_size % (2 * kb) == 0) kb *= 2;
+  return kb;
 }
 
 }  // namespace
+
+size_t chain_ws_bytes(const spec_kv_view& kv, int max_new, int hq) { return TreePlan(kv, max_new, hq).total; }
+
+int launch_chain_attention(const spec_kv_view& kv, int layer, const void* q, int n_rows, int n_seq, int max_new, int hq,
+                           const int32_t* row_start, const int32_t* n_new, const int32_t* cache_len, float scale_l2e,
+                           void* out, float* lse, void* ws, int32_t* err, int sms, cudaStream_t st) {
+  const TreePlan plan(kv, max_new, hq);
+  char* w = static_cast<char*>(ws);
+  const TreeArgs A{kv, q, out, cache_len, n_new, nullptr, row_start, lse, err, reinterpret_cast<float*>(w),
+                   reinterpret_cast<float2*>(w + plan.ml), reinterpret_cast<int4*>(w + plan.joint), layer, n_seq, max_new, hq,
+                   hq / kv.n_kv_heads, n_rows, plan.rows, plan.q_box, plan.tile_k, scale_l2e};
+  const int kb = key_box(kv.page_size), d = kv.head_dim, blocks = std::min(sms, plan.max_blocks);
+  CUtensorMap map, qmap;
+  if (q_make_map(&qmap, q, d, hq, (uint64_t)n_rows, A.G, plan.q_box / A.G) ||
+      kv_make_group_map(&map, kv.kv_dev, d, kv.page_size, (uint64_t)kv.n_pages * kv.n_layers * kv.n_kv_heads * 2, kb))
+    return set_last_error(SPEC_ERR_UNSUPPORTED, "tensor map encoding failed");
+  cudaError_t e = d == 128 ? launch_tc<128, true>(A, map, qmap, kb, blocks, st) : launch_tc<64, true>(A, map, qmap, kb, blocks, st);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
+}
+
 }  // namespace spec
 
 using namespace spec;
@@ -1171,21 +1232,20 @@ extern "C" int spec_tree_attention(const spec_kv_view* kv, int layer, const void
   const int sms = sm_count_once();
   if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
   char* w = static_cast<char*>(ws_dev);
-  const TreeArgs A{*kv, q_dev, out_dev, cache_len_dev, n_nodes_dev, parents_dev, err_dev, reinterpret_cast<float*>(w),
-                   reinterpret_cast<float2*>(w + plan.ml), reinterpret_cast<int4*>(w + plan.joint), layer, n_seq,
-                   max_nodes, n_q_heads, n_q_heads / kv->n_kv_heads, plan.rows, plan.q_box, plan.tile_k, scale * LOG2E};
+  const TreeArgs A{*kv, q_dev, out_dev, cache_len_dev, n_nodes_dev, parents_dev, nullptr, nullptr, err_dev,
+                   reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + plan.ml), reinterpret_cast<int4*>(w + plan.joint),
+                   layer, n_seq, max_nodes, n_q_heads, n_q_heads / kv->n_kv_heads, n_seq * max_nodes, plan.rows, plan.q_box,
+                   plan.tile_k, scale * LOG2E};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   const int blocks = std::min((plan.tc ? 1 : 2) * sms, plan.max_blocks);
   cudaError_t e;
   if (plan.tc) {
-    // a box never straddles pages: the largest power of two up to a tile that divides a page
-    int kb = 16;
-    while (kb < TT_KEYS && kv->page_size % (2 * kb) == 0) kb *= 2;
+    const int kb = key_box(kv->page_size);
     CUtensorMap map, qmap;
     if (q_make_map(&qmap, q_dev, d, n_q_heads, (uint64_t)n_seq * max_nodes, A.G, plan.q_box / A.G) ||
         kv_make_group_map(&map, kv->kv_dev, d, kv->page_size, (uint64_t)kv->n_pages * kv->n_layers * kv->n_kv_heads * 2, kb))
       return set_last_error(SPEC_ERR_UNSUPPORTED, "tensor map encoding failed");
-    e = d == 128 ? launch_tc<128>(A, map, qmap, kb, blocks, st) : launch_tc<64>(A, map, qmap, kb, blocks, st);
+    e = d == 128 ? launch_tc<128, false>(A, map, qmap, kb, blocks, st) : launch_tc<64, false>(A, map, qmap, kb, blocks, st);
   } else {
     e = d == 128 ? launch_fma<128>(A, blocks, st) : launch_fma<64>(A, blocks, st);
   }
