@@ -442,6 +442,549 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
   }
 }
 
+// ---------------------------------------------------------------------------
+// Tensor-core form (bf16 cache). One block per SM, eleven warps: a TMA producer of
+// keys and values, an MMA issuer, a loader (segments and their queries) and two
+// softmax groups of four warps. A tile has two groups of up to 128 rows (whole
+// tokens), which share each tile of 128 keys. S = Q K^T (128 x 128) of a group goes to
+// its half of tensor memory; a softmax thread owns a row (a TMEM lane), reads its
+// scores 32 at a time and writes the weights over them as bf16; O += P V takes them
+// from there, V as an MN-major operand. In issue order
+//   P V of group 0, tile i - 1; S of group 0, tile i; the same of group 1; ..
+// so that one group's exponentials run beside the other's MMAs. MMAs of one thread
+// execute in the order of their issue: S may go over the weights that the P V before
+// it reads, and a barrier that S completes tells that this P V is over too.
+//
+// A weight is 2^(x - m) with a whole number m, set 24 above the first scores' maximum:
+// weights are floats, whose precision another m leaves as it is, so no maximum is
+// looked for afterwards. A chunk of 32 scores whose weights sum past 2^9 (a score grew
+// by some 30 binary orders), or to no number, is done again by ch_slow, which moves m
+// and rescales O and the tile's earlier weights. Scores beyond 2^24, above which float
+// does not hold every whole number, are taken against the row's largest score itself,
+// also there. Rounding a weight to bf16 costs 2^-9 relative at most in each term, as
+// much as rounding the result does; the sum of weights is of the fp32 values.
+constexpr int CT_KEYS = 128;
+constexpr int CT_THREADS = 352;
+constexpr int CT_HALF = 128 * 128;               // bytes of 64 dims of 128 rows of Q
+constexpr int CT_OCOL = 256;                     // TMEM columns: S of a group at 128 g, its O behind at CT_OCOL + D g
+constexpr float CT_AHEAD = 24.f;                 // m is set to a score + 24
+constexpr float CT_MUCH = 512.f;                 // a chunk's weights sum to less while m stays
+constexpr float CT_GROW = 8.f;                   // and m moves where a score passes m - 24 + 32
+constexpr float CT_FAR = 16777216.f;             // scores up to here go by m alone
+
+template <int D>
+struct CtCfg {
+  static constexpr int BUF = CT_KEYS * D * 2;    // K or V of a tile
+  static constexpr int Q = 128 * D * 2;          // a group's queries
+  static constexpr int TAIL = 2048;              // alignment slack and the header
+  static constexpr int NBUF = (232448 - 512 - TAIL - 2 * Q) / BUF < 8 ? (232448 - 512 - TAIL - 2 * Q) / BUF : 8;
+  static constexpr int SMEM = NBUF * BUF + 2 * Q + TAIL;
+};
+
+template <int NBUF>
+struct CtHeader {
+  uint64_t kv_full[NBUF], kv_empty[NBUF], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2];
+  uint64_t q_full, q_free, fin;
+  uint32_t tmem;
+  int abort;
+  ChunkSeg seg[2];                               // nt = 0: no more
+};
+
+// Rows of group g of a segment, and the key tiles from t0 on that one of them sees.
+struct CtGroup {
+  int row0, rows, tiles, end;                    // first row, rows, tiles, positions that the last row sees
+  __device__ CtGroup(const ChunkArgs& A, const ChunkSeg& s, int g) {
+    const int rpg = A.rows / 2;
+    row0 = s.rt * A.rows + g * rpg;
+    rows = max(0, min(rpg, s.m * A.G - row0));
+    end = rows ? s.n + (row0 + rows - 1) / A.G + 1 : 0;
+    tiles = max(0, min(s.t1, (end + CT_KEYS - 1) / CT_KEYS) - s.t0);
+  }
+};
+
+// A lane's row of a segment so far: weights are 2^(sc (S - s0) - m), l their sum. s0
+// is 0, or the largest score (m = CT_AHEAD).
+struct CtLane {
+  float m, l, s0;
+};
+// Its scores of a tile.
+struct CtTile {
+  uint32_t s, o;               // tensor memory of S and O
+  float sc;                    // scale * log2 e
+  int seen;                    // keys of the tile that the row sees
+  bool first, live;            // no O yet; a row
+};
+
+__device__ __forceinline__ void ct_mask(uint32_t (&v)[32], int seen) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i >= seen) v[i] = 0xff800000u;
+}
+
+// Weights of one chunk in the place of its scores, whatever they are. Out of line:
+// a segment's first chunk, and rare ones.
+template <int D>
+__device__ __noinline__ CtLane ch_slow(CtTile T, int c, CtLane a) {
+  uint32_t v[32];
+  tmem_ld32(T.s + 32 * c, v);
+  ct_mask(v, T.seen - 32 * c);
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+  const float mt = (mx - a.s0) * T.sc;
+  const bool far = a.s0 != 0.f, grow = T.live && (far ? mx > a.s0 : mt > a.m + CT_GROW);
+  if (__any_sync(0xffffffffu, grow)) {
+    float corr = 1.f;
+    if (grow && (far || !(fabsf(mt) <= CT_FAR))) {   // (the score itself, so that equal ones differ by 0)
+      corr = ex2(a.m - mt - CT_AHEAD);
+      a.m = CT_AHEAD;
+      a.s0 = mx;
+    } else if (grow) {
+      const float to = ceilf(mt) + CT_AHEAD, by = to - a.m;
+      corr = by < 127.f ? __uint_as_float((127 - (int)by) << 23) : 0.f;    // 2^-by, exact
+      a.m = to;
+    }
+    a.l *= corr;
+    tmem_wait_st();                              // the chunks' weights are read back
+    if (!T.first) {                              // (the tile's S came after the group's last P V)
+#pragma unroll 1
+      for (int i = 0; i < D; i += 16) {
+        uint32_t o[16];
+        tmem_ld16(T.o + i, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+        tmem_st16(T.o + i, o);
+      }
+    }
+#pragma unroll 1
+    for (int i = 0; i < c; ++i) {
+      uint32_t w[16];
+      tmem_ld16(T.s + 32 * i, w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        w[j] = pack_bf16(__uint_as_float(w[j] << 16) * corr, __uint_as_float(w[j] & 0xFFFF0000u) * corr);
+      tmem_st16(T.s + 32 * i, w);
+    }
+  }
+  const float mb = a.m == -INFINITY ? 0.f : a.m;
+  float sum = 0.f;
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float p0 = ex2(fmaf(__uint_as_float(v[i]) - a.s0, T.sc, -mb)), p1 = ex2(fmaf(__uint_as_float(v[i + 1]) - a.s0, T.sc, -mb));
+    sum += p0 + p1;
+    w[i / 2] = pack_bf16(p0, p1);
+  }
+  tmem_st16(T.s + 32 * c, w);
+  a.l += sum;
+  return a;
+}
+
+template <int D>
+__global__ void __launch_bounds__(CT_THREADS, 1)
+    k_chunk_tc(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
+               const __grid_constant__ ChunkArgs A, int kb) {
+  using C = CtCfg<D>;
+  constexpr int HALVES = D / 64, NBUF = C::NBUF;
+  // a K or V tile lies as [8 keys][64-dim half][key][64 dims], as a box of whole pages brings it
+  constexpr int GROUP = 1024 * HALVES;
+  extern __shared__ unsigned char ct_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(ct_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* qsm = base + NBUF * C::BUF;
+  CtHeader<NBUF>& H = *reinterpret_cast<CtHeader<NBUF>*>(qsm + 2 * C::Q);
+  static_assert(sizeof(CtHeader<NBUF>) + 1024 <= C::TAIL, "header and alignment slack");
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const uint32_t bufs = sm_addr(base), q_addr = sm_addr(qsm);
+  if (t == 0) {
+    for (int i = 0; i < NBUF; ++i) {
+      mbar_init(H.kv_full + i, 1);
+      mbar_init(H.kv_empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(H.s_full + i, 1);
+      mbar_init(H.p_full + i, 4);
+      mbar_init(H.o_done + i, 1);
+      mbar_init(H.seg_full + i, 1);
+      mbar_init(H.seg_free + i, 8);              // the softmax warps
+    }
+    mbar_init(&H.q_full, 1);
+    mbar_init(&H.q_free, 1);                     // a segment's last S
+    mbar_init(&H.fin, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    H.abort = 0;
+  }
+  if (t == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kvmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&H.tmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (t == 0) A.joint[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (blockIdx.x == 0)
+    for (int s = t; s < A.ix.n_seq; s += CT_THREADS)
+      if (ChunkSeq(A.ix, s).bad) atomicOr(A.err, DERR_POS);
+  ChunkWalk walk;
+  tc_fence_before();
+  walk.init<CT_THREADS>(A);                      // two block barriers
+  tc_fence_after();
+  const uint32_t tmem = H.tmem;
+  // A wait that runs out raises the block's abort flag, which ends its other waits
+  // at once: producer, issuer and loader stop, the softmax warps finish the segment
+  // without a result and stop.
+  auto wait = [&](const uint64_t* bar, uint32_t parity) {
+    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err);
+  };
+  auto waitw = [&](const uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+  const int P = A.kv.page_size;
+
+  if (warp == 8) {
+    // ---- producer: K, V, K, V, .. of the tiles, a box for each kb keys of a page ----
+    const int nbox = CT_KEYS / kb, j = lane;
+    const int planes = A.kv.n_layers * A.kv.n_kv_heads * 2;
+    int b = 0;
+    uint32_t turn = 0;                           // passes over the ring
+    bool ok = true;
+    ChunkSeg g;
+    while (ok && walk.next(g)) {
+      const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
+      const int plane = (A.layer * A.kv.n_kv_heads + g.hk) * 2;
+      auto page_of = [&](int tile) {             // of this lane's box; -1 reads zeros
+        const int key = tile * CT_KEYS + kb * j;
+        int page = -1;
+        if (lane < nbox && tile < g.t1 && key < g.n + g.m) {
+          page = bt[key / P];
+          if (page < 0 || page >= A.kv.n_pages) {
+            page = -1;
+            atomicOr(A.err, DERR_PAGE);
+          }
+        }
+        return page;
+      };
+      int page = page_of(g.t0), next = page_of(g.t0 + 1);
+      for (int i = 0, n = 2 * (g.t1 - g.t0); i < n; ++i) {
+        const int tile = g.t0 + i / 2, key = tile * CT_KEYS + kb * j, v = i & 1;
+        if (!v && i > 0) {
+          page = next;
+          next = page_of(tile + 1);
+        }
+        if (turn > 0 && !waitw(H.kv_empty + b, turn - 1)) { ok = false; break; }
+        const uint32_t full = sm_addr(H.kv_full + b);
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"((uint32_t)C::BUF) : "memory");
+        __syncwarp();
+        if (lane < nbox)
+          asm volatile(
+              "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
+              ::"r"(bufs + b * C::BUF + j * kb * D * 2), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0), "r"(key % P / 8),
+                "r"(page < 0 ? -1 : page * planes + plane + v), "r"(full)
+              : "memory");
+        if (++b == NBUF) { b = 0; ++turn; }
+      }
+    }
+    // shared memory outlives the copies (over, unless the issuer gave up a wait): each buffer's last one
+    for (int i = 0; i < NBUF; ++i) mbar_wait_deadline(sm_addr(H.kv_full + i), (i < b ? turn : turn - 1) & 1, nullptr);
+  } else if (warp == 9) {
+    // ---- MMA issuer. The whole warp runs the loop on values that are the same in
+    // every lane, so that the descriptors stay in uniform registers; one lane issues.
+    // instruction descriptors: bf16 x bf16 -> f32, M = 128; V is MN-major
+    const uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(CT_KEYS >> 3) << 17) | (8u << 24);
+    const uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | (8u << 24);
+    const uint32_t one = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    uint32_t jobs[2] = {0, 0};                   // P V's of the groups so far
+    int rbuf = 0, rturn = 0;                     // ring position of the next load
+    auto step = [&]() {
+      if (++rbuf == NBUF) { rbuf = 0; ++rturn; }
+    };
+    bool ok = true;
+    for (uint32_t seg = 0; ok; ++seg) {
+      const int sb = seg & 1;
+      if (!(ok = waitw(H.seg_full + sb, seg >> 1))) break;
+      ChunkSeg g = H.seg[sb];
+      g.nt = same(g.nt); g.t0 = same(g.t0); g.t1 = same(g.t1); g.n = same(g.n); g.m = same(g.m); g.rt = same(g.rt);
+      if (g.nt == 0) break;
+      const CtGroup G0(A, g, 0), G1(A, g, 1);
+      const int nt = g.t1 - g.t0, n0 = same(G0.tiles), n1 = same(G1.tiles), e0 = same(G0.end), e1 = same(G1.end);
+      if (!(ok = waitw(&H.q_full, seg))) break;
+      // iteration i: P V of tile i - 1 (its V is the ring's next), S of tile i (its K behind)
+      for (int i = 0; ok && i <= nt; ++i) {
+        int vbuf = 0, kbuf = 0;
+        uint32_t kturn = 0;
+        if (i > 0) {
+          vbuf = rbuf;
+          if (!(ok = waitw(H.kv_full + vbuf, rturn))) break;
+          step();
+          // slots past the sequence's last may hold anything: those that the last MMA reads become zeros
+          const int nk = g.n + g.m - (g.t0 + i - 1) * CT_KEYS;
+          if (nk < CT_KEYS && nk % 16) {
+            unsigned char* vb = base + vbuf * C::BUF;
+            const int rows = 16 - nk % 16;
+            for (int x = lane; x < rows * HALVES * 8; x += 32) {
+              const int key = nk + x / (HALVES * 8), hf = x / 8 % HALVES;
+              *reinterpret_cast<uint4*>(vb + key / 8 * GROUP + hf * 1024 + key % 8 * 128 + (x % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+        }
+        if (i < nt) {
+          kbuf = rbuf;
+          kturn = rturn;
+          step();
+        }
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+          const int ng = gr ? n1 : n0, end = gr ? e1 : e0;
+          if (ok && i > 0 && i <= ng) {
+            if (!(ok = waitw(H.p_full + gr, jobs[gr]++))) break;
+            tc_fence_after();
+            const uint32_t d = tm + CT_OCOL + gr * D, a = tm + gr * 128;
+            const uint64_t bd = tt_desc(bufs + vbuf * C::BUF, 1024, GROUP);
+            const int steps = (min(CT_KEYS, end - (g.t0 + i - 1) * CT_KEYS) + 15) / 16;
+            // 16 keys a step: their weights lie in columns 32 (k / 2) + 8 (k % 2) ..
+            auto part = [&](int k, bool acc) { mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1), bd + (uint64_t)(k * 2 * GROUP >> 4), id_o, acc, one); };
+            part(0, i > 1);
+            if (steps == CT_KEYS / 16) {
+#pragma unroll
+              for (int k = 1; k < CT_KEYS / 16; ++k) part(k, true);
+            } else {
+#pragma unroll 1
+              for (int k = 1; k < steps; ++k) part(k, true);
+            }
+            if (i == ng) tc_commit(sm_addr(H.o_done + gr), one);
+          }
+          if (ok && i < ng) {
+            if (!(ok = waitw(H.kv_full + kbuf, kturn))) break;
+            tc_fence_after();
+            const uint64_t ad = tt_desc(q_addr + gr * C::Q, 16, 1024), bd = tt_desc(bufs + kbuf * C::BUF, 16, GROUP);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(tm + gr * 128, ad + (uint64_t)(((k & 3) * 32 + (k >> 2) * CT_HALF) >> 4),
+                     bd + (uint64_t)(((k & 3) * 32 + (k >> 2) * 1024) >> 4), id_s, k > 0, one);
+            tc_commit(sm_addr(H.s_full + gr), one);
+          }
+        }
+        if (!ok) break;
+        if (i > 0) tc_commit(sm_addr(H.kv_empty + vbuf), one);
+        if (i < nt) tc_commit(sm_addr(H.kv_empty + kbuf), one);
+        if (i == nt - 1) tc_commit(sm_addr(&H.q_free), one);
+      }
+    }
+    // everything issued is done before TMEM is freed (also after an abort)
+    tc_commit(sm_addr(&H.fin), one);
+    mbar_wait_deadline(sm_addr(&H.fin), 0, nullptr);
+  } else if (warp == 10) {
+    // ---- loader: the segments and their queries ----
+    ChunkSeg g;
+    const int tpg = A.rows / 2 / A.G;            // tokens of a group
+    uint32_t asked = 0;                          // segments whose queries were asked for
+    for (uint32_t seg = 0;; ++seg) {
+      const int sb = seg & 1;
+      const bool have = walk.next(g);
+      if (seg >= 2 && !waitw(H.seg_free + sb, (seg >> 1) - 1)) break;
+      if (!have) g.nt = 0;
+      if (lane == 0) {
+        H.seg[sb] = g;
+        mbar_arrive(sm_addr(H.seg_full + sb));
+      }
+      if (!have) break;
+      if (seg > 0 && !waitw(&H.q_free, seg - 1)) break;
+      const int groups = CtGroup(A, g, 1).rows > 0 ? 2 : 1, copies = groups * HALVES;
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                     ::"r"(sm_addr(&H.q_full)), "r"((uint32_t)(copies * tpg * A.G * 128)) : "memory");
+      __syncwarp();
+      ++asked;
+      if (lane < copies) {
+        const int half = lane % HALVES, gr = lane / HALVES;
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+            ::"r"(q_addr + gr * C::Q + half * CT_HALF), "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(0), "r"(half),
+              "r"(g.hk * A.G), "r"(g.r0 + (g.rt * 2 + gr) * tpg), "r"(sm_addr(&H.q_full))
+            : "memory");
+      }
+    }
+    if (asked > 0) mbar_wait_deadline(sm_addr(&H.q_full), (asked - 1) & 1, nullptr);   // (over, unless aborted)
+  } else {
+    // ---- softmax groups; their warps go on apart ----
+    const int gr = warp >> 2, r = t & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sT = tmem + lanes + gr * 128, oT = tmem + lanes + CT_OCOL + gr * D;
+    const float sc = A.scale_l2e;
+    const unsigned long long sc2 = pair(sc, sc);
+    uint32_t jobs = 0, ends = 0;                 // tiles; segments with tiles
+    for (uint32_t seg = 0;; ++seg) {
+      const int sb = seg & 1;
+      if (!waitw(H.seg_full + sb, seg >> 1)) break;
+      const ChunkSeg g = H.seg[sb];
+      if (g.nt == 0) break;
+      const CtGroup R(A, g, gr);
+      const bool live = r < R.rows, any_live = __any_sync(0xffffffffu, live);
+      const int rr = R.row0 + r, tok = rr / A.G;
+      CtLane st{-INFINITY, 0.f, 0.f};
+      bool far = false;                          // a lane of the warp goes by its largest score
+      // keys that the lane sees, from the segment's first on; the warp's fewest
+      int seen = live ? g.n + tok + 1 - g.t0 * CT_KEYS : 0;
+      const int least = __reduce_min_sync(0xffffffffu, live ? seen : 0x7fffffff);
+      for (int ti = 0; ti < R.tiles; ++ti, seen -= CT_KEYS) {
+        waitw(H.s_full + gr, jobs++);
+        tc_fence_after();
+        if (any_live) {
+          const CtTile T{sT, oT, sc, seen, ti == 0, live};
+          const bool cut = least - ti * CT_KEYS < CT_KEYS;
+#pragma unroll 1
+          for (int c = 0; c < CT_KEYS / 32; ++c) {
+            bool again = far || (ti == 0 && c == 0);
+            if (!again) {
+              uint32_t v[32];
+              tmem_ld32(sT + 32 * c, v);
+              if (cut) ct_mask(v, seen - 32 * c);
+              const float mb = st.m == -INFINITY ? 0.f : st.m;
+              const unsigned long long nm2 = pair(-mb, -mb);
+              unsigned long long sum[2] = {0, 0};
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = halves(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2));
+                const float p0 = ex2(y.x), p1 = ex2(y.y);
+                sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(p0, p1));
+                w[i / 2] = pack_bf16(p0, p1);
+              }
+              const float2 s2 = halves(add2(sum[0], sum[1]));
+              const float s1 = s2.x + s2.y;
+              again = __any_sync(0xffffffffu, live && !(s1 <= CT_MUCH));
+              if (!again) {
+                tmem_st16(sT + 32 * c, w);
+                st.l += s1;
+              }
+            }
+            if (again) {
+              st = ch_slow<D>(T, c, st);
+              far = __any_sync(0xffffffffu, st.s0 != 0.f);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm_addr(H.p_full + gr));
+      }
+
+      // ---- the segment's end ----
+      const int part = part_of(g);
+      const float ref = fminf(fmaxf(fmaf(st.s0, sc, st.m), -3e38f), 3e38f);   // (finite, whatever the scores)
+      const bool some = st.m != -INFINITY;
+      const size_t pr = (((size_t)blockIdx.x * 2 + part) * 2 + gr) * 128 + r;       // (part >= 0)
+      if (part >= 0 && live) A.part_ml[pr] = make_float2(some ? ref : -INFINITY, some ? st.l : 0.f);
+      if (R.tiles > 0) {
+        waitw(H.o_done + gr, ends++);
+        tc_fence_after();
+        if (any_live) {
+          const size_t row = ((size_t)g.r0 + tok) * A.hq + g.hk * A.G + (rr - tok * A.G);
+          const float inv = 1.f / st.l;
+          if (part < 0 && live && A.lse) A.lse[row] = (ref + log2f(st.l)) * LN2;
+          uint4* og = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + row * D);
+          // a part lies as [4 dims][row]
+          float4* pg = reinterpret_cast<float4*>(A.part_o) + (((size_t)blockIdx.x * 2 + part) * 2 + gr) * 128 * (D / 4) + r;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(oT + 32 * c, v);
+            if (part < 0) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * inv);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 y;
+                y.x = pack_bf16(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]));
+                y.y = pack_bf16(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]));
+                y.z = pack_bf16(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]));
+                y.w = pack_bf16(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]));
+                if (live) og[4 * c + i] = y;
+              }
+            } else if (live) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                pg[(8 * c + i) * 128] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                    __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+            }
+          }
+        }
+      }
+      if (part == 1 && t == 0) A.joint[blockIdx.x] = joint_of(walk, g, min(A.rows, g.m * A.G - g.rt * A.rows));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm_addr(H.seg_free + sb));
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+// Joins the parts of a shared segment, as k_chunk_join does; the parts lie as [4 dims]
+// [row of a group], so a warp takes 32 rows and 4 dims of each at a time, and rows go
+// out through shared memory. grid (blocks, groups of 32 rows).
+constexpr int CX_WARPS = 8;
+
+template <int D>
+__global__ void __launch_bounds__(CX_WARPS * 32) k_chunk_tc_join(const __grid_constant__ ChunkArgs A) {
+  __shared__ __align__(16) uint2 y[32][D / 4 + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int4 jt = __ldcg(A.joint + blockIdx.x);
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = blockIdx.y / 4, r = blockIdx.y % 4 * 32 + lane;
+  const int parts = jt.w >> 16, rpg = A.rows / 2, rows = min(rpg, (jt.w & 0xFFFF) - gr * rpg);   // of the group
+  if (parts == 0 || (int)(blockIdx.y % 4) * 32 >= rows) return;
+  const bool live = r < rows;
+  // part 0 of the join is this block's part 1, then part 0 of the blocks after it
+  auto at = [&](int c) { return ((size_t)(blockIdx.x + c) * 2 + (c == 0 ? 1 : 0)) * 2 + gr; };
+  float M = -INFINITY, L = 0.f;
+  for (int c = 0; c < parts; ++c) {
+    const float2 ml = live ? __ldcg(A.part_ml + at(c) * 128 + r) : make_float2(0.f, 1.f);
+    const float mn = fmaxf(M, ml.x);
+    if (ml.y > 0.f) L = L * exp2f(M - mn) + ml.y * exp2f(ml.x - mn);
+    M = mn;
+  }
+  const float inv = 1.f / L;
+  const int rr = jt.y * A.rows + gr * rpg + r;
+  if (A.lse && w == 0 && live) A.lse[((size_t)jt.x + rr / A.G) * A.hq + jt.z * A.G + rr % A.G] = (M + log2f(L)) * LN2;
+  constexpr int PER = D / 4 / CX_WARPS;          // pieces of 4 dims a warp
+  float4 o[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < parts; ++c) {
+    const float2 ml = live ? __ldcg(A.part_ml + at(c) * 128 + r) : make_float2(0.f, 0.f);
+    const float4* p = reinterpret_cast<const float4*>(A.part_o) + at(c) * 128 * (D / 4) + r;
+    if (ml.y > 0.f) {                            // (a part that saw nothing of the row may hold anything)
+      const float f = exp2f(ml.x - M) * inv;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float4 v = __ldcg(p + (w * PER + i) * 128);
+        o[i].x = fmaf(v.x, f, o[i].x);
+        o[i].y = fmaf(v.y, f, o[i].y);
+        o[i].z = fmaf(v.z, f, o[i].z);
+        o[i].w = fmaf(v.w, f, o[i].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) y[lane][w * PER + i] = make_uint2(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i].z, o[i].w));
+  __syncthreads();
+  for (int x = threadIdx.x; x < 32 * (D / 4); x += CX_WARPS * 32) {
+    const int row = x / (D / 4), c = x % (D / 4), q = blockIdx.y % 4 * 32 + row;
+    if (q >= rows) continue;
+    const int z = jt.y * A.rows + gr * rpg + q;
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.out) + (((size_t)jt.x + z / A.G) * A.hq + jt.z * A.G + z % A.G) * D)[c] = y[row][c];
+  }
+}
+
 // Shape of a launch, from sizes and types alone.
 struct ChunkPlan {
   int rows, tile_k;
@@ -454,11 +997,13 @@ struct ChunkPlan {
       total = chain_ws_bytes(kv, max_new, hq);
       return;
     }
-    rows = CF_ROWS;
-    tile_k = CF_KEYS;
-    max_blocks = 320;       // two blocks per SM
-    ml = (size_t)max_blocks * 2 * rows * kv.head_dim * sizeof(float);
-    joint = (ml + (size_t)max_blocks * 2 * rows * sizeof(float2) + 15) / 16 * 16;
+    const bool tc = kv.dtype == SPEC_BF16;
+    rows = tc ? 2 * (128 / (hq / kv.n_kv_heads)) * (hq / kv.n_kv_heads) : CF_ROWS;   // (two groups of whole tokens)
+    tile_k = tc ? CT_KEYS : CF_KEYS;
+    max_blocks = tc ? 160 : 320;                 // one block per SM, or two
+    const int lie = tc ? 256 : CF_ROWS;          // rows of a part
+    ml = (size_t)max_blocks * 2 * lie * kv.head_dim * sizeof(float);
+    joint = (ml + (size_t)max_blocks * 2 * lie * sizeof(float2) + 15) / 16 * 16;
     total = joint + (size_t)max_blocks * sizeof(int4);
   }
 };
@@ -473,6 +1018,13 @@ int check_attention(const spec_kv_view* kv, int n_seq, int max_new, int hq) {
       (double)std::min<int64_t>(max_new, (int64_t)kv->max_pages * kv->page_size) * (hq / kv->n_kv_heads) > 2e9)
     return set_last_error(SPEC_ERR_UNSUPPORTED, "block table too long for this many heads");
   return SPEC_OK;
+}
+
+template <int D>
+cudaError_t launch_tc(const ChunkArgs& A, const CUtensorMap& map, const CUtensorMap& qmap, int kb, int blocks, cudaStream_t st) {
+  cudaError_t e = allow_dyn_smem_once<k_chunk_tc<D>>();
+  if (e == cudaSuccess) e = launch_k(k_chunk_tc<D>, dim3(blocks), dim3(CT_THREADS), CtCfg<D>::SMEM, st, map, qmap, A, kb);
+  return e == cudaSuccess ? launch_k(k_chunk_tc_join<D>, dim3(blocks, 8), dim3(CX_WARPS * 32), 0, st, A) : e;
 }
 
 template <int D, class KT>
@@ -523,10 +1075,21 @@ extern "C" int spec_chunk_attention(const spec_kv_view* kv, int layer, const voi
                     q_dev, out_dev, out_lse_dev, err_dev, reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + plan.ml),
                     reinterpret_cast<int4*>(w + plan.joint), layer, n_q_heads, n_q_heads / kv->n_kv_heads, plan.rows,
                     plan.tile_k, scale * LOG2E};
-  const int blocks = std::min(2 * sms, plan.max_blocks);
   cudaError_t e;
-  if (kv->dtype == SPEC_F32) e = d == 128 ? launch_fma<128, float>(A, blocks, st) : launch_fma<64, float>(A, blocks, st);
-  else e = d == 128 ? launch_fma<128, bf16_t>(A, blocks, st) : launch_fma<64, bf16_t>(A, blocks, st);
+  if (kv->dtype == SPEC_F32) {
+    const int blocks = std::min(2 * sms, plan.max_blocks);
+    e = d == 128 ? launch_fma<128, float>(A, blocks, st) : launch_fma<64, float>(A, blocks, st);
+  } else {
+    // a box of keys never straddles pages: the largest power of two up to a tile that divides a page
+    int kb = 16;
+    while (kb < CT_KEYS && kv->page_size % (2 * kb) == 0) kb *= 2;
+    CUtensorMap map, qmap;
+    if (q_make_map(&qmap, q_dev, d, n_q_heads, (uint64_t)n_rows, A.G, plan.rows / 2 / A.G) ||
+        kv_make_group_map(&map, kv->kv_dev, d, kv->page_size, (uint64_t)kv->n_pages * kv->n_layers * kv->n_kv_heads * 2, kb))
+      return set_last_error(SPEC_ERR_UNSUPPORTED, "tensor map encoding failed");
+    const int blocks = std::min(sms, plan.max_blocks);
+    e = d == 128 ? launch_tc<128>(A, map, qmap, kb, blocks, st) : launch_tc<64>(A, map, qmap, kb, blocks, st);
+  }
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
 }
