@@ -4,9 +4,11 @@
 // over j <= n + i, w the softmax of scale q.K_j, and lse = log sum_j exp(scale q.K_j).
 // The rows of the query heads that share a kv head (row r = token r / G, head r % G,
 // G query heads per kv head) meet the same keys, so a (sequence, row tile, kv head)
-// reads its keys, those up to its last token's position, once for all of its rows.
+// reads its keys, those up to its last token's position, once for all of its rows. A
+// row tile has whole tokens; where one token's heads are too many for it (FMA form),
+// the heads of a kv head are several parts, each of which counts as a kv head.
 //
-// Work split. Units of tile_k keys are numbered sequence by sequence, row tile by row
+// Work split. Units of 64 or 128 keys are numbered sequence by sequence, row tile by row
 // tile, kv head by kv head; block c of B takes units [c U / B, (c + 1) U / B) of all U,
 // whatever the lengths, which stay on the device. At most two of a block's (sequence,
 // tile, head) segments are shared with other blocks: of a shared one, each block
@@ -35,13 +37,16 @@ struct ChunkArgs {
   float* part_o;       // [blocks][2][rows][d]: part 0 of a block began in an earlier block, part 1 goes on in the next
   float2* part_ml;     // [blocks][2][rows]: maximum (log2 units), sum
   int4* joint;         // [blocks]: (first row, row tile, kv head, parts and rows) of the shared segment that starts in a block
-  int layer, hq, G;
-  int rows;            // rows of a tile
-  int tile_k;          // keys of a unit
+  int layer, hq;
+  int G;               // heads of a part
+  int parts, heads;    // parts of a kv head's heads; kv heads x parts
+  int tok;             // tokens of a row tile
+  int rows;            // tok G
+  int key_bits;        // log2 of a unit's keys
   float scale_l2e;     // scale * log2 e
 };
 
-// Segment: tiles [t0, t1) of nt key tiles of (sequence s, row tile rt, kv head hk).
+// Segment: tiles [t0, t1) of nt key tiles of (sequence s, row tile rt, head part hk).
 struct ChunkSeg {
   int s, rt, hk, nt, t0, t1;
   int n, m, r0;                                  // positions before the chunk, its tokens, its first row
@@ -49,12 +54,9 @@ struct ChunkSeg {
 
 // Key tiles of row tile rt: up to the position of its last token.
 __device__ __forceinline__ int chunk_tiles(const ChunkArgs& A, int n, int m, int rt) {
-  const int last = min(m - 1, (int)(((long long)(rt + 1) * A.rows - 1) / A.G));
-  return (n + last + A.tile_k) / A.tile_k;
+  return (n + min(m, (rt + 1) * A.tok) + (1 << A.key_bits) - 1) >> A.key_bits;
 }
-__device__ __forceinline__ int chunk_row_tiles(const ChunkArgs& A, int m) {
-  return (int)(((long long)m * A.G + A.rows - 1) / A.rows);
-}
+__device__ __forceinline__ int chunk_row_tiles(const ChunkArgs& A, int m) { return (m + A.tok - 1) / A.tok; }
 
 // A block's walk over its units. All threads of the block call init (it has
 // block barriers); next() is called by whole warps.
@@ -68,7 +70,7 @@ struct ChunkWalk {
     const ChunkSeq z(A.ix, s);
     long long sum = 0;
     for (int rt = 0, nrt = chunk_row_tiles(A, z.m); rt < nrt; ++rt) sum += chunk_tiles(A, z.n, z.m, rt);
-    return sum * A.kv.n_kv_heads;
+    return sum * A.heads;
   }
   template <int THREADS>
   __device__ void init(const ChunkArgs& args) {
@@ -105,7 +107,7 @@ struct ChunkWalk {
       int i = a, r = 0;
       for (long long c; at + (c = units_of(args, i)) <= u; ++i) at += c;
       const ChunkSeq z(args.ix, i);
-      for (long long c; at + (c = (long long)chunk_tiles(args, z.n, z.m, r) * args.kv.n_kv_heads) <= u; ++r) at += c;
+      for (long long c; at + (c = (long long)chunk_tiles(args, z.n, z.m, r) * args.heads) <= u; ++r) at += c;
       s_seq = i;
       s_rt = r;
       s_in = (int)(u - at);
@@ -123,7 +125,7 @@ struct ChunkWalk {
     for (;;) {
       if (rt < chunk_row_tiles(*A, z.m)) {
         g.nt = chunk_tiles(*A, z.n, z.m, rt);
-        if (in < g.nt * A->kv.n_kv_heads) break;
+        if (in < g.nt * A->heads) break;
         in = 0;
         ++rt;
         continue;
@@ -158,6 +160,11 @@ struct ChunkWalk {
 // segment alone), 0 or 1.
 __device__ __forceinline__ int part_of(const ChunkSeg& g) { return g.t0 > 0 ? 0 : (g.t1 < g.nt ? 1 : -1); }
 
+// Of a row: its place in rows of [token][query head]; x = its number in the segment's tile.
+__device__ __forceinline__ size_t row_at(const ChunkArgs& A, int r0, int rt, int hk, int x) {
+  return ((size_t)r0 + (size_t)rt * A.tok + x / A.G) * A.hq + hk * A.G + x % A.G;
+}
+
 // Description of the shared segment that starts in this block (the walk is behind
 // its first part): the blocks up to that of its last unit have parts of it (unit u
 // is in block floor(((u + 1) blocks - 1) / U)).
@@ -175,7 +182,7 @@ __device__ __forceinline__ int4 joint_of(const ChunkWalk& w, const ChunkSeg& g, 
 // all banks.
 constexpr int CF_THREADS = 128;
 constexpr int CF_ROWS = 32;
-constexpr int CF_KEYS = 64;
+constexpr int CF_KEYS = 64;                      // 2^6 (key_bits)
 
 template <int D>
 struct CfSmem {
@@ -187,18 +194,7 @@ struct CfSmem {
   int page[CF_KEYS];
 };
 
-template <class KT>
-__device__ __forceinline__ float4 load4(const void* base, size_t e) {
-  if constexpr (sizeof(KT) == 4) {
-    return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + e);
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + e);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
-  }
-}
-
-template <class KT, int D>
+template <int D>
 __global__ void __launch_bounds__(CF_THREADS) k_chunk_fma(const __grid_constant__ ChunkArgs A) {
   using L = CfSmem<D>;
   extern __shared__ __align__(16) unsigned char sm_raw[];
@@ -217,19 +213,16 @@ __global__ void __launch_bounds__(CF_THREADS) k_chunk_fma(const __grid_constant_
   const size_t page_elems = (size_t)A.kv.n_layers * A.kv.n_kv_heads * 2 * P * D;
   ChunkSeg g;
   while (walk.next(g)) {
-    const int row0 = g.rt * CF_ROWS, nrows = min(CF_ROWS, g.m * A.G - row0);
+    const int ntok = min(A.tok, g.m - g.rt * A.tok), nrows = ntok * A.G;
     const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
-    const size_t plane = (((size_t)A.layer * A.kv.n_kv_heads + g.hk) * 2) * P * D;
-    auto q_at = [&](int r) {                     // of row r of the tile
-      const int rr = row0 + r;
-      return (((size_t)g.r0 + rr / A.G) * A.hq + g.hk * A.G + rr % A.G) * D;
-    };
+    const size_t plane = (((size_t)A.layer * A.kv.n_kv_heads + g.hk / A.parts) * 2) * P * D;
+    auto q_at = [&](int r) { return row_at(A, g.r0, g.rt, g.hk, r) * D; };
     __syncthreads();                             // the last segment's reads of q are done
     for (int i = t; i < CF_ROWS * (D / 4); i += CF_THREADS) {
       const int r = i / (D / 4), c = 4 * (i % (D / 4));
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < nrows) {
-        v = load4<KT>(A.q, q_at(r) + c);
+        v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + q_at(r) + c);
         v = make_float4(v.x * A.scale_l2e, v.y * A.scale_l2e, v.z * A.scale_l2e, v.w * A.scale_l2e);
       }
       *reinterpret_cast<float4*>(&sm.q[r][c]) = v;
@@ -241,7 +234,7 @@ __global__ void __launch_bounds__(CF_THREADS) k_chunk_fma(const __grid_constant_
     for (int i = 0; i < 4; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
-      seen[i] = g.n + min(row0 + 4 * ty + i, g.m * A.G - 1) / A.G + 1;
+      seen[i] = g.n + g.rt * A.tok + min(4 * ty + i, nrows - 1) / A.G + 1;
 #pragma unroll
       for (int j = 0; j < NV; ++j) o[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -265,9 +258,9 @@ __global__ void __launch_bounds__(CF_THREADS) k_chunk_fma(const __grid_constant_
         const int key = i / (D / 4), c = 4 * (i % (D / 4)), page = sm.page[key];
         float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
         if (page >= 0) {
-          const size_t e = page * page_elems + plane + (size_t)((k0 + key) % P) * D + c;
-          kk = load4<KT>(A.kv.kv_dev, e);
-          vv = load4<KT>(A.kv.kv_dev, e + (size_t)P * D);
+          const float* e = static_cast<const float*>(A.kv.kv_dev) + page * page_elems + plane + (size_t)((k0 + key) % P) * D + c;
+          kk = *reinterpret_cast<const float4*>(e);
+          vv = *reinterpret_cast<const float4*>(e + (size_t)P * D);
         }
         *reinterpret_cast<float4*>(&sm.k[key][c]) = kk;
         *reinterpret_cast<float4*>(&sm.v[key][c]) = vv;
@@ -356,15 +349,11 @@ __global__ void __launch_bounds__(CF_THREADS) k_chunk_fma(const __grid_constant_
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           const float4 y = make_float4(o[i][j].x * inv, o[i][j].y * inv, o[i][j].z * inv, o[i][j].w * inv);
-          if constexpr (sizeof(KT) == 4)
-            *reinterpret_cast<float4*>(static_cast<float*>(A.out) + e + 4 * tx + 64 * j) = y;
-          else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.out) + e + 4 * tx + 64 * j) =
-                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+          *reinterpret_cast<float4*>(static_cast<float*>(A.out) + e + 4 * tx + 64 * j) = y;
         }
         if (A.lse && tx == 0) A.lse[e / D] = (m[i] + log2f(l[i])) * LN2;
       } else {
-        const size_t pr = ((size_t)blockIdx.x * 2 + part) * A.rows + r;
+        const size_t pr = ((size_t)blockIdx.x * 2 + part) * CF_ROWS + r;
 #pragma unroll
         for (int j = 0; j < NV; ++j) *reinterpret_cast<float4*>(A.part_o + pr * D + 4 * tx + 64 * j) = o[i][j];
         if (tx == 0) A.part_ml[pr] = make_float2(m[i], l[i]);
@@ -382,16 +371,16 @@ __global__ void __launch_bounds__(CF_THREADS) k_chunk_fma(const __grid_constant_
 // l = 0; the one with the row's first key has not.)
 constexpr int CJ_WARPS = 8;
 
-template <int D, class KT>
+template <int D>
 __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_constant__ ChunkArgs A) {
   pdl_wait();
   pdl_trigger();
   const int4 jt = __ldcg(A.joint + blockIdx.x);
   const int r = blockIdx.y * CJ_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int parts = jt.w >> 16, rr = jt.y * A.rows + r;
+  const int parts = jt.w >> 16;
   if (r >= (jt.w & 0xFFFF)) return;
   // part 0 of the join is this block's part 1, then part 0 of the blocks after it
-  auto at = [&](int c) { return ((size_t)(blockIdx.x + c) * 2 + (c == 0 ? 1 : 0)) * A.rows + r; };
+  auto at = [&](int c) { return ((size_t)(blockIdx.x + c) * 2 + (c == 0 ? 1 : 0)) * CF_ROWS + r; };
   constexpr int NV = D / 32, FLY = 8;            // values a lane; parts in flight at once
   float v[FLY][NV];
   auto fetch = [&](int c0) {
@@ -427,19 +416,12 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
     if ((c0 += FLY) >= parts) break;
     fetch(c0);
   }
-  const size_t row = ((size_t)jt.x + rr / A.G) * A.hq + jt.z * A.G + rr % A.G;
-  KT* og = static_cast<KT*>(A.out) + row * D + NV * lane;
+  const size_t row = row_at(A, jt.x, jt.y, jt.z, r);
+  float* og = static_cast<float*>(A.out) + row * D + NV * lane;
   const float inv = 1.f / l;
   if (A.lse && lane == 0) A.lse[row] = (M + log2f(l)) * LN2;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) o[i] *= inv;
-  if constexpr (sizeof(KT) == 4) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) og[i] = o[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; i += 2) reinterpret_cast<uint32_t*>(og)[i / 2] = pack_bf16(o[i], o[i + 1]);
-  }
+  for (int i = 0; i < NV; ++i) og[i] = o[i] * inv;
 }
 
 // ---------------------------------------------------------------------------
@@ -463,7 +445,7 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
 // does not hold every whole number, are taken against the row's largest score itself,
 // also there. Rounding a weight to bf16 costs 2^-9 relative at most in each term, as
 // much as rounding the result does; the sum of weights is of the fp32 values.
-constexpr int CT_KEYS = 128;
+constexpr int CT_KEYS = 128;                     // 2^7 (key_bits)
 constexpr int CT_THREADS = 352;
 constexpr int CT_HALF = 128 * 128;               // bytes of 64 dims of 128 rows of Q
 constexpr int CT_OCOL = 256;                     // TMEM columns: S of a group at 128 g, its O behind at CT_OCOL + D g
@@ -492,12 +474,12 @@ struct CtHeader {
 
 // Rows of group g of a segment, and the key tiles from t0 on that one of them sees.
 struct CtGroup {
-  int row0, rows, tiles, end;                    // first row, rows, tiles, positions that the last row sees
+  int row0, rows, tiles, end;                    // first row in the tile, rows, tiles, positions that the last row sees
   __device__ CtGroup(const ChunkArgs& A, const ChunkSeg& s, int g) {
-    const int rpg = A.rows / 2;
-    row0 = s.rt * A.rows + g * rpg;
-    rows = max(0, min(rpg, s.m * A.G - row0));
-    end = rows ? s.n + (row0 + rows - 1) / A.G + 1 : 0;
+    const int half = A.tok / 2, tok0 = s.rt * A.tok + g * half, n = max(0, min(half, s.m - tok0));
+    row0 = g * half * A.G;
+    rows = n * A.G;
+    end = n ? s.n + tok0 + n : 0;
     tiles = max(0, min(s.t1, (end + CT_KEYS - 1) / CT_KEYS) - s.t0);
   }
 };
@@ -780,7 +762,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
   } else if (warp == 10) {
     // ---- loader: the segments and their queries ----
     ChunkSeg g;
-    const int tpg = A.rows / 2 / A.G;            // tokens of a group
+    const int tpg = A.tok / 2;                   // tokens of a group
     uint32_t asked = 0;                          // segments whose queries were asked for
     for (uint32_t seg = 0;; ++seg) {
       const int sb = seg & 1;
@@ -824,11 +806,10 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
       if (g.nt == 0) break;
       const CtGroup R(A, g, gr);
       const bool live = r < R.rows, any_live = __any_sync(0xffffffffu, live);
-      const int rr = R.row0 + r, tok = rr / A.G;
       CtLane st{-INFINITY, 0.f, 0.f};
       bool far = false;                          // a lane of the warp goes by its largest score
       // keys that the lane sees, from the segment's first on; the warp's fewest
-      int seen = live ? g.n + tok + 1 - g.t0 * CT_KEYS : 0;
+      int seen = live ? g.n + g.rt * A.tok + (R.row0 + r) / A.G + 1 - g.t0 * CT_KEYS : 0;
       const int least = __reduce_min_sync(0xffffffffu, live ? seen : 0x7fffffff);
       for (int ti = 0; ti < R.tiles; ++ti, seen -= CT_KEYS) {
         waitw(H.s_full + gr, jobs++);
@@ -884,7 +865,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
         waitw(H.o_done + gr, ends++);
         tc_fence_after();
         if (any_live) {
-          const size_t row = ((size_t)g.r0 + tok) * A.hq + g.hk * A.G + (rr - tok * A.G);
+          const size_t row = row_at(A, g.r0, g.rt, g.hk, R.row0 + r);
           const float inv = 1.f / st.l;
           if (part < 0 && live && A.lse) A.lse[row] = (ref + log2f(st.l)) * LN2;
           uint4* og = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + row * D);
@@ -915,7 +896,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
           }
         }
       }
-      if (part == 1 && t == 0) A.joint[blockIdx.x] = joint_of(walk, g, min(A.rows, g.m * A.G - g.rt * A.rows));
+      if (part == 1 && t == 0) A.joint[blockIdx.x] = joint_of(walk, g, min(A.tok, g.m - g.rt * A.tok) * A.G);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sm_addr(H.seg_free + sb));
@@ -953,8 +934,7 @@ __global__ void __launch_bounds__(CX_WARPS * 32) k_chunk_tc_join(const __grid_co
     M = mn;
   }
   const float inv = 1.f / L;
-  const int rr = jt.y * A.rows + gr * rpg + r;
-  if (A.lse && w == 0 && live) A.lse[((size_t)jt.x + rr / A.G) * A.hq + jt.z * A.G + rr % A.G] = (M + log2f(L)) * LN2;
+  if (A.lse && w == 0 && live) A.lse[row_at(A, jt.x, jt.y, jt.z, gr * rpg + r)] = (M + log2f(L)) * LN2;
   constexpr int PER = D / 4 / CX_WARPS;          // pieces of 4 dims a warp
   float4 o[PER];
 #pragma unroll
@@ -980,14 +960,13 @@ __global__ void __launch_bounds__(CX_WARPS * 32) k_chunk_tc_join(const __grid_co
   for (int x = threadIdx.x; x < 32 * (D / 4); x += CX_WARPS * 32) {
     const int row = x / (D / 4), c = x % (D / 4), q = blockIdx.y % 4 * 32 + row;
     if (q >= rows) continue;
-    const int z = jt.y * A.rows + gr * rpg + q;
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.out) + (((size_t)jt.x + z / A.G) * A.hq + jt.z * A.G + z % A.G) * D)[c] = y[row][c];
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.out) + row_at(A, jt.x, jt.y, jt.z, gr * rpg + q) * D)[c] = y[row][c];
   }
 }
 
 // Shape of a launch, from sizes and types alone.
 struct ChunkPlan {
-  int rows, tile_k;
+  int G, parts, tok, key_bits;
   int max_blocks;           // of any grid (the workspace is sized without a device)
   size_t ml, joint, total;  // workspace: outputs at 0, statistics, joints
   bool chain;               // few tokens: the tree attention's kernel, each node the next one's parent
@@ -998,8 +977,12 @@ struct ChunkPlan {
       return;
     }
     const bool tc = kv.dtype == SPEC_BF16;
-    rows = tc ? 2 * (128 / (hq / kv.n_kv_heads)) * (hq / kv.n_kv_heads) : CF_ROWS;   // (two groups of whole tokens)
-    tile_k = tc ? CT_KEYS : CF_KEYS;
+    const int heads = hq / kv.n_kv_heads;
+    parts = 1;
+    while (!tc && (heads % parts || heads / parts > CF_ROWS)) ++parts;
+    G = heads / parts;
+    tok = tc ? 2 * (128 / G) : CF_ROWS / G;
+    key_bits = tc ? 7 : 6;
     max_blocks = tc ? 160 : 320;                 // one block per SM, or two
     const int lie = tc ? 256 : CF_ROWS;          // rows of a part
     ml = (size_t)max_blocks * 2 * lie * kv.head_dim * sizeof(float);
@@ -1014,7 +997,7 @@ int check_attention(const spec_kv_view* kv, int n_seq, int max_new, int hq) {
   if (max_new < 1) return set_last_error(SPEC_ERR_ARG, "max_new >= 1 required");
   if (hq / kv->n_kv_heads > CH_MAX_G) return set_last_error(SPEC_ERR_UNSUPPORTED, "more than 128 query heads per kv head");
   // a row tile's units, and a sequence's rows of a kv head, are counted in 32 bits
-  if ((double)kv->max_pages * kv->page_size / CF_KEYS * kv->n_kv_heads > 2e9 ||
+  if ((double)kv->max_pages * kv->page_size / CF_KEYS * hq > 2e9 ||
       (double)std::min<int64_t>(max_new, (int64_t)kv->max_pages * kv->page_size) * (hq / kv->n_kv_heads) > 2e9)
     return set_last_error(SPEC_ERR_UNSUPPORTED, "block table too long for this many heads");
   return SPEC_OK;
@@ -1027,12 +1010,12 @@ cudaError_t launch_tc(const ChunkArgs& A, const CUtensorMap& map, const CUtensor
   return e == cudaSuccess ? launch_k(k_chunk_tc_join<D>, dim3(blocks, 8), dim3(CX_WARPS * 32), 0, st, A) : e;
 }
 
-template <int D, class KT>
+template <int D>
 cudaError_t launch_fma(const ChunkArgs& A, int blocks, cudaStream_t st) {
-  cudaError_t e = allow_dyn_smem_once<k_chunk_fma<KT, D>>();
-  if (e == cudaSuccess) e = launch_k(k_chunk_fma<KT, D>, dim3(blocks), dim3(CF_THREADS), sizeof(CfSmem<D>), st, A);
+  cudaError_t e = allow_dyn_smem_once<k_chunk_fma<D>>();
+  if (e == cudaSuccess) e = launch_k(k_chunk_fma<D>, dim3(blocks), dim3(CF_THREADS), sizeof(CfSmem<D>), st, A);
   if (e != cudaSuccess) return e;
-  return launch_k(k_chunk_join<D, KT>, dim3(blocks, (A.rows + CJ_WARPS - 1) / CJ_WARPS), dim3(CJ_WARPS * 32), 0, st, A);
+  return launch_k(k_chunk_join<D>, dim3(blocks, CF_ROWS / CJ_WARPS), dim3(CJ_WARPS * 32), 0, st, A);
 }
 
 }  // namespace
@@ -1073,18 +1056,18 @@ extern "C" int spec_chunk_attention(const spec_kv_view* kv, int layer, const voi
   char* w = static_cast<char*>(ws_dev);
   const ChunkArgs A{*kv, ChunkIndex{row_start_dev, n_new_dev, cache_len_dev, n_seq, n_rows, max_new, kv->max_pages * kv->page_size},
                     q_dev, out_dev, out_lse_dev, err_dev, reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + plan.ml),
-                    reinterpret_cast<int4*>(w + plan.joint), layer, n_q_heads, n_q_heads / kv->n_kv_heads, plan.rows,
-                    plan.tile_k, scale * LOG2E};
+                    reinterpret_cast<int4*>(w + plan.joint), layer, n_q_heads, plan.G, plan.parts, kv->n_kv_heads * plan.parts,
+                    plan.tok, plan.tok * plan.G, plan.key_bits, scale * LOG2E};
   cudaError_t e;
   if (kv->dtype == SPEC_F32) {
     const int blocks = std::min(2 * sms, plan.max_blocks);
-    e = d == 128 ? launch_fma<128, float>(A, blocks, st) : launch_fma<64, float>(A, blocks, st);
+    e = d == 128 ? launch_fma<128>(A, blocks, st) : launch_fma<64>(A, blocks, st);
   } else {
     // a box of keys never straddles pages: the largest power of two up to a tile that divides a page
     int kb = 16;
     while (kb < CT_KEYS && kv->page_size % (2 * kb) == 0) kb *= 2;
     CUtensorMap map, qmap;
-    if (q_make_map(&qmap, q_dev, d, n_q_heads, (uint64_t)n_rows, A.G, plan.rows / 2 / A.G) ||
+    if (q_make_map(&qmap, q_dev, d, n_q_heads, (uint64_t)n_rows, A.G, plan.tok / 2) ||
         kv_make_group_map(&map, kv->kv_dev, d, kv->page_size, (uint64_t)kv->n_pages * kv->n_layers * kv->n_kv_heads * 2, kb))
       return set_last_error(SPEC_ERR_UNSUPPORTED, "tensor map encoding failed");
     const int blocks = std::min(sms, plan.max_blocks);
