@@ -13,7 +13,8 @@
 // whatever the lengths, which stay on the device. At most two of a block's (sequence,
 // tile, head) segments are shared with other blocks: of a shared one, each block
 // leaves (output, maximum, sum) in the workspace and a second launch joins the parts
-// in key order.
+// in key order. A segment begins with a few units without keys, for what its start and
+// its end take.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -43,6 +44,7 @@ struct ChunkArgs {
   int tok;             // tokens of a row tile
   int rows;            // tok G
   int key_bits;        // log2 of a unit's keys
+  int extra;           // units without keys of a segment
   float scale_l2e;     // scale * log2 e
 };
 
@@ -69,7 +71,7 @@ struct ChunkWalk {
   __device__ static long long units_of(const ChunkArgs& A, int s) {
     const ChunkSeq z(A.ix, s);
     long long sum = 0;
-    for (int rt = 0, nrt = chunk_row_tiles(A, z.m); rt < nrt; ++rt) sum += chunk_tiles(A, z.n, z.m, rt);
+    for (int rt = 0, nrt = chunk_row_tiles(A, z.m); rt < nrt; ++rt) sum += chunk_tiles(A, z.n, z.m, rt) + A.extra;
     return sum * A.heads;
   }
   template <int THREADS>
@@ -107,7 +109,7 @@ struct ChunkWalk {
       int i = a, r = 0;
       for (long long c; at + (c = units_of(args, i)) <= u; ++i) at += c;
       const ChunkSeq z(args.ix, i);
-      for (long long c; at + (c = (long long)chunk_tiles(args, z.n, z.m, r) * args.heads) <= u; ++r) at += c;
+      for (long long c; at + (c = (long long)(chunk_tiles(args, z.n, z.m, r) + args.extra) * args.heads) <= u; ++r) at += c;
       s_seq = i;
       s_rt = r;
       s_in = (int)(u - at);
@@ -120,39 +122,44 @@ struct ChunkWalk {
     }
   }
   __device__ bool next(ChunkSeg& g) {
-    if (u >= u1) return false;
-    ChunkSeq z(A->ix, s);
-    for (;;) {
-      if (rt < chunk_row_tiles(*A, z.m)) {
-        g.nt = chunk_tiles(*A, z.n, z.m, rt);
-        if (in < g.nt * A->heads) break;
+    ChunkSeq z(A->ix, u < u1 ? s : 0);
+    while (u < u1) {
+      if (rt >= chunk_row_tiles(*A, z.m)) {
+        in = rt = 0;                             // the next sequence that is not padded, of 32 at a time
+        for (++s;; s += 32) {
+          if (s >= A->ix.n_seq) return false;    // (only if the lengths changed meanwhile)
+          const int i = s + (threadIdx.x & 31);
+          const uint32_t live = __ballot_sync(0xffffffffu, i < A->ix.n_seq && ChunkSeq(A->ix, i).m > 0);
+          if (live) {
+            s += __ffs(live) - 1;
+            break;
+          }
+        }
+        z = ChunkSeq(A->ix, s);
+        continue;
+      }
+      g.nt = chunk_tiles(*A, z.n, z.m, rt);
+      const int len = g.nt + A->extra;
+      if (in >= len * A->heads) {
         in = 0;
         ++rt;
         continue;
       }
-      in = rt = 0;                               // the next sequence that is not padded, of 32 at a time
-      for (++s;; s += 32) {
-        if (s >= A->ix.n_seq) return false;      // (only if the lengths changed meanwhile)
-        const int i = s + (threadIdx.x & 31);
-        const uint32_t live = __ballot_sync(0xffffffffu, i < A->ix.n_seq && ChunkSeq(A->ix, i).m > 0);
-        if (live) {
-          s += __ffs(live) - 1;
-          break;
-        }
-      }
-      z = ChunkSeq(A->ix, s);
+      g.hk = in / len;
+      const int from = in - g.hk * len, take = (int)min((long long)(len - from), u1 - u);
+      u += take;
+      in += take;
+      g.t0 = max(0, from - A->extra);
+      g.t1 = from + take - A->extra;
+      if (g.t1 <= g.t0) continue;                // (none with keys)
+      g.s = s;
+      g.n = z.n;
+      g.m = z.m;
+      g.r0 = z.r0;
+      g.rt = rt;
+      return true;
     }
-    g.s = s;
-    g.n = z.n;
-    g.m = z.m;
-    g.r0 = z.r0;
-    g.rt = rt;
-    g.hk = in / g.nt;
-    g.t0 = in - g.hk * g.nt;
-    g.t1 = (int)min((long long)g.nt, g.t0 + (u1 - u));
-    u += g.t1 - g.t0;
-    in += g.t1 - g.t0;
-    return true;
+    return false;
   }
 };
 
@@ -439,18 +446,19 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
 //
 // A weight is 2^(x - m) with a whole number m, set 24 above the first scores' maximum:
 // weights are floats, whose precision another m leaves as it is, so no maximum is
-// looked for afterwards. A chunk of 32 scores whose weights sum past 2^9 (a score grew
-// by some 30 binary orders), or to no number, is done again by ch_slow, which moves m
-// and rescales O and the tile's earlier weights. Scores beyond 2^24, above which float
+// looked for afterwards. A tile whose weights sum past 2^9 (a score grew by some 30
+// binary orders), or to no number, is done again by ch_slow, which moves m and rescales
+// O and the tile's earlier weights. Scores beyond 2^24, above which float
 // does not hold every whole number, are taken against the row's largest score itself,
 // also there. Rounding a weight to bf16 costs 2^-9 relative at most in each term, as
 // much as rounding the result does; the sum of weights is of the fp32 values.
 constexpr int CT_KEYS = 128;                     // 2^7 (key_bits)
 constexpr int CT_THREADS = 352;
+constexpr int CT_EXTRA = 2;                      // units' time that a segment's start and end take
 constexpr int CT_HALF = 128 * 128;               // bytes of 64 dims of 128 rows of Q
 constexpr int CT_OCOL = 256;                     // TMEM columns: S of a group at 128 g, its O behind at CT_OCOL + D g
 constexpr float CT_AHEAD = 24.f;                 // m is set to a score + 24
-constexpr float CT_MUCH = 512.f;                 // a chunk's weights sum to less while m stays
+constexpr float CT_MUCH = 512.f;                 // a tile's weights sum to less while m stays
 constexpr float CT_GROW = 8.f;                   // and m moves where a score passes m - 24 + 32
 constexpr float CT_FAR = 16777216.f;             // scores up to here go by m alone
 
@@ -503,8 +511,7 @@ __device__ __forceinline__ void ct_mask(uint32_t (&v)[32], int seen) {
     if (i >= seen) v[i] = 0xff800000u;
 }
 
-// Weights of one chunk in the place of its scores, whatever they are. Out of line:
-// a segment's first chunk, and rare ones.
+// Weights of one chunk of 32 scores, whatever they are. Out of line and rare.
 template <int D>
 __device__ __noinline__ CtLane ch_slow(CtTile T, int c, CtLane a) {
   uint32_t v[32];
@@ -541,11 +548,11 @@ __device__ __noinline__ CtLane ch_slow(CtTile T, int c, CtLane a) {
 #pragma unroll 1
     for (int i = 0; i < c; ++i) {
       uint32_t w[16];
-      tmem_ld16(T.s + 32 * i, w);
+      tmem_ld16(T.s + 16 * i, w);
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         w[j] = pack_bf16(__uint_as_float(w[j] << 16) * corr, __uint_as_float(w[j] & 0xFFFF0000u) * corr);
-      tmem_st16(T.s + 32 * i, w);
+      tmem_st16(T.s + 16 * i, w);
     }
   }
   const float mb = a.m == -INFINITY ? 0.f : a.m;
@@ -557,9 +564,22 @@ __device__ __noinline__ CtLane ch_slow(CtTile T, int c, CtLane a) {
     sum += p0 + p1;
     w[i / 2] = pack_bf16(p0, p1);
   }
-  tmem_st16(T.s + 32 * c, w);
+  tmem_st16(T.s + 16 * c, w);                    // (over scores that are read already)
   a.l += sum;
   return a;
+}
+
+// Weights 2^(sc v - m) of 32 scores as bf16 pairs, w[AT] .. w[AT + 15], and their sums.
+template <int AT>
+__device__ __forceinline__ void ch_weights(const uint32_t (&v)[32], uint32_t (&w)[64], unsigned long long sc2,
+                                           unsigned long long nm2, unsigned long long (&sum)[2]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y = halves(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2));
+    const float p0 = ex2(y.x), p1 = ex2(y.y);
+    sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(p0, p1));
+    w[AT + i / 2] = pack_bf16(p0, p1);
+  }
 }
 
 template <int D>
@@ -727,8 +747,8 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
             const uint32_t d = tm + CT_OCOL + gr * D, a = tm + gr * 128;
             const uint64_t bd = tt_desc(bufs + vbuf * C::BUF, 1024, GROUP);
             const int steps = (min(CT_KEYS, end - (g.t0 + i - 1) * CT_KEYS) + 15) / 16;
-            // 16 keys a step: their weights lie in columns 32 (k / 2) + 8 (k % 2) ..
-            auto part = [&](int k, bool acc) { mma_ts(d, a + 32 * (k / 2) + 8 * (k & 1), bd + (uint64_t)(k * 2 * GROUP >> 4), id_o, acc, one); };
+            // 16 keys a step: their weights lie in columns 8 k ..
+            auto part = [&](int k, bool acc) { mma_ts(d, a + 8 * k, bd + (uint64_t)(k * 2 * GROUP >> 4), id_o, acc, one); };
             part(0, i > 1);
             if (steps == CT_KEYS / 16) {
 #pragma unroll
@@ -817,36 +837,53 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
         if (any_live) {
           const CtTile T{sT, oT, sc, seen, ti == 0, live};
           const bool cut = least - ti * CT_KEYS < CT_KEYS;
-#pragma unroll 1
-          for (int c = 0; c < CT_KEYS / 32; ++c) {
-            bool again = far || (ti == 0 && c == 0);
-            if (!again) {
-              uint32_t v[32];
-              tmem_ld32(sT + 32 * c, v);
-              if (cut) ct_mask(v, seen - 32 * c);
-              const float mb = st.m == -INFINITY ? 0.f : st.m;
-              const unsigned long long nm2 = pair(-mb, -mb);
-              unsigned long long sum[2] = {0, 0};
-              uint32_t w[16];
+          bool again = far;
+          if (ti == 0) {                         // m: from the first keys
+            uint32_t v[32];
+            tmem_ld32(sT, v);
+            if (cut) ct_mask(v, seen);
+            float mx = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y = halves(fma2(pair(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, nm2));
-                const float p0 = ex2(y.x), p1 = ex2(y.y);
-                sum[i / 2 & 1] = add2(sum[i / 2 & 1], pair(p0, p1));
-                w[i / 2] = pack_bf16(p0, p1);
-              }
-              const float2 s2 = halves(add2(sum[0], sum[1]));
-              const float s1 = s2.x + s2.y;
-              again = __any_sync(0xffffffffu, live && !(s1 <= CT_MUCH));
-              if (!again) {
-                tmem_st16(sT + 32 * c, w);
-                st.l += s1;
-              }
+            for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            mx *= sc;
+            if (fabsf(mx) <= CT_FAR) st.m = ceilf(mx) + CT_AHEAD;
+            again = __any_sync(0xffffffffu, live && seen > 0 && !(fabsf(mx) <= CT_FAR));
+          }
+          if (!again) {
+            // scores on their way beside the exponentials; nothing is written before all of them are known to do
+            const float mb = st.m == -INFINITY ? 0.f : st.m;
+            const unsigned long long nm2 = pair(-mb, -mb);
+            uint32_t va[32], vb[32], w[64];
+            unsigned long long sum[2] = {0, 0};
+            tmem_ld32_start(sT, va);
+            tmem_ld32_done(va);
+            tmem_ld32_start(sT + 32, vb);
+            if (cut) ct_mask(va, seen);
+            ch_weights<0>(va, w, sc2, nm2, sum);
+            tmem_ld32_done(vb);
+            tmem_ld32_start(sT + 64, va);
+            if (cut) ct_mask(vb, seen - 32);
+            ch_weights<16>(vb, w, sc2, nm2, sum);
+            tmem_ld32_done(va);
+            tmem_ld32_start(sT + 96, vb);
+            if (cut) ct_mask(va, seen - 64);
+            ch_weights<32>(va, w, sc2, nm2, sum);
+            tmem_ld32_done(vb);
+            if (cut) ct_mask(vb, seen - 96);
+            ch_weights<48>(vb, w, sc2, nm2, sum);
+            const float2 s2 = halves(add2(sum[0], sum[1]));
+            const float s1 = s2.x + s2.y;
+            again = __any_sync(0xffffffffu, live && !(s1 <= CT_MUCH));
+            if (!again) {
+              tmem_st32_from<0>(sT, w);
+              tmem_st32_from<32>(sT + 32, w);
+              st.l += s1;
             }
-            if (again) {
-              st = ch_slow<D>(T, c, st);
-              far = __any_sync(0xffffffffu, st.s0 != 0.f);
-            }
+          }
+          if (again) {
+#pragma unroll 1
+            for (int c = 0; c < CT_KEYS / 32; ++c) st = ch_slow<D>(T, c, st);
+            far = __any_sync(0xffffffffu, st.s0 != 0.f);
           }
           tmem_wait_st();
         }
@@ -966,7 +1003,7 @@ __global__ void __launch_bounds__(CX_WARPS * 32) k_chunk_tc_join(const __grid_co
 
 // Shape of a launch, from sizes and types alone.
 struct ChunkPlan {
-  int G, parts, tok, key_bits;
+  int G, parts, tok, key_bits, extra;
   int max_blocks;           // of any grid (the workspace is sized without a device)
   size_t ml, joint, total;  // workspace: outputs at 0, statistics, joints
   bool chain;               // few tokens: the tree attention's kernel, each node the next one's parent
@@ -983,6 +1020,7 @@ struct ChunkPlan {
     G = heads / parts;
     tok = tc ? 2 * (128 / G) : CF_ROWS / G;
     key_bits = tc ? 7 : 6;
+    extra = tc ? CT_EXTRA : 0;
     max_blocks = tc ? 160 : 320;                 // one block per SM, or two
     const int lie = tc ? 256 : CF_ROWS;          // rows of a part
     ml = (size_t)max_blocks * 2 * lie * kv.head_dim * sizeof(float);
@@ -1057,7 +1095,7 @@ extern "C" int spec_chunk_attention(const spec_kv_view* kv, int layer, const voi
   const ChunkArgs A{*kv, ChunkIndex{row_start_dev, n_new_dev, cache_len_dev, n_seq, n_rows, max_new, kv->max_pages * kv->page_size},
                     q_dev, out_dev, out_lse_dev, err_dev, reinterpret_cast<float*>(w), reinterpret_cast<float2*>(w + plan.ml),
                     reinterpret_cast<int4*>(w + plan.joint), layer, n_q_heads, plan.G, plan.parts, kv->n_kv_heads * plan.parts,
-                    plan.tok, plan.tok * plan.G, plan.key_bits, scale * LOG2E};
+                    plan.tok, plan.tok * plan.G, plan.key_bits, plan.extra, scale * LOG2E};
   cudaError_t e;
   if (kv->dtype == SPEC_F32) {
     const int blocks = std::min(2 * sms, plan.max_blocks);
