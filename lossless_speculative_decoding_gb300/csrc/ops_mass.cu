@@ -6,8 +6,9 @@
 // rows stays with the position. A unit is (sequence, tile of keys, kv head): it
 // brings its keys once, goes over the counted rows that see them, and writes its
 // positions alone, so nothing is summed by atomics. Units of a sequence are
-// numbered from its first keys on, which the most rows see; block b takes units b,
-// b + B, ..
+// numbered from its first keys on, which the most rows see; of each B units block b
+// takes the b-th, and of the next B the b-th from their end, so that the sums of what
+// the blocks do stay close.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -30,6 +31,8 @@ struct MassArgs {
   int32_t* err;
   long long ld;
   int layer, hq, G, last;
+  int tok;             // tokens of a tile of rows (tensor-core form)
+  int nk, nq, q_half;  // its rings: tiles of keys and of queries in shared memory, bytes of 64 dims of a tile of queries
   float scale_l2e;     // scale * log2 e
 };
 
@@ -39,16 +42,17 @@ struct MassUnit {
   int n, m, r0, i0;
 };
 
-// A warp's walk over the units first, first + step, .. .
+// A warp's walk over its block's units.
 template <int KEYS>
 struct MassWalk {
-  long long u, before;                           // next unit; units before sequence s
+  long long round, before;                       // gridDim.x units each; units before sequence s
   int s;
   const MassArgs* A;
-  __device__ MassWalk(const MassArgs& args, long long first) : u(first), before(0), s(0), A(&args) {}
+  __device__ MassWalk(const MassArgs& args) : round(0), before(0), s(0), A(&args) {}
   __device__ static int tiles(int n, int m) { return (n + m + KEYS - 1) / KEYS; }
-  __device__ bool next(MassUnit& g, int step) {
+  __device__ bool next(MassUnit& g) {
     const int lane = threadIdx.x & 31, hkv = A->kv.n_kv_heads;
+    const long long u = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     for (;;) {                                   // sequences 32 at a time
       if (s >= A->ix.n_seq) return false;
       const bool on = s + lane < A->ix.n_seq;
@@ -79,7 +83,7 @@ struct MassWalk {
     g.tile = in / hkv;
     g.hk = in % hkv;
     g.i0 = max(g.m - min(A->last, g.m), g.tile * KEYS - g.n);   // (the counted ones; of them, those that see the first key)
-    u += step;
+    ++round;
     return true;
   }
 };
@@ -101,18 +105,7 @@ struct MfSmem {
   int page[MF_KEYS];
 };
 
-template <class KT>
-__device__ __forceinline__ float4 load4(const void* base, size_t e) {
-  if constexpr (sizeof(KT) == 4) {
-    return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + e);
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + e);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
-  }
-}
-
-template <class KT, int D>
+template <int D>
 __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__ MassArgs A) {
   using L = MfSmem<D>;
   extern __shared__ __align__(16) unsigned char sm_raw[];
@@ -125,9 +118,9 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
     for (int s = t; s < A.ix.n_seq; s += MF_THREADS)
       if (ChunkSeq(A.ix, s).bad) atomicOr(A.err, DERR_POS);
   const size_t page_elems = (size_t)A.kv.n_layers * A.kv.n_kv_heads * 2 * P * D;
-  MassWalk<MF_KEYS> walk(A, blockIdx.x);
+  MassWalk<MF_KEYS> walk(A);
   MassUnit g;
-  while (walk.next(g, gridDim.x)) {
+  while (walk.next(g)) {
     const int k0 = g.tile * MF_KEYS, nk = min(MF_KEYS, g.n + g.m - k0);
     const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
     const size_t plane = (((size_t)A.layer * A.kv.n_kv_heads + g.hk) * 2) * P * D;
@@ -148,7 +141,9 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
     for (int i = t; i < MF_KEYS * (D / 4); i += MF_THREADS) {
       const int key = i / (D / 4), c = 4 * (i % (D / 4)), page = sm.page[key];
       float4 kk = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (page >= 0) kk = load4<KT>(A.kv.kv_dev, page * page_elems + plane + (size_t)((k0 + key) % P) * D + c);
+      if (page >= 0)
+        kk = *reinterpret_cast<const float4*>(static_cast<const float*>(A.kv.kv_dev) + page * page_elems + plane +
+                                              (size_t)((k0 + key) % P) * D + c);
       *reinterpret_cast<float4*>(&sm.k[key][c]) = kk;
     }
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -160,7 +155,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (rr < end) {
           const size_t row = ((size_t)g.r0 + rr / A.G) * A.hq + g.hk * A.G + rr % A.G;
-          v = load4<KT>(A.q, row * D + c);
+          v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + row * D + c);
           v = make_float4(v.x * A.scale_l2e, v.y * A.scale_l2e, v.z * A.scale_l2e, v.w * A.scale_l2e);
           if (c == 0) sm.lse[r] = A.lse[row] * LOG2E;
         }
@@ -215,10 +210,354 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
   }
 }
 
-template <int D, class KT>
+// ---------------------------------------------------------------------------
+// Tensor-core form (bf16 cache). One block per SM, eleven warps: a TMA producer, an MMA
+// issuer, a loader of the rows' lse and two groups of four warps that sum. A unit has two
+// tiles of 128 keys; against each tile of up to 128 rows (whole tokens), S = K Q^T goes
+// to tensor memory with the keys on the lanes, so that a thread sums its key's columns
+// in registers and no sum crosses threads. The groups take the tiles of rows in turn,
+// both tiles of keys of each: -lse, the same for all lanes, is read from shared memory
+// once for both. Four tiles of S make up tensor memory; one is given back as soon as
+// its scores are in registers.
+//
+// Sums: 128 weights in fp32, the tiles of rows by a compensated sum (its rounding error
+// is carried along), so that thousands of rows lose no bits.
+constexpr int MT_KEYS = 128;
+constexpr int MT_UNIT = 2 * MT_KEYS;
+constexpr int MT_THREADS = 352;
+constexpr int MT_MAX_NK = 8, MT_MAX_NQ = 4;
+
+template <int D>
+struct MtCfg {
+  static constexpr int BUF = MT_KEYS * D * 2;    // a tile of keys
+  static constexpr int TAIL = 8192;              // alignment slack and the header
+  static constexpr int ROOM = 232448 - 512 - TAIL;
+  static constexpr int SMEM = ROOM + TAIL;
+};
+
+struct MtHeader {
+  uint64_t k_full[MT_MAX_NK], k_empty[MT_MAX_NK], q_full[MT_MAX_NQ], q_empty[MT_MAX_NQ], s_full[4], s_empty[4];
+  uint64_t sum_full[2], sum_empty[2], fin;
+  uint32_t tmem;
+  int abort;
+  __align__(16) float nlse[MT_MAX_NQ][128];      // -lse log2 e of a tile's rows
+  float sum[2][MT_UNIT];                         // one group's sums of a unit, for the other
+};
+
+// A sum with the rounding error that it has not taken in.
+struct Comp {
+  float s, e;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, b = t - s;
+    e += (s - (t - b)) + (x - b);
+    s = t;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(MT_THREADS, 1)
+    k_mass_tc(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap qmap,
+              const __grid_constant__ MassArgs A, int kb) {
+  using C = MtCfg<D>;
+  constexpr int HALVES = D / 64;
+  // a tile of keys lies as [8 keys][64-dim half][key][64 dims], as a box of whole pages brings it
+  constexpr int GROUP = 1024 * HALVES;
+  extern __shared__ unsigned char mt_raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(mt_raw) + 1023) & ~uintptr_t(1023));
+  MtHeader& H = *reinterpret_cast<MtHeader*>(base + C::ROOM);
+  static_assert(sizeof(MtHeader) + 1024 <= C::TAIL, "header and alignment slack");
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int NK = A.nk, NQ = A.nq, q_bytes = HALVES * A.q_half;
+  const uint32_t kbufs = sm_addr(base), qbufs = kbufs + NK * C::BUF;
+  if (t == 0) {
+    for (int i = 0; i < MT_MAX_NK; ++i) {
+      mbar_init(H.k_full + i, 1);
+      mbar_init(H.k_empty + i, 1);
+    }
+    for (int i = 0; i < MT_MAX_NQ; ++i) {
+      mbar_init(H.q_full + i, 2);                // queries, lse
+      mbar_init(H.q_empty + i, 5);               // the MMAs, a group's warps
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(H.s_full + i, 1);
+      mbar_init(H.s_empty + i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(H.sum_full + i, 4);
+      mbar_init(H.sum_empty + i, 4);
+    }
+    mbar_init(&H.fin, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    H.abort = 0;
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&H.tmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0)
+    for (int s = t; s < A.ix.n_seq; s += MT_THREADS)
+      if (ChunkSeq(A.ix, s).bad) atomicOr(A.err, DERR_POS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = H.tmem;
+  // A wait that runs out raises the block's abort flag, which ends its other waits at
+  // once: every role leaves its loops (the sums of a unit that is not over are not written).
+  auto waitw = [&](const uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err)) != 0;
+  };
+  const int P = A.kv.page_size;
+  MassWalk<MT_UNIT> walk(A);
+  MassUnit g;
+
+  if (warp == 8) {
+    // ---- producer: a unit's keys (a box for each kb keys of a page), then its tiles of queries ----
+    const int nbox = MT_KEYS / kb;
+    const int planes = A.kv.n_layers * A.kv.n_kv_heads * 2;
+    int kn = 0, qn = 0;                          // ring positions
+    uint32_t kturn = 0, qturn = 0;               // passes over the rings
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
+      const int plane = (A.layer * A.kv.n_kv_heads + g.hk) * 2;
+      int page[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = g.tile * MT_UNIT + h * MT_KEYS + kb * lane;
+        page[h] = -1;                            // reads zeros
+        if (lane < nbox && key < g.n + g.m) {
+          page[h] = bt[key / P];
+          if (page[h] < 0 || page[h] >= A.kv.n_pages) {
+            page[h] = -1;
+            atomicOr(A.err, DERR_PAGE);
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k0 = g.tile * MT_UNIT + h * MT_KEYS, key = k0 + kb * lane;
+        if (!ok || k0 >= g.n + g.m) break;
+        if (kturn > 0 && !waitw(H.k_empty + kn, kturn - 1)) { ok = false; break; }
+        const uint32_t full = sm_addr(H.k_full + kn);
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"((uint32_t)C::BUF) : "memory");
+        __syncwarp();
+        if (lane < nbox)
+          asm volatile(
+              "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
+              ::"r"(kbufs + kn * C::BUF + lane * kb * D * 2), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0), "r"(key % P / 8),
+                "r"(page[h] < 0 ? -1 : page[h] * planes + plane), "r"(full)
+              : "memory");
+        if (++kn == NK) { kn = 0; ++kturn; }
+      }
+      for (int i = g.i0; ok && i < g.m; i += A.tok) {
+        if (qturn > 0 && !waitw(H.q_empty + qn, qturn - 1)) { ok = false; break; }
+        const uint32_t full = sm_addr(H.q_full + qn);
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                       ::"r"(full), "r"((uint32_t)(HALVES * A.tok * A.G * 128)) : "memory");
+        __syncwarp();
+        if (lane < HALVES)
+          asm volatile(
+              "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+              ::"r"(qbufs + qn * q_bytes + lane * A.q_half), "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(0), "r"(lane),
+                "r"(g.hk * A.G), "r"(g.r0 + i), "r"(full)
+              : "memory");
+        if (++qn == NQ) { qn = 0; ++qturn; }
+      }
+    }
+    // shared memory outlives the copies (over, unless a wait was given up): each buffer's last one
+    for (int i = 0; i < NK; ++i) mbar_wait_deadline(sm_addr(H.k_full + i), (i < kn ? kturn : kturn - 1) & 1, nullptr);
+    for (int i = 0; i < NQ; ++i) mbar_wait_deadline(sm_addr(H.q_full + i), (i < qn ? qturn : qturn - 1) & 1, nullptr);
+  } else if (warp == 9) {
+    // ---- MMA issuer (the whole warp, on values that are the same in every lane; one lane issues) ----
+    const uint32_t one = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    int kn = 0, qn = 0;
+    uint32_t kturn = 0, qturn = 0, tiles = 0;
+    uint32_t used[4] = {0, 0, 0, 0};
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const int nh = same(g.n + g.m - g.tile * MT_UNIT > MT_KEYS ? 2 : 1), i0 = same(g.i0), m = same(g.m);
+      for (int i = i0; ok && i < m; i += A.tok, ++tiles) {
+        const int rows = min(A.tok, m - i) * A.G, gr = tiles & 1;
+        // bf16 x bf16 -> f32, M = 128, N the rows in whole 16s
+        const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)((rows + 15) / 16 * 2) << 17) | (8u << 24);
+        if (!(ok = waitw(H.q_full + qn, qturn))) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || h >= nh) break;
+          const int kbuf = kn + h < NK ? kn + h : kn + h - NK;
+          const uint32_t kt = kn + h < NK ? kturn : kturn + 1;
+          if (i == i0 && !(ok = waitw(H.k_full + kbuf, kt))) break;
+          const uint32_t k = gr ? used[2 + h]++ : used[h]++;
+          if (k > 0 && !(ok = waitw(H.s_empty + 2 * gr + h, k - 1))) break;
+          tc_fence_after();
+          const uint64_t ad = tt_desc(kbufs + kbuf * C::BUF, 16, GROUP), bd = tt_desc(qbufs + qn * q_bytes, 16, 1024);
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d)
+            mma_ss(tm + (2 * gr + h) * 128, ad + (uint64_t)(((d & 3) * 32 + (d >> 2) * 1024) >> 4),
+                   bd + (uint64_t)(((d & 3) * 32 + (d >> 2) * A.q_half) >> 4), id, d > 0, one);
+          tc_commit(sm_addr(H.s_full + 2 * gr + h), one);
+        }
+        if (!ok) break;
+        tc_commit(sm_addr(H.q_empty + qn), one);
+        if (++qn == NQ) { qn = 0; ++qturn; }
+      }
+      for (int h = 0; ok && h < nh; ++h) {
+        tc_commit(sm_addr(H.k_empty + kn), one);
+        if (++kn == NK) { kn = 0; ++kturn; }
+      }
+    }
+    // everything issued is done before TMEM is freed (also after an abort)
+    tc_commit(sm_addr(&H.fin), one);
+    mbar_wait_deadline(sm_addr(&H.fin), 0, nullptr);
+  } else if (warp == 10) {
+    // ---- loader of -lse log2 e ----
+    int at[4];                                   // of row lane + 32 k of a tile
+#pragma unroll
+    for (int k = 0; k < 4; ++k) at[k] = (lane + 32 * k) / A.G * A.hq + (lane + 32 * k) % A.G;
+    int qn = 0;
+    uint32_t qturn = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      for (int i = g.i0; i < g.m; i += A.tok) {
+        const float* src = A.lse + (size_t)(g.r0 + i) * A.hq + g.hk * A.G;
+        const int rows = min(A.tok, g.m - i) * A.G;
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < rows ? -src[at[k]] * LOG2E : 0.f;
+        if (qturn > 0 && !waitw(H.q_empty + qn, qturn - 1)) { ok = false; break; }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) H.nlse[qn][lane + 32 * k] = v[k];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm_addr(H.q_full + qn));
+        if (++qn == NQ) { qn = 0; ++qturn; }
+      }
+    }
+  } else {
+    // ---- the groups that sum ----
+    const int gr = warp >> 2, r = t & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const unsigned long long sc2 = pair(A.scale_l2e, A.scale_l2e);
+    uint32_t tiles = 0, used[2] = {0, 0}, shared = 0;
+    int qn = 0;
+    uint32_t qturn = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      const int k0 = g.tile * MT_UNIT + r, nh = g.n + g.m - g.tile * MT_UNIT > MT_KEYS ? 2 : 1;
+      const int nt = max(0, (g.m - g.i0 + A.tok - 1) / A.tok);
+      const bool owner = nt == 0 ? gr == 0 : ((tiles + nt - 1) & 1) == (uint32_t)gr;       // (has the unit's last tile)
+      const size_t e = ((size_t)g.s * A.kv.n_kv_heads + g.hk) * A.ld + k0;
+      float before[2] = {0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (owner && A.mass && k0 + h * MT_KEYS < g.n) before[h] = A.mass[e + h * MT_KEYS];
+      Comp sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+      for (int i = g.i0; i < g.m; i += A.tok, ++tiles) {
+        const int q = qn;
+        const uint32_t qt = qturn;
+        if (++qn == NQ) { qn = 0; ++qturn; }
+        if ((tiles & 1) != (uint32_t)gr) continue;
+        const int rows = min(A.tok, g.m - i) * A.G, chunks = (rows + 31) / 32;
+        if (!(ok = waitw(H.q_full + q, qt))) break;        // (lse)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || h >= nh) break;
+          // the first row that sees the key
+          const long long lo64 = (long long)(k0 + h * MT_KEYS - g.n - i) * A.G;
+          const int lo = lo64 > 128 ? 128 : lo64 < 0 ? 0 : (int)lo64;
+          const bool cut = rows < 32 * chunks || __any_sync(0xffffffffu, lo > 0);
+          const uint32_t sT = tmem + lanes + (2 * gr + h) * 128;
+          if (!(ok = waitw(H.s_full + 2 * gr + h, used[h]++))) break;
+          tc_fence_after();
+          unsigned long long part[2] = {0, 0};
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            uint32_t v[32];
+            tmem_ld32(sT + 32 * c, v);
+            if (c == chunks - 1) {               // the scores are read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(sm_addr(H.s_empty + 2 * gr + h));
+            }
+            if (cut) {
+              const int a = lo - 32 * c, b = rows - 32 * c;
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (x < a || x >= b) v[x] = 0xff800000u;
+            }
+            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(&H.nlse[q][32 * c]);
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              const ulonglong2 n2 = nl[x / 4];
+              const float2 y = halves(fma2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sc2, n2.x));
+              const float2 z = halves(fma2(pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sc2, n2.y));
+              part[0] = add2(part[0], pair(ex2(y.x), ex2(y.y)));
+              part[1] = add2(part[1], pair(ex2(z.x), ex2(z.y)));
+            }
+          }
+          const float2 p = halves(add2(part[0], part[1]));
+          sum[h].add(p.x + p.y);
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm_addr(H.q_empty + q));
+      }
+      if (!ok) break;
+      if (nt > 1) {
+        const uint32_t p = shared & 1, turn = shared >> 1;
+        ++shared;
+        if (!owner) {
+          if (turn > 0 && !(ok = waitw(H.sum_empty + p, turn - 1))) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) H.sum[p][h * MT_KEYS + r] = sum[h].s + sum[h].e;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sm_addr(H.sum_full + p));
+        } else {
+          if (!(ok = waitw(H.sum_full + p, turn))) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) sum[h].add(H.sum[p][h * MT_KEYS + r]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sm_addr(H.sum_empty + p));
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (owner && k0 + h * MT_KEYS < g.n + g.m) A.out[e + h * MT_KEYS] = before[h] + (sum[h].s + sum[h].e);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+template <int D>
+cudaError_t launch_mass_tc(MassArgs A, int blocks, cudaStream_t st) {
+  // a box of keys never straddles pages: the largest power of two up to a tile that divides a page
+  int kb = 16;
+  while (kb < MT_KEYS && A.kv.page_size % (2 * kb) == 0) kb *= 2;
+  // tiles of rows: whole tokens, no more than a chunk counts; where they are small, the room goes to keys
+  A.tok = std::max(1, std::min(128 / A.G, std::min(A.last, A.ix.max_new)));
+  A.q_half = (A.tok * A.G + 15) / 16 * 16 * 128;
+  A.nq = A.q_half <= 4096 ? 4 : 3;
+  A.nk = std::min(MT_MAX_NK, (MtCfg<D>::ROOM - A.nq * A.q_half * (D / 64)) / MtCfg<D>::BUF);
+  CUtensorMap map, qmap;
+  if (q_make_map(&qmap, A.q, D, A.hq, (uint64_t)A.ix.n_rows, A.G, A.tok) ||
+      kv_make_group_map(&map, A.kv.kv_dev, D, A.kv.page_size, (uint64_t)A.kv.n_pages * A.kv.n_layers * A.kv.n_kv_heads * 2, kb))
+    return cudaErrorInvalidValue;
+  cudaError_t e = allow_dyn_smem_once<k_mass_tc<D>>();
+  return e == cudaSuccess ? launch_k(k_mass_tc<D>, dim3(blocks), dim3(MT_THREADS), MtCfg<D>::SMEM, st, map, qmap, A, kb) : e;
+}
+
+template <int D>
 cudaError_t launch_mass_fma(const MassArgs& A, int blocks, cudaStream_t st) {
-  cudaError_t e = allow_dyn_smem_once<k_mass_fma<KT, D>>();
-  return e == cudaSuccess ? launch_k(k_mass_fma<KT, D>, dim3(blocks), dim3(MF_THREADS), sizeof(MfSmem<D>), st, A) : e;
+  cudaError_t e = allow_dyn_smem_once<k_mass_fma<D>>();
+  return e == cudaSuccess ? launch_k(k_mass_fma<D>, dim3(blocks), dim3(MF_THREADS), sizeof(MfSmem<D>), st, A) : e;
 }
 
 }  // namespace
@@ -251,12 +590,11 @@ extern "C" int spec_attention_mass(const spec_kv_view* kv, int layer, const void
   if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
   const int d = kv->head_dim;
   const MassArgs A{*kv, ChunkIndex{row_start_dev, n_new_dev, cache_len_dev, n_seq, n_rows, max_new, (int)capacity}, q_dev, lse_dev,
-                   mass_dev, out_mass_dev, err_dev, ld, layer, n_q_heads, n_q_heads / kv->n_kv_heads, last, scale * LOG2E};
+                   mass_dev, out_mass_dev, err_dev, ld, layer, n_q_heads, n_q_heads / kv->n_kv_heads, last, 0, 0, 0, 0, scale * LOG2E};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
-  const int blocks = 3 * sms;
   cudaError_t e;
-  if (kv->dtype == SPEC_F32) e = d == 128 ? launch_mass_fma<128, float>(A, blocks, st) : launch_mass_fma<64, float>(A, blocks, st);
-  else e = d == 128 ? launch_mass_fma<128, bf16_t>(A, blocks, st) : launch_mass_fma<64, bf16_t>(A, blocks, st);
+  if (kv->dtype == SPEC_F32) e = d == 128 ? launch_mass_fma<128>(A, 3 * sms, st) : launch_mass_fma<64>(A, 3 * sms, st);
+  else e = d == 128 ? launch_mass_tc<128>(A, sms, st) : launch_mass_tc<64>(A, sms, st);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
 }
