@@ -10,9 +10,9 @@
 // `recent` last positions.
 //
 // k_evict_move, blocks per (plane, K | V, piece of a row): slot j <- slot kept[j] >=
-// j. A batch of rows is loaded, then, behind a barrier, stored. Later batches read
-// from kept[j'] >= j' past every slot stored so far, so batches need no barrier
-// between them, and rows that stay are not touched.
+// j. Rows come to shared memory in batches, a few batches ahead, and a batch is stored
+// when all of it is there. Batches on their way read from kept[j'] >= j' past every
+// slot that earlier ones are stored to, and rows that stay are not touched.
 //
 // Bound: HBM, by the rows moved.
 #include <cuda_runtime.h>
@@ -27,7 +27,9 @@ namespace {
 constexpr int EV_THREADS = 512;
 constexpr int EV_BINS = 2048;
 constexpr int MV_THREADS = 256;
-constexpr int MV_ROWS = 8;                       // rows a thread has in flight
+constexpr int MV_ROWS = 4;                       // pieces of a batch for each thread
+constexpr int MV_STAGES = 4;                     // batches in shared memory
+constexpr int MV_SMEM = MV_STAGES * MV_ROWS * MV_THREADS * 16;
 
 struct EvictArgs {
   spec_kv_view kv;
@@ -178,11 +180,27 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_consta
   }
 }
 
+// n / d for 0 <= n < 2^31, 1 <= d <= 2^30: with 2^s >= d and f = ceil(2^(31 + s) / d), f d
+// is above 2^(31 + s) by less than 2^s, so n f / 2^(31 + s) is above n / d by less than 1 / d.
+struct FastDiv {
+  uint32_t d, f, s;
+  explicit FastDiv(uint32_t by) : d(by), s(0) {
+    while ((1u << s) < by) ++s;
+    f = (uint32_t)(((1ull << (31 + s)) + by - 1) / by);
+  }
+  __device__ int div(int n) const { return (int)((uint64_t)(uint32_t)n * f >> (31 + s)); }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
+}
+
 // grid (planes x pieces of a row, K | V); SPAN 16-byte columns a block.
 template <int SPAN>
-__global__ void __launch_bounds__(MV_THREADS) k_evict_move(const __grid_constant__ EvictArgs A, int row16) {
-  constexpr int ROWS = MV_THREADS / SPAN;        // rows of the block at once
-  const int t = threadIdx.x, cols = row16 / SPAN;
+__global__ void __launch_bounds__(MV_THREADS, 3) k_evict_move(const __grid_constant__ EvictArgs A, int row16, FastDiv P) {
+  constexpr int ROWS = MV_THREADS / SPAN, BATCH = ROWS * MV_ROWS;        // rows of the block at once, of a batch
+  extern __shared__ uint4 mv_stage[];
+  const int t = threadIdx.x, r = t / SPAN, cols = row16 / SPAN;
   pdl_wait();
   pdl_trigger();
   const int plane = blockIdx.x / cols, c = blockIdx.x % cols * SPAN + t % SPAN;
@@ -192,32 +210,57 @@ __global__ void __launch_bounds__(MV_THREADS) k_evict_move(const __grid_constant
   const int32_t* kept = A.kept + (size_t)plane * A.budget;
   if (kept[A.budget - 1] < 0) return;            // (a bad page)
   const int32_t* bt = A.kv.block_table_dev + (size_t)s * A.kv.max_pages;
-  const int P = A.kv.page_size;
-  const size_t page16 = (size_t)A.kv.n_layers * A.kv.n_kv_heads * 2 * P * row16;
-  uint4* base = static_cast<uint4*>(A.kv.kv_dev) + (((size_t)layer * A.kv.n_kv_heads + h) * 2 + blockIdx.y) * P * row16 + c;
-  auto at = [&](int pos) { return base + bt[pos / P] * page16 + (size_t)(pos % P) * row16; };
-  for (int j0 = 0; j0 < A.budget; j0 += ROWS * MV_ROWS) {
-    uint4 v[MV_ROWS];
-    bool mv[MV_ROWS];
+  const size_t page16 = (size_t)A.kv.n_layers * A.kv.n_kv_heads * 2 * P.d * row16;
+  uint4* base = static_cast<uint4*>(A.kv.kv_dev) + (((size_t)layer * A.kv.n_kv_heads + h) * 2 + blockIdx.y) * P.d * row16 + c;
+  auto at = [&](int pos) {
+    const int page = P.div(pos);
+    return base + bt[page] * page16 + (size_t)(pos - page * (int)P.d) * row16;
+  };
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(mv_stage + t);
+  const int batches = (A.budget + BATCH - 1) / BATCH;
+  int from[MV_ROWS];                             // old slots of the next batch to be asked for (the slot itself: nothing to move)
+  auto look = [&](int b) {
 #pragma unroll
     for (int u = 0; u < MV_ROWS; ++u) {
-      const int j = j0 + u * ROWS + t / SPAN;
-      const int from = j < A.budget ? kept[j] : j;
-      mv[u] = from > j;
-      if (mv[u]) v[u] = *at(from);
+      const int j = b * BATCH + u * ROWS + r;
+      from[u] = j < A.budget ? kept[j] : j;
     }
-    __syncthreads();
+  };
+  uint32_t moves = 0;                            // MV_ROWS bits for each batch on its way, the newest lowest
+  auto ask = [&](int b) {
+    moves <<= MV_ROWS;
+    if (b < batches) {
 #pragma unroll
-    for (int u = 0; u < MV_ROWS; ++u) {
-      const int j = j0 + u * ROWS + t / SPAN;
-      if (mv[u]) *at(j) = v[u];
+      for (int u = 0; u < MV_ROWS; ++u)
+        if (from[u] > b * BATCH + u * ROWS + r) {
+          moves |= 1u << u;
+          cp_async16(mine + (b % MV_STAGES * MV_ROWS + u) * MV_THREADS * 16, at(from[u]));
+        }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    look(b + 1);
+  };
+  look(0);
+#pragma unroll 1
+  for (int b = 0; b < MV_STAGES - 1; ++b) ask(b);
+#pragma unroll 1
+  for (int b = 0; b < batches; ++b) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(MV_STAGES - 2) : "memory");
+    __syncthreads();                             // the whole batch is there, and nobody asks for more of it
+    const uint32_t bits = moves >> (MV_ROWS * (MV_STAGES - 2));
+#pragma unroll
+    for (int u = 0; u < MV_ROWS; ++u)
+      if (bits >> u & 1) *at(b * BATCH + u * ROWS + r) = mv_stage[(b % MV_STAGES * MV_ROWS + u) * MV_THREADS + t];
+    ask(b + MV_STAGES - 1);
   }
 }
 
 template <int SPAN>
 cudaError_t launch_move(const EvictArgs& A, int64_t planes, int row16, cudaStream_t st) {
-  return launch_k(k_evict_move<SPAN>, dim3((unsigned)(planes * (row16 / SPAN)), 2), dim3(MV_THREADS), 0, st, A, row16);
+  cudaError_t e = allow_dyn_smem_once<k_evict_move<SPAN>>();
+  if (e != cudaSuccess) return e;
+  return launch_k(k_evict_move<SPAN>, dim3((unsigned)(planes * (row16 / SPAN)), 2), dim3(MV_THREADS), MV_SMEM, st, A, row16,
+                  FastDiv(A.kv.page_size));
 }
 
 }  // namespace
@@ -252,7 +295,7 @@ extern "C" int spec_kv_evict(const spec_kv_view* kv, int n_seq, const int32_t* c
                     (int)std::min<int64_t>(ld, (int64_t)kv->max_pages * kv->page_size)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = launch_k(k_evict_select, dim3((unsigned)planes), dim3(EV_THREADS), 0, st, A);
-  if (e == cudaSuccess) e = launch_move<8>(A, planes, row16, st);
+  if (e == cudaSuccess) e = row16 % 16 ? launch_move<8>(A, planes, row16, st) : launch_move<16>(A, planes, row16, st);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
 }

@@ -2,11 +2,13 @@
 // the way of their keys and values into the paged cache.
 //
 // A head of d values lies on LPH = d / (16 bytes) lanes, one 16-byte piece each,
-// so that a warp holds one to four heads of a row. A lane's piece is the same in
-// every head, so its cosines and sines are computed once for a row and kind: with
-// gamma folded in, y[i] = r (x[i] C[i] + x'[i] S[i]), x' the partner's piece (a
-// shuffle), r = 1 / sqrt(mean x^2 + eps), C = gamma cos, S = -+ gamma' sin. Pieces
-// behind the rotated dims have C = gamma, S = 0.
+// so that a warp holds one to four heads of a row. A block takes 16 tokens at a time:
+// their places, the cosines and sines of their angles into shared memory, then the
+// heads, a few of a lane's on their way at once. A lane's piece is the same in every
+// head, so what it is multiplied by is made once for a row and kind: with gamma folded
+// in, y[i] = r (x[i] C[i] + x'[i] S[i]), x' the partner's piece (a shuffle), r =
+// 1 / sqrt(mean x^2 + eps), C = gamma cos, S = -+ gamma' sin. Pieces behind the rotated
+// dims have C = gamma, S = 0.
 //
 // The angle of position p is p F of a 64-bit turn, F = freq / 2 pi in units of
 // 2^-64 of a turn: the product wraps as the angle does, so it is as exact at
@@ -20,12 +22,13 @@
 #include <cmath>
 
 #include "chunk.cuh"
+#include "tc_attn.cuh"
 
 namespace spec {
 namespace {
 
 constexpr int RP_THREADS = 256;
-constexpr int RP_TOKENS = 64;                    // tokens whose places a block looks up at once
+constexpr int RP_TOKENS = 16;                    // tokens of a block at a time
 constexpr int RP_FLY = 4;                        // heads a lane has in flight
 
 struct RopeArgs {
@@ -55,11 +58,6 @@ __device__ __forceinline__ void turn_cos_sin(uint32_t a, float& c, float& s) {
   s = quarter >= 2 ? -y : y;
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
 template <int NV>
 __device__ __forceinline__ uint4 pack_piece(const float (&y)[NV]) {
   uint4 r;
@@ -67,23 +65,40 @@ __device__ __forceinline__ uint4 pack_piece(const float (&y)[NV]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (NV == 4) w[i] = __float_as_uint(y[i]);
-    else w[i] = bf16_pair(y[2 * i], y[2 * i + 1]);
+    else w[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
   }
   return r;
 }
 
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Pairs of a piece's values.
+template <class KT>
+__device__ __forceinline__ void unpack2(const uint4& v, unsigned long long (&f)[Elt<KT>::per16 / 2]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (Elt<KT>::per16 == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) f[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+}
+
 template <class KT, int D>
-__global__ void __launch_bounds__(RP_THREADS) k_qk_norm_rope(const __grid_constant__ RopeArgs A) {
-  constexpr int NV = Elt<KT>::per16, LPH = D / NV, GROUPS = RP_THREADS / LPH;
+__global__ void __launch_bounds__(RP_THREADS, 3) k_qk_norm_rope(const __grid_constant__ RopeArgs A) {
+  constexpr int NV = Elt<KT>::per16, N2 = NV / 2, LPH = D / NV, GROUPS = RP_THREADS / LPH;
   __shared__ long long w_sum[RP_THREADS / 32];
-  __shared__ long long s_before;
-  __shared__ int s_seq;
   __shared__ int t_seq[RP_TOKENS], t_row[RP_TOKENS], t_pos[RP_TOKENS], t_page[RP_TOKENS];
+  __shared__ __align__(16) float t_cos[RP_TOKENS][D / 2], t_sin[RP_TOKENS][D / 2];
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   pdl_wait();
   pdl_trigger();
 
-  // this block's tokens: [c T / B, (c + 1) T / B) of all T
+  // this thread's sequences, the tokens before them and of them
   const int per = (A.ix.n_seq + RP_THREADS - 1) / RP_THREADS;
   const int a = min(t * per, A.ix.n_seq), a1 = min(a + per, A.ix.n_seq);
   long long sum = 0;
@@ -101,69 +116,38 @@ __global__ void __launch_bounds__(RP_THREADS) k_qk_norm_rope(const __grid_consta
   if (lane == 31) w_sum[w] = inc;
   __syncthreads();
   long long before = 0, total = 0;
+#pragma unroll
   for (int i = 0; i < RP_THREADS / 32; ++i) {
     if (i < w) before += w_sum[i];
     total += w_sum[i];
   }
+  before += inc - sum;
+  // this block's tokens: [c T / B, (c + 1) T / B) of all T
   const long long blocks = gridDim.x, blk = blockIdx.x;
   const long long k0 = total / blocks * blk + total % blocks * blk / blocks;
   const long long k1 = total / blocks * (blk + 1) + total % blocks * (blk + 1) / blocks;
-  if (k0 >= k1) return;
-  long long at = before + inc - sum;
-  if (at <= k0 && k0 < at + sum) {               // one thread's sequences hold token k0
-    int i = a;
-    for (int c; at + (c = ChunkSeq(A.ix, i).m) <= k0; ++i) at += c;
-    s_seq = i;
-    s_before = at;
-  }
-  __syncthreads();
-  int seq = s_seq;                               // warp 0's: where the next token may be, tokens before it
-  long long first = s_before;
 
-  const int g = t / LPH, gl = t % LPH, heads = A.hq + 2 * A.kv.n_kv_heads;
+  const int g = t / LPH, gl = t % LPH;
   const uint32_t gmask = LPH == 32 ? 0xffffffffu : ((1u << (LPH & 31)) - 1) << (lane / LPH * LPH);
-  const int rotated = 2 * A.half8;               // pieces
-  const int partner = gl < A.half8 ? gl + A.half8 : gl < rotated ? gl - A.half8 : gl;
+  const int half = A.half8 * NV, rotated = 2 * A.half8;
+  const bool low = gl < A.half8, turns = gl < rotated;
+  const int partner = low ? gl + A.half8 : turns ? gl - A.half8 : gl, p0 = (low ? gl : gl - A.half8) * NV;
   const size_t plane16 = (size_t)A.kv.page_size * LPH;
   uint4* const cache = static_cast<uint4*>(A.kv.kv_dev);
   for (long long k = k0; k < k1; k += RP_TOKENS) {
     const int nt = (int)min((long long)RP_TOKENS, k1 - k);
     __syncthreads();                             // the last tokens' places are read
-    if (w == 0) {
-      // tokens k .. k + nt - 1: sequences 32 at a time, each one's tokens by the whole warp
-      for (;;) {
-        const bool on = seq + lane < A.ix.n_seq;
-        const ChunkSeq z(A.ix, on ? seq + lane : seq);
-        const int m = on ? z.m : 0;
-        long long end = m;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xffffffffu, end, o);
-          if (lane >= o) end += v;
+    if (before < k + nt && before + sum > k) {   // tokens k .. k + nt - 1: some are of this thread's sequences
+      long long lo = before;
+      for (int i = a; i < a1 && lo < k + nt; ++i) {
+        const ChunkSeq z(A.ix, i);
+        for (long long x = max(lo, k); x < min(lo + z.m, k + nt); ++x) {
+          const int slot = (int)(x - k), c = (int)(x - lo);
+          t_seq[slot] = i;
+          t_row[slot] = z.r0 + c;
+          t_pos[slot] = z.n + c;
         }
-        end += first;
-        uint32_t some = __ballot_sync(0xffffffffu, m > 0 && end > k && end - m < k + nt);
-        for (; some; some &= some - 1) {
-          const int l = __ffs(some) - 1;
-          const long long lo = __shfl_sync(0xffffffffu, end - m, l), hi = __shfl_sync(0xffffffffu, end, l);
-          const int n = __shfl_sync(0xffffffffu, z.n, l), r0 = __shfl_sync(0xffffffffu, z.r0, l);
-          for (long long x = max(lo, k) + lane; x < min(hi, k + nt); x += 32) {
-            const int slot = (int)(x - k), i = (int)(x - lo);
-            t_seq[slot] = seq + l;
-            t_row[slot] = r0 + i;
-            t_pos[slot] = n + i;
-          }
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, end > k + nt);
-        if (past) {                              // the next tokens are there
-          const int l = __ffs(past) - 1;
-          first = __shfl_sync(0xffffffffu, end - m, l);
-          seq += l;
-          break;
-        }
-        first = __shfl_sync(0xffffffffu, end, 31);
-        seq += 32;
-        if (first >= k1 || seq >= A.ix.n_seq) break;
+        lo += z.m;
       }
     }
     __syncthreads();
@@ -177,79 +161,92 @@ __global__ void __launch_bounds__(RP_THREADS) k_qk_norm_rope(const __grid_consta
       t_page[t] = page;
       t_pos[t] = pos % A.kv.page_size;
     }
+    for (int x = t; x < nt * half; x += RP_THREADS) {
+      const int tok = x / half, p = x - tok * half;
+      const int64_t pos = A.positions[(size_t)A.axis[p] * A.ix.n_rows + t_row[tok]];
+      turn_cos_sin((uint32_t)(((uint64_t)pos * A.turn[p]) >> 32), t_cos[tok][p], t_sin[tok][p]);
+    }
     __syncthreads();
     // a lane group takes a token's heads share, share + parts, ..
     for (int x = g; x < nt * A.parts; x += GROUPS) {
-      const int tok = x / A.parts, share = x % A.parts, row = t_row[tok], page = t_page[tok];
-      const char* src = A.qkv + row * A.ld + gl * 16;
-      float c[NV], sn[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        c[i] = 1.f;
-        sn[i] = 0.f;
-      }
-      if (gl < rotated) {
-        const bool low = gl < A.half8;
-        const int p0 = (low ? gl : gl - A.half8) * NV;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int64_t pos = A.positions[(size_t)A.axis[p0 + i] * A.ix.n_rows + row];
-          turn_cos_sin((uint32_t)(((uint64_t)pos * A.turn[p0 + i]) >> 32), c[i], sn[i]);
-          if (low) sn[i] = -sn[i];
-        }
-      }
+      const int tok = x / A.parts, share = x - tok * A.parts, row = t_row[tok], page = t_page[tok];
+      const uint4* src = reinterpret_cast<const uint4*>(A.qkv + row * A.ld) + gl;
       uint4* kd = page < 0 ? nullptr
                            : cache + (((size_t)page * A.kv.n_layers + A.layer) * A.kv.n_kv_heads * 2) * plane16 +
                                  (size_t)t_pos[tok] * LPH + gl;
       uint4* qd = reinterpret_cast<uint4*>(A.q_out) + ((size_t)row * A.hq) * LPH + gl;
 #pragma unroll 1
-      for (int kind = 0; kind < 2; ++kind) {     // queries, then keys
-        const float* gm = A.gamma[kind];
-        float C[NV], S[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          C[i] = gm ? c[i] * __ldg(gm + gl * NV + i) : c[i];
-          S[i] = gm ? sn[i] * __ldg(gm + partner * NV + i) : sn[i];
-        }
-        const int h0 = kind ? A.hq : 0, h1 = kind ? A.hq + A.kv.n_kv_heads : A.hq;
+      for (int kind = 0; kind < 3; ++kind) {     // queries, keys, values
+        const float* gm = kind < 2 ? A.gamma[kind] : nullptr;
+        const int h0 = kind == 0 ? 0 : kind == 1 ? A.hq : A.hq + A.kv.n_kv_heads;
+        const int h1 = kind == 0 ? A.hq : h0 + A.kv.n_kv_heads;
+        uint4* dst = kind == 0 ? qd : kd ? kd + (kind - 1) * plane16 : nullptr;
+        const size_t step = kind == 0 ? LPH : 2 * plane16;
+        unsigned long long C[N2], S[N2];
+        bool have = kind == 2;
         for (int h = h0 + share; h < h1; h += A.parts * RP_FLY) {
           uint4 v[RP_FLY];
 #pragma unroll
           for (int u = 0; u < RP_FLY; ++u)
-            if (h + u * A.parts < h1) v[u] = ld_stream(src + (size_t)(h + u * A.parts) * LPH * 16);
+            if (h + u * A.parts < h1) v[u] = ld_stream(src + (size_t)(h + u * A.parts) * LPH);
+          if (!have) {                           // (beside the first loads)
+            have = true;
+            float c[NV], s[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+              c[i] = turns ? t_cos[tok][p0 + i] : 1.f;
+              s[i] = turns ? t_sin[tok][p0 + i] : 0.f;
+              if (low) s[i] = -s[i];
+              if (gm) {
+                c[i] *= __ldg(gm + gl * NV + i);
+                s[i] *= __ldg(gm + partner * NV + i);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < N2; ++i) {
+              C[i] = pair(c[2 * i], c[2 * i + 1]);
+              S[i] = pair(s[2 * i], s[2 * i + 1]);
+            }
+          }
 #pragma unroll
           for (int u = 0; u < RP_FLY; ++u) {
             const int hh = h + u * A.parts;
             if (hh >= h1) break;
-            float f[NV], o[NV], y[NV];
-            unpack<KT>(v[u], f);
-            float r = 1.f;
-            if (gm) {
-              float ss = 0.f;
+            if (kind < 2) {
+              unsigned long long f[N2], o[N2];
+              unpack2<KT>(v[u], f);
+              float r = 1.f;
+              if (gm) {
+                unsigned long long s2 = mul2(f[0], f[0]);
 #pragma unroll
-              for (int i = 0; i < NV; ++i) ss = fmaf(f[i], f[i], ss);
+                for (int i = 1; i < N2; ++i) s2 = fma2(f[i], f[i], s2);
+                const float2 sq = halves(s2);
+                float ss = sq.x + sq.y;
 #pragma unroll
-              for (int o2 = 1; o2 < LPH; o2 <<= 1) ss += __shfl_xor_sync(gmask, ss, o2, LPH);
-              r = rsqrtf(ss * (1.f / D) + A.eps);
+                for (int d = 1; d < LPH; d <<= 1) ss += __shfl_xor_sync(gmask, ss, d, LPH);
+                r = rsqrtf(ss * (1.f / D) + A.eps);
+              }
+              uint4 pv;
+              pv.x = __shfl_sync(gmask, v[u].x, partner, LPH);
+              pv.y = __shfl_sync(gmask, v[u].y, partner, LPH);
+              pv.z = __shfl_sync(gmask, v[u].z, partner, LPH);
+              pv.w = __shfl_sync(gmask, v[u].w, partner, LPH);
+              if (!turns) pv = make_uint4(0u, 0u, 0u, 0u);     // (also where the piece is not finite)
+              unpack2<KT>(pv, o);
+              const unsigned long long r2 = pair(r, r);
+              float y[NV];
+#pragma unroll
+              for (int i = 0; i < N2; ++i) {
+                const float2 z = halves(mul2(r2, fma2(f[i], C[i], mul2(o[i], S[i]))));
+                y[2 * i] = z.x;
+                y[2 * i + 1] = z.y;
+              }
+              v[u] = pack_piece<NV>(y);
             }
-            uint4 pv;
-            pv.x = __shfl_sync(gmask, v[u].x, partner, LPH);
-            pv.y = __shfl_sync(gmask, v[u].y, partner, LPH);
-            pv.z = __shfl_sync(gmask, v[u].z, partner, LPH);
-            pv.w = __shfl_sync(gmask, v[u].w, partner, LPH);
-            unpack<KT>(pv, o);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) y[i] = r * fmaf(f[i], C[i], o[i] * S[i]);
-            const uint4 out = pack_piece<NV>(y);
-            if (kind == 0) qd[(size_t)hh * LPH] = out;
-            else if (kd) kd[(size_t)(hh - A.hq) * 2 * plane16] = out;
+            if (dst) dst[(size_t)(hh - h0) * step] = v[u];
           }
         }
       }
-      const int v0 = A.hq + A.kv.n_kv_heads;
-      if (kd)
-        for (int h = v0 + share; h < heads; h += A.parts)
-          kd[((size_t)(h - v0) * 2 + 1) * plane16] = ld_stream(src + (size_t)h * LPH * 16);
     }
   }
 }
@@ -301,11 +298,11 @@ extern "C" int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* 
   if (spans_meet(qkv_dev, in_bytes, kv->kv_dev, cache_bytes(*kv))) return set_last_error(SPEC_ERR_ARG, "qkv overlaps the cache");
   const int sms = sm_count_once();
   if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
-  // few rows: each group of lanes takes RP_FLY heads of one; many: as many parts as keep the SMs full
+  // few rows: each group of lanes takes RP_FLY heads of one; many: two or fewer take a row
   const int groups = RP_THREADS / (d * esz / 16), most = (n_q_heads + RP_FLY - 1) / RP_FLY;
-  const int64_t room = (int64_t)sms * 8 * groups;
+  const int64_t room = (int64_t)sms * 3 * groups;
   A.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, room / n_rows));
-  const int blocks = (int)std::min<int64_t>(((int64_t)n_rows * A.parts + groups - 1) / groups, sms * 8);
+  const int blocks = (int)std::min<int64_t>(((int64_t)n_rows * A.parts + groups - 1) / groups, sms * 3);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaError_t e;
   if (esz == 2) e = d == 128 ? launch_rope<bf16_t, 128>(A, blocks, st) : launch_rope<bf16_t, 64>(A, blocks, st);
