@@ -25,6 +25,7 @@ namespace spec {
 namespace {
 
 constexpr int EV_THREADS = 512;
+constexpr int EV_HOLD = 16;                      // keys a thread holds; of longer sequences they are read again
 constexpr int EV_BINS = 2048;
 constexpr int MV_THREADS = 256;
 constexpr int MV_ROWS = 4;                       // pieces of a batch for each thread
@@ -49,31 +50,21 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Exclusive prefix sum over the block; total in every thread. red: one per warp.
-__device__ __forceinline__ long long block_scan(long long v, long long* red, long long& total) {
+// Sum of the last lanes' v of the warps before this one.
+__device__ __forceinline__ int warps_before(int v, int* red) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  long long inc = v;
+  __syncthreads();
+  if (lane == 31) red[w] = v;
+  __syncthreads();
+  int before = lane < w ? red[lane] : 0;         // (no more warps than lanes)
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  __syncthreads();
-  if (lane == 31) red[w] = inc;
-  __syncthreads();
-  long long before = 0;
-  total = 0;
-  for (int i = 0; i < EV_THREADS / 32; ++i) {
-    const long long x = red[i];
-    if (i < w) before += x;
-    total += x;
-  }
-  return before + inc - v;
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  return before;
 }
 
 __global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_constant__ EvictArgs A) {
   __shared__ int hist[EV_BINS];
-  __shared__ long long red[EV_THREADS / 32];
+  __shared__ int red[EV_THREADS / 32];
   __shared__ uint32_t s_digit;
   __shared__ int s_left;
   const int t = threadIdx.x;
@@ -82,6 +73,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_consta
   // planes [layer][sequence][head]
   const int plane = blockIdx.x, s = plane / A.kv.n_kv_heads % A.n_seq;
   const int n = A.cache_len[s];
+  const int32_t* bt = A.kv.block_table_dev + (size_t)s * A.kv.max_pages;
   const float* mass = A.mass + (size_t)plane * A.ld;
   float* out_mass = A.out_mass + (size_t)plane * A.ld;
   int32_t* kept = A.kept + (size_t)plane * A.budget;
@@ -91,7 +83,6 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_consta
   if (ok && n > A.budget) {
     // every page up to n: the sequence moves in all planes or in none
     bool bad = false;
-    const int32_t* bt = A.kv.block_table_dev + (size_t)s * A.kv.max_pages;
     for (int i = t; i < (n + A.kv.page_size - 1) / A.kv.page_size; i += EV_THREADS)
       bad |= bt[i] < 0 || bt[i] >= A.kv.n_pages;
     if (__syncthreads_or(bad)) {
@@ -107,6 +98,30 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_consta
     return;
   }
   const int old = n - A.recent;                  // positions that compete
+  // warp w has positions w len .. , 32 at a time
+  const int lane = t & 31, w = t >> 5, len = (n + EV_THREADS - 1) / EV_THREADS * 32, w0 = w * len;
+  const bool hold = len <= EV_HOLD * 32;
+  uint32_t keys[EV_HOLD];
+  if (hold) {
+#pragma unroll
+    for (int u = 0; u < EV_HOLD; ++u) {
+      const int i = w0 + 32 * u + lane;
+      keys[u] = 32 * u < len && i < old ? mass_key(mass[i]) : 0;
+    }
+  }
+  // f(position, key) for this thread's positions, all of a warp's lanes together (i may be n or more)
+  auto each = [&](auto&& f) {
+    if (hold) {
+#pragma unroll
+      for (int u = 0; u < EV_HOLD; ++u)
+        if (32 * u < len) f(w0 + 32 * u + lane, keys[u]);
+    } else {
+      for (int u = 0; u < len; u += 32) {
+        const int i = w0 + u + lane;
+        f(i, i < old ? mass_key(mass[i]) : 0u);
+      }
+    }
+  };
   int left = A.budget - A.recent;                // of them to be kept; those equal to the threshold at last
   uint32_t key = 0, known = 0;                   // the threshold's digits so far, their bits
   if (left > 0) {
@@ -115,26 +130,30 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_consta
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
       for (int i = t; i < EV_BINS; i += EV_THREADS) hist[i] = 0;
       __syncthreads();
-      for (int i = t; i < old; i += EV_THREADS) {
-        const uint32_t x = mass_key(mass[i]);
-        if ((x & known) == key) atomicAdd(&hist[(x >> shift) & (bins - 1)], 1);
-      }
+      each([&](int i, uint32_t x) {
+        if (i < old && (x & known) == key) atomicAdd(&hist[(x >> shift) & (bins - 1)], 1);
+      });
       __syncthreads();
       // bins from the top: thread t has bins top - 4 t ..; the digit is where the count reaches `left`
       constexpr int PER = EV_BINS / EV_THREADS;
-      int c[PER];
-      long long sum = 0, total;
+      int c[PER], sum = 0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         c[i] = hist[EV_BINS - 1 - (t * PER + i)];
         sum += c[i];
       }
-      long long above = block_scan(sum, red, total);
+      int inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      int above = warps_before(inc, red) + inc - sum;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         if (above < left && above + c[i] >= left) {
           s_digit = EV_BINS - 1 - (t * PER + i);
-          s_left = left - (int)above;
+          s_left = left - above;
         }
         above += c[i];
       }
@@ -146,38 +165,27 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_consta
   }
   // kept positions in order: above the threshold, the first `left` equal to it, the last `recent`
   const bool any = A.budget > A.recent;
-  const int per = (n + EV_THREADS - 1) / EV_THREADS;
-  const int a = min(t * per, n), a1 = min(a + per, n);
-  int above = 0, equal = 0;
-  for (int i = a; i < a1; ++i) {
-    if (i >= old) ++above;
-    else if (any) {
-      const uint32_t x = mass_key(mass[i]);
-      above += x > key;
-      equal += x == key;
-    }
-  }
-  long long total;
-  const long long at = block_scan((long long)above << 32 | equal, red, total);
-  int up = (int)(at >> 32), eq = (int)(at & 0xffffffff);
-  for (int i = a; i < a1; ++i) {
-    const float f = mass[i];
-    bool keep = i >= old;
-    if (!keep && any) {
-      const uint32_t x = mass_key(f);
-      keep = x > key || (x == key && eq < left);
-      if (x == key) {
-        if (keep) { kept[up + eq] = i; out_mass[up + eq] = f; }
-        ++eq;
-        continue;
-      }
-    }
-    if (keep) {
-      const int j = up++ + min(eq, left);
+  auto is_above = [&](int i, uint32_t x) { return i < n && (i >= old || (any && x > key)); };
+  auto is_equal = [&](int i, uint32_t x) { return i < old && any && x == key; };
+  int up = 0, eq = 0;
+  each([&](int i, uint32_t x) {
+    up += __popc(__ballot_sync(0xffffffffu, is_above(i, x)));
+    eq += __popc(__ballot_sync(0xffffffffu, is_equal(i, x)));
+  });
+  up = warps_before(up, red);
+  eq = warps_before(eq, red);
+  const uint32_t lower = (1u << lane) - 1;
+  each([&](int i, uint32_t x) {
+    const uint32_t a = __ballot_sync(0xffffffffu, is_above(i, x)), e = __ballot_sync(0xffffffffu, is_equal(i, x));
+    const int me = eq + __popc(e & lower);       // equal ones before this position
+    if ((a >> lane & 1) || ((e >> lane & 1) && me < left)) {
+      const int j = up + __popc(a & lower) + min(me, left);
       kept[j] = i;
-      out_mass[j] = f;
+      out_mass[j] = mass[i];
     }
-  }
+    up += __popc(a);
+    eq += __popc(e);
+  });
 }
 
 // n / d for 0 <= n < 2^31, 1 <= d <= 2^30: with 2^s >= d and f = ceil(2^(31 + s) / d), f d

@@ -4,8 +4,8 @@
 // A head of d values lies on LPH = d / (16 bytes) lanes, one 16-byte piece each,
 // so that a warp holds one to four heads of a row. A block takes 16 tokens at a time:
 // their places, the cosines and sines of their angles into shared memory, then the
-// heads, a few of a lane's on their way at once. A lane's piece is the same in every
-// head, so what it is multiplied by is made once for a row and kind: with gamma folded
+// heads, up to eight of a lane's on their way at once. A lane's piece is the same in every
+// head, so what it is multiplied by is made once for them: with gamma folded
 // in, y[i] = r (x[i] C[i] + x'[i] S[i]), x' the partner's piece (a shuffle), r =
 // 1 / sqrt(mean x^2 + eps), C = gamma cos, S = -+ gamma' sin. Pieces behind the rotated
 // dims have C = gamma, S = 0.
@@ -29,7 +29,7 @@ namespace {
 
 constexpr int RP_THREADS = 256;
 constexpr int RP_TOKENS = 16;                    // tokens of a block at a time
-constexpr int RP_FLY = 4;                        // heads a lane has in flight
+constexpr int RP_FLY = 8;                        // heads a lane has in flight
 
 struct RopeArgs {
   spec_kv_view kv;
@@ -41,7 +41,7 @@ struct RopeArgs {
   int32_t* err;
   long long ld;                                  // bytes of a row
   int layer, hq, half8;                          // half8: rotated pairs / values of a piece
-  int parts;                                     // lane groups that share a row's heads
+  int chunks[2], heads[2];                       // of queries, of keys (and values): lane groups that share a token's, heads of each
   float eps;
   uint64_t turn[SPEC_ROPE_MAX_PAIRS];            // freq in 2^-64 turns
   uint8_t axis[SPEC_ROPE_MAX_PAIRS];
@@ -89,15 +89,19 @@ __device__ __forceinline__ void unpack2(const uint4& v, unsigned long long (&f)[
 }
 
 template <class KT, int D>
-__global__ void __launch_bounds__(RP_THREADS, 3) k_qk_norm_rope(const __grid_constant__ RopeArgs A) {
+__global__ void __launch_bounds__(RP_THREADS, 2) k_qk_norm_rope(const __grid_constant__ RopeArgs A) {
   constexpr int NV = Elt<KT>::per16, N2 = NV / 2, LPH = D / NV, GROUPS = RP_THREADS / LPH;
   __shared__ long long w_sum[RP_THREADS / 32];
   __shared__ int t_seq[RP_TOKENS], t_row[RP_TOKENS], t_pos[RP_TOKENS], t_page[RP_TOKENS];
-  __shared__ __align__(16) float t_cos[RP_TOKENS][D / 2], t_sin[RP_TOKENS][D / 2];
+  __shared__ __align__(16) float t_cos[RP_TOKENS][D / 2], t_sin[RP_TOKENS][D / 2], gam[2][D];
   const int t = threadIdx.x, lane = t & 31, w = t >> 5;
   pdl_wait();
   pdl_trigger();
 
+  for (int i = t; i < 2 * D; i += RP_THREADS) {
+    const float* gm = A.gamma[i / D];
+    gam[i / D][i % D] = gm ? gm[i % D] : 1.f;
+  }
   // this thread's sequences, the tokens before them and of them
   const int per = (A.ix.n_seq + RP_THREADS - 1) / RP_THREADS;
   const int a = min(t * per, A.ix.n_seq), a1 = min(a + per, A.ix.n_seq);
@@ -167,85 +171,95 @@ __global__ void __launch_bounds__(RP_THREADS, 3) k_qk_norm_rope(const __grid_con
       turn_cos_sin((uint32_t)(((uint64_t)pos * A.turn[p]) >> 32), t_cos[tok][p], t_sin[tok][p]);
     }
     __syncthreads();
-    // a lane group takes a token's heads share, share + parts, ..
-    for (int x = g; x < nt * A.parts; x += GROUPS) {
-      const int tok = x / A.parts, share = x - tok * A.parts, row = t_row[tok], page = t_page[tok];
-      const uint4* src = reinterpret_cast<const uint4*>(A.qkv + row * A.ld) + gl;
-      uint4* kd = page < 0 ? nullptr
-                           : cache + (((size_t)page * A.kv.n_layers + A.layer) * A.kv.n_kv_heads * 2) * plane16 +
-                                 (size_t)t_pos[tok] * LPH + gl;
-      uint4* qd = reinterpret_cast<uint4*>(A.q_out) + ((size_t)row * A.hq) * LPH + gl;
-#pragma unroll 1
-      for (int kind = 0; kind < 3; ++kind) {     // queries, keys, values
-        const float* gm = kind < 2 ? A.gamma[kind] : nullptr;
-        const int h0 = kind == 0 ? 0 : kind == 1 ? A.hq : A.hq + A.kv.n_kv_heads;
-        const int h1 = kind == 0 ? A.hq : h0 + A.kv.n_kv_heads;
-        uint4* dst = kind == 0 ? qd : kd ? kd + (kind - 1) * plane16 : nullptr;
-        const size_t step = kind == 0 ? LPH : 2 * plane16;
+    // a lane group takes up to RP_FLY heads of a token
+    const int items = A.chunks[0] + 2 * A.chunks[1];
+    for (int x = g; x < nt * items; x += GROUPS) {
+      const int tok = x / items, row = t_row[tok], page = t_page[tok];
+      int c = x - tok * items, kind = 0;         // queries, keys, values
+      if (c >= A.chunks[0]) {
+        c -= A.chunks[0];
+        kind = 1;
+        if (c >= A.chunks[1]) {
+          c -= A.chunks[1];
+          kind = 2;
+        }
+      }
+      const int k1 = kind > 0, hk = k1 ? A.kv.n_kv_heads : A.hq, h0 = c * A.heads[k1], nh = min(A.heads[k1], hk - h0);
+      const int in0 = h0 + (kind == 0 ? 0 : kind == 1 ? A.hq : A.hq + A.kv.n_kv_heads);
+      const uint4* src = reinterpret_cast<const uint4*>(A.qkv + row * A.ld) + (size_t)in0 * LPH + gl;
+      uint4 v[RP_FLY];
+#pragma unroll
+      for (int u = 0; u < RP_FLY; ++u)
+        if (u < nh) v[u] = ld_stream(src + u * LPH);
+      uint4* dst = reinterpret_cast<uint4*>(A.q_out) + ((size_t)row * A.hq + h0) * LPH + gl;
+      size_t step = LPH;
+      if (k1) {
+        step = 2 * plane16;
+        dst = page < 0 ? nullptr
+                       : cache + (((size_t)page * A.kv.n_layers + A.layer) * A.kv.n_kv_heads + h0) * step +
+                             (kind - 1) * plane16 + (size_t)t_pos[tok] * LPH + gl;
+      }
+      if (kind < 2) {
+        const bool norm = A.gamma[kind] != nullptr;
         unsigned long long C[N2], S[N2];
-        bool have = kind == 2;
-        for (int h = h0 + share; h < h1; h += A.parts * RP_FLY) {
-          uint4 v[RP_FLY];
+        {
+          float cs[NV], s[NV];
 #pragma unroll
-          for (int u = 0; u < RP_FLY; ++u)
-            if (h + u * A.parts < h1) v[u] = ld_stream(src + (size_t)(h + u * A.parts) * LPH);
-          if (!have) {                           // (beside the first loads)
-            have = true;
-            float c[NV], s[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-              c[i] = turns ? t_cos[tok][p0 + i] : 1.f;
-              s[i] = turns ? t_sin[tok][p0 + i] : 0.f;
-              if (low) s[i] = -s[i];
-              if (gm) {
-                c[i] *= __ldg(gm + gl * NV + i);
-                s[i] *= __ldg(gm + partner * NV + i);
-              }
+          for (int i = 0; i < NV; i += 4) {
+            float4 a4 = make_float4(1.f, 1.f, 1.f, 1.f), b4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (turns) {
+              a4 = *reinterpret_cast<const float4*>(&t_cos[tok][p0 + i]);
+              b4 = *reinterpret_cast<const float4*>(&t_sin[tok][p0 + i]);
             }
-#pragma unroll
-            for (int i = 0; i < N2; ++i) {
-              C[i] = pair(c[2 * i], c[2 * i + 1]);
-              S[i] = pair(s[2 * i], s[2 * i + 1]);
-            }
+            const float4 ga = *reinterpret_cast<const float4*>(&gam[kind][gl * NV + i]);
+            const float4 gb = *reinterpret_cast<const float4*>(&gam[kind][partner * NV + i]);
+            cs[i] = a4.x * ga.x; cs[i + 1] = a4.y * ga.y; cs[i + 2] = a4.z * ga.z; cs[i + 3] = a4.w * ga.w;
+            s[i] = b4.x * gb.x; s[i + 1] = b4.y * gb.y; s[i + 2] = b4.z * gb.z; s[i + 3] = b4.w * gb.w;
           }
 #pragma unroll
-          for (int u = 0; u < RP_FLY; ++u) {
-            const int hh = h + u * A.parts;
-            if (hh >= h1) break;
-            if (kind < 2) {
-              unsigned long long f[N2], o[N2];
-              unpack2<KT>(v[u], f);
-              float r = 1.f;
-              if (gm) {
-                unsigned long long s2 = mul2(f[0], f[0]);
-#pragma unroll
-                for (int i = 1; i < N2; ++i) s2 = fma2(f[i], f[i], s2);
-                const float2 sq = halves(s2);
-                float ss = sq.x + sq.y;
-#pragma unroll
-                for (int d = 1; d < LPH; d <<= 1) ss += __shfl_xor_sync(gmask, ss, d, LPH);
-                r = rsqrtf(ss * (1.f / D) + A.eps);
-              }
-              uint4 pv;
-              pv.x = __shfl_sync(gmask, v[u].x, partner, LPH);
-              pv.y = __shfl_sync(gmask, v[u].y, partner, LPH);
-              pv.z = __shfl_sync(gmask, v[u].z, partner, LPH);
-              pv.w = __shfl_sync(gmask, v[u].w, partner, LPH);
-              if (!turns) pv = make_uint4(0u, 0u, 0u, 0u);     // (also where the piece is not finite)
-              unpack2<KT>(pv, o);
-              const unsigned long long r2 = pair(r, r);
-              float y[NV];
-#pragma unroll
-              for (int i = 0; i < N2; ++i) {
-                const float2 z = halves(mul2(r2, fma2(f[i], C[i], mul2(o[i], S[i]))));
-                y[2 * i] = z.x;
-                y[2 * i + 1] = z.y;
-              }
-              v[u] = pack_piece<NV>(y);
-            }
-            if (dst) dst[(size_t)(hh - h0) * step] = v[u];
+          for (int i = 0; i < N2; ++i) {
+            C[i] = pair(cs[2 * i], cs[2 * i + 1]);
+            S[i] = low ? pair(-s[2 * i], -s[2 * i + 1]) : pair(s[2 * i], s[2 * i + 1]);
           }
         }
+#pragma unroll
+        for (int u = 0; u < RP_FLY; ++u) {
+          if (u >= nh) break;
+          unsigned long long f[N2], o[N2];
+          unpack2<KT>(v[u], f);
+          float r = 1.f;
+          if (norm) {
+            unsigned long long s2 = mul2(f[0], f[0]);
+#pragma unroll
+            for (int i = 1; i < N2; ++i) s2 = fma2(f[i], f[i], s2);
+            const float2 sq = halves(s2);
+            float ss = sq.x + sq.y;
+#pragma unroll
+            for (int d = 1; d < LPH; d <<= 1) ss += __shfl_xor_sync(gmask, ss, d, LPH);
+            r = rsqrtf(ss * (1.f / D) + A.eps);
+          }
+          uint4 pv;
+          pv.x = __shfl_sync(gmask, v[u].x, partner, LPH);
+          pv.y = __shfl_sync(gmask, v[u].y, partner, LPH);
+          pv.z = __shfl_sync(gmask, v[u].z, partner, LPH);
+          pv.w = __shfl_sync(gmask, v[u].w, partner, LPH);
+          if (!turns) pv = make_uint4(0u, 0u, 0u, 0u);         // (also where the piece is not finite)
+          unpack2<KT>(pv, o);
+          const unsigned long long r2 = pair(r, r);
+          float y[NV];
+#pragma unroll
+          for (int i = 0; i < N2; ++i) {
+            const float2 z = halves(mul2(r2, fma2(f[i], C[i], mul2(o[i], S[i]))));
+            y[2 * i] = z.x;
+            y[2 * i + 1] = z.y;
+          }
+          v[u] = pack_piece<NV>(y);
+        }
+      }
+      if (dst) {
+#pragma unroll
+        for (int u = 0; u < RP_FLY; ++u)
+          if (u < nh) dst[u * step] = v[u];
       }
     }
   }
@@ -283,7 +297,7 @@ extern "C" int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* 
   if (rope->dim > 0 && !positions_dev) return set_last_error(SPEC_ERR_ARG, "null positions");
   RopeArgs A{*kv, ChunkIndex{row_start_dev, n_new_dev, cache_len_dev, n_seq, n_rows, n_rows, kv->max_pages * kv->page_size},
              static_cast<const char*>(qkv_dev), static_cast<char*>(q_out_dev), positions_dev, {q_gamma_dev, k_gamma_dev},
-             err_dev, ld * esz, layer, n_q_heads, rope->dim / 2 / (16 / esz), 1, eps, {}, {}};
+             err_dev, ld * esz, layer, n_q_heads, rope->dim / 2 / (16 / esz), {}, {}, eps, {}, {}};
   for (int p = 0; p < rope->dim / 2; ++p) {
     if (!std::isfinite(rope->freq[p])) return set_last_error(SPEC_ERR_ARG, "a frequency is not finite");
     if (rope->axis[p] >= rope->n_axes) return set_last_error(SPEC_ERR_ARG, "a pair's axis is out of range");
@@ -298,11 +312,16 @@ extern "C" int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* 
   if (spans_meet(qkv_dev, in_bytes, kv->kv_dev, cache_bytes(*kv))) return set_last_error(SPEC_ERR_ARG, "qkv overlaps the cache");
   const int sms = sm_count_once();
   if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
-  // few rows: each group of lanes takes RP_FLY heads of one; many: two or fewer take a row
-  const int groups = RP_THREADS / (d * esz / 16), most = (n_q_heads + RP_FLY - 1) / RP_FLY;
-  const int64_t room = (int64_t)sms * 3 * groups;
-  A.parts = (int)std::max<int64_t>(1, std::min<int64_t>(most, room / n_rows));
-  const int blocks = (int)std::min<int64_t>(((int64_t)n_rows * A.parts + groups - 1) / groups, sms * 3);
+  int items = 0;
+  for (int i = 0; i < 2; ++i) {
+    const int n = i ? kv->n_kv_heads : n_q_heads;
+    A.chunks[i] = (n + RP_FLY - 1) / RP_FLY;
+    A.heads[i] = (n + A.chunks[i] - 1) / A.chunks[i];
+    A.chunks[i] = (n + A.heads[i] - 1) / A.heads[i];
+    items += (i + 1) * A.chunks[i];
+  }
+  const int groups = RP_THREADS / (d * esz / 16);
+  const int blocks = (int)std::min<int64_t>(((int64_t)n_rows * items + groups - 1) / groups, sms * 2);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaError_t e;
   if (esz == 2) e = d == 128 ? launch_rope<bf16_t, 128>(A, blocks, st) : launch_rope<bf16_t, 64>(A, blocks, st);
