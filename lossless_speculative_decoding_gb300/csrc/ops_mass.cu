@@ -6,9 +6,9 @@
 // rows stays with the position. A unit is (sequence, tile of keys, kv head): it
 // brings its keys once, goes over the counted rows that see them, and writes its
 // positions alone, so nothing is summed by atomics. Units of a sequence are
-// numbered from its first keys on, which the most rows see; of each B units block b
-// takes the b-th, and of the next B the b-th from their end, so that the sums of what
-// the blocks do stay close.
+// numbered from its first keys on, which the most rows see; of each B units worker b
+// (a block, or a pair of blocks) takes the b-th, and of the next B the b-th from their
+// end, so that the sums of what the workers do stay close.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -33,7 +33,9 @@ struct MassArgs {
   int layer, hq, G, last;
   int tok;             // tokens of a tile of rows (tensor-core form)
   int nk, nq, q_half;  // its rings: tiles of keys and of queries in shared memory, bytes of 64 dims of a tile of queries
+  int pair;            // blocks that share a unit's rows: 1 or 2
   float scale_l2e;     // scale * log2 e
+  float inv_scale;
 };
 
 // Unit: key tile `tile` of (sequence s, kv head hk), its rows from token i0 on.
@@ -42,17 +44,17 @@ struct MassUnit {
   int n, m, r0, i0;
 };
 
-// A warp's walk over its block's units.
+// A warp's walk over the units of worker `me` of `workers`.
 template <int KEYS>
 struct MassWalk {
-  long long round, before;                       // gridDim.x units each; units before sequence s
-  int s;
+  long long round, before;                       // `workers` units each; units before sequence s
+  int s, me, workers;
   const MassArgs* A;
-  __device__ MassWalk(const MassArgs& args) : round(0), before(0), s(0), A(&args) {}
+  __device__ MassWalk(const MassArgs& args, int me, int workers) : round(0), before(0), s(0), me(me), workers(workers), A(&args) {}
   __device__ static int tiles(int n, int m) { return (n + m + KEYS - 1) / KEYS; }
   __device__ bool next(MassUnit& g) {
     const int lane = threadIdx.x & 31, hkv = A->kv.n_kv_heads;
-    const long long u = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    const long long u = round * workers + (round & 1 ? workers - 1 - me : me);
     for (;;) {                                   // sequences 32 at a time
       if (s >= A->ix.n_seq) return false;
       const bool on = s + lane < A->ix.n_seq;
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
     for (int s = t; s < A.ix.n_seq; s += MF_THREADS)
       if (ChunkSeq(A.ix, s).bad) atomicOr(A.err, DERR_POS);
   const size_t page_elems = (size_t)A.kv.n_layers * A.kv.n_kv_heads * 2 * P * D;
-  MassWalk<MF_KEYS> walk(A);
+  MassWalk<MF_KEYS> walk(A, blockIdx.x, gridDim.x);
   MassUnit g;
   while (walk.next(g)) {
     const int k0 = g.tile * MF_KEYS, nk = min(MF_KEYS, g.n + g.m - k0);
@@ -211,37 +213,46 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// Tensor-core form (bf16 cache). One block per SM, eleven warps: a TMA producer, an MMA
-// issuer, a loader of the rows' lse and two groups of four warps that sum. A unit has two
-// tiles of 128 keys; against each tile of up to 128 rows (whole tokens), S = K Q^T goes
-// to tensor memory with the keys on the lanes, so that a thread sums its key's columns
-// in registers and no sum crosses threads. The groups take the tiles of rows in turn,
-// both tiles of keys of each: -lse, the same for all lanes, is read from shared memory
-// once for both. Four tiles of S make up tensor memory; one is given back as soon as
-// its scores are in registers.
+// Tensor-core form (bf16 cache). One block per SM, nineteen warps: a TMA producer, an MMA
+// issuer, a loader of the rows' lse and four groups of four warps that sum. A unit has
+// two tiles of 128 keys; against each tile of up to 128 rows (whole tokens), S = K Q^T
+// goes to tensor memory with the keys on the lanes, so that a thread sums its key's
+// columns in registers and no sum crosses threads. One more MMA adds -lse / scale to
+// every column: as three bf16 parts (24 bits) in three more dims of a row, against ones
+// in those of a key. (From shared memory, read by every thread, it took its bandwidth
+// from the MMAs: 218 us for ???.) Groups 0 and 1 take the even tiles of rows, 2 and 3 the
+// odd ones, each group one tile of keys; each has a quarter of tensor memory, which it
+// gives back as soon as its scores are in registers.
+//
+// Where units have many tiles of rows, two blocks (a cluster) share a unit, each every
+// other tile of rows, so that the few units of a single prompt's first keys do not
+// outlast the others; the second block's sums go to the first one's shared memory.
 //
 // Sums: 128 weights in fp32, the tiles of rows by a compensated sum (its rounding error
 // is carried along), so that thousands of rows lose no bits.
 constexpr int MT_KEYS = 128;
 constexpr int MT_UNIT = 2 * MT_KEYS;
-constexpr int MT_THREADS = 352;
+constexpr int MT_SUM = 16;                       // warps that sum
+constexpr int MT_THREADS = 32 * (MT_SUM + 3);
 constexpr int MT_MAX_NK = 8, MT_MAX_NQ = 4;
+constexpr int MT_PAIR_TILES = 8;                 // tiles of rows of a unit from which on blocks work in pairs
+constexpr int MT_EXT = 128 * 16;                 // bytes of 8 more dims of 128 rows
 
 template <int D>
 struct MtCfg {
   static constexpr int BUF = MT_KEYS * D * 2;    // a tile of keys
-  static constexpr int TAIL = 8192;              // alignment slack and the header
-  static constexpr int ROOM = 232448 - 512 - TAIL;
-  static constexpr int SMEM = ROOM + TAIL;
+  static constexpr int TAIL = 6144;              // alignment slack and the header
+  static constexpr int EXT = MT_EXT * (MT_MAX_NQ + 2);       // of each tile of rows; of keys: ones; zeros
+  static constexpr int ROOM = (232448 - 512 - TAIL - EXT) / 1024 * 1024;
+  static constexpr int SMEM = ROOM + EXT + TAIL;
 };
 
 struct MtHeader {
   uint64_t k_full[MT_MAX_NK], k_empty[MT_MAX_NK], q_full[MT_MAX_NQ], q_empty[MT_MAX_NQ], s_full[4], s_empty[4];
-  uint64_t sum_full[2], sum_empty[2], fin;
+  uint64_t sum_full[2][2], sum_empty[2][2], pair_full[2][2], pair_empty[2][2], fin;     // [turn][tile of keys]
   uint32_t tmem;
   int abort;
-  __align__(16) float nlse[MT_MAX_NQ][128];      // -lse log2 e of a tile's rows
-  float sum[2][MT_UNIT];                         // one group's sums of a unit, for the other
+  float sum[2][MT_UNIT], pair[2][MT_UNIT];       // sums of a unit: of the odd or even tiles, of the other block
 };
 
 // A sum with the rounding error that it has not taken in.
@@ -264,11 +275,13 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
   constexpr int GROUP = 1024 * HALVES;
   extern __shared__ unsigned char mt_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(mt_raw) + 1023) & ~uintptr_t(1023));
-  MtHeader& H = *reinterpret_cast<MtHeader*>(base + C::ROOM);
+  unsigned char* ext = base + C::ROOM;           // [tile of rows][row][8 dims], ones, zeros
+  MtHeader& H = *reinterpret_cast<MtHeader*>(ext + C::EXT);
   static_assert(sizeof(MtHeader) + 1024 <= C::TAIL, "header and alignment slack");
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int NK = A.nk, NQ = A.nq, q_bytes = HALVES * A.q_half;
   const uint32_t kbufs = sm_addr(base), qbufs = kbufs + NK * C::BUF;
+  const int rank = A.pair > 1 ? (int)cluster_rank() : 0;
   if (t == 0) {
     for (int i = 0; i < MT_MAX_NK; ++i) {
       mbar_init(H.k_full + i, 1);
@@ -276,21 +289,25 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     }
     for (int i = 0; i < MT_MAX_NQ; ++i) {
       mbar_init(H.q_full + i, 2);                // queries, lse
-      mbar_init(H.q_empty + i, 5);               // the MMAs, a group's warps
+      mbar_init(H.q_empty + i, 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(H.s_full + i, 1);
       mbar_init(H.s_empty + i, 4);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(H.sum_full + i, 4);
-      mbar_init(H.sum_empty + i, 4);
+      mbar_init(&H.sum_full[0][0] + i, 4);
+      mbar_init(&H.sum_empty[0][0] + i, 4);
+      mbar_init(&H.pair_full[0][0] + i, 4);
+      mbar_init(&H.pair_empty[0][0] + i, 4);
     }
     mbar_init(&H.fin, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     H.abort = 0;
   }
-  if (warp == 9) {
+  // ones in the first three dims behind a key's; zeros behind all
+  for (int i = t; i < 2 * 128; i += MT_THREADS)
+    *reinterpret_cast<uint4*>(ext + (MT_MAX_NQ * 128 + i) * 16) = i < 128 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  if (warp == MT_SUM + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&H.tmem)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -301,18 +318,27 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
       if (ChunkSeq(A.ix, s).bad) atomicOr(A.err, DERR_POS);
   tc_fence_before();
   __syncthreads();
+  if (A.pair > 1) cluster_sync();                // the other block's barriers are there
   tc_fence_after();
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other waits at
-  // once: every role leaves its loops (the sums of a unit that is not over are not written).
+  // once: every role leaves its loops (the sums of a unit that is not over are not
+  // written), and so does the other block of a pair when its own wait runs out.
   auto waitw = [&](const uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err)) != 0;
   };
+  // the same for a barrier that the other block arrives at
+  auto waitw_pair = [&](const uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_try_cluster(sm_addr(bar), parity & 1) ||
+                    (wait_long(sm_addr(bar), parity & 1, &H.abort, A.err) && mbar_try_cluster(sm_addr(bar), parity & 1));
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
   const int P = A.kv.page_size;
-  MassWalk<MT_UNIT> walk(A);
+  MassWalk<MT_UNIT> walk(A, blockIdx.x / A.pair, gridDim.x / A.pair);
   MassUnit g;
+  const int first = rank * A.tok, stride = A.pair * A.tok;   // this block's tiles of rows
 
-  if (warp == 8) {
+  if (warp == MT_SUM) {
     // ---- producer: a unit's keys (a box for each kb keys of a page), then its tiles of queries ----
     const int nbox = MT_KEYS / kb;
     const int planes = A.kv.n_layers * A.kv.n_kv_heads * 2;
@@ -320,6 +346,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     uint32_t kturn = 0, qturn = 0;               // passes over the rings
     bool ok = true;
     while (ok && walk.next(g)) {
+      if (g.i0 + first >= g.m) continue;         // (none of this block's)
       const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
       const int plane = (A.layer * A.kv.n_kv_heads + g.hk) * 2;
       int page[2];
@@ -352,7 +379,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
               : "memory");
         if (++kn == NK) { kn = 0; ++kturn; }
       }
-      for (int i = g.i0; ok && i < g.m; i += A.tok) {
+      for (int i = g.i0 + first; ok && i < g.m; i += stride) {
         if (qturn > 0 && !waitw(H.q_empty + qn, qturn - 1)) { ok = false; break; }
         const uint32_t full = sm_addr(H.q_full + qn);
         if (lane == 0)
@@ -371,17 +398,19 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     // shared memory outlives the copies (over, unless a wait was given up): each buffer's last one
     for (int i = 0; i < NK; ++i) mbar_wait_deadline(sm_addr(H.k_full + i), (i < kn ? kturn : kturn - 1) & 1, nullptr);
     for (int i = 0; i < NQ; ++i) mbar_wait_deadline(sm_addr(H.q_full + i), (i < qn ? qturn : qturn - 1) & 1, nullptr);
-  } else if (warp == 9) {
+  } else if (warp == MT_SUM + 1) {
     // ---- MMA issuer (the whole warp, on values that are the same in every lane; one lane issues) ----
-    const uint32_t one = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t one = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0), exts = sm_addr(ext);
+    const uint32_t ones = exts + MT_MAX_NQ * MT_EXT, zeros = ones + MT_EXT;
     auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     int kn = 0, qn = 0;
     uint32_t kturn = 0, qturn = 0, tiles = 0;
     uint32_t used[4] = {0, 0, 0, 0};
     bool ok = true;
     while (ok && walk.next(g)) {
-      const int nh = same(g.n + g.m - g.tile * MT_UNIT > MT_KEYS ? 2 : 1), i0 = same(g.i0), m = same(g.m);
-      for (int i = i0; ok && i < m; i += A.tok, ++tiles) {
+      const int nh = same(g.n + g.m - g.tile * MT_UNIT > MT_KEYS ? 2 : 1), i0 = same(g.i0) + first, m = same(g.m);
+      if (i0 >= m) continue;
+      for (int i = i0; ok && i < m; i += stride, ++tiles) {
         const int rows = min(A.tok, m - i) * A.G, gr = tiles & 1;
         // bf16 x bf16 -> f32, M = 128, N the rows in whole 16s
         const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)((rows + 15) / 16 * 2) << 17) | (8u << 24);
@@ -396,10 +425,12 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
           if (k > 0 && !(ok = waitw(H.s_empty + 2 * gr + h, k - 1))) break;
           tc_fence_after();
           const uint64_t ad = tt_desc(kbufs + kbuf * C::BUF, 16, GROUP), bd = tt_desc(qbufs + qn * q_bytes, 16, 1024);
+          const uint32_t d = tm + (2 * gr + h) * 128, qx = exts + qn * MT_EXT;
+          mma_ss(d, plain_desc(ones, zeros - ones, 128), plain_desc(qx, zeros - qx, 128), id, false, one);
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d)
-            mma_ss(tm + (2 * gr + h) * 128, ad + (uint64_t)(((d & 3) * 32 + (d >> 2) * 1024) >> 4),
-                   bd + (uint64_t)(((d & 3) * 32 + (d >> 2) * A.q_half) >> 4), id, d > 0, one);
+          for (int x = 0; x < D / 16; ++x)
+            mma_ss(d, ad + (uint64_t)(((x & 3) * 32 + (x >> 2) * 1024) >> 4),
+                   bd + (uint64_t)(((x & 3) * 32 + (x >> 2) * A.q_half) >> 4), id, true, one);
           tc_commit(sm_addr(H.s_full + 2 * gr + h), one);
         }
         if (!ok) break;
@@ -414,8 +445,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     // everything issued is done before TMEM is freed (also after an abort)
     tc_commit(sm_addr(&H.fin), one);
     mbar_wait_deadline(sm_addr(&H.fin), 0, nullptr);
-  } else if (warp == 10) {
-    // ---- loader of -lse log2 e ----
+  } else if (warp == MT_SUM + 2) {
+    // ---- loader of -lse / scale: three bf16 parts, each the rounding of what the ones before leave ----
     int at[4];                                   // of row lane + 32 k of a tile
 #pragma unroll
     for (int k = 0; k < 4; ++k) at[k] = (lane + 32 * k) / A.G * A.hq + (lane + 32 * k) % A.G;
@@ -423,117 +454,116 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     uint32_t qturn = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
-      for (int i = g.i0; i < g.m; i += A.tok) {
+      for (int i = g.i0 + first; i < g.m; i += stride) {
         const float* src = A.lse + (size_t)(g.r0 + i) * A.hq + g.hk * A.G;
         const int rows = min(A.tok, g.m - i) * A.G;
         float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < rows ? -src[at[k]] * LOG2E : 0.f;
+        for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < rows ? -src[at[k]] * A.inv_scale : 0.f;
         if (qturn > 0 && !waitw(H.q_empty + qn, qturn - 1)) { ok = false; break; }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) H.nlse[qn][lane + 32 * k] = v[k];
+        for (int k = 0; k < 4; ++k) {
+          uint16_t p[3];
+          split_parts(v[k], 0, 3, p);
+          *reinterpret_cast<uint4*>(ext + qn * MT_EXT + (lane + 32 * k) * 16) = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2], 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(sm_addr(H.q_full + qn));
         if (++qn == NQ) { qn = 0; ++qturn; }
       }
     }
   } else {
-    // ---- the groups that sum ----
-    const int gr = warp >> 2, r = t & 127;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    // ---- the groups that sum: tiles of rows gr, gr + 2, .. against tile h of the unit's keys ----
+    const int h = warp >> 2 & 1, gr = warp >> 3, r = t & 127;
+    const uint32_t sT = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (2 * gr + h) * 128;
     const unsigned long long sc2 = pair(A.scale_l2e, A.scale_l2e);
-    uint32_t tiles = 0, used[2] = {0, 0}, shared = 0;
-    int qn = 0;
-    uint32_t qturn = 0;
+    uint32_t tiles = 0, used = 0, shared = 0, paired = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
-      const int k0 = g.tile * MT_UNIT + r, nh = g.n + g.m - g.tile * MT_UNIT > MT_KEYS ? 2 : 1;
-      const int nt = max(0, (g.m - g.i0 + A.tok - 1) / A.tok);
-      const bool owner = nt == 0 ? gr == 0 : ((tiles + nt - 1) & 1) == (uint32_t)gr;       // (has the unit's last tile)
+      const int k0 = g.tile * MT_UNIT + h * MT_KEYS + r;
+      const int all = (g.m - g.i0 + A.tok - 1) / A.tok, nt = (all - rank + A.pair - 1) / A.pair;    // tiles of rows; this block's
+      const int other = A.pair > 1 ? all - (all + 1) / 2 : 0;                                     // the second block's
+      const uint32_t t0 = tiles;
+      tiles += nt;
+      if (k0 - r >= g.n + g.m) continue;         // (the unit has no second tile)
+      const bool owner = nt > 0 && ((t0 + nt - 1) & 1) == (uint32_t)gr;        // (has the block's last tile of the unit)
       const size_t e = ((size_t)g.s * A.kv.n_kv_heads + g.hk) * A.ld + k0;
-      float before[2] = {0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (owner && A.mass && k0 + h * MT_KEYS < g.n) before[h] = A.mass[e + h * MT_KEYS];
-      Comp sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-      for (int i = g.i0; i < g.m; i += A.tok, ++tiles) {
-        const int q = qn;
-        const uint32_t qt = qturn;
-        if (++qn == NQ) { qn = 0; ++qturn; }
-        if ((tiles & 1) != (uint32_t)gr) continue;
-        const int rows = min(A.tok, g.m - i) * A.G, chunks = (rows + 31) / 32;
-        if (!(ok = waitw(H.q_full + q, qt))) break;        // (lse)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok || h >= nh) break;
-          // the first row that sees the key
-          const long long lo64 = (long long)(k0 + h * MT_KEYS - g.n - i) * A.G;
-          const int lo = lo64 > 128 ? 128 : lo64 < 0 ? 0 : (int)lo64;
-          const bool cut = rows < 32 * chunks || __any_sync(0xffffffffu, lo > 0);
-          const uint32_t sT = tmem + lanes + (2 * gr + h) * 128;
-          if (!(ok = waitw(H.s_full + 2 * gr + h, used[h]++))) break;
-          tc_fence_after();
-          unsigned long long part[2] = {0, 0};
+      const float before = owner && rank == 0 && A.mass && k0 < g.n ? A.mass[e] : 0.f;
+      Comp sum{0.f, 0.f};
+      for (int j = (int)((t0 ^ gr) & 1); j < nt; j += 2) {
+        const int i = g.i0 + first + j * stride, rows = min(A.tok, g.m - i) * A.G, chunks = (rows + 31) / 32;
+        // the first row that sees the key
+        const long long lo64 = (long long)(k0 - g.n - i) * A.G;
+        const int lo = lo64 > 128 ? 128 : lo64 < 0 ? 0 : (int)lo64;
+        const bool cut = rows < 32 * chunks || __any_sync(0xffffffffu, lo > 0);
+        if (!(ok = waitw(H.s_full + 2 * gr + h, used++))) break;
+        tc_fence_after();
+        unsigned long long part[2] = {0, 0};
 #pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            uint32_t v[32];
-            tmem_ld32(sT + 32 * c, v);
-            if (c == chunks - 1) {               // the scores are read
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(sm_addr(H.s_empty + 2 * gr + h));
-            }
-            if (cut) {
-              const int a = lo - 32 * c, b = rows - 32 * c;
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (x < a || x >= b) v[x] = 0xff800000u;
-            }
-            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(&H.nlse[q][32 * c]);
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              const ulonglong2 n2 = nl[x / 4];
-              const float2 y = halves(fma2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sc2, n2.x));
-              const float2 z = halves(fma2(pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sc2, n2.y));
-              part[0] = add2(part[0], pair(ex2(y.x), ex2(y.y)));
-              part[1] = add2(part[1], pair(ex2(z.x), ex2(z.y)));
-            }
+        for (int c = 0; c < chunks; ++c) {
+          uint32_t v[32];
+          tmem_ld32(sT + 32 * c, v);
+          if (c == chunks - 1) {                 // the scores are read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sm_addr(H.s_empty + 2 * gr + h));
           }
-          const float2 p = halves(add2(part[0], part[1]));
-          sum[h].add(p.x + p.y);
+          if (cut) {
+            const int a = lo - 32 * c, b = rows - 32 * c;
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (x < a || x >= b) v[x] = 0xff800000u;
+          }
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const float2 y = halves(mul2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sc2));
+            part[x / 2 & 1] = add2(part[x / 2 & 1], pair(ex2(y.x), ex2(y.y)));
+          }
         }
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sm_addr(H.q_empty + q));
+        const float2 p = halves(add2(part[0], part[1]));
+        sum.add(p.x + p.y);
       }
       if (!ok) break;
-      if (nt > 1) {
+      if (nt > 1) {                              // the other group's tiles
         const uint32_t p = shared & 1, turn = shared >> 1;
         ++shared;
         if (!owner) {
-          if (turn > 0 && !(ok = waitw(H.sum_empty + p, turn - 1))) break;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) H.sum[p][h * MT_KEYS + r] = sum[h].s + sum[h].e;
+          if (turn > 0 && !(ok = waitw(&H.sum_empty[p][h], turn - 1))) break;
+          H.sum[p][h * MT_KEYS + r] = sum.s + sum.e;
           __syncwarp();
-          if (lane == 0) mbar_arrive(sm_addr(H.sum_full + p));
+          if (lane == 0) mbar_arrive(sm_addr(&H.sum_full[p][h]));
         } else {
-          if (!(ok = waitw(H.sum_full + p, turn))) break;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) sum[h].add(H.sum[p][h * MT_KEYS + r]);
+          if (!(ok = waitw(&H.sum_full[p][h], turn))) break;
+          sum.add(H.sum[p][h * MT_KEYS + r]);
           __syncwarp();
-          if (lane == 0) mbar_arrive(sm_addr(H.sum_empty + p));
+          if (lane == 0) mbar_arrive(sm_addr(&H.sum_empty[p][h]));
         }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (owner && k0 + h * MT_KEYS < g.n + g.m) A.out[e + h * MT_KEYS] = before[h] + (sum[h].s + sum[h].e);
+      if (other > 0) {                           // the other block's
+        const uint32_t p = paired & 1, turn = paired >> 1;
+        ++paired;
+        if (owner && rank > 0) {
+          if (turn > 0 && !(ok = waitw_pair(&H.pair_empty[p][h], turn - 1))) break;
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to(sm_addr(&H.pair[p][h * MT_KEYS + r]), 0)), "f"(sum.s + sum.e) : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(map_to(sm_addr(&H.pair_full[p][h]), 0));
+        } else if (owner) {
+          if (!(ok = waitw_pair(&H.pair_full[p][h], turn))) break;
+          sum.add(H.pair[p][h * MT_KEYS + r]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(map_to(sm_addr(&H.pair_empty[p][h]), 1));
+        }
+      }
+      if (owner && rank == 0 && k0 < g.n + g.m) A.out[e] = before + (sum.s + sum.e);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (warp == MT_SUM + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (A.pair > 1) cluster_sync();                // nothing is on its way to this block any more
 }
 
 template <int D>
@@ -546,12 +576,16 @@ cudaError_t launch_mass_tc(MassArgs A, int blocks, cudaStream_t st) {
   A.q_half = (A.tok * A.G + 15) / 16 * 16 * 128;
   A.nq = A.q_half <= 4096 ? 4 : 3;
   A.nk = std::min(MT_MAX_NK, (MtCfg<D>::ROOM - A.nq * A.q_half * (D / 64)) / MtCfg<D>::BUF);
+  // pairs of blocks: a prompt of 5,288 tokens, 32 on 8 heads, ??? us for ???
+  A.pair = (std::min(A.last, A.ix.max_new) + A.tok - 1) / A.tok >= MT_PAIR_TILES ? 2 : 1;
   CUtensorMap map, qmap;
   if (q_make_map(&qmap, A.q, D, A.hq, (uint64_t)A.ix.n_rows, A.G, A.tok) ||
       kv_make_group_map(&map, A.kv.kv_dev, D, A.kv.page_size, (uint64_t)A.kv.n_pages * A.kv.n_layers * A.kv.n_kv_heads * 2, kb))
     return cudaErrorInvalidValue;
   cudaError_t e = allow_dyn_smem_once<k_mass_tc<D>>();
-  return e == cudaSuccess ? launch_k(k_mass_tc<D>, dim3(blocks), dim3(MT_THREADS), MtCfg<D>::SMEM, st, map, qmap, A, kb) : e;
+  return e == cudaSuccess ? launch_clusters(k_mass_tc<D>, dim3(blocks / A.pair * A.pair), dim3(MT_THREADS), MtCfg<D>::SMEM, A.pair,
+                                            st, map, qmap, A, kb)
+                          : e;
 }
 
 template <int D>
@@ -578,6 +612,7 @@ extern "C" int spec_attention_mass(const spec_kv_view* kv, int layer, const void
   if (n_q_heads / kv->n_kv_heads > MS_MAX_G) return set_last_error(SPEC_ERR_UNSUPPORTED, "more than 128 query heads per kv head");
   if (!(scale > 0.f) || !(scale * LOG2E < INFINITY)) return set_last_error(SPEC_ERR_ARG, "scale must be positive, and finite times log2 e");
   if (!aligned16(q_dev)) return set_last_error(SPEC_ERR_ARG, "q must be 16-byte aligned");
+  if (scale < 5.4e-20f || scale > 1.9e19f) return set_last_error(SPEC_ERR_UNSUPPORTED, "scale beyond 2^-64 .. 2^64");
   if (ld < 1 || ld > ((int64_t)1 << 31)) return set_last_error(SPEC_ERR_ARG, "1 <= ld <= 2^31 required");
   const int64_t capacity = std::min<int64_t>((int64_t)kv->max_pages * kv->page_size, ld);
   // a sequence's units, and its rows of a kv head, are counted in 32 bits
@@ -590,7 +625,7 @@ extern "C" int spec_attention_mass(const spec_kv_view* kv, int layer, const void
   if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
   const int d = kv->head_dim;
   const MassArgs A{*kv, ChunkIndex{row_start_dev, n_new_dev, cache_len_dev, n_seq, n_rows, max_new, (int)capacity}, q_dev, lse_dev,
-                   mass_dev, out_mass_dev, err_dev, ld, layer, n_q_heads, n_q_heads / kv->n_kv_heads, last, 0, 0, 0, 0, scale * LOG2E};
+                   mass_dev, out_mass_dev, err_dev, ld, layer, n_q_heads, n_q_heads / kv->n_kv_heads, last, 0, 0, 0, 0, 1, scale * LOG2E, 1.f / scale};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaError_t e;
   if (kv->dtype == SPEC_F32) e = d == 128 ? launch_mass_fma<128>(A, 3 * sms, st) : launch_mass_fma<64>(A, 3 * sms, st);

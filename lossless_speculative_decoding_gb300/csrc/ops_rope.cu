@@ -70,11 +70,6 @@ __device__ __forceinline__ uint4 pack_piece(const float (&y)[NV]) {
   return r;
 }
 
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // Pairs of a piece's values.
 template <class KT>
 __device__ __forceinline__ void unpack2(const uint4& v, unsigned long long (&f)[Elt<KT>::per16 / 2]) {
