@@ -20,6 +20,7 @@ namespace spec {
 namespace {
 
 constexpr int MS_MAX_G = 128;                    // query heads per kv head
+constexpr float LN2_LO = -1.9046543e-9f;         // log 2 = LN2 (as a float) + LN2_LO
 
 struct MassArgs {
   spec_kv_view kv;
@@ -213,13 +214,16 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// Tensor-core form (bf16 cache). One block per SM, nineteen warps: a TMA producer, an MMA
-// issuer, a loader of the rows' lse and four groups of four warps that sum. A unit has
+// Tensor-core form (bf16 cache). One block per SM, twenty warps: a TMA producer, a loader
+// of the rows' lse, four groups of four warps that sum and an MMA issuer for each tile of
+// keys (an issue waits until the MMAs before it are nearly over, so one issuer's waits
+// would leave the tensor cores idle). A unit has
 // two tiles of 128 keys; against each tile of up to 128 rows (whole tokens), S = K Q^T
 // goes to tensor memory with the keys on the lanes, so that a thread sums its key's
-// columns in registers and no sum crosses threads. One more MMA adds -lse / scale to
-// every column: as three bf16 parts (24 bits) in three more dims of a row, against ones
-// in those of a key. (From shared memory, read by every thread, it took its bandwidth
+// columns in registers and no sum crosses threads. One more MMA adds (c - lse) / scale
+// to every column: as three bf16 parts (24 bits) in three more dims of a row, against
+// ones in those of a key. (c, a whole number of log 2, is near the unit's first lse, so
+// that what the tensor cores add stays small: their sums are cut, not rounded.) (From shared memory, read by every thread, it took its bandwidth
 // from the MMAs: 218 us for ???.) Groups 0 and 1 take the even tiles of rows, 2 and 3 the
 // odd ones, each group one tile of keys; each has a quarter of tensor memory, which it
 // gives back as soon as its scores are in registers.
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
 constexpr int MT_KEYS = 128;
 constexpr int MT_UNIT = 2 * MT_KEYS;
 constexpr int MT_SUM = 16;                       // warps that sum
-constexpr int MT_THREADS = 32 * (MT_SUM + 3);
+constexpr int MT_THREADS = 32 * (MT_SUM + 4);
 constexpr int MT_MAX_NK = 8, MT_MAX_NQ = 4;
 constexpr int MT_PAIR_TILES = 8;                 // tiles of rows of a unit from which on blocks work in pairs
 constexpr int MT_EXT = 128 * 16;                 // bytes of 8 more dims of 128 rows
@@ -249,11 +253,14 @@ struct MtCfg {
 
 struct MtHeader {
   uint64_t k_full[MT_MAX_NK], k_empty[MT_MAX_NK], q_full[MT_MAX_NQ], q_empty[MT_MAX_NQ], s_full[4], s_empty[4];
-  uint64_t sum_full[2][2], sum_empty[2][2], pair_full[2][2], pair_empty[2][2], fin;     // [turn][tile of keys]
+  uint64_t sum_full[2][2], sum_empty[2][2], pair_full[2][2], pair_empty[2][2], fin[2];  // [turn][tile of keys]
   uint32_t tmem;
   int abort;
   float sum[2][MT_UNIT], pair[2][MT_UNIT];       // sums of a unit: of the odd or even tiles, of the other block
 };
+
+// The whole number of log 2 near x.
+__device__ __forceinline__ float mt_near(float x) { return rintf(x * LOG2E); }
 
 // A sum with the rounding error that it has not taken in.
 struct Comp {
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     }
     for (int i = 0; i < MT_MAX_NQ; ++i) {
       mbar_init(H.q_full + i, 2);                // queries, lse
-      mbar_init(H.q_empty + i, 1);
+      mbar_init(H.q_empty + i, 2);               // the issuers
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(H.s_full + i, 1);
@@ -299,7 +306,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
       mbar_init(&H.pair_full[0][0] + i, 4);
       mbar_init(&H.pair_empty[0][0] + i, 4);
     }
-    mbar_init(&H.fin, 1);
+    mbar_init(H.fin, 1);
+    mbar_init(H.fin + 1, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     H.abort = 0;
   }
@@ -307,7 +315,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
   for (int i = t; i < 2 * 128; i += MT_THREADS)
     *reinterpret_cast<uint4*>(ext + (MT_MAX_NQ * 128 + i) * 16) = i < 128 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  if (warp == MT_SUM + 1) {
+  if (warp == MT_SUM) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm_addr(&H.tmem)), "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -398,53 +406,51 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     // shared memory outlives the copies (over, unless a wait was given up): each buffer's last one
     for (int i = 0; i < NK; ++i) mbar_wait_deadline(sm_addr(H.k_full + i), (i < kn ? kturn : kturn - 1) & 1, nullptr);
     for (int i = 0; i < NQ; ++i) mbar_wait_deadline(sm_addr(H.q_full + i), (i < qn ? qturn : qturn - 1) & 1, nullptr);
-  } else if (warp == MT_SUM + 1) {
-    // ---- MMA issuer (the whole warp, on values that are the same in every lane; one lane issues) ----
+  } else if (warp == MT_SUM + 1 || warp == MT_SUM + 3) {
+    // ---- MMA issuer of a unit's tile h of keys (the whole warp, on values that are the same in every lane) ----
+    auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const int h = same(warp) == MT_SUM + 3;
     const uint32_t one = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0), exts = sm_addr(ext);
     const uint32_t ones = exts + MT_MAX_NQ * MT_EXT, zeros = ones + MT_EXT;
-    auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     int kn = 0, qn = 0;
     uint32_t kturn = 0, qturn = 0, tiles = 0;
-    uint32_t used[4] = {0, 0, 0, 0};
+    uint32_t used[2] = {0, 0};
     bool ok = true;
     while (ok && walk.next(g)) {
       const int nh = same(g.n + g.m - g.tile * MT_UNIT > MT_KEYS ? 2 : 1), i0 = same(g.i0) + first, m = same(g.m);
       if (i0 >= m) continue;
-      for (int i = i0; ok && i < m; i += stride, ++tiles) {
+      const int kbuf = kn + h < NK ? kn + h : kn + h - NK;
+      if (h < nh && !(ok = waitw(H.k_full + kbuf, kn + h < NK ? kturn : kturn + 1))) break;
+      const uint64_t ad = tt_desc(kbufs + kbuf * C::BUF, 16, GROUP);
+      for (int i = i0; i < m; i += stride, ++tiles) {
         const int rows = min(A.tok, m - i) * A.G, gr = tiles & 1;
-        // bf16 x bf16 -> f32, M = 128, N the rows in whole 16s
-        const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)((rows + 15) / 16 * 2) << 17) | (8u << 24);
-        if (!(ok = waitw(H.q_full + qn, qturn))) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok || h >= nh) break;
-          const int kbuf = kn + h < NK ? kn + h : kn + h - NK;
-          const uint32_t kt = kn + h < NK ? kturn : kturn + 1;
-          if (i == i0 && !(ok = waitw(H.k_full + kbuf, kt))) break;
-          const uint32_t k = gr ? used[2 + h]++ : used[h]++;
+        if (!(ok = waitw(H.q_full + qn, qturn))) break;          // (also where there is no tile h: one arrival a turn)
+        if (h < nh) {
+          // bf16 x bf16 -> f32, M = 128, N the rows in whole 16s
+          const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)((rows + 15) / 16 * 2) << 17) | (8u << 24);
+          const uint32_t k = gr ? used[1]++ : used[0]++;
           if (k > 0 && !(ok = waitw(H.s_empty + 2 * gr + h, k - 1))) break;
           tc_fence_after();
-          const uint64_t ad = tt_desc(kbufs + kbuf * C::BUF, 16, GROUP), bd = tt_desc(qbufs + qn * q_bytes, 16, 1024);
+          const uint64_t bd = tt_desc(qbufs + qn * q_bytes, 16, 1024);
           const uint32_t d = tm + (2 * gr + h) * 128, qx = exts + qn * MT_EXT;
-          mma_ss(d, plain_desc(ones, zeros - ones, 128), plain_desc(qx, zeros - qx, 128), id, false, one);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x)
             mma_ss(d, ad + (uint64_t)(((x & 3) * 32 + (x >> 2) * 1024) >> 4),
-                   bd + (uint64_t)(((x & 3) * 32 + (x >> 2) * A.q_half) >> 4), id, true, one);
+                   bd + (uint64_t)(((x & 3) * 32 + (x >> 2) * A.q_half) >> 4), id, x > 0, one);
+          mma_ss(d, plain_desc(ones, zeros - ones, 128), plain_desc(qx, zeros - qx, 128), id, true, one);
           tc_commit(sm_addr(H.s_full + 2 * gr + h), one);
         }
-        if (!ok) break;
         tc_commit(sm_addr(H.q_empty + qn), one);
         if (++qn == NQ) { qn = 0; ++qturn; }
       }
-      for (int h = 0; ok && h < nh; ++h) {
-        tc_commit(sm_addr(H.k_empty + kn), one);
+      if (!ok) break;
+      if (h < nh) tc_commit(sm_addr(H.k_empty + kbuf), one);
+      for (int x = 0; x < nh; ++x)
         if (++kn == NK) { kn = 0; ++kturn; }
-      }
     }
     // everything issued is done before TMEM is freed (also after an abort)
-    tc_commit(sm_addr(&H.fin), one);
-    mbar_wait_deadline(sm_addr(&H.fin), 0, nullptr);
+    tc_commit(sm_addr(H.fin + h), one);
+    mbar_wait_deadline(sm_addr(H.fin + h), 0, nullptr);
   } else if (warp == MT_SUM + 2) {
     // ---- loader of -lse / scale: three bf16 parts, each the rounding of what the ones before leave ----
     int at[4];                                   // of row lane + 32 k of a tile
@@ -454,12 +460,13 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     uint32_t qturn = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
+      const float c = mt_near(A.lse[(size_t)(g.r0 + g.i0) * A.hq + g.hk * A.G]);
       for (int i = g.i0 + first; i < g.m; i += stride) {
         const float* src = A.lse + (size_t)(g.r0 + i) * A.hq + g.hk * A.G;
         const int rows = min(A.tok, g.m - i) * A.G;
         float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < rows ? -src[at[k]] * A.inv_scale : 0.f;
+        for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < rows ? fmaf(c, LN2_LO, fmaf(c, LN2, -src[at[k]])) * A.inv_scale : 0.f;
         if (qturn > 0 && !waitw(H.q_empty + qn, qturn - 1)) { ok = false; break; }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -489,6 +496,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
       if (k0 - r >= g.n + g.m) continue;         // (the unit has no second tile)
       const bool owner = nt > 0 && ((t0 + nt - 1) & 1) == (uint32_t)gr;        // (has the block's last tile of the unit)
       const size_t e = ((size_t)g.s * A.kv.n_kv_heads + g.hk) * A.ld + k0;
+      const float c = mt_near(A.lse[(size_t)(g.r0 + g.i0) * A.hq + g.hk * A.G]);
+      const unsigned long long nc2 = pair(-c, -c);
       const float before = owner && rank == 0 && A.mass && k0 < g.n ? A.mass[e] : 0.f;
       Comp sum{0.f, 0.f};
       for (int j = (int)((t0 ^ gr) & 1); j < nt; j += 2) {
@@ -501,23 +510,23 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
         tc_fence_after();
         unsigned long long part[2] = {0, 0};
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
+        for (int ch = 0; ch < chunks; ++ch) {
           uint32_t v[32];
-          tmem_ld32(sT + 32 * c, v);
-          if (c == chunks - 1) {                 // the scores are read
+          tmem_ld32(sT + 32 * ch, v);
+          if (ch == chunks - 1) {                 // the scores are read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(sm_addr(H.s_empty + 2 * gr + h));
           }
           if (cut) {
-            const int a = lo - 32 * c, b = rows - 32 * c;
+            const int a = lo - 32 * ch, b = rows - 32 * ch;
 #pragma unroll
             for (int x = 0; x < 32; ++x)
               if (x < a || x >= b) v[x] = 0xff800000u;
           }
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
-            const float2 y = halves(mul2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sc2));
+            const float2 y = halves(fma2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sc2, nc2));
             part[x / 2 & 1] = add2(part[x / 2 & 1], pair(ex2(y.x), ex2(y.y)));
           }
         }
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == MT_SUM + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  if (warp == MT_SUM) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   if (A.pair > 1) cluster_sync();                // nothing is on its way to this block any more
 }
 
