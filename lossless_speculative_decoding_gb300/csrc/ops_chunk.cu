@@ -74,29 +74,17 @@ struct ChunkWalk {
     for (int rt = 0, nrt = chunk_row_tiles(A, z.m); rt < nrt; ++rt) sum += chunk_tiles(A, z.n, z.m, rt) + A.extra;
     return sum * A.heads;
   }
-  template <int THREADS>
-  __device__ void init(const ChunkArgs& args) {
-    __shared__ long long w_sum[THREADS / 32];
-    __shared__ int s_seq, s_rt, s_in;
-    A = &args;
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int per = (args.ix.n_seq + THREADS - 1) / THREADS;
-    const int a = min(t * per, args.ix.n_seq), a1 = min(a + per, args.ix.n_seq);
-    long long sum = 0;
-    for (int i = a; i < a1; ++i) sum += units_of(args, i);
-    long long inc = sum;
+  // Inclusive prefix sum over a warp.
+  __device__ static long long scan(long long v) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const long long x = __shfl_up_sync(0xffffffffu, v, o);
+      if ((threadIdx.x & 31) >= o) v += x;
     }
-    if (lane == 31) w_sum[w] = inc;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int i = 0; i < THREADS / 32; ++i) {
-      if (i < w) before += w_sum[i];
-      total += w_sum[i];
-    }
+    return v;
+  }
+  // This block's share of U units.
+  __device__ void share(long long total) {
     U = total;
     blocks = (int)min((long long)gridDim.x, max(U, 1ll));
     // floor(U b / blocks) = (U / blocks) b + floor((U % blocks) b / blocks)
@@ -104,21 +92,78 @@ struct ChunkWalk {
     const int rest = (int)(U - each * blocks), b = min((int)blockIdx.x, blocks), b1 = min((int)blockIdx.x + 1, blocks);
     u = each * b + rest * b / blocks;
     u1 = each * b1 + rest * b1 / blocks;
+  }
+  // The row tile of sequence s, whose units start at `at`, that has unit u; by a warp.
+  __device__ void find_tile(long long at) {
+    const int lane = threadIdx.x & 31;
+    const ChunkSeq z(A->ix, s);
+    for (rt = 0;; rt += 32) {
+      const int r = rt + lane;
+      const long long mine = r < chunk_row_tiles(*A, z.m) ? (long long)(chunk_tiles(*A, z.n, z.m, r) + A->extra) * A->heads : 0;
+      const long long end = at + scan(mine);
+      const uint32_t past = __ballot_sync(0xffffffffu, end > u);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        in = (int)(u - __shfl_sync(0xffffffffu, end - mine, l));
+        rt += l;
+        return;
+      }
+      at = __shfl_sync(0xffffffffu, end, 31);
+      if (rt > chunk_row_tiles(*A, z.m)) return;   // (only if the lengths changed meanwhile)
+    }
+  }
+  template <int THREADS>
+  __device__ void init(const ChunkArgs& args) {
+    __shared__ long long w_sum[32];
+    __shared__ long long s_at;
+    __shared__ int s_seq;
+    A = &args;
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    s = rt = in = 0;
+    if (args.ix.n_seq <= 32) {
+      // few sequences: a warp adds up the row tiles of one
+      for (int i = w; i < args.ix.n_seq; i += THREADS / 32) {
+        const ChunkSeq z(args.ix, i);
+        long long sum = 0;
+        for (int r = lane, nrt = chunk_row_tiles(args, z.m); r < nrt; r += 32) sum += chunk_tiles(args, z.n, z.m, r) + args.extra;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) w_sum[i] = sum * args.heads;
+      }
+      __syncthreads();
+      const long long mine = lane < args.ix.n_seq ? w_sum[lane] : 0, end = scan(mine);
+      share(__shfl_sync(0xffffffffu, end, 31));
+      if (u < u1) {
+        s = __ffs(__ballot_sync(0xffffffffu, end > u)) - 1;
+        find_tile(__shfl_sync(0xffffffffu, end - mine, s));
+      }
+      return;
+    }
+    // many: a thread adds up the sequences of its share
+    const int per = (args.ix.n_seq + THREADS - 1) / THREADS;
+    const int a = min(t * per, args.ix.n_seq), a1 = min(a + per, args.ix.n_seq);
+    long long sum = 0;
+    for (int i = a; i < a1; ++i) sum += units_of(args, i);
+    const long long inc = scan(sum);
+    if (lane == 31) w_sum[w] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int i = 0; i < THREADS / 32; ++i) {
+      if (i < w) before += w_sum[i];
+      total += w_sum[i];
+    }
+    share(total);
     long long at = before + inc - sum;
     if (u < u1 && at <= u && u < at + sum) {     // one thread's sequences hold unit u
-      int i = a, r = 0;
+      int i = a;
       for (long long c; at + (c = units_of(args, i)) <= u; ++i) at += c;
-      const ChunkSeq z(args.ix, i);
-      for (long long c; at + (c = (long long)(chunk_tiles(args, z.n, z.m, r) + args.extra) * args.heads) <= u; ++r) at += c;
       s_seq = i;
-      s_rt = r;
-      s_in = (int)(u - at);
+      s_at = at;
     }
     __syncthreads();
     if (u < u1) {
       s = s_seq;
-      rt = s_rt;
-      in = s_in;
+      find_tile(s_at);
     }
   }
   __device__ bool next(ChunkSeg& g) {
@@ -505,7 +550,9 @@ struct CtTile {
   bool first, live;            // no O yet; a row
 };
 
+// (The volatile statement keeps it behind its branch: predicated, it is half of a tile's instructions.)
 __device__ __forceinline__ void ct_mask(uint32_t (&v)[32], int seen) {
+  asm volatile("" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     if (i >= seen) v[i] = 0xff800000u;
@@ -631,7 +678,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
       if (ChunkSeq(A.ix, s).bad) atomicOr(A.err, DERR_POS);
   ChunkWalk walk;
   tc_fence_before();
-  walk.init<CT_THREADS>(A);                      // two block barriers
+  walk.init<CT_THREADS>(A);                      // (a block barrier at least)
   tc_fence_after();
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other waits
@@ -963,33 +1010,48 @@ __global__ void __launch_bounds__(CX_WARPS * 32) k_chunk_tc_join(const __grid_co
   const bool live = r < rows;
   // part 0 of the join is this block's part 1, then part 0 of the blocks after it
   auto at = [&](int c) { return ((size_t)(blockIdx.x + c) * 2 + (c == 0 ? 1 : 0)) * 2 + gr; };
+  constexpr int PER = D / 4 / CX_WARPS, FLY = 2;  // pieces of 4 dims a warp; parts on their way at once
+  float4 v[FLY][PER];
+  float2 ml[FLY];
+  auto fetch = [&](int c0) {
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+      const bool on = live && c0 + f < parts;
+      ml[f] = on ? __ldcg(A.part_ml + at(c0 + f) * 128 + r) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (on) v[f][i] = __ldcg(reinterpret_cast<const float4*>(A.part_o) + at(c0 + f) * 128 * (D / 4) + (w * PER + i) * 128 + r);
+    }
+  };
   float M = -INFINITY, L = 0.f;
-  for (int c = 0; c < parts; ++c) {
-    const float2 ml = live ? __ldcg(A.part_ml + at(c) * 128 + r) : make_float2(0.f, 1.f);
-    const float mn = fmaxf(M, ml.x);
-    if (ml.y > 0.f) L = L * exp2f(M - mn) + ml.y * exp2f(ml.x - mn);
-    M = mn;
-  }
-  const float inv = 1.f / L;
-  if (A.lse && w == 0 && live) A.lse[row_at(A, jt.x, jt.y, jt.z, gr * rpg + r)] = (M + log2f(L)) * LN2;
-  constexpr int PER = D / 4 / CX_WARPS;          // pieces of 4 dims a warp
   float4 o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = 0; c < parts; ++c) {
-    const float2 ml = live ? __ldcg(A.part_ml + at(c) * 128 + r) : make_float2(0.f, 0.f);
-    const float4* p = reinterpret_cast<const float4*>(A.part_o) + at(c) * 128 * (D / 4) + r;
-    if (ml.y > 0.f) {                            // (a part that saw nothing of the row may hold anything)
-      const float f = exp2f(ml.x - M) * inv;
+  for (int c0 = 0; c0 < parts; c0 += FLY) {
+    fetch(c0);
+#pragma unroll
+    for (int f = 0; f < FLY; ++f) {
+      if (!(ml[f].y > 0.f)) continue;            // (a part that saw nothing of the row may hold anything)
+      const float mn = fmaxf(M, ml[f].x), a = exp2f(M - mn), b = exp2f(ml[f].x - mn);
+      M = mn;
+      L = L * a + ml[f].y * b;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const float4 v = __ldcg(p + (w * PER + i) * 128);
-        o[i].x = fmaf(v.x, f, o[i].x);
-        o[i].y = fmaf(v.y, f, o[i].y);
-        o[i].z = fmaf(v.z, f, o[i].z);
-        o[i].w = fmaf(v.w, f, o[i].w);
+        o[i].x = fmaf(v[f][i].x, b, o[i].x * a);
+        o[i].y = fmaf(v[f][i].y, b, o[i].y * a);
+        o[i].z = fmaf(v[f][i].z, b, o[i].z * a);
+        o[i].w = fmaf(v[f][i].w, b, o[i].w * a);
       }
     }
+  }
+  const float inv = 1.f / L;
+  if (A.lse && w == 0 && live) A.lse[row_at(A, jt.x, jt.y, jt.z, gr * rpg + r)] = (M + log2f(L)) * LN2;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    o[i].x *= inv;
+    o[i].y *= inv;
+    o[i].z *= inv;
+    o[i].w *= inv;
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) y[lane][w * PER + i] = make_uint2(pack_bf16(o[i].x, o[i].y), pack_bf16(o[i].z, o[i].w));

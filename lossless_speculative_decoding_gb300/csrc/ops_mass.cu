@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
             if (lane == 0) mbar_arrive(sm_addr(H.s_empty + 2 * gr + h));
           }
           if (cut) {
+            asm volatile("" ::: "memory");       // (behind a branch, not predicated)
             const int a = lo - 32 * ch, b = rows - 32 * ch;
 #pragma unroll
             for (int x = 0; x < 32; ++x)
