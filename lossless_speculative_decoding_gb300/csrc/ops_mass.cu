@@ -232,6 +232,10 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
 // other tile of rows, so that the few units of a single prompt's first keys do not
 // outlast the others; the second block's sums go to the first one's shared memory.
 //
+// The loader walks over the units and hands them to the other roles, with their pages,
+// through a small ring: twenty warps that each looked for themselves took a third of the
+// issue slots where a unit has one row (126 us for ???).
+//
 // Sums: 128 weights in fp32, the tiles of rows by a compensated sum (its rounding error
 // is carried along), so that thousands of rows lose no bits.
 constexpr int MT_KEYS = 128;
@@ -241,6 +245,7 @@ constexpr int MT_THREADS = 32 * (MT_SUM + 4);
 constexpr int MT_MAX_NK = 8, MT_MAX_NQ = 4;
 constexpr int MT_PAIR_TILES = 8;                 // tiles of rows of a unit from which on blocks work in pairs
 constexpr int MT_EXT = 128 * 16;                 // bytes of 8 more dims of 128 rows
+constexpr int MT_RING = 4;                       // units handed over at once
 
 template <int D>
 struct MtCfg {
@@ -254,8 +259,12 @@ struct MtCfg {
 struct MtHeader {
   uint64_t k_full[MT_MAX_NK], k_empty[MT_MAX_NK], q_full[MT_MAX_NQ], q_empty[MT_MAX_NQ], s_full[4], s_empty[4];
   uint64_t sum_full[2][2], sum_empty[2][2], pair_full[2][2], pair_empty[2][2], fin[2];  // [turn][tile of keys]
+  uint64_t unit_full[MT_RING], unit_empty[MT_RING];
   uint32_t tmem;
   int abort;
+  MassUnit unit[MT_RING];                        // s < 0: no more
+  float near[MT_RING];                           // mt_near of the unit's first lse
+  int page[MT_RING][2][MT_KEYS / 16];            // of each box of keys; -1 reads zeros
   float sum[2][MT_UNIT], pair[2][MT_UNIT];       // sums of a unit: of the odd or even tiles, of the other block
 };
 
@@ -306,6 +315,10 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
       mbar_init(&H.pair_full[0][0] + i, 4);
       mbar_init(&H.pair_empty[0][0] + i, 4);
     }
+    for (int i = 0; i < MT_RING; ++i) {
+      mbar_init(H.unit_full + i, 1);
+      mbar_init(H.unit_empty + i, MT_SUM + 3);   // every other warp
+    }
     mbar_init(H.fin, 1);
     mbar_init(H.fin + 1, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -342,8 +355,19 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     return __all_sync(0xffffffffu, ok) != 0;
   };
   const int P = A.kv.page_size;
-  MassWalk<MT_UNIT> walk(A, blockIdx.x / A.pair, gridDim.x / A.pair);
   MassUnit g;
+  // the next unit of the ring; what else is of it is read before `taken`
+  uint32_t units = 0;
+  auto take = [&]() {
+    if (!waitw(H.unit_full + units % MT_RING, units / MT_RING)) return false;
+    g = H.unit[units % MT_RING];
+    return g.s >= 0;
+  };
+  auto taken = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm_addr(H.unit_empty + units % MT_RING));
+    ++units;
+  };
   const int first = rank * A.tok, stride = A.pair * A.tok;   // this block's tiles of rows
 
   if (warp == MT_SUM) {
@@ -353,27 +377,17 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     int kn = 0, qn = 0;                          // ring positions
     uint32_t kturn = 0, qturn = 0;               // passes over the rings
     bool ok = true;
-    while (ok && walk.next(g)) {
-      if (g.i0 + first >= g.m) continue;         // (none of this block's)
-      const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
-      const int plane = (A.layer * A.kv.n_kv_heads + g.hk) * 2;
+    while (ok && take()) {
+      const MassUnit n = g;
       int page[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = g.tile * MT_UNIT + h * MT_KEYS + kb * lane;
-        page[h] = -1;                            // reads zeros
-        if (lane < nbox && key < g.n + g.m) {
-          page[h] = bt[key / P];
-          if (page[h] < 0 || page[h] >= A.kv.n_pages) {
-            page[h] = -1;
-            atomicOr(A.err, DERR_PAGE);
-          }
-        }
-      }
+      for (int h = 0; h < 2; ++h) page[h] = lane < nbox ? H.page[units % MT_RING][h][lane] : -1;
+      taken();
+      const int plane = (A.layer * A.kv.n_kv_heads + n.hk) * 2;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k0 = g.tile * MT_UNIT + h * MT_KEYS, key = k0 + kb * lane;
-        if (!ok || k0 >= g.n + g.m) break;
+        const int k0 = n.tile * MT_UNIT + h * MT_KEYS, key = k0 + kb * lane;
+        if (!ok || k0 >= n.n + n.m) break;
         if (kturn > 0 && !waitw(H.k_empty + kn, kturn - 1)) { ok = false; break; }
         const uint32_t full = sm_addr(H.k_full + kn);
         if (lane == 0)
@@ -387,7 +401,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
               : "memory");
         if (++kn == NK) { kn = 0; ++kturn; }
       }
-      for (int i = g.i0 + first; ok && i < g.m; i += stride) {
+      for (int i = n.i0 + first; ok && i < n.m; i += stride) {
         if (qturn > 0 && !waitw(H.q_empty + qn, qturn - 1)) { ok = false; break; }
         const uint32_t full = sm_addr(H.q_full + qn);
         if (lane == 0)
@@ -398,7 +412,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
           asm volatile(
               "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
               ::"r"(qbufs + qn * q_bytes + lane * A.q_half), "l"(reinterpret_cast<uint64_t>(&qmap)), "r"(0), "r"(lane),
-                "r"(g.hk * A.G), "r"(g.r0 + i), "r"(full)
+                "r"(n.hk * A.G), "r"(n.r0 + i), "r"(full)
               : "memory");
         if (++qn == NQ) { qn = 0; ++qturn; }
       }
@@ -416,9 +430,9 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     uint32_t kturn = 0, qturn = 0, tiles = 0;
     uint32_t used[2] = {0, 0};
     bool ok = true;
-    while (ok && walk.next(g)) {
+    while (ok && take()) {
+      taken();
       const int nh = same(g.n + g.m - g.tile * MT_UNIT > MT_KEYS ? 2 : 1), i0 = same(g.i0) + first, m = same(g.m);
-      if (i0 >= m) continue;
       const int kbuf = kn + h < NK ? kn + h : kn + h - NK;
       if (h < nh && !(ok = waitw(H.k_full + kbuf, kn + h < NK ? kturn : kturn + 1))) break;
       const uint64_t ad = tt_desc(kbufs + kbuf * C::BUF, 16, GROUP);
@@ -452,33 +466,81 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     tc_commit(sm_addr(H.fin + h), one);
     mbar_wait_deadline(sm_addr(H.fin + h), 0, nullptr);
   } else if (warp == MT_SUM + 2) {
-    // ---- loader of -lse / scale: three bf16 parts, each the rounding of what the ones before leave ----
+    // ---- loader: the units, and (c - lse) / scale of their rows as three bf16 parts, each the rounding of
+    // what the ones before leave. It reads for the next tile of rows before it waits for a place for this one.
+    MassWalk<MT_UNIT> walk(A, blockIdx.x / A.pair, gridDim.x / A.pair);
+    const int nbox = MT_KEYS / kb;
     int at[4];                                   // of row lane + 32 k of a tile
 #pragma unroll
     for (int k = 0; k < 4; ++k) at[k] = (lane + 32 * k) / A.G * A.hq + (lane + 32 * k) % A.G;
-    int qn = 0;
+    int qn = 0, i = 0;
     uint32_t qturn = 0;
-    bool ok = true;
-    while (ok && walk.next(g)) {
-      const float c = mt_near(A.lse[(size_t)(g.r0 + g.i0) * A.hq + g.hk * A.G]);
-      for (int i = g.i0 + first; i < g.m; i += stride) {
-        const float* src = A.lse + (size_t)(g.r0 + i) * A.hq + g.hk * A.G;
-        const int rows = min(A.tok, g.m - i) * A.G;
-        float v[4];
+    float lse[4], near0 = 0.f;                   // of the next tile of rows; the unit's first lse
+    int rows = 0, page[2];                       // (of the unit's boxes)
+    bool fresh = true, have = false, ok = true;  // the tile is its unit's first
+    auto look = [&]() {                          // the next tile of rows
+      if (have) i += stride;
+      fresh = !have || i >= g.m;
+      if (fresh) {
+        do {
+          if (!walk.next(g)) return false;
+          i = g.i0 + first;
+        } while (i >= g.m);                      // (none of this block's)
+        near0 = A.lse[(size_t)(g.r0 + g.i0) * A.hq + g.hk * A.G];
+        const int32_t* bt = A.kv.block_table_dev + (size_t)g.s * A.kv.max_pages;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < rows ? fmaf(c, LN2_LO, fmaf(c, LN2, -src[at[k]])) * A.inv_scale : 0.f;
-        if (qturn > 0 && !waitw(H.q_empty + qn, qturn - 1)) { ok = false; break; }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint16_t p[3];
-          split_parts(v[k], 0, 3, p);
-          *reinterpret_cast<uint4*>(ext + qn * MT_EXT + (lane + 32 * k) * 16) = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2], 0u, 0u);
+        for (int h = 0; h < 2; ++h) {
+          const int key = g.tile * MT_UNIT + h * MT_KEYS + kb * lane;
+          page[h] = lane < nbox && key < g.n + g.m ? bt[key / P] : -1;
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sm_addr(H.q_full + qn));
-        if (++qn == NQ) { qn = 0; ++qturn; }
       }
+      const float* src = A.lse + (size_t)(g.r0 + i) * A.hq + g.hk * A.G;
+      rows = min(A.tok, g.m - i) * A.G;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) lse[k] = lane + 32 * k < rows ? src[at[k]] : 0.f;
+      return true;
+    };
+    have = look();
+    while (have) {
+      const float c = mt_near(near0);
+      if (fresh) {
+        const int u = units % MT_RING;
+        if (units >= MT_RING && !(ok = waitw(H.unit_empty + u, units / MT_RING - 1))) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (lane < nbox) {
+            const bool bad = page[h] < 0 || page[h] >= A.kv.n_pages;
+            if (bad && g.tile * MT_UNIT + h * MT_KEYS + kb * lane < g.n + g.m) atomicOr(A.err, DERR_PAGE);
+            H.page[u][h][lane] = bad ? -1 : page[h];
+          }
+        }
+        if (lane == 0) {
+          H.unit[u] = g;
+          H.near[u] = c;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm_addr(H.unit_full + u));
+        ++units;
+      }
+      uint16_t p[4][3];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        split_parts(lane + 32 * k < rows ? fmaf(c, LN2_LO, fmaf(c, LN2, -lse[k])) * A.inv_scale : 0.f, 0, 3, p[k]);
+      have = look();
+      if (qturn > 0 && !(ok = waitw(H.q_empty + qn, qturn - 1))) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(ext + qn * MT_EXT + (lane + 32 * k) * 16) = make_uint4(p[k][0] | (uint32_t)p[k][1] << 16, p[k][2], 0u, 0u);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm_addr(H.q_full + qn));
+      if (++qn == NQ) { qn = 0; ++qturn; }
+    }
+    // no more units (after an abort every wait ends by itself)
+    const int u = units % MT_RING;
+    if (ok && (units < MT_RING || waitw(H.unit_empty + u, units / MT_RING - 1)) && lane == 0) {
+      H.unit[u].s = -1;
+      mbar_arrive(sm_addr(H.unit_full + u));
     }
   } else {
     // ---- the groups that sum: tiles of rows gr, gr + 2, .. against tile h of the unit's keys ----
@@ -487,17 +549,18 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     const unsigned long long sc2 = pair(A.scale_l2e, A.scale_l2e);
     uint32_t tiles = 0, used = 0, shared = 0, paired = 0;
     bool ok = true;
-    while (ok && walk.next(g)) {
+    while (ok && take()) {
+      const float c = H.near[units % MT_RING];
+      taken();
+      const unsigned long long nc2 = pair(-c, -c);
       const int k0 = g.tile * MT_UNIT + h * MT_KEYS + r;
-      const int all = (g.m - g.i0 + A.tok - 1) / A.tok, nt = (all - rank + A.pair - 1) / A.pair;    // tiles of rows; this block's
-      const int other = A.pair > 1 ? all - (all + 1) / 2 : 0;                                     // the second block's
+      const int all = (g.m - g.i0 + A.tok - 1) / A.tok, nt = (all - rank + A.pair - 1) / A.pair;   // tiles of rows; this block's
+      const int other = A.pair > 1 ? all / 2 : 0;          // the second block's
       const uint32_t t0 = tiles;
       tiles += nt;
       if (k0 - r >= g.n + g.m) continue;         // (the unit has no second tile)
-      const bool owner = nt > 0 && ((t0 + nt - 1) & 1) == (uint32_t)gr;        // (has the block's last tile of the unit)
+      const bool owner = ((t0 + nt - 1) & 1) == (uint32_t)gr;        // (has the block's last tile of the unit)
       const size_t e = ((size_t)g.s * A.kv.n_kv_heads + g.hk) * A.ld + k0;
-      const float c = mt_near(A.lse[(size_t)(g.r0 + g.i0) * A.hq + g.hk * A.G]);
-      const unsigned long long nc2 = pair(-c, -c);
       const float before = owner && rank == 0 && A.mass && k0 < g.n ? A.mass[e] : 0.f;
       Comp sum{0.f, 0.f};
       for (int j = (int)((t0 ^ gr) & 1); j < nt; j += 2) {
