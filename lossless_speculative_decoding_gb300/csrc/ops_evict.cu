@@ -29,8 +29,13 @@ constexpr int EV_HOLD = 16;                      // keys a thread holds; of long
 constexpr int EV_BINS = 2048;
 constexpr int MV_THREADS = 256;
 constexpr int MV_ROWS = 4;                       // pieces of a batch for each thread
-constexpr int MV_STAGES = 4;                     // batches in shared memory
-constexpr int MV_SMEM = MV_STAGES * MV_ROWS * MV_THREADS * 16;
+// Batches in shared memory and blocks on an SM: 4 and 3, or 3 and 4 where there are
+// blocks enough: 576 planes of 2,048 rows 245 us with 4 and 3, 233 with 3 and 4; 120 of
+// 1,024 rows 42 and 46.5 (fewer columns a block, 46 and 264).
+template <int STAGES>
+struct MvShape {
+  static constexpr int BLOCKS = STAGES == 3 ? 4 : 3, SMEM = STAGES * MV_ROWS * MV_THREADS * 16;
+};
 
 struct EvictArgs {
   spec_kv_view kv;
@@ -204,8 +209,8 @@ __device__ __forceinline__ void cp_async16(uint32_t smem, const void* gmem) {
 }
 
 // grid (planes x pieces of a row, K | V); SPAN 16-byte columns a block.
-template <int SPAN>
-__global__ void __launch_bounds__(MV_THREADS, 3) k_evict_move(const __grid_constant__ EvictArgs A, int row16, FastDiv P) {
+template <int SPAN, int STAGES>
+__global__ void __launch_bounds__(MV_THREADS, MvShape<STAGES>::BLOCKS) k_evict_move(const __grid_constant__ EvictArgs A, int row16, FastDiv P) {
   constexpr int ROWS = MV_THREADS / SPAN, BATCH = ROWS * MV_ROWS;        // rows of the block at once, of a batch
   extern __shared__ uint4 mv_stage[];
   const int t = threadIdx.x, r = t / SPAN, cols = row16 / SPAN;
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(MV_THREADS, 3) k_evict_move(const __grid_const
       for (int u = 0; u < MV_ROWS; ++u)
         if (from[u] > b * BATCH + u * ROWS + r) {
           moves |= 1u << u;
-          cp_async16(mine + (b % MV_STAGES * MV_ROWS + u) * MV_THREADS * 16, at(from[u]));
+          cp_async16(mine + (b % STAGES * MV_ROWS + u) * MV_THREADS * 16, at(from[u]));
         }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -250,24 +255,24 @@ __global__ void __launch_bounds__(MV_THREADS, 3) k_evict_move(const __grid_const
   };
   look(0);
 #pragma unroll 1
-  for (int b = 0; b < MV_STAGES - 1; ++b) ask(b);
+  for (int b = 0; b < STAGES - 1; ++b) ask(b);
 #pragma unroll 1
   for (int b = 0; b < batches; ++b) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(MV_STAGES - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
     __syncthreads();                             // the whole batch is there, and nobody asks for more of it
-    const uint32_t bits = moves >> (MV_ROWS * (MV_STAGES - 2));
+    const uint32_t bits = moves >> (MV_ROWS * (STAGES - 2));
 #pragma unroll
     for (int u = 0; u < MV_ROWS; ++u)
-      if (bits >> u & 1) *at(b * BATCH + u * ROWS + r) = mv_stage[(b % MV_STAGES * MV_ROWS + u) * MV_THREADS + t];
-    ask(b + MV_STAGES - 1);
+      if (bits >> u & 1) *at(b * BATCH + u * ROWS + r) = mv_stage[(b % STAGES * MV_ROWS + u) * MV_THREADS + t];
+    ask(b + STAGES - 1);
   }
 }
 
-template <int SPAN>
-cudaError_t launch_move(const EvictArgs& A, int64_t planes, int row16, cudaStream_t st) {
-  cudaError_t e = allow_dyn_smem_once<k_evict_move<SPAN>>();
+template <int SPAN, int STAGES>
+cudaError_t launch_move(const EvictArgs& A, int64_t blocks, int row16, cudaStream_t st) {
+  cudaError_t e = allow_dyn_smem_once<k_evict_move<SPAN, STAGES>>();
   if (e != cudaSuccess) return e;
-  return launch_k(k_evict_move<SPAN>, dim3((unsigned)(planes * (row16 / SPAN)), 2), dim3(MV_THREADS), MV_SMEM, st, A, row16,
+  return launch_k(k_evict_move<SPAN, STAGES>, dim3((unsigned)blocks, 2), dim3(MV_THREADS), MvShape<STAGES>::SMEM, st, A, row16,
                   FastDiv(A.kv.page_size));
 }
 
@@ -299,11 +304,17 @@ extern "C" int spec_kv_evict(const spec_kv_view* kv, int n_seq, const int32_t* c
     for (int j = 0; j < i; ++j)
       if (spans_meet(out[i].p, out[i].n, out[j].p, out[j].n)) return set_last_error(SPEC_ERR_ARG, "two outputs overlap");
   }
+  const int sms = sm_count_once();
+  if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
   const EvictArgs A{*kv, cache_len_dev, mass_dev, out_mass_dev, out_kept_dev, out_len_dev, err_dev, ld, n_seq, budget, recent,
                     (int)std::min<int64_t>(ld, (int64_t)kv->max_pages * kv->page_size)};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = launch_k(k_evict_select, dim3((unsigned)planes), dim3(EV_THREADS), 0, st, A);
-  if (e == cudaSuccess) e = row16 % 16 ? launch_move<8>(A, planes, row16, st) : launch_move<16>(A, planes, row16, st);
+  const int span = row16 % 16 ? 8 : 16;
+  const int64_t blocks = planes * (row16 / span);
+  const bool many = 2 * blocks >= 4 * (int64_t)sms;
+  if (e == cudaSuccess && span == 8) e = many ? launch_move<8, 3>(A, blocks, row16, st) : launch_move<8, 4>(A, blocks, row16, st);
+  else if (e == cudaSuccess) e = many ? launch_move<16, 3>(A, blocks, row16, st) : launch_move<16, 4>(A, blocks, row16, st);
   if (e == cudaSuccess) e = cudaGetLastError();
   return e == cudaSuccess ? SPEC_OK : set_last_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
 }

@@ -2,9 +2,9 @@
 // the way of their keys and values into the paged cache.
 //
 // A head of d values lies on LPH = d / (16 bytes) lanes, one 16-byte piece each,
-// so that a warp holds one to four heads of a row. A block takes 16 tokens at a time:
+// so that a warp holds one to four heads of a row. A block takes 8 tokens at a time:
 // their places, the cosines and sines of their angles into shared memory, then the
-// heads, up to eight of a lane's on their way at once. A lane's piece is the same in every
+// heads, up to four of a lane's on their way at once. A lane's piece is the same in every
 // head, so what it is multiplied by is made once for them: with gamma folded
 // in, y[i] = r (x[i] C[i] + x'[i] S[i]), x' the partner's piece (a shuffle), r =
 // 1 / sqrt(mean x^2 + eps), C = gamma cos, S = -+ gamma' sin. Pieces behind the rotated
@@ -28,8 +28,9 @@ namespace spec {
 namespace {
 
 constexpr int RP_THREADS = 256;
-constexpr int RP_TOKENS = 16;                    // tokens of a block at a time
-constexpr int RP_FLY = 8;                        // heads a lane has in flight
+constexpr int RP_TOKENS = 8;                     // tokens of a block at a time
+constexpr int RP_FLY = 4;                        // heads a lane has in flight
+constexpr int RP_BLOCKS = 4;                     // on an SM
 
 struct RopeArgs {
   spec_kv_view kv;
@@ -84,7 +85,7 @@ __device__ __forceinline__ void unpack2(const uint4& v, unsigned long long (&f)[
 }
 
 template <class KT, int D>
-__global__ void __launch_bounds__(RP_THREADS, 2) k_qk_norm_rope(const __grid_constant__ RopeArgs A) {
+__global__ void __launch_bounds__(RP_THREADS, RP_BLOCKS) k_qk_norm_rope(const __grid_constant__ RopeArgs A) {
   constexpr int NV = Elt<KT>::per16, N2 = NV / 2, LPH = D / NV, GROUPS = RP_THREADS / LPH;
   __shared__ long long w_sum[RP_THREADS / 32];
   __shared__ int t_seq[RP_TOKENS], t_row[RP_TOKENS], t_pos[RP_TOKENS], t_page[RP_TOKENS];
@@ -316,7 +317,7 @@ extern "C" int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* 
     items += (i + 1) * A.chunks[i];
   }
   const int groups = RP_THREADS / (d * esz / 16);
-  const int blocks = (int)std::min<int64_t>(((int64_t)n_rows * items + groups - 1) / groups, sms * 2);
+  const int blocks = (int)std::min<int64_t>(((int64_t)n_rows * items + groups - 1) / groups, sms * RP_BLOCKS);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(cuda_stream);
   cudaError_t e;
   if (esz == 2) e = d == 128 ? launch_rope<bf16_t, 128>(A, blocks, st) : launch_rope<bf16_t, 64>(A, blocks, st);
