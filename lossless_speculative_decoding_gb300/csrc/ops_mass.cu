@@ -33,7 +33,7 @@ struct MassArgs {
   long long ld;
   int layer, hq, G, last;
   int tok;             // tokens of a tile of rows (tensor-core form)
-  int nk, nq, q_half;  // its rings: tiles of keys and of queries in shared memory, bytes of 64 dims of a tile of queries
+  int nk, nq, q_half;  // its rings: tiles of keys (two rings) and of queries in shared memory, bytes of 64 dims of a tile of queries
   int pair;            // blocks that share a unit's rows: 1 or 2
   float scale_l2e;     // scale * log2 e
   float inv_scale;
@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
   MtHeader& H = *reinterpret_cast<MtHeader*>(ext + C::EXT);
   static_assert(sizeof(MtHeader) + 1024 <= C::TAIL, "header and alignment slack");
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int NK = A.nk, NQ = A.nq, q_bytes = HALVES * A.q_half;
-  const uint32_t kbufs = sm_addr(base), qbufs = kbufs + NK * C::BUF;
+  const int NH = A.nk / 2, NQ = A.nq, q_bytes = HALVES * A.q_half;
+  const uint32_t kbufs = sm_addr(base), qbufs = kbufs + A.nk * C::BUF;
   const int rank = A.pair > 1 ? (int)cluster_rank() : 0;
   if (t == 0) {
     for (int i = 0; i < MT_MAX_NK; ++i) {
@@ -374,8 +374,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     // ---- producer: a unit's keys (a box for each kb keys of a page), then its tiles of queries ----
     const int nbox = MT_KEYS / kb;
     const int planes = A.kv.n_layers * A.kv.n_kv_heads * 2;
-    int kn = 0, qn = 0;                          // ring positions
-    uint32_t kturn = 0, qturn = 0;               // passes over the rings
+    int kn[2] = {0, 0}, qn = 0;                  // ring positions
+    uint32_t kturn[2] = {0, 0}, qturn = 0;       // passes over the rings
     bool ok = true;
     while (ok && take()) {
       const MassUnit n = g;
@@ -388,18 +388,19 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
       for (int h = 0; h < 2; ++h) {
         const int k0 = n.tile * MT_UNIT + h * MT_KEYS, key = k0 + kb * lane;
         if (!ok || k0 >= n.n + n.m) break;
-        if (kturn > 0 && !waitw(H.k_empty + kn, kturn - 1)) { ok = false; break; }
-        const uint32_t full = sm_addr(H.k_full + kn);
+        const int kbuf = h * NH + kn[h];
+        if (kturn[h] > 0 && !waitw(H.k_empty + kbuf, kturn[h] - 1)) { ok = false; break; }
+        const uint32_t full = sm_addr(H.k_full + kbuf);
         if (lane == 0)
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"((uint32_t)C::BUF) : "memory");
         __syncwarp();
         if (lane < nbox)
           asm volatile(
               "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
-              ::"r"(kbufs + kn * C::BUF + lane * kb * D * 2), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0), "r"(key % P / 8),
+              ::"r"(kbufs + kbuf * C::BUF + lane * kb * D * 2), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0), "r"(key % P / 8),
                 "r"(page[h] < 0 ? -1 : page[h] * planes + plane), "r"(full)
               : "memory");
-        if (++kn == NK) { kn = 0; ++kturn; }
+        if (++kn[h] == NH) { kn[h] = 0; ++kturn[h]; }
       }
       for (int i = n.i0 + first; ok && i < n.m; i += stride) {
         if (qturn > 0 && !waitw(H.q_empty + qn, qturn - 1)) { ok = false; break; }
@@ -418,7 +419,9 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
       }
     }
     // shared memory outlives the copies (over, unless a wait was given up): each buffer's last one
-    for (int i = 0; i < NK; ++i) mbar_wait_deadline(sm_addr(H.k_full + i), (i < kn ? kturn : kturn - 1) & 1, nullptr);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      for (int i = 0; i < NH; ++i) mbar_wait_deadline(sm_addr(H.k_full + h * NH + i), (i < kn[h] ? kturn[h] : kturn[h] - 1) & 1, nullptr);
     for (int i = 0; i < NQ; ++i) mbar_wait_deadline(sm_addr(H.q_full + i), (i < qn ? qturn : qturn - 1) & 1, nullptr);
   } else if (warp == MT_SUM + 1 || warp == MT_SUM + 3) {
     // ---- MMA issuer of a unit's tile h of keys (the whole warp, on values that are the same in every lane) ----
@@ -433,8 +436,8 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     while (ok && take()) {
       taken();
       const int nh = same(g.n + g.m - g.tile * MT_UNIT > MT_KEYS ? 2 : 1), i0 = same(g.i0) + first, m = same(g.m);
-      const int kbuf = kn + h < NK ? kn + h : kn + h - NK;
-      if (h < nh && !(ok = waitw(H.k_full + kbuf, kn + h < NK ? kturn : kturn + 1))) break;
+      const int kbuf = h * NH + kn;
+      if (h < nh && !(ok = waitw(H.k_full + kbuf, kturn))) break;
       const uint64_t ad = tt_desc(kbufs + kbuf * C::BUF, 16, GROUP);
       for (int i = i0; i < m; i += stride, ++tiles) {
         const int rows = min(A.tok, m - i) * A.G, gr = tiles & 1;
@@ -458,9 +461,10 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
         if (++qn == NQ) { qn = 0; ++qturn; }
       }
       if (!ok) break;
-      if (h < nh) tc_commit(sm_addr(H.k_empty + kbuf), one);
-      for (int x = 0; x < nh; ++x)
-        if (++kn == NK) { kn = 0; ++kturn; }
+      if (h < nh) {
+        tc_commit(sm_addr(H.k_empty + kbuf), one);
+        if (++kn == NH) { kn = 0; ++kturn; }
+      }
     }
     // everything issued is done before TMEM is freed (also after an abort)
     tc_commit(sm_addr(H.fin + h), one);
@@ -647,8 +651,8 @@ cudaError_t launch_mass_tc(MassArgs A, int blocks, cudaStream_t st) {
   // tiles of rows: whole tokens, no more than a chunk counts; where they are small, the room goes to keys
   A.tok = std::max(1, std::min(128 / A.G, std::min(A.last, A.ix.max_new)));
   A.q_half = (A.tok * A.G + 15) / 16 * 16 * 128;
-  A.nq = A.q_half <= 4096 ? 4 : 3;
-  A.nk = std::min(MT_MAX_NK, (MtCfg<D>::ROOM - A.nq * A.q_half * (D / 64)) / MtCfg<D>::BUF);
+  A.nq = A.q_half <= 4096 ? 4 : 2;
+  A.nk = std::min(MT_MAX_NK, (MtCfg<D>::ROOM - A.nq * A.q_half * (D / 64)) / MtCfg<D>::BUF / 2 * 2);   // a ring for each issuer
   // pairs of blocks: a prompt of 5,288 tokens, 32 on 8 heads, ??? us for ???
   A.pair = (std::min(A.last, A.ix.max_new) + A.tok - 1) / A.tok >= MT_PAIR_TILES ? 2 : 1;
   CUtensorMap map, qmap;
