@@ -666,9 +666,12 @@ int spec_chunk_attention(const spec_kv_view* kv, int layer, const void* q_dev, i
  *   mass_dev, out_mass_dev [n_seq][n_kv_heads][ld] f32, out_mass_dev the same
  *     array or one that does not overlap it; mass_dev may be NULL (zeros). A
  *     sequence of more than ld positions is left out (SPEC_DEV_ERR_POS).
- * fp32, in a fixed order: the same call gives the same bits. Positions on a bad
- * page get no usable value (SPEC_DEV_ERR_PAGE).
- * Errors: as spec_chunk_attention. */
+ * lse finite where a token is counted. fp32, in a fixed order: the same call gives
+ * the same bits. The exponent's terms are rounded before they cancel, so a weight is
+ * off by some 2^-21 of scale * sum |q_i K_i| + |lse|, relative to itself. Positions
+ * on a bad page get no usable value (SPEC_DEV_ERR_PAGE).
+ * Errors: as spec_chunk_attention; SPEC_ERR_UNSUPPORTED also for a scale beyond
+ * 2^-64 .. 2^64. */
 int spec_attention_mass(const spec_kv_view* kv, int layer, const void* q_dev, const float* lse_dev, int n_rows,
                         int n_seq, int max_new, int last, int n_q_heads, const int32_t* row_start_dev,
                         const int32_t* n_new_dev, const int32_t* cache_len_dev, float scale, const float* mass_dev,

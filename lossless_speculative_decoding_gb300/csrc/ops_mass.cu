@@ -214,27 +214,35 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// Tensor-core form (bf16 cache). One block per SM, twenty warps: a TMA producer, a loader
-// of the rows' lse, four groups of four warps that sum and an MMA issuer for each tile of
-// keys (an issue waits until the MMAs before it are nearly over, so one issuer's waits
-// would leave the tensor cores idle). A unit has
-// two tiles of 128 keys; against each tile of up to 128 rows (whole tokens), S = K Q^T
-// goes to tensor memory with the keys on the lanes, so that a thread sums its key's
-// columns in registers and no sum crosses threads. One more MMA adds (c - lse) / scale
-// to every column: as three bf16 parts (24 bits) in three more dims of a row, against
-// ones in those of a key. (c, a whole number of log 2, is near the unit's first lse, so
-// that what the tensor cores add stays small: their sums are cut, not rounded.) (From shared memory, read by every thread, it took its bandwidth
-// from the MMAs: 218 us for ???.) Groups 0 and 1 take the even tiles of rows, 2 and 3 the
-// odd ones, each group one tile of keys; each has a quarter of tensor memory, which it
-// gives back as soon as its scores are in registers.
+// Tensor-core form (bf16 cache). One block per SM, twenty warps: a TMA producer, a
+// loader of the rows' lse, four groups of four warps that sum and an MMA issuer for
+// each tile of keys (an issue waits until the MMAs before it are nearly over, so that
+// one issuer's waits leave the tensor cores idle: 113 us for 105). A unit has two tiles
+// of 128 keys; against each tile of up to 128 rows (whole tokens), S = K Q^T goes to
+// tensor memory with the keys on the lanes, so that a thread sums its key's columns in
+// registers and no sum crosses threads. Groups 0 and 1 take the even tiles of rows, 2
+// and 3 the odd ones, each group one tile of keys; each has a quarter of tensor memory,
+// which it gives back as soon as its scores are in registers.
 //
-// Where units have many tiles of rows, two blocks (a cluster) share a unit, each every
-// other tile of rows, so that the few units of a single prompt's first keys do not
-// outlast the others; the second block's sums go to the first one's shared memory.
+// One more MMA adds (c - lse) / scale to every column: as three bf16 parts (24 bits) in
+// three more dims of a row, against ones in those of a key. c, a whole number of log 2,
+// is near the unit's first lse, so that what the tensor cores add stays small: their
+// sums are cut, not rounded. (Read from shared memory by every thread, lse took the
+// bandwidth that the MMAs need: 218 us for 113.)
+//
+// Where units have many tiles of rows and are few, two blocks (a cluster) share a unit,
+// each every other tile of rows, so that the few units of a single prompt's first keys
+// do not outlast the others; the second block's sums go to the first one's shared memory.
 //
 // The loader walks over the units and hands them to the other roles, with their pages,
 // through a small ring: twenty warps that each looked for themselves took a third of the
-// issue slots where a unit has one row (126 us for ???).
+// issue slots where a unit has one row (129 us for 87).
+//
+// Measured, L2 cold. Every token of a prompt of 5,288, 32 on 8 heads: 104 us, 0.56 of
+// the MMA rate for 115 GFLOP (the added MMA is an eighth more, tiles on the diagonal are
+// whole, and beside the MMAs every score is read from tensor memory and takes its
+// exponential: 48 us of the special function units). One token of each of 64
+// sequences of 336 .. 5,236 positions, 10 heads: 87 us, 0.81 of the copy rate.
 //
 // Sums: 128 weights in fp32, the tiles of rows by a compensated sum (its rounding error
 // is carried along), so that thousands of rows lose no bits.
@@ -243,7 +251,8 @@ constexpr int MT_UNIT = 2 * MT_KEYS;
 constexpr int MT_SUM = 16;                       // warps that sum
 constexpr int MT_THREADS = 32 * (MT_SUM + 4);
 constexpr int MT_MAX_NK = 8, MT_MAX_NQ = 4;
-constexpr int MT_PAIR_TILES = 8;                 // tiles of rows of a unit from which on blocks work in pairs
+constexpr int MT_PAIR_TILES = 8;                 // blocks work in pairs from so many tiles of rows a unit on,
+constexpr int MT_PAIR_PLANES = 16;               // on up to so many (sequence, kv head)
 constexpr int MT_EXT = 128 * 16;                 // bytes of 8 more dims of 128 rows
 constexpr int MT_RING = 4;                       // units handed over at once
 
@@ -258,7 +267,7 @@ struct MtCfg {
 
 struct MtHeader {
   uint64_t k_full[MT_MAX_NK], k_empty[MT_MAX_NK], q_full[MT_MAX_NQ], q_empty[MT_MAX_NQ], s_full[4], s_empty[4];
-  uint64_t sum_full[2][2], sum_empty[2][2], pair_full[2][2], pair_empty[2][2], fin[2];  // [turn][tile of keys]
+  uint64_t sum_full[2][2], sum_empty[2][2], pair_full[2][2], pair_empty[2][2], fin[2];  // [owner][tile of keys]
   uint64_t unit_full[MT_RING], unit_empty[MT_RING];
   uint32_t tmem;
   int abort;
@@ -551,7 +560,10 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
     const int h = warp >> 2 & 1, gr = warp >> 3, r = t & 127;
     const uint32_t sT = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (2 * gr + h) * 128;
     const unsigned long long sc2 = pair(A.scale_l2e, A.scale_l2e);
-    uint32_t tiles = 0, used = 0, shared = 0, paired = 0;
+    uint32_t tiles = 0, used = 0;
+    // Units whose sum is joined take turns: group p finishes every other one, alike in both blocks. So each of
+    // the barriers has one group that waits on it, and that one sees its every phase.
+    uint32_t joined = 0, got = 0, gave = 0;
     bool ok = true;
     while (ok && take()) {
       const float c = H.near[units % MT_RING];
@@ -563,7 +575,11 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
       const uint32_t t0 = tiles;
       tiles += nt;
       if (k0 - r >= g.n + g.m) continue;         // (the unit has no second tile)
-      const bool owner = ((t0 + nt - 1) & 1) == (uint32_t)gr;        // (has the block's last tile of the unit)
+      const bool join = nt > 1 || other > 0;
+      const uint32_t p = join ? joined & 1 : t0 & 1, turn = joined >> 1;
+      joined += join;
+      const bool owner = p == (uint32_t)gr;
+      const bool give = nt > 1 || (t0 & 1) != p;           // (the other group has tiles too)
       const size_t e = ((size_t)g.s * A.kv.n_kv_heads + g.hk) * A.ld + k0;
       const float before = owner && rank == 0 && A.mass && k0 < g.n ? A.mass[e] : 0.f;
       Comp sum{0.f, 0.f};
@@ -602,30 +618,27 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
         sum.add(p.x + p.y);
       }
       if (!ok) break;
-      if (nt > 1) {                              // the other group's tiles
-        const uint32_t p = shared & 1, turn = shared >> 1;
-        ++shared;
+      if (give) {                                // the other group's tiles
         if (!owner) {
-          if (turn > 0 && !(ok = waitw(&H.sum_empty[p][h], turn - 1))) break;
+          if (gave > 0 && !(ok = waitw(&H.sum_empty[p][h], gave - 1))) break;
+          ++gave;
           H.sum[p][h * MT_KEYS + r] = sum.s + sum.e;
           __syncwarp();
           if (lane == 0) mbar_arrive(sm_addr(&H.sum_full[p][h]));
         } else {
-          if (!(ok = waitw(&H.sum_full[p][h], turn))) break;
+          if (!(ok = waitw(&H.sum_full[p][h], got++))) break;
           sum.add(H.sum[p][h * MT_KEYS + r]);
           __syncwarp();
           if (lane == 0) mbar_arrive(sm_addr(&H.sum_empty[p][h]));
         }
       }
-      if (other > 0) {                           // the other block's
-        const uint32_t p = paired & 1, turn = paired >> 1;
-        ++paired;
-        if (owner && rank > 0) {
+      if (other > 0 && owner) {                  // the other block's
+        if (rank > 0) {
           if (turn > 0 && !(ok = waitw_pair(&H.pair_empty[p][h], turn - 1))) break;
           asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to(sm_addr(&H.pair[p][h * MT_KEYS + r]), 0)), "f"(sum.s + sum.e) : "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive_at(map_to(sm_addr(&H.pair_full[p][h]), 0));
-        } else if (owner) {
+        } else {
           if (!(ok = waitw_pair(&H.pair_full[p][h], turn))) break;
           sum.add(H.pair[p][h * MT_KEYS + r]);
           __syncwarp();
@@ -653,8 +666,13 @@ cudaError_t launch_mass_tc(MassArgs A, int blocks, cudaStream_t st) {
   A.q_half = (A.tok * A.G + 15) / 16 * 16 * 128;
   A.nq = A.q_half <= 4096 ? 4 : 2;
   A.nk = std::min(MT_MAX_NK, (MtCfg<D>::ROOM - A.nq * A.q_half * (D / 64)) / MtCfg<D>::BUF / 2 * 2);   // a ring for each issuer
-  // pairs of blocks: a prompt of 5,288 tokens, 32 on 8 heads, ??? us for ???
-  A.pair = (std::min(A.last, A.ix.max_new) + A.tok - 1) / A.tok >= MT_PAIR_TILES ? 2 : 1;
+  // Pairs of blocks where units are long and few, alone and paired: every token of a prompt of 5,288 on 8 kv heads
+  // 150 and 104 us, two of them 217 and 201, four 448 and 435, four of 2,000 93 and 98, the last 512 tokens of eight
+  // prompts 101 and 113; the last 32 (one tile of rows) 22 and 30.
+  A.pair = (std::min(A.last, A.ix.max_new) + A.tok - 1) / A.tok >= MT_PAIR_TILES &&
+                   (int64_t)A.ix.n_seq * A.kv.n_kv_heads <= MT_PAIR_PLANES
+               ? 2
+               : 1;
   CUtensorMap map, qmap;
   if (q_make_map(&qmap, A.q, D, A.hq, (uint64_t)A.ix.n_rows, A.G, A.tok) ||
       kv_make_group_map(&map, A.kv.kv_dev, D, A.kv.page_size, (uint64_t)A.kv.n_pages * A.kv.n_layers * A.kv.n_kv_heads * 2, kb))

@@ -100,7 +100,7 @@ def test_mass_refusals(B):
     cases = SIZES + SCALES + [({k: None}, -1) for k in ("q_dev", "lse_dev", "row_start_dev", "n_new_dev", "cache_len_dev",
                                                         "out_mass_dev", "err_dev")]
     cases += [(dict(max_new=0), -1), (dict(last=0), -1), (dict(n_q_heads=258), -6), (dict(ld=0), -1), (dict(ld=1 << 32), -1),
-              (dict(q_dev=FAKE + 2), -1)]
+              (dict(q_dev=FAKE + 2), -1), (dict(scale=5e-20), -6), (dict(scale=2e19), -6)]
     # 2 sequences x 2 heads x 64 f32: 1 KB
     cases += [(dict(mass_dev=(FAKE << 1) + x), -1) for x in (4, 1020, -4, -1020)]
     _all(B, B.spec_attention_mass, ok, cases)

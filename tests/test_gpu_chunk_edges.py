@@ -317,3 +317,28 @@ def test_mass_with_weights_of_far_apart_rows(dtype):
     got, err = mass(c, 0, q, lse, rows, [n], scale, m)
     w, e = ref_mass(c, 0, 0, q[:m], lse[:m], n, m, scale, m)
     assert err == 0 and bool(((got[0, :, :n + m].double() - w).abs() <= w * e + 1e-30).all())
+
+
+@pytest.mark.parametrize("hkv", [1, 2])
+def test_mass_of_a_prompt_beside_short_chunks(hkv):
+    """Units of many tiles of rows and of one to five side by side: what two blocks share, and what one has alone."""
+    import torch
+    rng = np.random.default_rng(11)
+    lens = [2000] + [int(x) for x in rng.integers(3000, 9000, 15)]
+    new = [200] + [int(x) for x in rng.integers(1, 80, 15)]
+    c = _cache(lens, new, hkv=hkv)
+    rows = Rows(new)
+    q = queries(rows, 8 * hkv, 128, BF16, 5)
+    scale = 128 ** -0.5
+    lse = torch.zeros((rows.n, 8 * hkv), device="cuda")
+    for s, n in enumerate(lens):
+        x, _ = scores(c, s, 0, q[rows.of(s)], n, new[s], scale)
+        lse[rows.of(s)] = torch.logsumexp(x, -1).permute(2, 0, 1).reshape(new[s], 8 * hkv).float()
+    first, err = mass(c, 0, q, lse, rows, lens, scale, 200)
+    assert err == 0
+    for s, n in enumerate(lens):
+        w, e = ref_mass(c, s, 0, q[rows.of(s)], lse[rows.of(s)], n, new[s], scale, 200)
+        assert bool(((first[s, :, :n + new[s]].double() - w).abs() <= w * e + 1e-37).all()), s
+    for _ in range(20):
+        got, err = mass(c, 0, q, lse, rows, lens, scale, 200)
+        assert err == 0 and torch.equal(got, first)
