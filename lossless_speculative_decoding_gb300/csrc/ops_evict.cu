@@ -289,6 +289,7 @@ extern "C" int spec_kv_evict(const spec_kv_view* kv, int n_seq, const int32_t* c
   if (!cache_len_dev || !mass_dev || !out_mass_dev || !out_kept_dev || !out_len_dev || !err_dev)
     return set_last_error(SPEC_ERR_ARG, "null pointer argument");
   if (budget < 1 || recent < 0 || recent > budget) return set_last_error(SPEC_ERR_ARG, "1 <= budget and 0 <= recent <= budget required");
+  if (budget > (1 << 30)) return set_last_error(SPEC_ERR_UNSUPPORTED, "budget above 2^30");   // (nor is a sequence longer)
   if (ld < 1 || ld > ((int64_t)1 << 31)) return set_last_error(SPEC_ERR_ARG, "1 <= ld <= 2^31 required");
   const int64_t planes = (int64_t)kv->n_layers * n_seq * kv->n_kv_heads;
   const int row16 = kv->head_dim * (kv->dtype == SPEC_F32 ? 4 : 2) / 16;

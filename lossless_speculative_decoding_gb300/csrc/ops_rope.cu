@@ -1,25 +1,32 @@
 // Kernel-level entry point: norm and rotation of new tokens' queries and keys, and
 // the way of their keys and values into the paged cache.
 //
-// A head of d values lies on LPH = d / (16 bytes) lanes, one 16-byte piece each,
-// so that a warp holds one to four heads of a row. A block takes 8 tokens at a time:
-// their places, the cosines and sines of their angles into shared memory, then the
-// heads, up to four of a lane's on their way at once. A lane's piece is the same in every
-// head, so what it is multiplied by is made once for them: with gamma folded
-// in, y[i] = r (x[i] C[i] + x'[i] S[i]), x' the partner's piece (a shuffle), r =
-// 1 / sqrt(mean x^2 + eps), C = gamma cos, S = -+ gamma' sin. Pieces behind the rotated
-// dims have C = gamma, S = 0.
+// A head of d values lies on LPH = d / (16 bytes) lanes, so that a warp holds one to
+// four heads of a row. A lane has 8 bytes of the lower half of the rotated dims and
+// their partners of the upper half (behind the rotated dims any 16 bytes), so a turn
+// crosses no lanes. A block takes 4 tokens at a time: their places, the cosines and sines
+// of their angles into shared memory, then the heads, up to four of a lane's on their
+// way at once, whose sums of squares cross the lanes together. A lane's dims are the
+// same in every head, so what they are multiplied by is made once for them: with gamma
+// folded in, y_lo = r (lo CL + hi SL), y_hi = r (hi CH + lo SH), r = 1 / sqrt(mean x^2 +
+// eps), CL = gamma cos, SL = -gamma' sin ..; behind the rotated dims C = gamma, S = 0.
 //
 // The angle of position p is p F of a 64-bit turn, F = freq / 2 pi in units of
 // 2^-64 of a turn: the product wraps as the angle does, so it is as exact at
 // position 2^31 as at 1. Its upper 32 bits, reduced to an eighth of a turn either
 // way, go to sincospif.
 //
-// Bound: HBM, by the bytes of the rows.
+// Bound: HBM, by the bytes of the rows, and below some 10^4 tokens the way there: places,
+// angles, rows and results follow one another, in one turn or two of a block. Measured, L2
+// cold, bf16, 32 query and 8 kv heads of 128: 16,000 tokens 79 us, 0.75 of the copy rate;
+// 4,628 tokens 29.7 us, 0.58. (Pieces of 16 bytes with their partners by shuffle: 31.5;
+// the next heads' loads beside a head's arithmetic, which takes the registers of a
+// block in four: 35.6, or 33.0 with three blocks; 8 tokens at a time 30.5.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "chunk.cuh"
 #include "tc_attn.cuh"
@@ -28,7 +35,7 @@ namespace spec {
 namespace {
 
 constexpr int RP_THREADS = 256;
-constexpr int RP_TOKENS = 8;                     // tokens of a block at a time
+constexpr int RP_TOKENS = 4;                     // tokens of a block at a time
 constexpr int RP_FLY = 4;                        // heads a lane has in flight
 constexpr int RP_BLOCKS = 4;                     // on an SM
 
@@ -41,7 +48,7 @@ struct RopeArgs {
   const float* gamma[2];                         // of queries, of keys
   int32_t* err;
   long long ld;                                  // bytes of a row
-  int layer, hq, half8;                          // half8: rotated pairs / values of a piece
+  int layer, hq, half8;                          // half8: rotated pairs / values of 8 bytes
   int chunks[2], heads[2];                       // of queries, of keys (and values): lane groups that share a token's, heads of each
   float eps;
   uint64_t turn[SPEC_ROPE_MAX_PAIRS];            // freq in 2^-64 turns
@@ -59,34 +66,36 @@ __device__ __forceinline__ void turn_cos_sin(uint32_t a, float& c, float& s) {
   s = quarter >= 2 ? -y : y;
 }
 
-template <int NV>
-__device__ __forceinline__ uint4 pack_piece(const float (&y)[NV]) {
-  uint4 r;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&r);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (NV == 4) w[i] = __float_as_uint(y[i]);
-    else w[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
-  }
-  return r;
-}
-
-// Pairs of a piece's values.
+// Pairs of the values of 8 bytes, and back.
 template <class KT>
-__device__ __forceinline__ void unpack2(const uint4& v, unsigned long long (&f)[Elt<KT>::per16 / 2]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack2(uint2 v, unsigned long long (&f)[Elt<KT>::per16 / 4]) {
   if constexpr (Elt<KT>::per16 == 4) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) f[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    f[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    f[0] = pair(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    f[1] = pair(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
   }
 }
+template <class KT>
+__device__ __forceinline__ uint2 pack2(const unsigned long long (&f)[Elt<KT>::per16 / 4]) {
+  const float2 x = halves(f[0]);
+  if constexpr (Elt<KT>::per16 == 4) {
+    return make_uint2(__float_as_uint(x.x), __float_as_uint(x.y));
+  } else {
+    const float2 y = halves(f[1]);
+    return make_uint2(pack_bf16(x.x, x.y), pack_bf16(y.x, y.y));
+  }
+}
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
 
-template <class KT, int D>
+// FULL: all dims turn (16,000 tokens 79 us, 81 without the choice of partners left out).
+template <class KT, int D, bool FULL>
 __global__ void __launch_bounds__(RP_THREADS, RP_BLOCKS) k_qk_norm_rope(const __grid_constant__ RopeArgs A) {
-  constexpr int NV = Elt<KT>::per16, N2 = NV / 2, LPH = D / NV, GROUPS = RP_THREADS / LPH;
+  constexpr int HV = Elt<KT>::per16 / 2, N2 = HV / 2, LPH = D / (2 * HV), GROUPS = RP_THREADS / LPH;
   __shared__ long long w_sum[RP_THREADS / 32];
   __shared__ int t_seq[RP_TOKENS], t_row[RP_TOKENS], t_pos[RP_TOKENS], t_page[RP_TOKENS];
   __shared__ __align__(16) float t_cos[RP_TOKENS][D / 2], t_sin[RP_TOKENS][D / 2], gam[2][D];
@@ -129,11 +138,12 @@ __global__ void __launch_bounds__(RP_THREADS, RP_BLOCKS) k_qk_norm_rope(const __
 
   const int g = t / LPH, gl = t % LPH;
   const uint32_t gmask = LPH == 32 ? 0xffffffffu : ((1u << (LPH & 31)) - 1) << (lane / LPH * LPH);
-  const int half = A.half8 * NV, rotated = 2 * A.half8;
-  const bool low = gl < A.half8, turns = gl < rotated;
-  const int partner = low ? gl + A.half8 : turns ? gl - A.half8 : gl, p0 = (low ? gl : gl - A.half8) * NV;
-  const size_t plane16 = (size_t)A.kv.page_size * LPH;
-  uint4* const cache = static_cast<uint4*>(A.kv.kv_dev);
+  const int half = A.half8 * HV;
+  // the lane's dims: lo .. and their partners hi ..; behind the rotated ones, any two pieces
+  const bool turns = FULL || gl < A.half8;
+  const int lo = turns ? gl * HV : 2 * half + 2 * (gl - A.half8) * HV, hi = turns ? half + lo : lo + HV;
+  const size_t plane = (size_t)A.kv.page_size * D;
+  KT* const cache = static_cast<KT*>(A.kv.kv_dev);
   for (long long k = k0; k < k1; k += RP_TOKENS) {
     const int nt = (int)min((long long)RP_TOKENS, k1 - k);
     __syncthreads();                             // the last tokens' places are read
@@ -171,91 +181,107 @@ __global__ void __launch_bounds__(RP_THREADS, RP_BLOCKS) k_qk_norm_rope(const __
     const int items = A.chunks[0] + 2 * A.chunks[1];
     for (int x = g; x < nt * items; x += GROUPS) {
       const int tok = x / items, row = t_row[tok], page = t_page[tok];
-      int c = x - tok * items, kind = 0;         // queries, keys, values
-      if (c >= A.chunks[0]) {
-        c -= A.chunks[0];
+      int part = x - tok * items, kind = 0;      // queries, keys, values
+      if (part >= A.chunks[0]) {
+        part -= A.chunks[0];
         kind = 1;
-        if (c >= A.chunks[1]) {
-          c -= A.chunks[1];
+        if (part >= A.chunks[1]) {
+          part -= A.chunks[1];
           kind = 2;
         }
       }
-      const int k1 = kind > 0, hk = k1 ? A.kv.n_kv_heads : A.hq, h0 = c * A.heads[k1], nh = min(A.heads[k1], hk - h0);
+      const int k1 = kind > 0, hk = k1 ? A.kv.n_kv_heads : A.hq, h0 = part * A.heads[k1], nh = min(A.heads[k1], hk - h0);
       const int in0 = h0 + (kind == 0 ? 0 : kind == 1 ? A.hq : A.hq + A.kv.n_kv_heads);
-      const uint4* src = reinterpret_cast<const uint4*>(A.qkv + row * A.ld) + (size_t)in0 * LPH + gl;
-      uint4 v[RP_FLY];
+      const KT* src = reinterpret_cast<const KT*>(A.qkv + row * A.ld) + (size_t)in0 * D;
+      uint2 vl[RP_FLY], vh[RP_FLY];
 #pragma unroll
-      for (int u = 0; u < RP_FLY; ++u)
-        if (u < nh) v[u] = ld_stream(src + u * LPH);
-      uint4* dst = reinterpret_cast<uint4*>(A.q_out) + ((size_t)row * A.hq + h0) * LPH + gl;
-      size_t step = LPH;
+      for (int u = 0; u < RP_FLY; ++u) {
+        vl[u] = vh[u] = make_uint2(0u, 0u);
+        if (u < nh) {
+          vl[u] = ld_stream8(src + u * D + lo);
+          vh[u] = ld_stream8(src + u * D + hi);
+        }
+      }
+      KT* dst = reinterpret_cast<KT*>(A.q_out) + ((size_t)row * A.hq + h0) * D;
+      size_t step = D;
       if (k1) {
-        step = 2 * plane16;
+        step = 2 * plane;
         dst = page < 0 ? nullptr
-                       : cache + (((size_t)page * A.kv.n_layers + A.layer) * A.kv.n_kv_heads + h0) * step +
-                             (kind - 1) * plane16 + (size_t)t_pos[tok] * LPH + gl;
+                       : cache + (((size_t)page * A.kv.n_layers + A.layer) * A.kv.n_kv_heads + h0) * step + (kind - 1) * plane +
+                             (size_t)t_pos[tok] * D;
       }
       if (kind < 2) {
-        const bool norm = A.gamma[kind] != nullptr;
-        unsigned long long C[N2], S[N2];
-        {
-          float cs[NV], s[NV];
+        float r = 1.f;                           // lane u < RP_FLY: of head u
+        if (A.gamma[kind]) {
+          float ss[RP_FLY];
 #pragma unroll
-          for (int i = 0; i < NV; i += 4) {
-            float4 a4 = make_float4(1.f, 1.f, 1.f, 1.f), b4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (turns) {
-              a4 = *reinterpret_cast<const float4*>(&t_cos[tok][p0 + i]);
-              b4 = *reinterpret_cast<const float4*>(&t_sin[tok][p0 + i]);
-            }
-            const float4 ga = *reinterpret_cast<const float4*>(&gam[kind][gl * NV + i]);
-            const float4 gb = *reinterpret_cast<const float4*>(&gam[kind][partner * NV + i]);
-            cs[i] = a4.x * ga.x; cs[i + 1] = a4.y * ga.y; cs[i + 2] = a4.z * ga.z; cs[i + 3] = a4.w * ga.w;
-            s[i] = b4.x * gb.x; s[i + 1] = b4.y * gb.y; s[i + 2] = b4.z * gb.z; s[i + 3] = b4.w * gb.w;
-          }
+          for (int u = 0; u < RP_FLY; ++u) {
+            unsigned long long fl[N2], fh[N2];
+            unpack2<KT>(vl[u], fl);
+            unpack2<KT>(vh[u], fh);
+            unsigned long long s2 = mul2(fl[0], fl[0]);
 #pragma unroll
-          for (int i = 0; i < N2; ++i) {
-            C[i] = pair(cs[2 * i], cs[2 * i + 1]);
-            S[i] = low ? pair(-s[2 * i], -s[2 * i + 1]) : pair(s[2 * i], s[2 * i + 1]);
+            for (int i = 1; i < N2; ++i) s2 = fma2(fl[i], fl[i], s2);
+#pragma unroll
+            for (int i = 0; i < N2; ++i) s2 = fma2(fh[i], fh[i], s2);
+            const float2 sq = halves(s2);
+            ss[u] = sq.x + sq.y;
           }
+          // four sums over the group's lanes at once: a lane keeps the heads of its two lowest bits
+          const bool b0 = gl & 1, b1 = gl & 2;
+          const float s0 = (b0 ? ss[1] : ss[0]) + __shfl_xor_sync(gmask, b0 ? ss[0] : ss[1], 1, LPH);
+          const float s1 = (b0 ? ss[3] : ss[2]) + __shfl_xor_sync(gmask, b0 ? ss[2] : ss[3], 1, LPH);
+          float sum4 = (b1 ? s1 : s0) + __shfl_xor_sync(gmask, b1 ? s0 : s1, 2, LPH);
+#pragma unroll
+          for (int d = 4; d < LPH; d <<= 1) sum4 += __shfl_xor_sync(gmask, sum4, d, LPH);
+          r = rsqrtf(sum4 * (1.f / D) + A.eps);
+        }
+        // y_lo = r (lo CL + hi SL), y_hi = r (hi CH + lo SH)
+        unsigned long long CL[N2], SL[N2], CH[N2], SH[N2];
+        using F = std::conditional_t<HV == 4, float4, float2>;
+        union Row { F f; float2 p[N2]; };
+        Row c, s, gl2, gh2;
+        if (turns) {
+          c.f = *reinterpret_cast<const F*>(&t_cos[tok][lo]);
+          s.f = *reinterpret_cast<const F*>(&t_sin[tok][lo]);
+        }
+        gl2.f = *reinterpret_cast<const F*>(&gam[kind][lo]);
+        gh2.f = *reinterpret_cast<const F*>(&gam[kind][hi]);
+#pragma unroll
+        for (int i = 0; i < N2; ++i) {
+          const float2 c2 = turns ? c.p[i] : make_float2(1.f, 1.f), s2 = turns ? s.p[i] : make_float2(0.f, 0.f), ga = gl2.p[i], gb = gh2.p[i];
+          CL[i] = pair(c2.x * ga.x, c2.y * ga.y);
+          SL[i] = pair(-s2.x * gb.x, -s2.y * gb.y);
+          CH[i] = pair(c2.x * gb.x, c2.y * gb.y);
+          SH[i] = pair(s2.x * ga.x, s2.y * ga.y);
         }
 #pragma unroll
         for (int u = 0; u < RP_FLY; ++u) {
           if (u >= nh) break;
-          unsigned long long f[N2], o[N2];
-          unpack2<KT>(v[u], f);
-          float r = 1.f;
-          if (norm) {
-            unsigned long long s2 = mul2(f[0], f[0]);
-#pragma unroll
-            for (int i = 1; i < N2; ++i) s2 = fma2(f[i], f[i], s2);
-            const float2 sq = halves(s2);
-            float ss = sq.x + sq.y;
-#pragma unroll
-            for (int d = 1; d < LPH; d <<= 1) ss += __shfl_xor_sync(gmask, ss, d, LPH);
-            r = rsqrtf(ss * (1.f / D) + A.eps);
-          }
-          uint4 pv;
-          pv.x = __shfl_sync(gmask, v[u].x, partner, LPH);
-          pv.y = __shfl_sync(gmask, v[u].y, partner, LPH);
-          pv.z = __shfl_sync(gmask, v[u].z, partner, LPH);
-          pv.w = __shfl_sync(gmask, v[u].w, partner, LPH);
-          if (!turns) pv = make_uint4(0u, 0u, 0u, 0u);         // (also where the piece is not finite)
-          unpack2<KT>(pv, o);
-          const unsigned long long r2 = pair(r, r);
-          float y[NV];
+          const float ru = __shfl_sync(gmask, r, u, LPH);
+          const unsigned long long r2 = pair(ru, ru);
+          unsigned long long fl[N2], fh[N2];
+          unpack2<KT>(vl[u], fl);
+          unpack2<KT>(vh[u], fh);
 #pragma unroll
           for (int i = 0; i < N2; ++i) {
-            const float2 z = halves(mul2(r2, fma2(f[i], C[i], mul2(o[i], S[i]))));
-            y[2 * i] = z.x;
-            y[2 * i + 1] = z.y;
+            // (where nothing turns, whatever the partner is)
+            const unsigned long long a2 = mul2(turns ? fh[i] : 0ull, SL[i]), b2 = mul2(turns ? fl[i] : 0ull, SH[i]);
+            fl[i] = mul2(r2, fma2(fl[i], CL[i], a2));
+            fh[i] = mul2(r2, fma2(fh[i], CH[i], b2));
           }
-          v[u] = pack_piece<NV>(y);
+          vl[u] = pack2<KT>(fl);
+          vh[u] = pack2<KT>(fh);
         }
       }
       if (dst) {
 #pragma unroll
-        for (int u = 0; u < RP_FLY; ++u)
-          if (u < nh) dst[u * step] = v[u];
+        for (int u = 0; u < RP_FLY; ++u) {
+          if (u < nh) {
+            *reinterpret_cast<uint2*>(dst + u * step + lo) = vl[u];
+            *reinterpret_cast<uint2*>(dst + u * step + hi) = vh[u];
+          }
+        }
       }
     }
   }
@@ -263,7 +289,8 @@ __global__ void __launch_bounds__(RP_THREADS, RP_BLOCKS) k_qk_norm_rope(const __
 
 template <class KT, int D>
 cudaError_t launch_rope(const RopeArgs& A, int blocks, cudaStream_t st) {
-  return launch_k(k_qk_norm_rope<KT, D>, dim3(blocks), dim3(RP_THREADS), 0, st, A);
+  return A.half8 * 8 * 2 == D * (int)sizeof(KT) ? launch_k(k_qk_norm_rope<KT, D, true>, dim3(blocks), dim3(RP_THREADS), 0, st, A)
+                                                : launch_k(k_qk_norm_rope<KT, D, false>, dim3(blocks), dim3(RP_THREADS), 0, st, A);
 }
 
 }  // namespace
@@ -284,8 +311,8 @@ extern "C" int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* 
   const int esz = kv->dtype == SPEC_F32 ? 4 : 2, d = kv->head_dim;
   const int64_t heads = (int64_t)n_q_heads + 2 * (int64_t)kv->n_kv_heads;
   if (heads > (1 << 20)) return set_last_error(SPEC_ERR_UNSUPPORTED, "more than 2^20 heads");
-  if (ld < heads * d || ld % (16 / esz) || ld > ((int64_t)1 << 40))
-    return set_last_error(SPEC_ERR_ARG, "ld: at least a row's heads, a multiple of 16 bytes");
+  if (ld < heads * d || ld % (16 / esz)) return set_last_error(SPEC_ERR_ARG, "ld: at least a row's heads, a multiple of 16 bytes");
+  if ((double)ld * n_rows > 1e18) return set_last_error(SPEC_ERR_UNSUPPORTED, "rows of more than 10^18 elements");
   if (!aligned16(qkv_dev) || !aligned16(q_out_dev)) return set_last_error(SPEC_ERR_ARG, "qkv and q must be 16-byte aligned");
   if (!(eps >= 0.f) || !(eps < INFINITY)) return set_last_error(SPEC_ERR_ARG, "eps must be finite and not negative");
   if (rope->dim < 0 || rope->dim > d || rope->dim % 16) return set_last_error(SPEC_ERR_ARG, "rope dim: a multiple of 16 up to head_dim");
@@ -293,7 +320,7 @@ extern "C" int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* 
   if (rope->dim > 0 && !positions_dev) return set_last_error(SPEC_ERR_ARG, "null positions");
   RopeArgs A{*kv, ChunkIndex{row_start_dev, n_new_dev, cache_len_dev, n_seq, n_rows, n_rows, kv->max_pages * kv->page_size},
              static_cast<const char*>(qkv_dev), static_cast<char*>(q_out_dev), positions_dev, {q_gamma_dev, k_gamma_dev},
-             err_dev, ld * esz, layer, n_q_heads, rope->dim / 2 / (16 / esz), {}, {}, eps, {}, {}};
+             err_dev, ld * esz, layer, n_q_heads, rope->dim / 2 / (8 / esz), {}, {}, eps, {}, {}};
   for (int p = 0; p < rope->dim / 2; ++p) {
     if (!std::isfinite(rope->freq[p])) return set_last_error(SPEC_ERR_ARG, "a frequency is not finite");
     if (rope->axis[p] >= rope->n_axes) return set_last_error(SPEC_ERR_ARG, "a pair's axis is out of range");

@@ -60,7 +60,7 @@ def test_rope_refusals(B):
 
     cases = SIZES + [({k: None}, -1) for k in ("qkv_dev", "row_start_dev", "n_new_dev", "cache_len_dev", "positions_dev",
                                                "q_out_dev", "err_dev")]
-    cases += [(dict(ld=1023), -1), (dict(ld=1016), -1), (dict(ld=1028), -1), (dict(qkv_dev=FAKE + 8), -1),
+    cases += [(dict(ld=1 << 61), -6), (dict(ld=1023), -1), (dict(ld=1016), -1), (dict(ld=1028), -1), (dict(qkv_dev=FAKE + 8), -1),
               (dict(q_out_dev=(FAKE << 1) + 4), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
               (rp(dim=-16), -1), (rp(dim=24), -1), (rp(dim=144), -1), (rp(n_axes=0), -1), (rp(n_axes=5), -1),
               (pair("freq", 31, float("nan")), -1), (pair("freq", 0, float("inf")), -1), (pair("axis", 7, 2), -1)]
@@ -111,7 +111,7 @@ def test_evict_refusals(B):
               out_kept_dev=4 * FAKE, out_len_dev=5 * FAKE, err_dev=6 * FAKE)
     cases = [({k: None}, -1) for k in ok if k.endswith("_dev")]
     cases += [(dict(n_seq=0), -1), (dict(n_seq=65536), -1), (dict(budget=0), -1), (dict(recent=-1), -1), (dict(recent=33), -1),
-              (dict(ld=0), -1), (dict(ld=1 << 32), -1)]
+              (dict(ld=0), -1), (dict(ld=1 << 32), -1), (dict(budget=(1 << 30) + 1), -6)]
     # masses: 2 layers x 2 sequences x 2 heads x 64 f32 = 2 KB, kept 1 KB, lengths 8 bytes
     cases += [(dict(out_mass_dev=2 * FAKE + x), -1) for x in (0, 2044, -2044)]
     cases += [(dict(out_kept_dev=2 * FAKE + x), -1) for x in (0, 2044, -1020)]
