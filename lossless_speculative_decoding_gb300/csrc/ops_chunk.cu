@@ -495,8 +495,19 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
 // binary orders), or to no number, is done again by ch_slow, which moves m and rescales
 // O and the tile's earlier weights. Scores beyond 2^24, above which float
 // does not hold every whole number, are taken against the row's largest score itself,
-// also there. Rounding a weight to bf16 costs 2^-9 relative at most in each term, as
-// much as rounding the result does; the sum of weights is of the fp32 values.
+// also there. Rounding a weight to bf16 costs at most 2^-8 relative in each term, as
+// rounding the result does: 0.0023 in all against 64 bits, 0.0017 with the result's
+// alone; a second bf16 part would be half of the MMAs again. The sum of weights is of
+// the fp32 values.
+//
+// Bound by the chain of an MMA's issue: S and P V of a group and tile are 16 MMAs of 64
+// cycles, and an issue waits until the MMAs before it are nearly over, so that every
+// wait of the issuer for weights or keys leaves the tensor cores idle: they are busy 0.6
+// to 0.77 of the time. Measured, L2 cold, 32 on 8 heads of 128: a chunk of 1,021 tokens
+// behind 65,521 730 us (0.77 of the MMA rate; 820 where the clocks have come down to the
+// power cap's), a prompt of 5,288 190 us (0.62), eight chunks of 17 to 701 behind 1,288 to
+// 5,288 143 us (0.62). Slower: an issuer for each group (951 us where one had 798),
+// sixteen softmax warps, scores summed one by one, the sum of the rounded weights.
 constexpr int CT_KEYS = 128;                     // 2^7 (key_bits)
 constexpr int CT_THREADS = 352;
 constexpr int CT_EXTRA = 2;                      // units' time that a segment's start and end take
@@ -1063,7 +1074,13 @@ __global__ void __launch_bounds__(CX_WARPS * 32) k_chunk_tc_join(const __grid_co
   }
 }
 
-// Shape of a launch, from sizes and types alone.
+// Shape of a launch, from sizes and types alone. Few bf16 tokens go by the tree attention's
+// kernel, whose weights have 16 bits: a token decoded alone and one verified in a tree
+// meet the same arithmetic, 0.0017 off a 64-bit result for 0.0023. Its time and that of
+// the tensor-core form here, one token each: one sequence of 5,236 on 10 heads 21.7 and
+// 24.0 us, 64 of 336 to 5,236 168 and 162, 16 of them 62 and 55; one of 65,521 on 8 heads
+// 59 and 64; 32 tokens on that 67 and 66, eight of 1,288 to 5,288 43 and 38. (With 256 rows
+// in place of 128, 64 tokens of the eight take 63 and 43.)
 struct ChunkPlan {
   int G, parts, tok, key_bits, extra;
   int max_blocks;           // of any grid (the workspace is sized without a device)

@@ -19,7 +19,7 @@
 // Bound: HBM, by the bytes of the rows, and below some 10^4 tokens the way there: places,
 // angles, rows and results follow one another, in one turn or two of a block. Measured, L2
 // cold, bf16, 32 query and 8 kv heads of 128: 16,000 tokens 79 us, 0.75 of the copy rate;
-// 4,628 tokens 29.7 us, 0.58. (Pieces of 16 bytes with their partners by shuffle: 31.5;
+// 4,677 tokens 29.7 us, 0.58. (Pieces of 16 bytes with their partners by shuffle: 31.5;
 // the next heads' loads beside a head's arithmetic, which takes the registers of a
 // block in four: 35.6, or 33.0 with three blocks; 8 tokens at a time 30.5.)
 #include <cuda_runtime.h>

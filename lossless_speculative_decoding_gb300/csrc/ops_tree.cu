@@ -16,6 +16,9 @@
 // times log2 e, weights 2^(x - m)). A segment that a block holds alone is
 // written as it ends; of a shared one, each block leaves (output, maximum,
 // sum) in the workspace and a second launch joins the parts in key order.
+//
+// Chunks of few new tokens go by the same kernels (CHAIN): node i's parent is node i - 1,
+// a sequence's rows begin where row_start says, and lse is wanted too.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -654,7 +657,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
       if (tree_size<CHAIN>(A, s).bad) atomicOr(A.err, DERR_POS);
   TreeWalk<CHAIN> walk;
   tc_fence_before();
-  walk.template init<TT_THREADS>(A);                      // two block barriers
+  walk.template init<TT_THREADS>(A);             // two block barriers
   tc_fence_after();
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other
