@@ -16,7 +16,9 @@
 //
 // Bound: HBM, by the rows moved. Measured, L2 cold: 36 layers x 2 x 8 heads of 3,288
 // and 5,288 positions to 2,048, 1.2 GB read and written: 232 us, 0.79 of the copy rate
-// (the selection 42, the rows 184); 12 layers x 10 heads of 1,357 to 1,024 40 us (13, 26).
+// (the selection 33, the rows 185: reads and writes of HBM in turn); 12 layers x 10 heads
+// of 1,357 to 1,024 40 us (11, 26). Keys in registers, where two blocks fit an SM: the
+// selection 42 and 13 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -27,7 +29,8 @@ namespace spec {
 namespace {
 
 constexpr int EV_THREADS = 512;
-constexpr int EV_HOLD = 16;                      // keys a thread holds; of longer sequences they are read again
+constexpr int EV_KEYS = 8192;                    // keys held in shared memory; of longer sequences they are read again
+constexpr int EV_BLOCKS = 4;                     // on an SM
 constexpr int EV_BINS = 2048;
 constexpr int MV_THREADS = 256;
 constexpr int MV_ROWS = 4;                       // pieces of a batch for each thread
@@ -69,8 +72,9 @@ __device__ __forceinline__ int warps_before(int v, int* red) {
   return before;
 }
 
-__global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_constant__ EvictArgs A) {
+__global__ void __launch_bounds__(EV_THREADS, EV_BLOCKS) k_evict_select(const __grid_constant__ EvictArgs A) {
   __shared__ int hist[EV_BINS];
+  __shared__ uint32_t keys[EV_KEYS];             // (a thread's own)
   __shared__ int red[EV_THREADS / 32];
   __shared__ uint32_t s_digit;
   __shared__ int s_left;
@@ -107,26 +111,18 @@ __global__ void __launch_bounds__(EV_THREADS) k_evict_select(const __grid_consta
   const int old = n - A.recent;                  // positions that compete
   // warp w has positions w len .. , 32 at a time
   const int lane = t & 31, w = t >> 5, len = (n + EV_THREADS - 1) / EV_THREADS * 32, w0 = w * len;
-  const bool hold = len <= EV_HOLD * 32;
-  uint32_t keys[EV_HOLD];
+  const bool hold = len * (EV_THREADS / 32) <= EV_KEYS;
   if (hold) {
-#pragma unroll
-    for (int u = 0; u < EV_HOLD; ++u) {
-      const int i = w0 + 32 * u + lane;
-      keys[u] = 32 * u < len && i < old ? mass_key(mass[i]) : 0;
-    }
+#pragma unroll 4
+    for (int i = w0 + lane; i < w0 + len; i += 32) keys[i] = i < old ? mass_key(mass[i]) : 0u;
   }
   // f(position, key) for this thread's positions, all of a warp's lanes together (i may be n or more)
   auto each = [&](auto&& f) {
     if (hold) {
-#pragma unroll
-      for (int u = 0; u < EV_HOLD; ++u)
-        if (32 * u < len) f(w0 + 32 * u + lane, keys[u]);
+#pragma unroll 4
+      for (int i = w0 + lane; i < w0 + len; i += 32) f(i, keys[i]);
     } else {
-      for (int u = 0; u < len; u += 32) {
-        const int i = w0 + u + lane;
-        f(i, i < old ? mass_key(mass[i]) : 0u);
-      }
+      for (int i = w0 + lane; i < w0 + len; i += 32) f(i, i < old ? mass_key(mass[i]) : 0u);
     }
   };
   int left = A.budget - A.recent;                // of them to be kept; those equal to the threshold at last
