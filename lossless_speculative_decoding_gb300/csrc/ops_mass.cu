@@ -669,7 +669,7 @@ cudaError_t launch_mass_tc(MassArgs A, int blocks, cudaStream_t st) {
   // Pairs of blocks where units are long and few, alone and paired: every token of a prompt of 5,288 on 8 kv heads
   // 150 and 104 us, two of them 217 and 201, four 448 and 435, four of 2,000 93 and 98, the last 512 tokens of eight
   // prompts 101 and 113; the last 32 (one tile of rows) 22 and 30.
-  A.pair = (std::min(A.last, A.ix.max_new) + A.tok - 1) / A.tok >= MT_PAIR_TILES &&
+  A.pair = (std::min({A.last, A.ix.max_new, A.ix.capacity}) + A.tok - 1) / A.tok >= MT_PAIR_TILES &&
                    (int64_t)A.ix.n_seq * A.kv.n_kv_heads <= MT_PAIR_PLANES
                ? 2
                : 1;
