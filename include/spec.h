@@ -634,7 +634,7 @@ int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* qkv_dev, in
  * on kv head h / (n_q_heads / n_kv_heads).
  *   q_dev, out_dev [n_rows][n_q_heads][head_dim] in the cache's dtype, 16-byte
  *     aligned; out_dev may be q_dev itself, but not overlap it otherwise.
- *   out_lse_dev [n_rows][n_q_heads] f32, or NULL.
+ *   out_lse_dev [n_rows][n_q_heads] f32, or NULL; overlaps neither q nor out.
  *   max_new: an upper bound of n_new (it chooses the kernel's form).
  *   ws_dev: spec_chunk_attention_ws_bytes bytes of device memory, 16-byte
  *     aligned; needs no initialisation; one call at a time per workspace.
@@ -664,8 +664,8 @@ int spec_chunk_attention(const spec_kv_view* kv, int layer, const void* q_dev, i
  *   q_dev, n_rows, max_new, row_start_dev, .. as in spec_chunk_attention, whose
  *     lse_dev [n_rows][n_q_heads] this takes.
  *   mass_dev, out_mass_dev [n_seq][n_kv_heads][ld] f32, out_mass_dev the same
- *     array or one that does not overlap it; mass_dev may be NULL (zeros). A
- *     sequence of more than ld positions is left out (SPEC_DEV_ERR_POS).
+ *     array or one that does not overlap it (nor q and lse); mass_dev may be NULL
+ *     (zeros). A sequence of more than ld positions is left out (SPEC_DEV_ERR_POS).
  * lse finite where a token is counted. fp32, in a fixed order: the same call gives
  * the same bits. The exponent's terms are rounded before they cancel, so a weight is
  * off by some 2^-21 of scale * sum |q_i K_i| + |lse|, relative to itself. Positions

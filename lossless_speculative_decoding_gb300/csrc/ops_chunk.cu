@@ -500,16 +500,20 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
 // alone; a second bf16 part would be half of the MMAs again. The sum of weights is of
 // the fp32 values.
 //
-// Bound by the chain of an MMA's issue: S and P V of a group and tile are 16 MMAs of 64
-// cycles, and an issue waits until the MMAs before it are nearly over, so that every
-// wait of the issuer for weights or keys leaves the tensor cores idle: they are busy 0.6
-// to 0.77 of the time. Measured, L2 cold, 32 on 8 heads of 128: a chunk of 1,021 tokens
-// behind 65,521 730 us (0.77 of the MMA rate; 820 where the clocks have come down to the
-// power cap's), a prompt of 5,288 190 us (0.62), eight chunks of 17 to 701 behind 1,288 to
-// 5,288 143 us (0.62). Slower: an issuer for each group (951 us where one had 798),
-// sixteen softmax warps, scores summed one by one, the sum of the rounded weights.
+// Bound by a group's chain S, softmax, P V: 512 cycles of MMAs, some 1,600 until its
+// weights are seen (scores read, 128 exponentials a thread, weights written), 512 again,
+// beside which the other group's MMAs take 1,024; so the tensor cores are busy 0.6 to 0.77
+// of the time. There is no room in tensor memory for a third S, and with 64 keys an S
+// MMA waits for shared memory (6 KB in 32 cycles). Measured, L2 cold, 32 on 8 heads of 128: a
+// chunk of 1,021 tokens behind 65,521 720 us (0.78 of the MMA rate; 800 where the clocks
+// have come down to the power cap's), a prompt of 5,288 188 us (0.62), eight chunks of 17
+// to 701 behind 1,288 to 5,288 142 us (0.63). Slower: an issuer for each group (951 us
+// where one had 798), sixteen softmax warps, scores summed one by one, the sum of the
+// rounded weights; barriers for each buffer in place of each iteration's (750 where this
+// has 735).
 constexpr int CT_KEYS = 128;                     // 2^7 (key_bits)
 constexpr int CT_THREADS = 352;
+constexpr int CT_RING = 16;                      // iterations whose barriers are told apart
 constexpr int CT_EXTRA = 2;                      // units' time that a segment's start and end take
 constexpr int CT_HALF = 128 * 128;               // bytes of 64 dims of 128 rows of Q
 constexpr int CT_OCOL = 256;                     // TMEM columns: S of a group at 128 g, its O behind at CT_OCOL + D g
@@ -529,7 +533,7 @@ struct CtCfg {
 
 template <int NBUF>
 struct CtHeader {
-  uint64_t kv_full[NBUF], kv_empty[NBUF], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2];
+  uint64_t full[CT_RING], done[CT_RING], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2];
   uint64_t q_full, q_free, fin;
   uint32_t tmem;
   int abort;
@@ -656,9 +660,9 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t bufs = sm_addr(base), q_addr = sm_addr(qsm);
   if (t == 0) {
-    for (int i = 0; i < NBUF; ++i) {
-      mbar_init(H.kv_full + i, 1);
-      mbar_init(H.kv_empty + i, 1);
+    for (int i = 0; i < CT_RING; ++i) {
+      mbar_init(H.full + i, 1);
+      mbar_init(H.done + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(H.s_full + i, 1);
@@ -702,11 +706,16 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
   const int P = A.kv.page_size;
 
   if (warp == 8) {
-    // ---- producer: K, V, K, V, .. of the tiles, a box for each kb keys of a page ----
+    // ---- producer: for each of the issuer's iterations V of a tile and K of the next, a box for each kb keys
+    // of a page. An iteration has one barrier that says its loads are there and one that says it is over, and
+    // with it the buffers that it read: a buffer's load waits for the iteration of the one before (lane b
+    // knows buffer b's). Every iteration has a load, so none is passed over, and CT_RING of them are more than
+    // there are buffers. ----
+    static_assert(NBUF < CT_RING, "iterations on their way");
     const int nbox = CT_KEYS / kb, j = lane;
     const int planes = A.kv.n_layers * A.kv.n_kv_heads * 2;
     int b = 0;
-    uint32_t turn = 0;                           // passes over the ring
+    uint32_t it = 0, last = 0, loads = 0;
     bool ok = true;
     ChunkSeg g;
     while (ok && walk.next(g)) {
@@ -724,29 +733,39 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
         }
         return page;
       };
-      int page = page_of(g.t0), next = page_of(g.t0 + 1);
-      for (int i = 0, n = 2 * (g.t1 - g.t0); i < n; ++i) {
-        const int tile = g.t0 + i / 2, key = tile * CT_KEYS + kb * j, v = i & 1;
-        if (!v && i > 0) {
-          page = next;
-          next = page_of(tile + 1);
-        }
-        if (turn > 0 && !waitw(H.kv_empty + b, turn - 1)) { ok = false; break; }
-        const uint32_t full = sm_addr(H.kv_full + b);
+      int page = -1, next = page_of(g.t0);
+      for (int i = 0, n = g.t1 - g.t0; ok && i <= n; ++i, ++it) {
+        const uint32_t full = sm_addr(H.full + it % CT_RING);
         if (lane == 0)
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full), "r"((uint32_t)C::BUF) : "memory");
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                       ::"r"(full), "r"((uint32_t)((i > 0 && i < n ? 2 : 1) * C::BUF)) : "memory");
         __syncwarp();
-        if (lane < nbox)
-          asm volatile(
-              "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
-              ::"r"(bufs + b * C::BUF + j * kb * D * 2), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0), "r"(key % P / 8),
-                "r"(page < 0 ? -1 : page * planes + plane + v), "r"(full)
-              : "memory");
-        if (++b == NBUF) { b = 0; ++turn; }
+#pragma unroll
+        for (int v = 1; v >= 0; --v) {           // V of tile i - 1, K of tile i
+          if (v ? i == 0 : i == n) continue;
+          const int tile = g.t0 + i - v, key = tile * CT_KEYS + kb * j;
+          if (!v) {
+            page = next;
+            next = page_of(tile + 1);
+          }
+          const uint32_t before = __shfl_sync(0xffffffffu, last, b);
+          if (ok && loads >= NBUF) ok = waitw(H.done + before % CT_RING, before / CT_RING);
+          if (!ok) break;
+          if (lane < nbox)
+            asm volatile(
+                "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
+                ::"r"(bufs + b * C::BUF + j * kb * D * 2), "l"(reinterpret_cast<uint64_t>(&kvmap)), "r"(0), "r"(key % P / 8),
+                  "r"(page < 0 ? -1 : page * planes + plane + v), "r"(full)
+                : "memory");
+          if (lane == b) last = it;
+          ++loads;
+          if (++b == NBUF) b = 0;
+        }
       }
     }
-    // shared memory outlives the copies (over, unless the issuer gave up a wait): each buffer's last one
-    for (int i = 0; i < NBUF; ++i) mbar_wait_deadline(sm_addr(H.kv_full + i), (i < b ? turn : turn - 1) & 1, nullptr);
+    // shared memory outlives the copies (over, unless a wait was given up): those of the last iterations
+    for (uint32_t k = it > CT_RING ? it - CT_RING : 0; k < it; ++k)
+      mbar_wait_deadline(sm_addr(H.full + k % CT_RING), k / CT_RING & 1, nullptr);
   } else if (warp == 9) {
     // ---- MMA issuer. The whole warp runs the loop on values that are the same in
     // every lane, so that the descriptors stay in uniform registers; one lane issues.
@@ -756,9 +775,12 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
     const uint32_t one = elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
     auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     uint32_t jobs[2] = {0, 0};                   // P V's of the groups so far
-    int rbuf = 0, rturn = 0;                     // ring position of the next load
+    int rbuf = 0;                                // ring position of the next load
+    uint32_t it = 0;                             // iterations so far
     auto step = [&]() {
-      if (++rbuf == NBUF) { rbuf = 0; ++rturn; }
+      const int b = rbuf;
+      if (++rbuf == NBUF) rbuf = 0;
+      return b;
     };
     bool ok = true;
     for (uint32_t seg = 0; ok; ++seg) {
@@ -771,13 +793,10 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
       const int nt = g.t1 - g.t0, n0 = same(G0.tiles), n1 = same(G1.tiles), e0 = same(G0.end), e1 = same(G1.end);
       if (!(ok = waitw(&H.q_full, seg))) break;
       // iteration i: P V of tile i - 1 (its V is the ring's next), S of tile i (its K behind)
-      for (int i = 0; ok && i <= nt; ++i) {
-        int vbuf = 0, kbuf = 0;
-        uint32_t kturn = 0;
+      for (int i = 0; ok && i <= nt; ++i, ++it) {
+        if (!(ok = waitw(H.full + it % CT_RING, it / CT_RING))) break;
+        const int vbuf = i > 0 ? step() : 0, kbuf = i < nt ? step() : 0;
         if (i > 0) {
-          vbuf = rbuf;
-          if (!(ok = waitw(H.kv_full + vbuf, rturn))) break;
-          step();
           // slots past the sequence's last may hold anything: those that the last MMA reads become zeros
           const int nk = g.n + g.m - (g.t0 + i - 1) * CT_KEYS;
           if (nk < CT_KEYS && nk % 16) {
@@ -790,11 +809,6 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
-        }
-        if (i < nt) {
-          kbuf = rbuf;
-          kturn = rturn;
-          step();
         }
 #pragma unroll
         for (int gr = 0; gr < 2; ++gr) {
@@ -818,8 +832,6 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
             if (i == ng) tc_commit(sm_addr(H.o_done + gr), one);
           }
           if (ok && i < ng) {
-            if (!(ok = waitw(H.kv_full + kbuf, kturn))) break;
-            tc_fence_after();
             const uint64_t ad = tt_desc(q_addr + gr * C::Q, 16, 1024), bd = tt_desc(bufs + kbuf * C::BUF, 16, GROUP);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
@@ -829,8 +841,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
           }
         }
         if (!ok) break;
-        if (i > 0) tc_commit(sm_addr(H.kv_empty + vbuf), one);
-        if (i < nt) tc_commit(sm_addr(H.kv_empty + kbuf), one);
+        tc_commit(sm_addr(H.done + it % CT_RING), one);
         if (i == nt - 1) tc_commit(sm_addr(&H.q_free), one);
       }
     }
@@ -1162,6 +1173,9 @@ extern "C" int spec_chunk_attention(const spec_kv_view* kv, int layer, const voi
   const int64_t bytes = (int64_t)n_rows * n_q_heads * d * (kv->dtype == SPEC_F32 ? 4 : 2);
   if (out_dev != q_dev && spans_meet(out_dev, bytes, q_dev, bytes))
     return set_last_error(SPEC_ERR_ARG, "out overlaps q without being the same array");
+  const int64_t lse_bytes = (int64_t)n_rows * n_q_heads * 4;
+  if (spans_meet(out_lse_dev, lse_bytes, q_dev, bytes) || spans_meet(out_lse_dev, lse_bytes, out_dev, bytes))
+    return set_last_error(SPEC_ERR_ARG, "lse overlaps q or out");
   const ChunkPlan plan(*kv, max_new, n_q_heads);
   if (ws_bytes < plan.total) return set_last_error(SPEC_ERR_ARG, "workspace too small");
   const int sms = sm_count_once();

@@ -716,6 +716,10 @@ extern "C" int spec_attention_mass(const spec_kv_view* kv, int layer, const void
   const int64_t mbytes = (int64_t)n_seq * kv->n_kv_heads * ld * 4;
   if (out_mass_dev != mass_dev && spans_meet(out_mass_dev, mbytes, mass_dev, mbytes))
     return set_last_error(SPEC_ERR_ARG, "out_mass overlaps mass without being the same array");
+  const int64_t rows = (int64_t)n_rows * n_q_heads;
+  if (spans_meet(out_mass_dev, mbytes, lse_dev, rows * 4) ||
+      spans_meet(out_mass_dev, mbytes, q_dev, rows * kv->head_dim * (kv->dtype == SPEC_F32 ? 4 : 2)))
+    return set_last_error(SPEC_ERR_ARG, "out_mass overlaps lse or q");
   const int sms = sm_count_once();
   if (sms < 1) return set_last_error(SPEC_ERR_CUDA, "no device");
   const int d = kv->head_dim;

@@ -86,6 +86,9 @@ def test_attention_refusals(B):
               (dict(q_dev=FAKE + 2), -1), (dict(out_dev=FAKE + 8), -1)]
     # out next to q is fine, over a part of it is not: 8 rows x 4 heads x 128 bf16 = 8 KB
     cases += [(dict(out_dev=FAKE + x), -1) for x in (16, 8192 - 16, -16)]
+    # lse, 128 bytes, over a part of either
+    cases += [(dict(out_lse_dev=FAKE + x), -1) for x in (0, 8192 - 4, -124)]
+    cases += [(dict(out_lse_dev=(FAKE << 1) + x), -1) for x in (0, 8192 - 4, -124)]
     cases += [(dict(kv=_view(B, max_pages=1 << 26, n_kv_heads=256), n_q_heads=256), -6),
               (dict(kv=_view(B, max_pages=1 << 26), n_q_heads=256, max_new=1 << 28), -6)]
     _all(B, B.spec_chunk_attention, ok, cases)
@@ -103,6 +106,8 @@ def test_mass_refusals(B):
               (dict(q_dev=FAKE + 2), -1), (dict(scale=5e-20), -6), (dict(scale=2e19), -6)]
     # 2 sequences x 2 heads x 64 f32: 1 KB
     cases += [(dict(mass_dev=(FAKE << 1) + x), -1) for x in (4, 1020, -4, -1020)]
+    cases += [(dict(out_mass_dev=FAKE + x), -1) for x in (0, 8192 - 4, -1020)]
+    cases += [(dict(lse_dev=(FAKE << 1) + x), -1) for x in (0, 1020, -124)]
     _all(B, B.spec_attention_mass, ok, cases)
 
 
