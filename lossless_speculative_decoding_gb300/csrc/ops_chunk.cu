@@ -500,17 +500,17 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
 // alone; a second bf16 part would be half of the MMAs again. The sum of weights is of
 // the fp32 values.
 //
-// Bound by a group's chain S, softmax, P V: 512 cycles of MMAs, some 1,600 until its
-// weights are seen (scores read, 128 exponentials a thread, weights written), 512 again,
-// beside which the other group's MMAs take 1,024; so the tensor cores are busy 0.6 to 0.77
-// of the time. There is no room in tensor memory for a third S, and with 64 keys an S
-// MMA waits for shared memory (6 KB in 32 cycles). Measured, L2 cold, 32 on 8 heads of 128: a
+// Bound by the MMAs and what feeds them: an iteration's two S and two P V are 2,048 cycles
+// of tensor cores, and as many of the shared memory's port (an S MMA reads 8 KB in its
+// 64 cycles, all that the port gives, and 64 KB of keys and values come in beside it);
+// with the issuer's waits it takes 2,600. Without the exponentials the kernel takes as long,
+// without any of the softmax's arithmetic 7% less. Measured, L2 cold, 32 on 8 heads of 128: a
 // chunk of 1,021 tokens behind 65,521 720 us (0.78 of the MMA rate; 800 where the clocks
 // have come down to the power cap's), a prompt of 5,288 188 us (0.62), eight chunks of 17
 // to 701 behind 1,288 to 5,288 142 us (0.63). Slower: an issuer for each group (951 us
 // where one had 798), sixteen softmax warps, scores summed one by one, the sum of the
 // rounded weights; barriers for each buffer in place of each iteration's (750 where this
-// has 735).
+// has 735). No faster: scores asked for two loads ahead.
 constexpr int CT_KEYS = 128;                     // 2^7 (key_bits)
 constexpr int CT_THREADS = 352;
 constexpr int CT_RING = 16;                      // iterations whose barriers are told apart
