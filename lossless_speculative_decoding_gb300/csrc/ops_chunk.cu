@@ -974,7 +974,16 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
           const size_t row = row_at(A, g.r0, g.rt, g.hk, R.row0 + r);
           const float inv = 1.f / st.l;
           if (part < 0 && live && A.lse) A.lse[row] = (ref + log2f(st.l)) * LN2;
-          uint4* og = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + row * D);
+          // Results go out by four lanes together, 64 bytes of a row: lane q of them has the q-th 16 bytes of the four rows.
+          const int q = lane & 3;
+          uint4* og[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int rj = (r & ~3) + j;
+            og[j] = part < 0 && rj < R.rows
+                        ? reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + row_at(A, g.r0, g.rt, g.hk, R.row0 + rj) * D) + q
+                        : nullptr;
+          }
           // a part lies as [4 dims][row]
           float4* pg = reinterpret_cast<float4*>(A.part_o) + (((size_t)blockIdx.x * 2 + part) * 2 + gr) * 128 * (D / 4) + r;
 #pragma unroll 1
@@ -984,15 +993,25 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
             if (part < 0) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * inv);
+              uint32_t y[4][4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 y;
-                y.x = pack_bf16(__uint_as_float(v[8 * i]), __uint_as_float(v[8 * i + 1]));
-                y.y = pack_bf16(__uint_as_float(v[8 * i + 2]), __uint_as_float(v[8 * i + 3]));
-                y.z = pack_bf16(__uint_as_float(v[8 * i + 4]), __uint_as_float(v[8 * i + 5]));
-                y.w = pack_bf16(__uint_as_float(v[8 * i + 6]), __uint_as_float(v[8 * i + 7]));
-                if (live) og[4 * c + i] = y;
-              }
+              for (int i = 0; i < 16; ++i) y[i / 4][i % 4] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+              // a transposition: by the lanes' first bit, then by their second
+#pragma unroll
+              for (int s = 1; s < 4; s <<= 1)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (i & s) continue;
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, q & s ? y[i][x] : y[i + s][x], s);
+                    if (q & s) y[i][x] = got;
+                    else y[i + s][x] = got;
+                  }
+                }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (og[j]) og[j][4 * c] = make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
             } else if (live) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
