@@ -506,11 +506,14 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
 // with the issuer's waits it takes 2,600. Without the exponentials the kernel takes as long,
 // without any of the softmax's arithmetic 7% less. Measured, L2 cold, 32 on 8 heads of 128: a
 // chunk of 1,021 tokens behind 65,521 720 us (0.78 of the MMA rate; 800 where the clocks
-// have come down to the power cap's), a prompt of 5,288 188 us (0.62), eight chunks of 17
-// to 701 behind 1,288 to 5,288 142 us (0.63). Slower: an issuer for each group (951 us
-// where one had 798), sixteen softmax warps, scores summed one by one, the sum of the
-// rounded weights; barriers for each buffer in place of each iteration's (750 where this
-// has 735). No faster: scores asked for two loads ahead.
+// have come down to the power cap's), a prompt of 5,288 175 us (0.67), eight chunks of 17
+// to 701 behind 1,288 to 5,288 139 us (0.64): a segment's switch is 10,000 cycles from its
+// last S to the next one's first weights (last weights and P V 3,000, results 3,500, the
+// next queries and S). Slower: an issuer for each group (951 us where one had 798), sixteen
+// softmax warps, scores summed one by one, the sum of the rounded weights; barriers for
+// each buffer in place of each iteration's (750 where this has 735); each lane its own
+// row's results (prompt 189, chunks 142); the next segment's S before the results are out
+// (chunks 150). No faster: scores asked for two loads ahead, the next queries into L2.
 constexpr int CT_KEYS = 128;                     // 2^7 (key_bits)
 constexpr int CT_THREADS = 352;
 constexpr int CT_RING = 16;                      // iterations whose barriers are told apart
