@@ -273,10 +273,7 @@ __global__ void __launch_bounds__(CF_THREADS) k_chunk_fma(const __grid_constant_
     for (int i = t; i < CF_ROWS * (D / 4); i += CF_THREADS) {
       const int r = i / (D / 4), c = 4 * (i % (D / 4));
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < nrows) {
-        v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + q_at(r) + c);
-        v = make_float4(v.x * A.scale_l2e, v.y * A.scale_l2e, v.z * A.scale_l2e, v.w * A.scale_l2e);
-      }
+      if (r < nrows) v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + q_at(r) + c);
       *reinterpret_cast<float4*>(&sm.q[r][c]) = v;
     }
     float m[4], l[4];
@@ -345,7 +342,8 @@ __global__ void __launch_bounds__(CF_THREADS) k_chunk_fma(const __grid_constant_
         float mt = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (k0 + tx + 16 * j >= seen[i]) x[i][j] = -INFINITY;
+          // (the product takes the scale: scale * q may be past the largest float where scale * q.K is not)
+          x[i][j] = k0 + tx + 16 * j < seen[i] ? x[i][j] * A.scale_l2e : -INFINITY;
           mt = fmaxf(mt, x[i][j]);
         }
 #pragma unroll

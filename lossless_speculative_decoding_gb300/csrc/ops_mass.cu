@@ -159,7 +159,6 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
         if (rr < end) {
           const size_t row = ((size_t)g.r0 + rr / A.G) * A.hq + g.hk * A.G + rr % A.G;
           v = *reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + row * D + c);
-          v = make_float4(v.x * A.scale_l2e, v.y * A.scale_l2e, v.z * A.scale_l2e, v.w * A.scale_l2e);
           if (c == 0) sm.lse[r] = A.lse[row] * LOG2E;
         }
         *reinterpret_cast<float4*>(&sm.q[r][c]) = v;
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
         const int seen = g.n + rr / A.G + 1 - k0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (tx + 16 * j < seen) sum[j] += exp2f(x[i][j] - lse);
+          if (tx + 16 * j < seen) sum[j] += exp2f(fmaf(x[i][j], A.scale_l2e, -lse));   // (scale * q may overflow)
       }
     }
     __syncthreads();
