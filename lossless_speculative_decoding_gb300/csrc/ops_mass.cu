@@ -91,9 +91,21 @@ struct MassWalk {
   }
 };
 
+// A sum with the rounding error that it has not taken in.
+struct Comp {
+  float s, e;
+  __device__ __forceinline__ void add(float x) {
+    const float t = s + x, b = t - s;
+    e += (s - (t - b)) + (x - b);
+    s = t;
+  }
+};
+
 // ---------------------------------------------------------------------------
 // FMA form. 128 threads, 64 keys, 32 rows at a time, fp32. Thread (ty, tx) = (t / 16,
-// t % 16) has rows 4 ty .. 4 ty + 3 and keys tx + 16 j of the score product.
+// t % 16) has rows 4 ty .. 4 ty + 3 and keys tx + 16 j of the score product. Its four
+// weights of a key are added, and the steps of 32 rows by a compensated sum: 65,536
+// equal rows were 7.6e-5 off in a plain one.
 constexpr int MF_THREADS = 128;
 constexpr int MF_ROWS = 32;
 constexpr int MF_KEYS = 64;
@@ -149,7 +161,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
                                               (size_t)((k0 + key) % P) * D + c);
       *reinterpret_cast<float4*>(&sm.k[key][c]) = kk;
     }
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    Comp sum[4] = {};
     const int end = g.m * A.G;
     for (int r0 = max(g.i0, 0) * A.G; r0 < end; r0 += MF_ROWS) {
       __syncthreads();
@@ -186,6 +198,7 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
             x[i][j] = fmaf(a[i].w, b[j].w, x[i][j]);
           }
       }
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int rr = r0 + 4 * ty + i;
@@ -194,12 +207,14 @@ __global__ void __launch_bounds__(MF_THREADS) k_mass_fma(const __grid_constant__
         const int seen = g.n + rr / A.G + 1 - k0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (tx + 16 * j < seen) sum[j] += exp2f(fmaf(x[i][j], A.scale_l2e, -lse));   // (scale * q may overflow)
+          if (tx + 16 * j < seen) part[j] += exp2f(fmaf(x[i][j], A.scale_l2e, -lse));   // (scale * q may overflow)
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j].add(part[j]);
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sm.sum[ty][tx + 16 * j] = sum[j];
+    for (int j = 0; j < 4; ++j) sm.sum[ty][tx + 16 * j] = sum[j].s + sum[j].e;
     __syncthreads();
     if (t < nk) {
       float y = 0.f;
@@ -278,16 +293,6 @@ struct MtHeader {
 
 // The whole number of log 2 near x.
 __device__ __forceinline__ float mt_near(float x) { return rintf(x * LOG2E); }
-
-// A sum with the rounding error that it has not taken in.
-struct Comp {
-  float s, e;
-  __device__ __forceinline__ void add(float x) {
-    const float t = s + x, b = t - s;
-    e += (s - (t - b)) + (x - b);
-    s = t;
-  }
-};
 
 template <int D>
 __global__ void __launch_bounds__(MT_THREADS, 1)

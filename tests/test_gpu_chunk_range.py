@@ -30,3 +30,19 @@ def test_queries_whose_scaled_values_overflow(dtype, most):
     got, err = mass(c, 0, q, lse, rows, [n], scale, most)
     w, e = ref_mass(c, 0, 0, q[:most], lse[:most], n, most, scale, most)
     assert err == 0 and bool(((got[0, :, :T].double() - w).abs() <= w * e + 1e-30).all())
+
+
+def test_mass_of_65536_rows_in_fp32():
+    """Equal weights of many rows: the sum's error does not grow with their number."""
+    import torch
+    m, G = 4096, 16
+    c = Cache(np.random.default_rng(1), [0], [m], dtype=F32, layers=1, hkv=1, d=64, page=64)
+    rows = Rows([m])
+    q = torch.zeros((rows.n, G, 64), device="cuda")
+    lse = torch.full((rows.n, G), 3.0, device="cuda")
+    got, err = mass(c, 0, q, lse, rows, [0], 0.125, m)
+    assert err == 0
+    want = G * torch.arange(m, 0, -1, device="cuda").double() * np.exp(-3.0)
+    # 3 log2 e: a rounded constant and a rounded product, 1.5 x 2^-24 of 3 in the exponent; exp2 2 ulp (4 x 2^-24); four
+    # weights added at a time and eight threads' sums, 3 + 7 roundings; a compensated sum between, 2; the result, 1
+    assert float(((got[0, 0, :m].double() - want).abs() / want).max()) <= (4.5 + 4 + 10 + 2 + 1) * 2.0 ** -24
