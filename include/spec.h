@@ -618,8 +618,9 @@ typedef struct spec_rope {
  * Key and value of token i go to slot n + i of layer `layer`; with n_nodes as
  * n_new and row_start = s max_nodes the same call serves spec_tree_attention.
  * A token whose page is bad (SPEC_DEV_ERR_PAGE) leaves its query alone.
- * Angles are exact to 2^-32 of a turn at any position (up to the rounding of
- * freq itself); norm and rotation are fp32.
+ * Angles (of freq as the double that it is, up to 10^9) are exact to 2^-32 of a
+ * turn at any position, and then, an eighth of a turn at most, rounded to fp32;
+ * norm and rotation are fp32.
  * Errors: SPEC_ERR_ARG; SPEC_ERR_UNSUPPORTED (cache view); SPEC_ERR_CUDA. */
 int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* qkv_dev, int64_t ld, int n_rows, int n_seq,
                       int n_q_heads, const int32_t* row_start_dev, const int32_t* n_new_dev,

@@ -12,9 +12,10 @@
 // eps), CL = gamma cos, SL = -gamma' sin ..; behind the rotated dims C = gamma, S = 0.
 //
 // The angle of position p is p F of a 64-bit turn, F = freq / 2 pi in units of
-// 2^-64 of a turn: the product wraps as the angle does, so it is as exact at
-// position 2^31 as at 1. Its upper 32 bits, reduced to an eighth of a turn either
-// way, go to sincospif.
+// 2^-64 of a turn: the product wraps as the angle does. F is off by one unit at most
+// (frequencies up to 10^9, of either sign), so p F is by 2^-33 of a turn at position 2^31,
+// and by as much again where its upper 32 bits are rounded. They go, reduced to an eighth
+// of a turn either way and rounded to fp32 (2^-28 at most), to sincospif.
 //
 // Bound: HBM, by the bytes of the rows, and below some 10^4 tokens the way there: places,
 // angles, rows and results follow one another, in one turn or two of a block. Measured, L2
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(RP_THREADS, RP_BLOCKS) k_qk_norm_rope(const __
     for (int x = t; x < nt * half; x += RP_THREADS) {
       const int tok = x / half, p = x - tok * half;
       const int64_t pos = A.positions[(size_t)A.axis[p] * A.ix.n_rows + t_row[tok]];
-      turn_cos_sin((uint32_t)(((uint64_t)pos * A.turn[p]) >> 32), t_cos[tok][p], t_sin[tok][p]);
+      turn_cos_sin((uint32_t)(((uint64_t)pos * A.turn[p] + 0x80000000u) >> 32), t_cos[tok][p], t_sin[tok][p]);
     }
     __syncthreads();
     // a lane group takes up to RP_FLY heads of a token
@@ -287,6 +288,17 @@ __global__ void __launch_bounds__(RP_THREADS, RP_BLOCKS) k_qk_norm_rope(const __
   }
 }
 
+// freq / 2 pi modulo 1 in units of 2^-64: the product with 1 / 2 pi as two doubles, each of
+// its two parts rounded to a unit. (The quotient in double would be off by 2^-53 of itself, which
+// far positions multiply, and a negative one by 2^-53 of a turn where it is brought to [0, 1).)
+uint64_t turn_of(double freq) {
+  constexpr double INV = 0.15915494309189535, INV_LO = -9.839338337591243e-18;
+  auto units = [](double x) { return (uint64_t)std::rint(std::ldexp(x - std::floor(x), 64)); };   // x >= 0
+  const double a = std::fabs(freq), hi = a * INV, lo = std::fma(a, INV, -hi) + a * INV_LO;
+  const uint64_t u = units(hi) + (lo < 0 ? 0 - units(-lo) : units(lo));
+  return freq < 0 ? 0 - u : u;
+}
+
 template <class KT, int D>
 cudaError_t launch_rope(const RopeArgs& A, int blocks, cudaStream_t st) {
   return A.half8 * 8 * 2 == D * (int)sizeof(KT) ? launch_k(k_qk_norm_rope<KT, D, true>, dim3(blocks), dim3(RP_THREADS), 0, st, A)
@@ -324,9 +336,7 @@ extern "C" int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* 
   for (int p = 0; p < rope->dim / 2; ++p) {
     if (!std::isfinite(rope->freq[p])) return set_last_error(SPEC_ERR_ARG, "a frequency is not finite");
     if (rope->axis[p] >= rope->n_axes) return set_last_error(SPEC_ERR_ARG, "a pair's axis is out of range");
-    double turn = rope->freq[p] / 6.283185307179586476925286766559;
-    turn -= std::floor(turn);                    // [0, 1]: whole turns do not matter
-    A.turn[p] = turn < 1.0 ? (uint64_t)std::ldexp(turn, 64) : 0;
+    A.turn[p] = turn_of(rope->freq[p]);
     A.axis[p] = rope->axis[p];
   }
   const int64_t in_bytes = ((n_rows - 1) * ld + heads * d) * esz, q_bytes = (int64_t)n_rows * n_q_heads * d * esz;

@@ -3,7 +3,7 @@ sequences, far positions, long caches, many planes."""
 import numpy as np
 import pytest
 
-from _chunk import BF16, F32, Cache, Rows, attention, check_attention, mass, ref_mass
+from _chunk import BF16, F32, Cache, Rows, attention, check_attention, dev, mass, ref_mass
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,41 @@ def test_mass_of_65536_rows_in_fp32():
     # 3 log2 e: a rounded constant and a rounded product, 1.5 x 2^-24 of 3 in the exponent; exp2 2 ulp (4 x 2^-24); four
     # weights added at a time and eight threads' sums, 3 + 7 roundings; a compensated sum between, 2; the result, 1
     assert float(((got[0, 0, :m].double() - want).abs() / want).max()) <= (4.5 + 4 + 10 + 2 + 1) * 2.0 ** -24
+
+
+PI = "3.14159265358979323846264338327950288419716939937510582097494459230781640628620899"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rotation_angles_at_far_positions(d):
+    """Frequencies of either sign, above and far below a turn, at positions up to 2^31: (1, 0) turns to (cos, sin)."""
+    import torch
+    from decimal import Decimal, localcontext
+    from lossless_speculative_decoding_gb300 import binding as B
+    rng = np.random.default_rng(d)
+    half, m = d // 2, 24
+    freq = np.exp(rng.uniform(np.log(1e-9), np.log(50.0), half)) * rng.choice([-1.0, 1.0], half)
+    freq[:6] = 1.0, -1.0, -1e-6, 2 * np.pi, -3e-20, 1e6
+    pos = rng.integers(-2 ** 31, 2 ** 31, m)
+    pos[:4] = 2 ** 31 - 1, -2 ** 31, 0, 1
+    c = Cache(rng, [0], [m], dtype=F32, layers=1, hkv=1, d=d, page=16)
+    rows = Rows([m])
+    x = torch.zeros((rows.n, 3, d), device="cuda")
+    x[:, :, :half] = 1.0
+    q = torch.zeros((rows.n, 1, d), device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    p = np.zeros((1, rows.n), np.int32)
+    p[0, rows.of(0)] = pos
+    B.spec_qk_norm_rope(c.view, 0, x, 3 * d, rows.n, 1, 1, dev(rows.start), dev(rows.new), dev([0]), B.make_rope(freq), dev(p), None,
+                        None, 0.0, q, err, 0)
+    torch.cuda.synchronize()
+    with localcontext() as ctx:
+        ctx.prec = 70
+        angle = np.array([[float(Decimal(int(a)) * Decimal(float(f)) % (2 * Decimal(PI))) for f in freq] for a in pos])
+    # the angle is off by 2^-32 of a turn and, an eighth of a turn at most, by its rounding to fp32 (2^-28); sine and cosine
+    # by 2 ulp below 1
+    e = 2 * np.pi * (2.0 ** -32 + 2.0 ** -28) + 2.0 ** -23
+    got = q[rows.of(0), 0].double().cpu().numpy()
+    assert int(err.item()) == 0
+    assert np.abs(got[:, :half] - np.cos(angle)).max() <= e
+    assert np.abs(got[:, half:] - np.sin(angle)).max() <= e
