@@ -46,6 +46,7 @@ struct ChunkArgs {
   int key_bits;        // log2 of a unit's keys
   int extra;           // units without keys of a segment
   float scale_l2e;     // scale * log2 e
+  __device__ int deadlines() const { return segment_deadlines(ix.capacity); }
 };
 
 // Segment: tiles [t0, t1) of nt key tiles of (sequence s, row tile rt, head part hk).
@@ -701,7 +702,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
   // at once: producer, issuer and loader stop, the softmax warps finish the segment
   // without a result and stop.
   auto wait = [&](const uint64_t* bar, uint32_t parity) {
-    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err);
+    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, &A);
   };
   auto waitw = [&](const uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   const int P = A.kv.page_size;
@@ -862,6 +863,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
       if (lane == 0) {
         H.seg[sb] = g;
         mbar_arrive(sm_addr(H.seg_full + sb));
+        if (have && part_of(g) == 1) A.joint[blockIdx.x] = joint_of(walk, g, min(A.tok, g.m - g.rt * A.tok) * A.G);
       }
       if (!have) break;
       if (seg > 0 && !waitw(&H.q_free, seg - 1)) break;
@@ -1022,7 +1024,6 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
           }
         }
       }
-      if (part == 1 && t == 0) A.joint[blockIdx.x] = joint_of(walk, g, min(A.tok, g.m - g.rt * A.tok) * A.G);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sm_addr(H.seg_free + sb));

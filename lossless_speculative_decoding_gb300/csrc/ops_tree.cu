@@ -51,6 +51,7 @@ struct TreeArgs {
   int q_box;           // rows of a box of the query's tensor map (tensor-core form)
   int tile_k;          // keys of a unit
   float scale_l2e;     // scale * log2 e
+  __device__ int deadlines() const { return segment_deadlines(kv.max_pages * kv.page_size); }
 };
 
 // Sizes of sequence s (k = 0: padded, or bad). A chunk's rows have to be there too.
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   // the segment without a result and stop, and so does the loader where a
   // segment's place is not free.
   auto wait = [&](const uint64_t* bar, uint32_t parity) {
-    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err);
+    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, &A);
   };
   const int P = A.kv.page_size;
 

@@ -139,13 +139,21 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // A wait that was not over at once, out of line: the waits are many, the code of
-// the roles is better short.
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int* abort, int32_t* err) {
-  if (mbar_wait_deadline(bar, parity, abort)) return true;
+// the roles is better short. (Args: a kernel's arguments, with its err and deadlines().)
+template <class Args>
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int* abort, const Args* A) {
+  int left = A->deadlines();
+  do {
+    if (mbar_wait_deadline(bar, parity, abort)) return true;
+  } while (--left > 0 && *reinterpret_cast<volatile int*>(abort) == 0);
   *reinterpret_cast<volatile int*>(abort) = DERR_TIMEOUT;
-  atomicOr(err, DERR_TIMEOUT);
+  atomicOr(A->err, DERR_TIMEOUT);
   return false;
 }
+// Deadlines of a wait that may last as long as a segment of all a cache's positions (up to 2^30;
+// a tile of 128 takes up to 1.5 us): the next segment's queries, and a group of rows that has
+// none in this one, wait for its end.
+__device__ __forceinline__ int segment_deadlines(int capacity) { return 1 + (capacity >> 22); }
 __device__ __forceinline__ void mbar_init(const uint64_t* bar, int count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sm_addr(bar)), "r"(count));
 }

@@ -84,3 +84,43 @@ def test_rotation_angles_at_far_positions(d):
     assert int(err.item()) == 0
     assert np.abs(got[:, :half] - np.cos(angle)).max() <= e
     assert np.abs(got[:, half:] - np.sin(angle)).max() <= e
+
+
+@pytest.mark.parametrize("most,G,n,spread", [(608, 128, 2 ** 25, 1), (3, 64, 2 ** 25, 304), (1, 1, 2 ** 26, 304)])
+def test_attention_over_tens_of_millions_of_positions(most, G, n, spread):
+    """Segments of 2^18 and 2^19 tiles, each of some 0.3 s, on every block: whole row tiles, row tiles with one group of
+    tokens, single tokens; `spread` sequences share the pages of their first n positions. Keys of zeros but for one, values
+    of ones but for its: even heads weigh all alike, odd ones take that one."""
+    import torch
+    from lossless_speculative_decoding_gb300 import binding as B
+    P, d, at = 2 ** 14, 64, n - 1000
+    m = most if spread == 1 else max(1, most - 1)
+    kv = torch.zeros((n // P + spread, 1, 1, 2, P, d), dtype=torch.bfloat16, device="cuda")
+    kv[:, :, :, 1] = 1.0
+    kv[at // P, 0, 0, 0, at % P, 0], kv[at // P, 0, 0, 1, at % P] = 1.0, 3.0
+    bt = torch.empty((spread, n // P + 1), dtype=torch.int32, device="cuda")
+    bt[:, :-1] = torch.arange(n // P, device="cuda")
+    bt[:, -1] = n // P + torch.arange(spread, device="cuda")
+    view = B.make_kv_view(kv, bt, dtype=BF16, n_pages=n // P + spread, n_layers=1, n_kv_heads=1, page_size=P, head_dim=d,
+                          max_pages=n // P + 1)
+    rows = Rows([m] * spread)
+    q = torch.zeros((rows.n, G, d), dtype=torch.bfloat16, device="cuda")
+    odd = torch.arange(rows.n * G, device="cuda").view(rows.n, G) % 2 == 1       # (a single head: odd rows)
+    q[..., 0] = torch.where(odd, 320.0, 0.0).bfloat16()
+    out, lse = torch.full_like(q, 77.0), torch.full((rows.n, G), 77.0, device="cuda")
+    nb = B.spec_chunk_attention_ws_bytes(view, spread, most, G)
+    ws, err = torch.empty(nb, dtype=torch.uint8, device="cuda"), dev([0])
+    B.spec_chunk_attention(view, 0, q, rows.n, spread, most, G, dev(rows.start), dev(rows.new), dev([n] * spread), 0.125, out, lse, ws,
+                           nb, err, 0)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    live, odd = spread * m, odd[:spread * m]
+    # the others' share of an odd head is 2^26 e^-40 at most, of an even head's value the one's 2 / n; a weight of one bf16
+    # part is off by 2^-8, and so is the result's rounding
+    want = torch.where(odd, 3.0, 1.0)[..., None]
+    assert bool(((out[:live].float() - want).abs() <= want * (2 * 2.0 ** -8 + 2.0 ** -16)).all()) and bool((out[live:] == 77).all())
+    seen = n + 1 + torch.arange(live, device="cuda") % m
+    z = torch.where(odd, 40.0 + 0 * seen[:, None], torch.log(seen.double())[:, None])
+    # sums of equal weights are whole multiples of one; the last of a tile, and each part's, may be rounded: 2^-24 for the
+    # segment and 160 parts; the logarithm's own size 40 in fp32 (6 roundings)
+    assert float((lse[:live].double() - z).abs().max()) <= 162 * 2.0 ** -24 + 6 * 40 * 2.0 ** -24
