@@ -699,8 +699,8 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other waits
-  // at once: producer, issuer and loader stop, the softmax warps finish the segment
-  // without a result and stop.
+  // at once: every role leaves its loops, a softmax warp in the middle of a segment too, which
+  // may have millions of tiles left. The segment has no result.
   auto wait = [&](const uint64_t* bar, uint32_t parity) {
     return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, &A);
   };
@@ -903,8 +903,9 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
       // keys that the lane sees, from the segment's first on; the warp's fewest
       int seen = live ? g.n + g.rt * A.tok + (R.row0 + r) / A.G + 1 - g.t0 * CT_KEYS : 0;
       const int least = __reduce_min_sync(0xffffffffu, live ? seen : 0x7fffffff);
+      bool ok = true;
       for (int ti = 0; ti < R.tiles; ++ti, seen -= CT_KEYS) {
-        waitw(H.s_full + gr, jobs++);
+        if (!(ok = waitw(H.s_full + gr, jobs++))) break;
         tc_fence_after();
         if (any_live) {
           const CtTile T{sT, oT, sc, seen, ti == 0, live};
@@ -963,6 +964,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(sm_addr(H.p_full + gr));
       }
+      if (!ok) break;                            // (aborted: no result)
 
       // ---- the segment's end ----
       const int part = part_of(g);
@@ -971,7 +973,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
       const size_t pr = (((size_t)blockIdx.x * 2 + part) * 2 + gr) * 128 + r;       // (part >= 0)
       if (part >= 0 && live) A.part_ml[pr] = make_float2(some ? ref : -INFINITY, some ? st.l : 0.f);
       if (R.tiles > 0) {
-        waitw(H.o_done + gr, ends++);
+        if (!waitw(H.o_done + gr, ends++)) break;
         tc_fence_after();
         if (any_live) {
           const size_t row = row_at(A, g.r0, g.rt, g.hk, R.row0 + r);

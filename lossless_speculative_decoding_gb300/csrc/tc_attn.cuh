@@ -143,9 +143,8 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 template <class Args>
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, int* abort, const Args* A) {
   int left = A->deadlines();
-  do {
+  while (left-- > 0 && *reinterpret_cast<volatile int*>(abort) == 0)
     if (mbar_wait_deadline(bar, parity, abort)) return true;
-  } while (--left > 0 && *reinterpret_cast<volatile int*>(abort) == 0);
   *reinterpret_cast<volatile int*>(abort) = DERR_TIMEOUT;
   atomicOr(A->err, DERR_TIMEOUT);
   return false;
