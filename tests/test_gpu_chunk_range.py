@@ -3,7 +3,7 @@ sequences, far positions, long caches, many planes."""
 import numpy as np
 import pytest
 
-from _chunk import BF16, F32, Cache, Rows, attention, check_attention, dev, mass, ref_mass
+from _chunk import (BF16, F32, Cache, Rows, attention, check_attention, dev, evict, mass, queries, ref_keep, ref_mass, slots)
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,128 @@ def test_attention_over_tens_of_millions_of_positions(most, G, n, spread):
     # sums of equal weights are whole multiples of one; the last of a tile, and each part's, may be rounded: 2^-24 for the
     # segment and 160 parts; the logarithm's own size 40 in fp32 (6 roundings)
     assert float((lse[:live].double() - z).abs().max()) <= 162 * 2.0 ** -24 + 6 * 40 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("most", [1, 40])
+def test_mass_of_many_sequences(dtype, most):
+    """700 sequences, most of them padded, the first live one behind the first 32."""
+    import torch
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 600, 700)
+    new = np.where(rng.random(700) < 0.7, 0, rng.integers(1, most + 1, 700))
+    new[:70] = 0
+    c = Cache(rng, lens, new, dtype=dtype, layers=1, hkv=2, d=64, page=16)
+    rows = Rows(new)
+    q = queries(rows, 4, 64, dtype, 3)
+    out, lse, err = attention(c, 0, q, rows, lens, 0.125)
+    assert err == 0
+    got, err = mass(c, 0, q, lse, rows, lens, 0.125, most)
+    assert err == 0
+    for s, n in enumerate(lens):
+        n, m = int(n), rows.new[s]
+        if m:
+            w, e = ref_mass(c, s, 0, q[rows.of(s)], lse[rows.of(s)], n, m, 0.125, most)
+            assert bool(((got[s, :, :n + m].double() - w).abs() <= w * e + 1e-37).all()), s
+        assert bool((got[s, :, n + m if m else 0:] == 77).all()), s
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("most", [1, 40])
+def test_rotation_of_many_sequences(dtype, most):
+    """700 sequences, most of them padded: rows find their slots (heads copied, none turned)."""
+    import torch
+    from lossless_speculative_decoding_gb300 import binding as B
+    rng = np.random.default_rng(6)
+    lens = rng.integers(0, 50, 700)
+    new = np.where(rng.random(700) < 0.7, 0, rng.integers(1, most + 1, 700))
+    c = Cache(rng, lens, new, dtype=dtype, layers=1, hkv=2, d=64, page=16)
+    rows = Rows(new, 1)
+    x = torch.randn((rows.n, 6, 64), device="cuda").to(c.kv.dtype)
+    q = torch.full((rows.n, 2, 64), 77.0, device="cuda", dtype=c.kv.dtype)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.spec_qk_norm_rope(c.view, 0, x, 384, rows.n, 700, 2, dev(rows.start), dev(rows.new), dev(lens), B.make_rope([]), None, None, None,
+                        0.0, q, err, 0)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    live = torch.zeros(rows.n, dtype=torch.bool, device="cuda")
+    for s, n in enumerate(lens):
+        m = rows.new[s]
+        if m:
+            at, n = rows.of(s), int(n)
+            live[at] = True
+            got = slots(c, s, n + m)
+            assert torch.equal(got[:n], c.rows[s][:n]), s
+            assert torch.equal(got[n:, 0].transpose(1, 2).reshape(m, 4, 64), x[at, 2:].double()), s
+    assert torch.equal(q[live], x[live, :2]) and bool((q[~live] == 77).all())
+
+
+def test_mass_rows_past_2_to_31_values():
+    """The last rows of a mass array start past 2^31 values; what was there is read from there."""
+    import torch
+    lens, new, ld = [50, 7], [4, 70], 2 ** 29
+    for dtype in (BF16, F32):
+        c = Cache(np.random.default_rng(3), lens, new, dtype=dtype, layers=1, hkv=4, d=128, page=16)
+        rows = Rows(new)
+        q = queries(rows, 8, 128, dtype, 5)
+        out, lse, err = attention(c, 0, q, rows, lens, 0.09)
+        assert err == 0
+        before, got = torch.empty((2, 4, ld), device="cuda"), torch.empty((2, 4, ld), device="cuda")
+        before[..., :200] = torch.rand((2, 4, 200), device="cuda") + 1
+        got, err = mass(c, 0, q, lse, rows, lens, 0.09, 70, before, out=got, ld=ld)
+        assert err == 0
+        for s, n in enumerate(lens):
+            w, e = ref_mass(c, s, 0, q[rows.of(s)], lse[rows.of(s)], n, new[s], 0.09, 70)
+            y = w.clone()
+            y[:, :n] += before[s, :, :n].double()
+            assert bool(((got[s, :, :n + new[s]].double() - y).abs() <= w * e + y * 2.0 ** -24 + 1e-37).all()), (dtype, s)
+        del before, got
+
+
+# --------------------------------------------------------------------------- eviction
+def check_evict(c, lens, x, budget, recent):
+    """Kept positions, their masses and their rows of every plane."""
+    import torch
+    old = [slots(c, s, n) for s, n in enumerate(lens)]
+    out, kept, ln, err = evict(c, lens, torch.from_numpy(x).cuda(), budget, recent)
+    assert err == 0 and ln.tolist() == [min(n, budget) for n in lens]
+    for s, n in enumerate(lens):
+        k = min(n, budget)
+        want = np.empty((c.layers, c.hkv, k), np.int64)
+        for layer in range(c.layers):
+            for h in range(c.hkv):
+                want[layer, h] = ref_keep(x[layer, s, h], n, budget, recent) if n > budget else np.arange(n)
+        assert np.array_equal(kept[:, s, :, :k], want) and (kept[:, s, :, k:] == -1).all()
+        assert np.array_equal(out[:, s, :, :k], np.take_along_axis(x[:, s], want, 2), equal_nan=True)
+        assert (out[:, s, :, k:] == 77).all()
+        at = torch.from_numpy(want).cuda().permute(2, 0, 1)[..., None, None].expand(-1, -1, -1, 2, c.d)
+        assert torch.equal(slots(c, s, k), torch.gather(old[s], 0, at)), s
+
+
+def masses(rng, shape, kind):
+    x = np.exp(3 * rng.standard_normal(shape)).astype(np.float32)
+    if kind == "ties":
+        x = np.floor(x).clip(0, 5).astype(np.float32)
+    elif kind == "nan":
+        x[rng.random(shape) < 0.3] = np.nan
+    return x
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 64), (BF16, 128), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("kind", ["plain", "ties"])
+@pytest.mark.parametrize("lens,budget", [([1500, 701, 40], 700), ([900, 1, 641], 640), ([500, 400, 30], 31)])
+def test_evict_many_planes(dtype, d, kind, lens, budget):
+    """480 planes: the form for many blocks, in batches of rows that end whole and within one."""
+    rng = np.random.default_rng(budget + d)
+    c = Cache(rng, lens, [0, 0, 0], dtype=dtype, layers=40, hkv=4, d=d, page=48)
+    check_evict(c, lens, masses(rng, (40, 3, 4, max(lens) + 1), kind), budget, 13)
+
+
+@pytest.mark.parametrize("kind", ["plain", "ties", "nan"])
+@pytest.mark.parametrize("budget,recent", [(4001, 100), (8192, 0), (1, 0), (8100, 8100)])
+def test_evict_long_sequences(kind, budget, recent):
+    """More positions than the selection holds, as many, and fewer."""
+    lens = [12011, 8193, 8192, 8191]
+    rng = np.random.default_rng(budget)
+    c = Cache(rng, lens, [0] * 4, dtype=BF16, layers=1, hkv=2, d=64, page=64)
+    check_evict(c, lens, masses(rng, (1, 4, 2, max(lens) + 3), kind), budget, recent)
