@@ -14,6 +14,14 @@ constexpr int TREE_N = SPEC_TREE_MAX_NODES;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Keys of a box that a tile of keys is brought in: a box never straddles pages, so it is the
+// largest power of two up to the tile that divides a page.
+inline int key_box(int page_size, int tile) {
+  int kb = 16;
+  while (kb < tile && page_size % (2 * kb) == 0) kb *= 2;
+  return kb;
+}
+
 // Host checks shared by the entry points; table: the block table is needed.
 inline int check_kv_view(const spec_kv_view* kv, bool table) {
   if (!kv || !kv->kv_dev || (table && !kv->block_table_dev)) return set_last_error(SPEC_ERR_ARG, "null cache view");

@@ -533,7 +533,6 @@ struct CtCfg {
   static constexpr int SMEM = NBUF * BUF + 2 * Q + TAIL;
 };
 
-template <int NBUF>
 struct CtHeader {
   uint64_t full[CT_RING], done[CT_RING], s_full[2], p_full[2], o_done[2], seg_full[2], seg_free[2];
   uint64_t q_full, q_free, fin;
@@ -657,8 +656,8 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
   extern __shared__ unsigned char ct_raw[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(ct_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* qsm = base + NBUF * C::BUF;
-  CtHeader<NBUF>& H = *reinterpret_cast<CtHeader<NBUF>*>(qsm + 2 * C::Q);
-  static_assert(sizeof(CtHeader<NBUF>) + 1024 <= C::TAIL, "header and alignment slack");
+  CtHeader& H = *reinterpret_cast<CtHeader*>(qsm + 2 * C::Q);
+  static_assert(sizeof(CtHeader) + 1024 <= C::TAIL, "header and alignment slack");
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const uint32_t bufs = sm_addr(base), q_addr = sm_addr(qsm);
   if (t == 0) {
@@ -1217,9 +1216,7 @@ extern "C" int spec_chunk_attention(const spec_kv_view* kv, int layer, const voi
     const int blocks = std::min(2 * sms, plan.max_blocks);
     e = d == 128 ? launch_fma<128>(A, blocks, st) : launch_fma<64>(A, blocks, st);
   } else {
-    // a box of keys never straddles pages: the largest power of two up to a tile that divides a page
-    int kb = 16;
-    while (kb < CT_KEYS && kv->page_size % (2 * kb) == 0) kb *= 2;
+    const int kb = key_box(kv->page_size, CT_KEYS);
     CUtensorMap map, qmap;
     if (q_make_map(&qmap, q_dev, d, n_q_heads, (uint64_t)n_rows, A.G, plan.tok / 2) ||
         kv_make_group_map(&map, kv->kv_dev, d, kv->page_size, (uint64_t)kv->n_pages * kv->n_layers * kv->n_kv_heads * 2, kb))

@@ -663,9 +663,7 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
 
 template <int D>
 cudaError_t launch_mass_tc(MassArgs A, int blocks, cudaStream_t st) {
-  // a box of keys never straddles pages: the largest power of two up to a tile that divides a page
-  int kb = 16;
-  while (kb < MT_KEYS && A.kv.page_size % (2 * kb) == 0) kb *= 2;
+  const int kb = key_box(A.kv.page_size, MT_KEYS);
   // tiles of rows: whole tokens, no more than a chunk counts; where they are small, the room goes to keys
   A.tok = std::max(1, std::min(128 / A.G, std::min(A.last, A.ix.max_new)));
   A.q_half = (A.tok * A.G + 15) / 16 * 16 * 128;

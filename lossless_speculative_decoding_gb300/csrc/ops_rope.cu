@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(RP_THREADS, RP_BLOCKS) k_qk_norm_rope(const __
 // far positions multiply, and a negative one by 2^-53 of a turn where it is brought to [0, 1).)
 uint64_t turn_of(double freq) {
   constexpr double INV = 0.15915494309189535, INV_LO = -9.839338337591243e-18;
-  auto units = [](double x) { return (uint64_t)std::rint(std::ldexp(x - std::floor(x), 64)); };   // x >= 0
+  auto units = [](double x) { return (uint64_t)std::rint((x - std::floor(x)) * 0x1p64); };   // x >= 0
   const double a = std::fabs(freq), hi = a * INV, lo = std::fma(a, INV, -hi) + a * INV_LO;
   const uint64_t u = units(hi) + (lo < 0 ? 0 - units(-lo) : units(lo));
   return freq < 0 ? 0 - u : u;

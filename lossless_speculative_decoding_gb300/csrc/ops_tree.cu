@@ -1179,13 +1179,6 @@ cudaError_t launch_tc(const TreeArgs& A, const CUtensorMap& map, const CUtensorM
   return e == cudaSuccess ? join<D, bf16_t, CHAIN>(A, blocks, st) : e;
 }
 
-// A box of keys never straddles pages: the largest power of two up to a tile that divides a page.
-int key_box(int page_size) {
-  int kb = 16;
-  while (kb < TT_KEYS && page_size % (2 * kb) == 0) kb *= 2;
-  return kb;
-}
-
 }  // namespace
 
 size_t chain_ws_bytes(const spec_kv_view& kv, int max_new, int hq) { return TreePlan(kv, max_new, hq).total; }
@@ -1198,7 +1191,7 @@ int launch_chain_attention(const spec_kv_view& kv, int layer, const void* q, int
   const TreeArgs A{kv, q, out, cache_len, n_new, nullptr, row_start, lse, err, reinterpret_cast<float*>(w),
                    reinterpret_cast<float2*>(w + plan.ml), reinterpret_cast<int4*>(w + plan.joint), layer, n_seq, max_new, hq,
                    hq / kv.n_kv_heads, n_rows, plan.rows, plan.q_box, plan.tile_k, scale_l2e};
-  const int kb = key_box(kv.page_size), d = kv.head_dim, blocks = std::min(sms, plan.max_blocks);
+  const int kb = key_box(kv.page_size, TT_KEYS), d = kv.head_dim, blocks = std::min(sms, plan.max_blocks);
   CUtensorMap map, qmap;
   if (q_make_map(&qmap, q, d, hq, (uint64_t)n_rows, A.G, plan.q_box / A.G) ||
       kv_make_group_map(&map, kv.kv_dev, d, kv.page_size, (uint64_t)kv.n_pages * kv.n_layers * kv.n_kv_heads * 2, kb))
@@ -1244,7 +1237,7 @@ extern "C" int spec_tree_attention(const spec_kv_view* kv, int layer, const void
   const int blocks = std::min((plan.tc ? 1 : 2) * sms, plan.max_blocks);
   cudaError_t e;
   if (plan.tc) {
-    const int kb = key_box(kv->page_size);
+    const int kb = key_box(kv->page_size, TT_KEYS);
     CUtensorMap map, qmap;
     if (q_make_map(&qmap, q_dev, d, n_q_heads, (uint64_t)n_seq * max_nodes, A.G, plan.q_box / A.G) ||
         kv_make_group_map(&map, kv->kv_dev, d, kv->page_size, (uint64_t)kv->n_pages * kv->n_layers * kv->n_kv_heads * 2, kb))
