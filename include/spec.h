@@ -488,8 +488,8 @@ typedef struct spec_kv_view {
  * weights); bf16 results are rounded once.
  * Slots past n + n_nodes[s] may hold anything. Every slot up to there has to
  * hold finite keys and values (a NaN of one node may reach the others). Scores
- * of any size are taken (q.K and scale * q.K below 2^126), told apart as far as
- * the rounding of fp32 sums of their size goes. The same call gives the same
+ * of any size are taken (q.K and scale * q.K below 2^126; fp32: the elements of
+ * scale * q too), told apart as far as the rounding of fp32 sums of their size goes. The same call gives the same
  * bits; where a sequence's keys are cut into parts summed apart depends on the
  * batch. A sequence with a bad length is left
  * out (SPEC_DEV_ERR_POS); rows that need a bad page hold no usable value
@@ -579,8 +579,11 @@ int spec_token_logprobs(const void* logits_dev, int dtype, int64_t ld, int n_row
  * one, one token of plain decoding, the rows of a verify step), whose rows are
  * row_start[s] .. row_start[s] + m - 1 of n_rows rows; token i belongs in slot
  * n + i and sees the positions 0 .. n + i. One step is
- *   spec_qk_norm_rope, spec_chunk_attention (or spec_tree_attention) and, where
- *   the cache is bounded, spec_attention_mass in every layer; then spec_kv_evict.
+ *   spec_qk_norm_rope, spec_chunk_attention and, where the cache is bounded,
+ *   spec_attention_mass in every layer; then spec_kv_evict.
+ * A tree of drafts goes by spec_qk_norm_rope and spec_tree_attention, which leaves
+ * no lse: its nodes' weights are not counted. (The accepted ones' can be, once
+ * they are committed, by another spec_chunk_attention of them as a chunk.)
  * Rows of no sequence are neither read into a result nor written; rows of two
  * sequences must not be the same. m = 0 is a padded sequence: nothing of it is
  * written. A sequence with n < 0, m < 0, rows outside [0, n_rows), more tokens
@@ -617,10 +620,10 @@ typedef struct spec_rope {
  *     neither qkv_dev nor the cache.
  * Key and value of token i go to slot n + i of layer `layer`; with n_nodes as
  * n_new and row_start = s max_nodes the same call serves spec_tree_attention.
- * A token whose page is bad (SPEC_DEV_ERR_PAGE) leaves its query alone.
+ * Of a token whose page is bad (SPEC_DEV_ERR_PAGE) only the query is written.
  * Angles (of freq as the double that it is, up to 10^9) are exact to 2^-32 of a
  * turn at any position, and then, an eighth of a turn at most, rounded to fp32;
- * norm and rotation are fp32.
+ * norm and rotation are fp32 (with gamma |x| below 2^60: its squares are summed).
  * Errors: SPEC_ERR_ARG; SPEC_ERR_UNSUPPORTED (cache view); SPEC_ERR_CUDA. */
 int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* qkv_dev, int64_t ld, int n_rows, int n_seq,
                       int n_q_heads, const int32_t* row_start_dev, const int32_t* n_new_dev,
@@ -642,9 +645,11 @@ int spec_qk_norm_rope(const spec_kv_view* kv, int layer, const void* qkv_dev, in
  * Scores, softmax statistics and sums are fp32 (the sum of weights is of the
  * fp32 weights). Against a bf16 cache a weight enters the sum of values as two
  * bf16 parts where every sequence has at most 64 tokens and 128 (token, head)
- * rows per kv head (max_new decides), as one bf16 value otherwise; bf16 results
- * are rounded once. Slots past n + m may hold anything; every slot up to there
- * has to hold finite keys and values. Scores of any size are taken (q.K and
+ * rows per kv head (max_new decides, for the whole batch: a single token beside a
+ * prompt has one part), as one bf16 value otherwise, off by 2^-8 of itself at most;
+ * bf16 results are rounded once. Slots past n + m may hold anything; every slot up
+ * to there has to hold finite keys, and values below 2^90 (they are summed before
+ * the division by the sum of weights). Scores of any size are taken (q.K and
  * scale * q.K below 2^126). The same call gives the same bits; where a
  * sequence's keys are cut into parts summed apart depends on the batch. Rows
  * that need a bad page hold no usable value (SPEC_DEV_ERR_PAGE). Errors:
@@ -668,8 +673,10 @@ int spec_chunk_attention(const spec_kv_view* kv, int layer, const void* q_dev, i
  *     array or one that does not overlap it (nor q and lse); mass_dev may be NULL
  *     (zeros). A sequence of more than ld positions is left out (SPEC_DEV_ERR_POS).
  * lse finite where a token is counted. fp32, in a fixed order: the same call gives
- * the same bits. The exponent's terms are rounded before they cancel, so a weight is
- * off by some 2^-21 of scale * sum |q_i K_i| + |lse|, relative to itself. Positions
+ * the same bits, and rows added with the rounding errors carried along. The
+ * exponent's terms are rounded before they cancel, so a weight is off, relative to
+ * itself, by some 2^-21 of scale * sum |q_i K_i| + |lse|, and by the rounding of a
+ * sum of head_dim products (head_dim 2^-24 of scale * sum |q_i K_i| at most). Positions
  * on a bad page get no usable value (SPEC_DEV_ERR_PAGE).
  * Errors: as spec_chunk_attention; SPEC_ERR_UNSUPPORTED also for a scale beyond
  * 2^-64 .. 2^64. */

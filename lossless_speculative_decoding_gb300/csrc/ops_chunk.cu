@@ -502,11 +502,12 @@ __global__ void __launch_bounds__(CJ_WARPS * 32) k_chunk_join(const __grid_const
 // Bound by the MMAs and what feeds them: an iteration's two S and two P V are 2,048 cycles
 // of tensor cores, and as many of the shared memory's port (an S MMA reads 8 KB in its
 // 64 cycles, all that the port gives, and 64 KB of keys and values come in beside it);
-// with the issuer's waits it takes 2,600. Without the exponentials the kernel takes as long,
+// with the issuer's waits it takes 2,600. (168 registers a thread and 16 bytes of
+// spills; with 72 the chunks took 142 us for 139.) Without the exponentials the kernel takes as long,
 // without any of the softmax's arithmetic 7% less. Measured, L2 cold, 32 on 8 heads of 128: a
-// chunk of 1,021 tokens behind 65,521 720 us (0.78 of the MMA rate; 800 where the clocks
-// have come down to the power cap's), a prompt of 5,288 175 us (0.67), eight chunks of 17
-// to 701 behind 1,288 to 5,288 139 us (0.64): a segment's switch is 10,000 cycles from its
+// chunk of 1,021 tokens behind 65,521 720 us (0.78 of the MMA rate; 780 to 810 where the
+// clocks have come down to the power cap's), a prompt of 5,288 174 us (0.67), eight chunks
+// of 17 to 701 behind 1,288 to 5,288 139 us (0.64): a segment's switch is 10,000 cycles from its
 // last S to the next one's first weights (last weights and P V 3,000, results 3,500, the
 // next queries and S). Slower: an issuer for each group (951 us where one had 798), sixteen
 // softmax warps, scores summed one by one, the sum of the rounded weights; barriers for
@@ -1107,9 +1108,10 @@ __global__ void __launch_bounds__(CX_WARPS * 32) k_chunk_tc_join(const __grid_co
   }
 }
 
-// Shape of a launch, from sizes and types alone. Few bf16 tokens go by the tree attention's
-// kernel, whose weights have 16 bits: a token decoded alone and one verified in a tree
-// meet the same arithmetic, 0.0017 off a 64-bit result for 0.0023. Its time and that of
+// Shape of a launch, from sizes and types alone. A batch of few bf16 tokens goes by the tree
+// attention's kernel, whose weights have 16 bits: tokens decoded without a prompt in the batch
+// meet the arithmetic of those verified in a tree, 0.0017 off a 64-bit result for 0.0023. (With a
+// prompt among them all go by the form here.) Its time and that of
 // the tensor-core form here, one token each: one sequence of 5,236 on 10 heads 21.7 and
 // 24.0 us, 64 of 336 to 5,236 168 and 162, 16 of them 62 and 55; one of 65,521 on 8 heads
 // 59 and 64; 32 tokens on that 67 and 66, eight of 1,288 to 5,288 43 and 38. (With 256 rows

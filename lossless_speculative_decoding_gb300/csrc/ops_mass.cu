@@ -671,7 +671,8 @@ cudaError_t launch_mass_tc(MassArgs A, int blocks, cudaStream_t st) {
   A.nk = std::min(MT_MAX_NK, (MtCfg<D>::ROOM - A.nq * A.q_half * (D / 64)) / MtCfg<D>::BUF / 2 * 2);   // a ring for each issuer
   // Pairs of blocks where units are long and few, alone and paired: every token of a prompt of 5,288 on 8 kv heads
   // 150 and 104 us, two of them 217 and 201, four 448 and 435, four of 2,000 93 and 98, the last 512 tokens of eight
-  // prompts 101 and 113; the last 32 (one tile of rows) 22 and 30.
+  // prompts 101 and 113; the last 32 (one tile of rows) 22 and 30. (Four of 5,288 would gain 3%, four of 2,000, as
+  // many planes, lose 5%; the rule leaves both alone.)
   A.pair = (std::min({A.last, A.ix.max_new, A.ix.capacity}) + A.tok - 1) / A.tok >= MT_PAIR_TILES &&
                    (int64_t)A.ix.n_seq * A.kv.n_kv_heads <= MT_PAIR_PLANES
                ? 2
