@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(CT_THREADS, 1)
   // at once: every role leaves its loops, a softmax warp in the middle of a segment too, which
   // may have millions of tiles left. The segment has no result.
   auto wait = [&](const uint64_t* bar, uint32_t parity) {
-    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, &A);
+    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err, A.deadlines());
   };
   auto waitw = [&](const uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   const int P = A.kv.page_size;

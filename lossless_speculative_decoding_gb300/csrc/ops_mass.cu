@@ -37,7 +37,6 @@ struct MassArgs {
   int pair;            // blocks that share a unit's rows: 1 or 2
   float scale_l2e;     // scale * log2 e
   float inv_scale;
-  __device__ int deadlines() const { return 1; }   // (no wait is for a whole unit)
 };
 
 // Unit: key tile `tile` of (sequence s, kv head hk), its rows from token i0 on.
@@ -358,14 +357,15 @@ __global__ void __launch_bounds__(MT_THREADS, 1)
   const uint32_t tmem = H.tmem;
   // A wait that runs out raises the block's abort flag, which ends its other waits at
   // once: every role leaves its loops (the sums of a unit that is not over are not
-  // written), and so does the other block of a pair when its own wait runs out.
+  // written), and so does the other block of a pair when its own wait runs out. (One
+  // deadline: no wait is for a whole unit.)
   auto waitw = [&](const uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, &A)) != 0;
+    return __all_sync(0xffffffffu, mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err, 1)) != 0;
   };
   // the same for a barrier that the other block arrives at
   auto waitw_pair = [&](const uint64_t* bar, uint32_t parity) {
     const bool ok = mbar_try_cluster(sm_addr(bar), parity & 1) ||
-                    (wait_long(sm_addr(bar), parity & 1, &H.abort, &A) && mbar_try_cluster(sm_addr(bar), parity & 1));
+                    (wait_long(sm_addr(bar), parity & 1, &H.abort, A.err, 1) && mbar_try_cluster(sm_addr(bar), parity & 1));
     return __all_sync(0xffffffffu, ok) != 0;
   };
   const int P = A.kv.page_size;

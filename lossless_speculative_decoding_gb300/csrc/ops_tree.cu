@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1)
   // the segment without a result and stop, and so does the loader where a
   // segment's place is not free.
   auto wait = [&](const uint64_t* bar, uint32_t parity) {
-    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, &A);
+    return mbar_try(sm_addr(bar), parity & 1) || wait_long(sm_addr(bar), parity & 1, &H.abort, A.err, A.deadlines());
   };
   const int P = A.kv.page_size;
 
